@@ -23,6 +23,8 @@ __all__ = [
     "build", "lib", "MoeError", "route", "route_stats", "load_stats", "dispatch", "dispatch_ep", "permute",
     "combine", "dispatch_workspace_size", "dispatch_workspace", "status_string", "ROUTE_AUTO", "ROUTE_TCGEN05",
     "ROUTE_SIMT", "SCALE_FP32", "SCALE_UE8M0", "Dispatch", "DispatchEP", "route_dispatch",
+    "quantize_weight", "expert_gemm", "expert_wgrad", "swiglu", "swiglu_backward", "moe_layer",
+    "layer_workspace_size", "layer_workspace", "SwiGLU", "SwiGLUGrad", "LayerOut",
 ]
 
 MOE_OK = 0
@@ -33,6 +35,7 @@ ERR_WORKSPACE = 4
 ERR_CUDA = 5
 ERR_TIMEOUT = 6
 ERR_BAD_INDEX = 7
+ERR_BAD_SCALE = 8
 
 ROUTE_AUTO = 0
 ROUTE_TCGEN05 = 1
@@ -44,7 +47,8 @@ EXPORTED_SYMBOLS = (
     "moe_route", "moe_route_ex", "moe_dispatch_workspace_size", "moe_dispatch",
     "moe_permute", "moe_combine", "moe_status_string", "moe_abi_version", "moe_dispatch_noalloc",
     "moe_combine_residual", "moe_dispatch_ex", "moe_permute_ex", "moe_route_stats", "moe_load_stats",
-    "moe_dispatch_ep", "moe_route_dispatch",
+    "moe_dispatch_ep", "moe_route_dispatch", "moe_quantize_weight", "moe_expert_gemm", "moe_expert_wgrad",
+    "moe_swiglu", "moe_swiglu_backward", "moe_layer_workspace_size", "moe_layer",
 )
 
 SCALE_FP32, SCALE_UE8M0 = 0, 1
@@ -112,6 +116,20 @@ def lib():
     L.moe_route_dispatch.argtypes = [P, P, P, I64, I32, I32, I32, I32, P, P, P, P, P, P, P, P, P, SZ,
                                      ctypes.POINTER(ctypes.c_int), P]
     L.moe_route_dispatch.restype = I32
+    L.moe_quantize_weight.argtypes = [P, I32, I32, I32, P, P, I32, P]
+    L.moe_quantize_weight.restype = I32
+    L.moe_expert_gemm.argtypes = [P, P, I32, P, P, I32, P, I64, I32, I32, I32, I32, P, P, P]
+    L.moe_expert_gemm.restype = I32
+    L.moe_expert_wgrad.argtypes = [P, P, P, I32, P, I64, I32, I32, I32, P, P, I32, P, P]
+    L.moe_expert_wgrad.restype = I32
+    L.moe_swiglu.argtypes = [P, I64, I32, P, P, P, P, I32, P]
+    L.moe_swiglu.restype = I32
+    L.moe_swiglu_backward.argtypes = [P, P, P, I32, I64, I32, P, P, P, I32, P, P]
+    L.moe_swiglu_backward.restype = I32
+    L.moe_layer_workspace_size.argtypes = [I32, I32, I32, I32, I32]
+    L.moe_layer_workspace_size.restype = SZ
+    L.moe_layer.argtypes = [P, P, P, P, P, P, P, I32, P, I32, I32, I32, I32, I32, I32, P, P, P, P, P, SZ, P]
+    L.moe_layer.restype = I32
     L.moe_status_string.argtypes = [I32]
     L.moe_status_string.restype = ctypes.c_char_p
     L.moe_abi_version.argtypes = []
@@ -477,3 +495,7 @@ def combine(Y: torch.Tensor, row_map: torch.Tensor, topk_w: torch.Tensor, out=No
                                           _ptr(out), _status_ptr(status), _stream(stream))
         _check(code, "moe_combine_residual")
     return out
+
+
+from .experts import (LayerOut, SwiGLU, SwiGLUGrad, expert_gemm, expert_wgrad, layer_workspace,  # noqa: E402
+                      layer_workspace_size, moe_layer, quantize_weight, swiglu, swiglu_backward)

@@ -1,0 +1,472 @@
+// expert_gemm.cu -- the experts' matrix products in E4M3 with power-of-two block
+// scales, over the ragged row groups that the dispatch writes.
+//
+//   Y[r, m] = sum_k x[r, k] sx[r, k/128] * w[e(r), m, k] sw[e(r), m/128, k/128]
+//
+// (m over the weight's rows, k over its columns; `transpose` swaps the two, which
+// is the product of the input gradient).  Every scale is a power of two, so the
+// tensor cores apply them themselves (tcgen05.mma kind::mxf8f6f4.block_scale, one
+// UE8M0 byte per row and K = 32 step): no partial sum leaves TMEM before the end
+// of the reduction, and the accumulation is fp32 throughout.
+//
+// The weights sit on the M side of the MMA (128 of their output features per
+// tile) and the tokens on the N side, whose size can be any multiple of 16: a
+// group of c rows is cut into ceil(c / 224) tiles of equal size, so that a ragged
+// group pays for at most 15 rows that it does not have.
+//
+// Persistent CTAs, one per SM; warp roles:
+//   warp 0      TMA producer (weights 128 x 128, tokens in boxes of 32 rows)
+//   warp 1      MMA issuer (one thread), copies the scales to TMEM (tcgen05.cp)
+//   warp 2      scale producer: gathers the bytes of four 128-blocks per row
+//   warp 3      allocates TMEM
+//   warps 4..7  epilogue: TMEM -> registers -> bf16, transposed through shared memory
+#include <mutex>
+
+#include "expert_internal.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTileM = 128;        // output features per tile
+constexpr int kTileN = 224;        // most tokens per tile: two accumulators and the scales fit TMEM
+constexpr int kBlk = 128;          // reduction block of a scale, and of a ring stage
+constexpr int kStages = 4;
+constexpr int kScaleSlots = 4;
+constexpr int kABytes = kTileM * kBlk;
+constexpr int kBBytes = kTileN * kBlk;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kScaleSlotBytes = 512 + 1024;   // 128 feature words, 256 token words
+constexpr int kEpiBytes = 4 * 32 * 64;        // per epilogue warp 32 tokens x 32 features
+constexpr int kThreads = 256;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSfCol = 2 * kTileN;       // scales behind the two accumulators: 2 x (4 + 8) columns
+constexpr int kMaxE = 256;
+
+struct Tail {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t sf_full[kScaleSlots], sf_empty[kScaleSlots];
+    uint64_t acc_full[2], acc_empty[2], drain;
+    uint32_t tmem_base;
+    int abort, bad_index, bad_scale;
+    int tiles;                    // token tiles of all groups
+    int first[kMaxE + 1];         // first token tile of each group
+    int begin[kMaxE], count[kMaxE];
+};
+
+constexpr size_t kSmemBytes =
+    1024 + kStages * kStageBytes + kScaleSlots * kScaleSlotBytes + kEpiBytes + sizeof(Tail);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+struct Params {
+    const void *X_scale, *W_scale;
+    const int32_t *offsets;
+    int64_t R;
+    int E, out, red;              // output features, reduction length
+    int transpose, x_ue8m0, w_ue8m0;
+    int m_tiles;
+    void *Y;
+    int32_t *status;
+};
+
+// One tile of a group: where its rows start, how many it holds.
+struct Tile {
+    int e, m0, rows;
+    int64_t row0;
+};
+
+__device__ __forceinline__ Tile find_tile(const Tail &t, int tile, int m_tiles, int E)
+{
+    const int j = tile / m_tiles;
+    int lo = 0, hi = E - 1;       // the last group whose first tile is <= j
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.first[mid] <= j)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    Tile r;
+    r.e = lo;
+    r.m0 = (tile - j * m_tiles) * kTileM;
+    const int c = t.count[lo], n = t.first[lo + 1] - t.first[lo], i = j - t.first[lo];
+    const int size = ((c + n - 1) / n + 15) & ~15;   // equal parts, whole in 16
+    r.row0 = static_cast<int64_t>(t.begin[lo]) + static_cast<int64_t>(i) * size;
+    const int left = c - i * size;
+    r.rows = left < size ? left : size;   // (never empty: size <= kTileN, and n - 1 tiles of that do not hold c)
+    return r;
+}
+
+// kind::mxf8f6f4, E4M3 x E4M3 -> fp32, UE8M0 scales; the scale byte of the word is `sf`.
+__device__ __forceinline__ uint32_t make_idesc(uint32_t N, uint32_t a_mn_major, uint32_t sf)
+{
+    return (sf << 4) | (a_mn_major << 15) | ((N >> 3) << 17) | (1u << 23) | ((kTileM >> 4) << 24) | (sf << 29);
+}
+
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                           uint32_t sfb, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// 32 rows of 16 bytes from shared memory to 4 TMEM columns, repeated in the four lane quarters.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr)
+{
+    const uint64_t desc = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
+                          (1ull << 46);   // no swizzle, 8-row groups 128 B apart
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    expert_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Params p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sf_ring = ring + kStages * kStageBytes;
+    uint8_t *epi = sf_ring + kScaleSlots * kScaleSlotBytes;
+    Tail &tail = *reinterpret_cast<Tail *>(epi + kEpiBytes);
+    volatile int *abort_flag = &tail.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&tail.full[s], 1);
+            mbar_init(&tail.empty[s], 1);
+        }
+        for (int s = 0; s < kScaleSlots; ++s) {
+            mbar_init(&tail.sf_full[s], 1);
+            mbar_init(&tail.sf_empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tail.acc_full[b], 1);
+            mbar_init(&tail.acc_empty[b], 4);
+        }
+        mbar_init(&tail.drain, 1);
+        tail.abort = tail.bad_index = tail.bad_scale = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+    }
+    if (warp == 3) {
+        tmem_alloc(&tail.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    // the groups: rows and token tiles of each (a group outside [0, R] holds none)
+    __syncthreads();
+    {
+        const int e = threadIdx.x;
+        int64_t a = 0, b = 0;
+        if (e < p.E) {
+            a = p.offsets ? p.offsets[e] : 0;
+            b = p.offsets ? p.offsets[e + 1] : p.R;
+            if (a < 0 || b < a || b > p.R) {
+                tail.bad_index = 1;
+                a = b = 0;
+            }
+            tail.begin[e] = static_cast<int>(a);
+            tail.count[e] = static_cast<int>(b - a);
+        }
+        int v = static_cast<int>((b - a + kTileN - 1) / kTileN);
+        // inclusive scan over the 256 threads
+        int x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        int *part = reinterpret_cast<int *>(epi);
+        if (lane == 31) part[warp] = x;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) x += part[w];
+        if (e < p.E) tail.first[e + 1] = x;
+        if (e == 0) tail.first[0] = 0;
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = tail.tmem_base;
+    const int tiles = tail.first[p.E] * p.m_tiles;
+    const int blocks = p.red / kBlk;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // weights of a group are read by several CTAs at about the same time, tokens too
+            const uint64_t keep = l2_policy_evict_normal();
+            uint32_t s = 0, ph = 0, issued = 0;
+            for (int tile = blockIdx.x; tile < tiles && !*abort_flag; tile += gridDim.x) {
+                const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
+                const int boxes = (t.rows + 31) >> 5;
+                for (int kb = 0; kb < blocks; ++kb) {
+                    if (!mbar_wait_bounded(&tail.empty[s], ph ^ 1u, abort_flag)) break;
+                    uint8_t *a = ring + s * kStageBytes, *b = a + kABytes;
+                    mbar_arrive_expect_tx(&tail.full[s], kABytes + boxes * 32 * kBlk);
+                    if (p.transpose)
+                        tma_load_3d(a, &tmW, &tail.full[s], t.m0, kb * kBlk, t.e, keep);
+                    else
+                        tma_load_3d(a, &tmW, &tail.full[s], kb * kBlk, t.m0, t.e, keep);
+                    for (int i = 0; i < boxes; ++i)
+                        tma_load_2d(b + i * 32 * kBlk, &tmX, &tail.full[s], kb * kBlk,
+                                    static_cast<int32_t>(t.row0) + i * 32, keep);
+                    ++issued;
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (*abort_flag) {
+                // let the copies already issued land before the CTA ends
+                const uint32_t from = issued > kStages ? issued - kStages : 0u;
+                for (uint32_t x = from; x < issued; ++x) {
+                    volatile int no_abort = 0;
+                    mbar_wait_bounded(&tail.full[x % kStages], (x / kStages) & 1u, &no_abort);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // A: the weights, K-major (128-byte rows of k) or, transposed, MN-major (rows of m); 8-row
+            // groups 1024 B apart either way.  A K = 32 step is 32 bytes of a row, or 32 rows.
+            const uint64_t a0 = make_smem_desc_sw128(smem_u32(ring), 16, 1024);
+            const uint64_t b0 = make_smem_desc_sw128(smem_u32(ring + kABytes), 16, 1024);
+            const uint32_t a_step = p.transpose ? 32 * 128 / 16 : 2;
+            uint32_t s = 0, ph = 0, q = 0, qph = 0;
+            int j = 0;
+            bool stop = false;
+            for (int tile = blockIdx.x; tile < tiles && !stop; tile += gridDim.x) {
+                const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
+                const int b = j & 1;
+                if (!mbar_wait_bounded(&tail.acc_empty[b], ((j >> 1) & 1) ^ 1, abort_flag)) break;
+                tc_fence_after_sync();
+                const uint32_t d = tmem + b * kTileN;
+                const uint32_t N = (t.rows + 15) & ~15;
+                uint32_t sfa = 0, sfb = 0;
+                for (int kb = 0; kb < blocks; ++kb) {
+                    if ((kb & 3) == 0) {
+                        if (!mbar_wait_bounded(&tail.sf_full[q], qph, abort_flag)) {
+                            stop = true;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        const uint32_t src = smem_u32(sf_ring + q * kScaleSlotBytes);
+                        sfa = tmem + kSfCol + (q & 1) * 12;
+                        sfb = sfa + 4;
+                        copy_scales(sfa, src);
+                        copy_scales(sfb, src + 512);
+                        copy_scales(sfb + 4, src + 1024);
+                        tc_commit(&tail.sf_empty[q]);
+                        if (++q == kScaleSlots) {
+                            q = 0;
+                            qph ^= 1u;
+                        }
+                    }
+                    if (!mbar_wait_bounded(&tail.full[s], ph, abort_flag)) {
+                        stop = true;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint64_t at = (s * kStageBytes) >> 4;
+                    const uint32_t idesc = make_idesc(N, p.transpose, kb & 3);
+#pragma unroll
+                    for (int i = 0; i < kBlk / 32; ++i)
+                        mma_scaled(d, a0 + at + i * a_step, b0 + at + i * 2, idesc, sfa, sfb, (kb | i) != 0);
+                    tc_commit(&tail.empty[s]);
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (stop) break;
+                tc_commit(&tail.acc_full[b]);
+                ++j;
+            }
+            tc_commit(&tail.drain);
+            volatile int no_abort = 0;
+            mbar_wait_bounded(&tail.drain, 0, &no_abort);
+        }
+    } else if (warp == 2) {
+        // Scale words: byte i of a row's word is the scale of 128-block 4 q + i.  Tokens: row r at
+        // lane r % 32, word r / 32 of a 128-row atom; features: one word for the whole 128.
+        const int m_blocks = (p.out + kBlk - 1) / kBlk;
+        uint32_t q = 0, qph = 0;
+        bool bad = false;
+        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+            const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
+            const int mb = t.m0 / kBlk;
+            bool ok = true;
+            for (int k0 = 0; k0 < blocks; k0 += 4) {
+                const int nk = blocks - k0 < 4 ? blocks - k0 : 4;
+                uint32_t wa = 0, wb[8];
+                for (int i = 0; i < nk; ++i) {
+                    const int64_t at = p.transpose
+                                           ? (static_cast<int64_t>(t.e) * blocks + k0 + i) * m_blocks + mb
+                                           : (static_cast<int64_t>(t.e) * m_blocks + mb) * blocks + k0 + i;
+                    wa |= load_scale_byte(p.W_scale, p.w_ue8m0, at, bad) << (8 * i);
+                }
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    wb[g] = 0;
+                    const int r = g * 32 + lane;
+                    if (r < t.rows) {
+                        const int64_t at = (t.row0 + r) * blocks + k0;
+                        for (int i = 0; i < nk; ++i)
+                            wb[g] |= load_scale_byte(p.X_scale, p.x_ue8m0, at + i, bad) << (8 * i);
+                    }
+                }
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.sf_empty[q], qph ^ 1u, abort_flag, 64));
+                if (!ok) break;
+                uint4 *slot = reinterpret_cast<uint4 *>(sf_ring + q * kScaleSlotBytes);
+                slot[lane] = make_uint4(wa, wa, wa, wa);
+                slot[32 + lane] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+                slot[64 + lane] = make_uint4(wb[4], wb[5], wb[6], wb[7]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tail.sf_full[q]);
+                if (++q == kScaleSlots) {
+                    q = 0;
+                    qph ^= 1u;
+                }
+            }
+            if (!ok) break;
+        }
+        if (bad) tail.bad_scale = 1;
+    } else if (warp >= 4) {
+        const int w = warp - 4;
+        uint8_t *buf = epi + w * 32 * 64;
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(w * 32) << 16);
+        int j = 0;
+        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+            const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
+            const int b = j & 1;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, abort_flag, 64))) break;
+            tc_fence_after_sync();
+            const int m = t.m0 + w * 32;                 // this warp's features
+            const int feats = p.out - m;                 // a multiple of 16, may be <= 0
+            for (int c = 0; c < t.rows; c += 32) {
+                float v[32];
+                tmem_ld_32x32b_x32(lane_addr + b * kTileN + c, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    *reinterpret_cast<__nv_bfloat16 *>(buf + i * 64 + lane * 2) = __float2bfloat16(v[i]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = i * 8 + (lane >> 2), part = lane & 3;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(buf + tok * 64 + part * 16);
+                    if (c + tok < t.rows && part * 8 < feats)
+                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.Y) +
+                                                   (t.row0 + c + tok) * p.out + m + part * 8) = x;
+                }
+                __syncwarp();
+            }
+            tc_fence_before_sync();
+            if (lane == 0) mbar_arrive(&tail.acc_empty[b]);
+            ++j;
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 3) tmem_dealloc(tmem, kTmemCols);
+    if (threadIdx.x == 0) {
+        if (tail.abort) report_status(p.status, MOE_ERR_TIMEOUT);
+        if (tail.bad_index) report_status(p.status, MOE_ERR_BAD_INDEX);
+        if (tail.bad_scale) report_status(p.status, MOE_ERR_BAD_SCALE);
+    }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled()
+{
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    });
+    return fn;
+}
+
+}  // namespace
+
+bool encode_map_sw128(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes, const void *base, int rank,
+                      const uint64_t *dims, const uint32_t *box)
+{
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    cuuint64_t d[5], strides[4];
+    cuuint32_t b[5], ones[5];
+    uint64_t bytes = elem_bytes;
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        ones[i] = 1;
+        bytes *= dims[i];
+        if (i + 1 < rank) strides[i] = bytes;
+    }
+    return fn(map, type, rank, const_cast<void *>(base), d, strides, b, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t stream)
+{
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (device_cc_major(dev) != 10) return cudaErrorNotSupported;
+    const int red = a.transpose ? a.rows : a.cols, out = a.transpose ? a.cols : a.rows;
+
+    CUtensorMap tmX, tmW;
+    const uint64_t xd[2] = {static_cast<uint64_t>(red), static_cast<uint64_t>(a.R)};
+    const uint32_t xb[2] = {kBlk, 32};
+    const uint64_t wd[3] = {static_cast<uint64_t>(a.cols), static_cast<uint64_t>(a.rows), static_cast<uint64_t>(a.E)};
+    const uint32_t wb[3] = {128, 128, 1};
+    if (!encode_map_sw128(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.X, 2, xd, xb) ||
+        !encode_map_sw128(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.W, 3, wd, wb))
+        return cudaErrorInvalidValue;
+
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        err = cudaFuncSetAttribute(expert_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(kSmemBytes));
+        if (err != cudaSuccess) return err;
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    Params p;
+    p.X_scale = a.X_scale;
+    p.W_scale = a.W_scale;
+    p.offsets = a.offsets;
+    p.R = a.R;
+    p.E = a.E;
+    p.out = out;
+    p.red = red;
+    p.transpose = a.transpose;
+    p.x_ue8m0 = a.x_ue8m0;
+    p.w_ue8m0 = a.w_ue8m0;
+    p.m_tiles = (out + kTileM - 1) / kTileM;
+    p.Y = a.Y;
+    p.status = a.status;
+    // the most tiles that R rows in E groups can make; no more CTAs than that
+    const int64_t most = (a.R / kTileN + (a.R < a.E ? a.R : a.E) + 1) * p.m_tiles;
+    const int sms = device_sm_count(dev);
+    const int grid = static_cast<int>(most < sms ? most : sms);
+    expert_gemm_kernel<<<grid, kThreads, kSmemBytes, stream>>>(tmX, tmW, p);
+    return cudaGetLastError();
+}
+
+}  // namespace moe

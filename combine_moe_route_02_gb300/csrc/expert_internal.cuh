@@ -1,0 +1,125 @@
+// expert_internal.cuh -- what the kernels behind the dispatch (expert products,
+// gated activation, few-token layer) share: power-of-two block scales, the E4M3
+// quantiser, the walk over ragged groups of rows, and their launchers.
+#pragma once
+
+#include "moe_internal.cuh"
+
+namespace moe {
+
+// ---------------------------------------------------------------------------
+// Power-of-two scales.  A scale travels as its UE8M0 byte b (s = 2^(b - 127)),
+// whichever of the two formats it is stored in.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kRcp448F32Bits = 0x3B124925u;  // fl32(1/448)
+
+// The byte of the block scale of a 128-block with this largest magnitude:
+// t = fl32(max(amax, 1e-4) * fl32(1/448)), rounded up to a power of two.
+__device__ __forceinline__ uint32_t block_scale_byte(float amax)
+{
+    const float t = __fmul_rn(fmaxf(amax, 1e-4f), __uint_as_float(kRcp448F32Bits));
+    uint16_t e;
+    asm("cvt.rp.satfinite.ue8m0x2.f32 %0, %1, %2;" : "=h"(e) : "f"(0.0f), "f"(t));
+    return e & 0xFFu;
+}
+
+// 2^(127 - b): the exact reciprocal of the scale with byte b in 1..253.
+__device__ __forceinline__ float scale_reciprocal(uint32_t b) { return __uint_as_float((254u - b) << 23); }
+__device__ __forceinline__ float scale_value(uint32_t b)
+{
+    return __uint_as_float(b ? b << 23 : 0x00400000u);  // byte 0 is 2^-127, a subnormal
+}
+
+// Four fp32 values to four E4M3 codes (round to nearest even, saturating), the first in the low byte.
+__device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float a, float b, float c, float d)
+{
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// Two E4M3 codes (low 16 bits of `q`) to fp32, exactly.
+__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t q)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(q)));
+    float2 f;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(h));
+    return f;
+}
+
+// Reads scale `at` of an array in either format as its byte.  `bad` is raised
+// where a float is not a positive normal power of two.
+__device__ __forceinline__ uint32_t load_scale_byte(const void *p, int ue8m0, int64_t at, bool &bad)
+{
+    if (ue8m0) return __ldg(static_cast<const uint8_t *>(p) + at);
+    const uint32_t w = __float_as_uint(__ldg(static_cast<const float *>(p) + at));
+    bad |= (w & 0x807FFFFFu) != 0 || w == 0;
+    return (w >> 23) & 0xFFu;
+}
+
+__device__ __forceinline__ void store_scale(void *p, int ue8m0, int64_t at, uint32_t byte)
+{
+    if (ue8m0)
+        static_cast<uint8_t *>(p)[at] = static_cast<uint8_t>(byte);
+    else
+        static_cast<float *>(p)[at] = __uint_as_float(byte << 23);
+}
+
+// ---------------------------------------------------------------------------
+// Launchers (validated arguments, the launch's cudaError_t)
+// ---------------------------------------------------------------------------
+struct ExpertGemmArgs {
+    const void *X, *X_scale;
+    const void *W, *W_scale;
+    const int32_t *offsets;  // [E + 1], or nullptr: one group of all R rows
+    int64_t R;
+    int E, rows, cols, transpose, x_ue8m0, w_ue8m0;
+    void *Y;
+    int32_t *status;
+};
+cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t stream);
+
+struct ExpertWgradArgs {
+    const void *dY;
+    const void *X, *X_scale;
+    const int32_t *offsets;
+    int64_t R;
+    int E, rows, cols, x_ue8m0, bf16_out;
+    const float *add;
+    void *dW;
+    int32_t *status;
+};
+cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream);
+
+cudaError_t launch_quantize_weight(const void *W, int E, int rows, int cols, void *q, void *scale, int ue8m0,
+                                   cudaStream_t stream);
+cudaError_t launch_swiglu(const void *GU, int64_t R, int I, void *A_fp8, void *A_scale, void *GU_fp8, void *GU_scale,
+                          int ue8m0, cudaStream_t stream);
+cudaError_t launch_swiglu_backward(const void *dA, const void *GU_fp8, const void *GU_scale, int gu_ue8m0, int64_t R,
+                                   int I, void *dGU, void *dGU_fp8, void *dGU_scale, int ue8m0, int32_t *status,
+                                   cudaStream_t stream);
+
+struct LayerArgs {
+    const void *X, *W_gate;
+    const float *bias;
+    const void *W1, *W1_scale, *W2, *W2_scale;
+    const void *residual;
+    int N, H, I, E, K, renorm, ue8m0;
+    int32_t *topk_idx;
+    float *topk_w;
+    void *out;
+    int32_t *status;
+    void *workspace;
+};
+size_t layer_workspace_bytes(int N, int H, int I, int E, int K);
+cudaError_t launch_layer(const LayerArgs &a, cudaStream_t stream);
+
+// A tiled tensor map with 128-byte swizzle; false if the driver refuses it.
+bool encode_map_sw128(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes, const void *base, int rank,
+                      const uint64_t *dims, const uint32_t *box);
+
+}  // namespace moe

@@ -101,6 +101,7 @@ const char *moe_status_string(moe_status s)
     case MOE_ERR_CUDA: return "MOE_ERR_CUDA: a CUDA runtime call or kernel launch failed";
     case MOE_ERR_TIMEOUT: return "MOE_ERR_TIMEOUT: a bounded device wait ran out";
     case MOE_ERR_BAD_INDEX: return "MOE_ERR_BAD_INDEX: an expert index or row index was out of range";
+    case MOE_ERR_BAD_SCALE: return "MOE_ERR_BAD_SCALE: an fp32 block scale is not a power of two";
     }
     return "unknown moe_status";
 }

@@ -1,0 +1,275 @@
+"""The experts: what runs between dispatch and combine (``include/moe_route.h``, "The experts").
+
+E4M3 tensors are uint8 codes with one power-of-two scale per block, float32 or uint8
+(UE8M0) as dispatch writes them: [R, C/128] for rows, [E, ceil(rows/128), ceil(cols/128)]
+for weights.  A training step of one layer's MLP::
+
+    W1q, W1s = quantize_weight(W1)                     # after each optimizer step
+    d  = dispatch(idx, E, X, fp8=True, bf16=False)
+    gu = expert_gemm(d.X_fp8, d.X_scale, W1q, W1s, d.expert_offsets)
+    h  = swiglu(gu)                                    # gu itself is not needed any more
+    y  = expert_gemm(h.A_fp8, h.A_scale, W2q, W2s, d.expert_offsets)
+    ...
+    dA  = expert_gemm(dY_fp8, dY_scale, W2q, W2s, d.expert_offsets, transpose=True)
+    dW2 = expert_wgrad(dY, h.A_fp8, h.A_scale, d.expert_offsets)
+    b   = swiglu_backward(dA, h.GU_fp8, h.GU_scale)
+    dX  = expert_gemm(b.dGU_fp8, b.dGU_scale, W1q, W1s, d.expert_offsets, transpose=True)
+    dW1 = expert_wgrad(b.dGU, d.X_fp8, d.X_scale, d.expert_offsets)
+
+Kept from the forward to the backward pass: E4M3 rows only.  For serving a few tokens,
+``moe_layer`` is the whole layer in one launch.
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import (_check, _need, _ptr, _scale_dtype, _scale_format, _status_ptr, _stream, _workspace_arg, lib)
+
+__all__ = ["quantize_weight", "expert_gemm", "expert_wgrad", "swiglu", "swiglu_backward", "moe_layer",
+           "layer_workspace_size", "layer_workspace", "SwiGLU", "SwiGLUGrad", "LayerOut"]
+
+BLOCK = 128
+
+
+def _blocks(n: int) -> int:
+    return -(-n // BLOCK)
+
+
+def _scales(t: torch.Tensor, name: str, shape) -> int:
+    """Checks block scales of either format and returns the format."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.float32, torch.uint8):
+        raise TypeError(f"{name} must be torch.float32 or torch.uint8 (UE8M0), got {t.dtype}")
+    _need(t, name, t.dtype, shape)
+    return 1 if t.dtype == torch.uint8 else 0
+
+
+def _dims(t: torch.Tensor, name: str, n: int):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
+    return tuple(t.shape)
+
+
+def _groups(expert_offsets: Optional[torch.Tensor], E: Optional[int]) -> int:
+    if expert_offsets is None:
+        if E not in (None, 1):
+            raise ValueError("expert_offsets is required for more than one expert")
+        return 1
+    n = _dims(expert_offsets, "expert_offsets", 1)[0] - 1
+    _need(expert_offsets, "expert_offsets", torch.int32, (n + 1 if E is None else E + 1,))
+    return n
+
+
+def quantize_weight(W: torch.Tensor, scale_format: str = "fp32", out=None, stream=None):
+    """bf16 [E, rows, cols] (or [rows, cols]) -> (E4M3 codes uint8, scales of 128x128 blocks).
+    `out`: the two tensors to write."""
+    fmt = _scale_format(scale_format)
+    _need(W, "W", torch.bfloat16)
+    if W.dim() not in (2, 3):
+        raise ValueError("W must be [E, rows, cols] or [rows, cols]")
+    lead, (rows, cols) = W.shape[:-2], W.shape[-2:]
+    E = lead[0] if lead else 1
+    shape = (*lead, _blocks(rows), _blocks(cols))
+    if out is None:
+        out = (torch.empty(W.shape, dtype=torch.uint8, device=W.device),
+               torch.empty(shape, dtype=_scale_dtype(scale_format), device=W.device))
+    q, s = out
+    _need(q, "W_fp8", torch.uint8, W.shape)
+    _need(s, "W_scale", _scale_dtype(scale_format), shape)
+    _check(lib().moe_quantize_weight(_ptr(W), E, rows, cols, _ptr(q), _ptr(s), fmt, _stream(stream)),
+           "moe_quantize_weight")
+    return q, s
+
+
+def expert_gemm(X_fp8: torch.Tensor, X_scale: torch.Tensor, W_fp8: torch.Tensor, W_scale: torch.Tensor,
+                expert_offsets: Optional[torch.Tensor] = None, transpose: bool = False, out=None, status=None,
+                stream=None) -> torch.Tensor:
+    """Each expert's rows times its weight [rows, cols], bf16: x W^T, or x W with `transpose`
+    (the gradient of the first one's input).  Without expert_offsets all rows are one group
+    (W [1, rows, cols] or [rows, cols]).  Rows of no group are left as `out` has them."""
+    if W_fp8.dim() == 2:
+        W_fp8, W_scale = W_fp8[None], W_scale[None]
+    E, rows, cols = _dims(W_fp8, "W_fp8", 3)
+    R, red = _dims(X_fp8, "X_fp8", 2)
+    if red != (rows if transpose else cols):
+        raise ValueError(f"X_fp8 has {red} columns, W_fp8 {tuple(W_fp8.shape)} takes {rows if transpose else cols}")
+    _need(X_fp8, "X_fp8", torch.uint8)
+    _need(W_fp8, "W_fp8", torch.uint8)
+    xf = _scales(X_scale, "X_scale", (R, red // BLOCK))
+    wf = _scales(W_scale, "W_scale", (E, _blocks(rows), _blocks(cols)))
+    _groups(expert_offsets, E)
+    n = cols if transpose else rows
+    if out is None:
+        out = torch.empty((R, n), dtype=torch.bfloat16, device=X_fp8.device)
+    _need(out, "out", torch.bfloat16, (R, n))
+    _check(lib().moe_expert_gemm(_ptr(X_fp8), _ptr(X_scale), xf, _ptr(W_fp8), _ptr(W_scale), wf, _ptr(expert_offsets),
+                                 R, E, rows, cols, int(bool(transpose)), _ptr(out), _status_ptr(status),
+                                 _stream(stream)), "moe_expert_gemm")
+    return out
+
+
+def expert_wgrad(dY: torch.Tensor, X_fp8: torch.Tensor, X_scale: torch.Tensor,
+                 expert_offsets: Optional[torch.Tensor] = None, dtype=torch.float32,
+                 add: Optional[torch.Tensor] = None, out=None, status=None, stream=None) -> torch.Tensor:
+    """Weight gradients [E, rows, cols] = add + dY^T x of each expert's rows, from the E4M3 rows that
+    went into expert_gemm; dtype float32 or bfloat16.  `out` may be `add` (float32): the sum is then
+    accumulated in place."""
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("dtype must be torch.float32 or torch.bfloat16")
+    R, rows = _dims(dY, "dY", 2)
+    cols = _dims(X_fp8, "X_fp8", 2)[1]
+    _need(dY, "dY", torch.bfloat16)
+    _need(X_fp8, "X_fp8", torch.uint8, (R, cols))
+    xf = _scales(X_scale, "X_scale", (R, cols // BLOCK))
+    E = _groups(expert_offsets, None)
+    if add is not None:
+        _need(add, "add", torch.float32, (E, rows, cols))
+    if out is None:
+        out = torch.empty((E, rows, cols), dtype=dtype, device=dY.device)
+    _need(out, "out", dtype, (E, rows, cols))
+    _check(lib().moe_expert_wgrad(_ptr(dY), _ptr(X_fp8), _ptr(X_scale), xf, _ptr(expert_offsets), R, E, rows, cols,
+                                  _ptr(add), _ptr(out), int(dtype == torch.bfloat16), _status_ptr(status),
+                                  _stream(stream)), "moe_expert_wgrad")
+    return out
+
+
+@dataclass
+class SwiGLU:
+    A_fp8: torch.Tensor
+    A_scale: torch.Tensor
+    GU_fp8: Optional[torch.Tensor] = None
+    GU_scale: Optional[torch.Tensor] = None
+
+
+@dataclass
+class SwiGLUGrad:
+    dGU: Optional[torch.Tensor]
+    dGU_fp8: Optional[torch.Tensor]
+    dGU_scale: Optional[torch.Tensor]
+
+
+def _coded(R: int, C: int, scale_format: str, device):
+    return (torch.empty((R, C), dtype=torch.uint8, device=device),
+            torch.empty((R, C // BLOCK), dtype=_scale_dtype(scale_format), device=device))
+
+
+def swiglu(GU: torch.Tensor, keep: bool = True, scale_format: str = "fp32", out: Optional[SwiGLU] = None,
+           stream=None) -> SwiGLU:
+    """silu(gate) * up of GU bf16 [R, 2I] (gate columns first) in E4M3; with `keep` also GU in E4M3,
+    which is all that swiglu_backward needs."""
+    fmt = _scale_format(scale_format)
+    R, C = _dims(GU, "GU", 2)
+    _need(GU, "GU", torch.bfloat16)
+    if C % (2 * BLOCK) != 0:
+        raise ValueError("GU must be [R, 2I] with I a multiple of 128")
+    I = C // 2
+    if out is None:
+        out = SwiGLU(*_coded(R, I, scale_format, GU.device), *(_coded(R, C, scale_format, GU.device) if keep else (None, None)))
+    _need(out.A_fp8, "A_fp8", torch.uint8, (R, I))
+    _need(out.A_scale, "A_scale", _scale_dtype(scale_format), (R, I // BLOCK))
+    if out.GU_fp8 is not None:
+        _need(out.GU_fp8, "GU_fp8", torch.uint8, (R, C))
+        _need(out.GU_scale, "GU_scale", _scale_dtype(scale_format), (R, C // BLOCK))
+    _check(lib().moe_swiglu(_ptr(GU), R, I, _ptr(out.A_fp8), _ptr(out.A_scale), _ptr(out.GU_fp8), _ptr(out.GU_scale),
+                            fmt, _stream(stream)), "moe_swiglu")
+    return out
+
+
+def swiglu_backward(dA: torch.Tensor, GU_fp8: torch.Tensor, GU_scale: torch.Tensor, bf16: bool = True, fp8: bool = True,
+                    scale_format: str = "fp32", out: Optional[SwiGLUGrad] = None, status=None,
+                    stream=None) -> SwiGLUGrad:
+    """Gradient of swiglu from its E4M3 checkpoint: dGU in bf16 (for expert_wgrad) and/or in E4M3 (for
+    the transposed expert_gemm)."""
+    fmt = _scale_format(scale_format)
+    R, I = _dims(dA, "dA", 2)
+    _need(dA, "dA", torch.bfloat16)
+    _need(GU_fp8, "GU_fp8", torch.uint8, (R, 2 * I))
+    gf = _scales(GU_scale, "GU_scale", (R, 2 * I // BLOCK))
+    if out is None:
+        out = SwiGLUGrad(torch.empty((R, 2 * I), dtype=torch.bfloat16, device=dA.device) if bf16 else None,
+                         *(_coded(R, 2 * I, scale_format, dA.device) if fp8 else (None, None)))
+    if out.dGU is not None:
+        _need(out.dGU, "dGU", torch.bfloat16, (R, 2 * I))
+    if out.dGU_fp8 is not None:
+        _need(out.dGU_fp8, "dGU_fp8", torch.uint8, (R, 2 * I))
+        _need(out.dGU_scale, "dGU_scale", _scale_dtype(scale_format), (R, 2 * I // BLOCK))
+    _check(lib().moe_swiglu_backward(_ptr(dA), _ptr(GU_fp8), _ptr(GU_scale), gf, R, I, _ptr(out.dGU),
+                                     _ptr(out.dGU_fp8), _ptr(out.dGU_scale), fmt, _status_ptr(status),
+                                     _stream(stream)), "moe_swiglu_backward")
+    return out
+
+
+@dataclass
+class LayerOut:
+    out: torch.Tensor
+    topk_idx: torch.Tensor
+    topk_w: torch.Tensor
+
+
+_layer_workspaces = {}
+
+
+def layer_workspace_size(N: int, H: int, I: int, E: int, K: int) -> int:
+    """Bytes of workspace moe_layer needs (0 for sizes it does not take)."""
+    return int(lib().moe_layer_workspace_size(N, H, I, E, K))
+
+
+def layer_workspace(N: int, H: int, I: int, E: int, K: int, device=None, stream=None) -> torch.Tensor:
+    """A workspace for moe_layer, cached per (device, stream, E, I) and grown where a call needs more.
+    Its counters start at zero and every call leaves them there, so one buffer serves all calls of one
+    stream; calls that may overlap on the GPU must not share it."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    need = layer_workspace_size(N, H, I, E, K)
+    key = (device.index, stream.cuda_stream, E, I)
+    ws = _layer_workspaces.get(key)
+    if ws is None or ws.numel() < need:
+        with torch.cuda.stream(stream):
+            ws = torch.zeros(need, dtype=torch.uint8, device=device)
+        _layer_workspaces[key] = ws
+    return ws
+
+
+def moe_layer(X: torch.Tensor, W_gate: torch.Tensor, K: int, W1_fp8: torch.Tensor, W1_scale: torch.Tensor,
+              W2_fp8: torch.Tensor, W2_scale: torch.Tensor, bias: Optional[torch.Tensor] = None, renorm: bool = True,
+              residual: Optional[torch.Tensor] = None, out: Optional[LayerOut] = None,
+              workspace: Optional[torch.Tensor] = None, status=None, stream=None) -> LayerOut:
+    """The whole layer (router, gated MLP of the K chosen experts, weighted sum, residual) for up to 64
+    tokens in one launch.  W1 [E, 2I, H] (gate rows first) and W2 [E, H, I] in E4M3 with 128x128 scales
+    of one format (quantize_weight); X bf16 [N, H].  `out.out` may be the residual."""
+    N, H = _dims(X, "X", 2)
+    _need(X, "X", torch.bfloat16)
+    E, two_i, _ = _dims(W1_fp8, "W1_fp8", 3)
+    I = two_i // 2
+    _need(W_gate, "W_gate", torch.bfloat16, (H, E))
+    _need(W1_fp8, "W1_fp8", torch.uint8, (E, 2 * I, H))
+    _need(W2_fp8, "W2_fp8", torch.uint8, (E, H, I))
+    fmt = _scales(W1_scale, "W1_scale", (E, _blocks(2 * I), _blocks(H)))
+    if _scales(W2_scale, "W2_scale", (E, _blocks(H), _blocks(I))) != fmt:
+        raise TypeError("W1_scale and W2_scale must be of one format")
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (E,))
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, (N, H))
+    dev = X.device
+    if out is None:
+        out = LayerOut(torch.empty((N, H), dtype=torch.bfloat16, device=dev),
+                       torch.empty((N, K), dtype=torch.int32, device=dev),
+                       torch.empty((N, K), dtype=torch.float32, device=dev))
+    _need(out.out, "out", torch.bfloat16, (N, H))
+    _need(out.topk_idx, "topk_idx", torch.int32, (N, K))
+    _need(out.topk_w, "topk_w", torch.float32, (N, K))
+    if workspace is None and layer_workspace_size(N, H, I, E, K):
+        workspace = layer_workspace(N, H, I, E, K, dev, stream)
+    _check(lib().moe_layer(_ptr(X), _ptr(W_gate), _ptr(bias), _ptr(W1_fp8), _ptr(W1_scale), _ptr(W2_fp8),
+                           _ptr(W2_scale), fmt, _ptr(residual), N, H, I, E, K, int(bool(renorm)), _ptr(out.topk_idx),
+                           _ptr(out.topk_w), _ptr(out.out), _status_ptr(status), *_workspace_arg(workspace),
+                           _stream(stream)), "moe_layer")
+    return out

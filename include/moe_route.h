@@ -60,7 +60,8 @@ typedef enum moe_status {
     MOE_ERR_WORKSPACE = 4,     /* workspace smaller than moe_dispatch_workspace_size() */
     MOE_ERR_CUDA = 5,          /* a CUDA runtime call or launch failed */
     MOE_ERR_TIMEOUT = 6,       /* (status_word only) a bounded device wait ran out */
-    MOE_ERR_BAD_INDEX = 7      /* (status_word only) topk_idx entry outside [0,E) */
+    MOE_ERR_BAD_INDEX = 7,     /* (status_word only) topk_idx entry outside [0,E) */
+    MOE_ERR_BAD_SCALE = 8      /* (status_word only) fp32 block scale not a power of two */
 } moe_status;
 
 /* Format of the E4M3 block scales (moe_dispatch_ex, moe_permute_ex). */
@@ -380,6 +381,120 @@ MOE_API moe_status moe_combine(const void *Y, const int32_t *row_map, const floa
 MOE_API moe_status moe_combine_residual(const void *Y, const int32_t *row_map, const float *topk_w,
                                 const void *residual, int64_t N, int H, int K, void *out,
                                 int32_t *status_word, moe_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The experts: what runs between dispatch and combine.
+ *
+ * E4M3 operands carry one power-of-two scale per block, as moe_dispatch_ex writes
+ * them: 1x128 blocks for rows ([R, C/128]), 128x128 blocks for weights
+ * ([E, ceil(rows/128), ceil(cols/128)], the last blocks cut at the edges), in
+ * either moe_scale_format.  A value is code * scale.  An fp32 scale that is not a
+ * positive normal power of two is reported as MOE_ERR_BAD_SCALE in status_word
+ * (its exponent is used).  A NaN code gives NaN results.
+ * expert_offsets is moe_dispatch's: int32 [E+1], the rows of expert e are
+ * [offsets[e], offsets[e+1]); a group may be empty.  NULL with E = 1 means one group
+ * of all R rows (a plain product).  A group that is not inside [0, R] or runs
+ * backwards is treated as empty and reported as MOE_ERR_BAD_INDEX; no access leaves
+ * the buffers.  All calls need a GPU of compute capability 10.x
+ * (MOE_ERR_UNSUPPORTED elsewhere).
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * moe_quantize_weight -- E4M3 weights from bf16 ones:
+ *   s = pow2ceil(fl32(max(amax of the 128x128 block, 1e-4) * fl32(1/448)))
+ *   W_fp8 = E4M3_rn_satfinite(W / s)
+ *   W bf16 [E, rows, cols], W_fp8 uint8 [E, rows, cols], W_scale as above
+ * E in 1..256, rows in 1..2^22, cols % 8 == 0.  One launch.
+ */
+MOE_API moe_status moe_quantize_weight(const void *W, int E, int rows, int cols, void *W_fp8, void *W_scale,
+                               int scale_format, moe_stream_t stream);
+
+/*
+ * moe_expert_gemm -- the experts' products, rows times weights (W is [E, rows, cols]):
+ *   transpose == 0:  Y[r, m] = sum_k x[r,k] W[e(r), m, k]    x [R, cols], Y [R, rows]
+ *   transpose != 0:  Y[r, k] = sum_m x[r,m] W[e(r), m, k]    x [R, rows], Y [R, cols]
+ * (the second is the gradient with respect to the first one's x).  fp32
+ * accumulation over the whole reduction, one rounding to bf16.
+ *   X_fp8 uint8 [R, red], X_scale [R, red/128], W_fp8 uint8 [E, rows, cols], W_scale
+ *   Y bf16; rows of no group are left as they are
+ * The reduction (cols, or rows when transposed) is a multiple of 128, the other
+ * side of 16.  R == 0 is a no-op.  One launch.
+ * Errors: MOE_ERR_INVALID_ARG (sizes, NULLs, expert_offsets NULL with E > 1),
+ * MOE_ERR_MISALIGNED, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.
+ */
+MOE_API moe_status moe_expert_gemm(const void *X_fp8, const void *X_scale, int x_scale_format,
+                           const void *W_fp8, const void *W_scale, int w_scale_format,
+                           const int32_t *expert_offsets, int64_t R, int E, int rows, int cols, int transpose,
+                           void *Y, int32_t *status_word, moe_stream_t stream);
+
+/*
+ * moe_expert_wgrad -- the weight gradient of moe_expert_gemm (transpose == 0), from
+ * the E4M3 rows that went into it:
+ *   dW[e, m, k] = add[e, m, k] + sum_{r in group e} dY[r, m] * x[r, k]
+ *   dY bf16 [R, rows], X_fp8 uint8 [R, cols], X_scale [R, cols/128]
+ *   add fp32 [E, rows, cols] or NULL (nothing is added); may be dW itself when that is fp32
+ *   dW  fp32 (dw_bf16 == 0) or bf16 [E, rows, cols]; an empty group gives add, or zeros
+ * x is a bf16 number exactly (an E4M3 value times a power of two), the products are
+ * accumulated in fp32.  rows % 8 == 0, cols % 128 == 0.  One launch.
+ */
+MOE_API moe_status moe_expert_wgrad(const void *dY, const void *X_fp8, const void *X_scale, int x_scale_format,
+                            const int32_t *expert_offsets, int64_t R, int E, int rows, int cols,
+                            const float *add, void *dW, int dw_bf16, int32_t *status_word, moe_stream_t stream);
+
+/*
+ * moe_swiglu -- the gated activation between the two products:
+ *   GU bf16 [R, 2I]: gate columns, then up columns;  a = g / (1 + exp(-g)) * u
+ *   A_fp8 uint8 [R, I], A_scale [R, I/128]: a in E4M3 (the rule of moe_permute)
+ *   GU_fp8 uint8 [R, 2I], GU_scale [R, 2I/128], or both NULL: GU in E4M3, the
+ *   checkpoint that moe_swiglu_backward reads instead of GU
+ * I % 128 == 0.  One launch.
+ */
+MOE_API moe_status moe_swiglu(const void *GU, int64_t R, int I, void *A_fp8, void *A_scale,
+                      void *GU_fp8, void *GU_scale, int scale_format, moe_stream_t stream);
+
+/*
+ * moe_swiglu_backward -- its gradient, from the E4M3 checkpoint:
+ *   s = 1 / (1 + exp(-g));  dg = da u s (1 + g (1 - s));  du = da g s
+ *   dA bf16 [R, I], GU_fp8 and GU_scale (gu_scale_format) as moe_swiglu wrote them
+ *   dGU bf16 [R, 2I] or NULL (what moe_expert_wgrad reads)
+ *   dGU_fp8, dGU_scale (scale_format) or both NULL (what the transposed
+ *   moe_expert_gemm reads); quantised from the unrounded gradient
+ * One of the two outputs is required.  One launch.
+ */
+MOE_API moe_status moe_swiglu_backward(const void *dA, const void *GU_fp8, const void *GU_scale, int gu_scale_format,
+                               int64_t R, int I, void *dGU, void *dGU_fp8, void *dGU_scale, int scale_format,
+                               int32_t *status_word, moe_stream_t stream);
+
+/* Bytes of device workspace moe_layer needs. */
+MOE_API size_t moe_layer_workspace_size(int N, int H, int I, int E, int K);
+
+/*
+ * moe_layer -- the whole layer for a few tokens (N <= 64) in one cooperative launch:
+ *   topk_idx, topk_w   as moe_route_ex(X, W_gate, bias, renorm)
+ *   gu  = W1[e] q(x) (fp32);  a = g / (1 + exp(-g)) * u;  y = W2[e] q(a) (fp32)
+ *   out = sum_k topk_w[n,k] y_k (+ residual), one rounding to bf16
+ * with q the E4M3 rounding with 1x128 scales of moe_permute: what dispatch (E4M3),
+ * moe_expert_gemm, moe_swiglu, moe_expert_gemm and combine compute, without the bf16
+ * roundings between them.  The weights of every expert that is chosen are read once.
+ *   X bf16 [N,H], W_gate bf16 [H,E], bias fp32 [E] or NULL
+ *   W1_fp8 uint8 [E, 2I, H] (gate rows, then up rows), W1_scale [E, 2I/128, H/128]
+ *   W2_fp8 uint8 [E, H, I], W2_scale [E, H/128, I/128]; both in scale_format
+ *   residual bf16 [N,H] or NULL (may be out)
+ *   topk_idx int32 [N,K], topk_w fp32 [N,K], out bf16 [N,H]: outputs
+ *   workspace  moe_layer_workspace_size() bytes, 256-byte aligned; its first
+ *              256 + 4 * E * (I/128) bytes zero before the first call with these sizes
+ *              (every call leaves them zero).  Calls that may overlap need their own.
+ * H % 128 == 0, I % 128 == 0, both <= 65536, 1 <= K <= min(E, 16), E <= 256.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_MISALIGNED, MOE_ERR_WORKSPACE,
+ * MOE_ERR_UNSUPPORTED (N > 64), MOE_ERR_CUDA; status_word: MOE_ERR_TIMEOUT, MOE_ERR_BAD_SCALE.
+ */
+MOE_API moe_status moe_layer(const void *X, const void *W_gate, const float *bias,
+                     const void *W1_fp8, const void *W1_scale, const void *W2_fp8, const void *W2_scale,
+                     int scale_format, const void *residual, int N, int H, int I, int E, int K, int renorm,
+                     int32_t *topk_idx, float *topk_w, void *out, int32_t *status_word,
+                     void *workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* A static, human-readable name for a status code. */
 MOE_API const char *moe_status_string(moe_status status);
