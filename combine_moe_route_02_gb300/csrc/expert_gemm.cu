@@ -17,8 +17,8 @@
 // Persistent CTAs, one per SM; warp roles:
 //   warp 0      TMA producer (weights 128 x 128, tokens in boxes of 32 rows)
 //   warp 1      MMA issuer (one thread), copies the scales to TMEM (tcgen05.cp)
-//   warp 2      scale producer: gathers the bytes of four 128-blocks per row
-//   warp 3      allocates TMEM
+//   warps 2, 3  scale producers: gather the bytes of four 128-blocks per row; warp 3
+//               allocates TMEM
 //   warps 4..7  epilogue: TMEM -> registers -> bf16, transposed through shared memory
 #include <mutex>
 
@@ -63,6 +63,7 @@ struct Params {
     int64_t R;
     int E, out, red;              // output features, reduction length
     int transpose, x_ue8m0, w_ue8m0;
+    int x_vec;                    // a row's four scales can be loaded as one vector
     int m_tiles;
     void *Y;
     int32_t *status;
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&tail.empty[s], 1);
         }
         for (int s = 0; s < kScaleSlots; ++s) {
-            mbar_init(&tail.sf_full[s], 1);
+            mbar_init(&tail.sf_full[s], 2);
             mbar_init(&tail.sf_empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -288,10 +289,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             volatile int no_abort = 0;
             mbar_wait_bounded(&tail.drain, 0, &no_abort);
         }
-    } else if (warp == 2) {
+    } else if (warp == 2 || warp == 3) {
         // Scale words: byte i of a row's word is the scale of 128-block 4 q + i.  Tokens: row r at
-        // lane r % 32, word r / 32 of a 128-row atom; features: one word for the whole 128.
+        // lane r % 32, word r / 32 of a 128-row atom; features: one word for the whole 128.  A warp
+        // gathers one atom, all its loads in flight together and ahead of the ring's free slot.
         const int m_blocks = (p.out + kBlk - 1) / kBlk;
+        const int half = warp - 2;
         uint32_t q = 0, qph = 0;
         bool bad = false;
         for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -300,29 +303,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int k0 = 0; k0 < blocks; k0 += 4) {
                 const int nk = blocks - k0 < 4 ? blocks - k0 : 4;
-                uint32_t wa = 0, wb[8];
-                for (int i = 0; i < nk; ++i) {
-                    const int64_t at = p.transpose
-                                           ? (static_cast<int64_t>(t.e) * blocks + k0 + i) * m_blocks + mb
-                                           : (static_cast<int64_t>(t.e) * m_blocks + mb) * blocks + k0 + i;
-                    wa |= load_scale_byte(p.W_scale, p.w_ue8m0, at, bad) << (8 * i);
+                uint32_t wa = 0, wb[4];
+                if (half == 0) {
+                    const int64_t at = p.transpose ? (static_cast<int64_t>(t.e) * blocks + k0) * m_blocks + mb
+                                                   : (static_cast<int64_t>(t.e) * m_blocks + mb) * blocks + k0;
+                    wa = load_scale_word(p.W_scale, p.w_ue8m0, at, p.transpose ? m_blocks : 1, nk, false, bad);
                 }
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
+                for (int g = 0; g < 4; ++g) {
                     wb[g] = 0;
-                    const int r = g * 32 + lane;
-                    if (r < t.rows) {
-                        const int64_t at = (t.row0 + r) * blocks + k0;
-                        for (int i = 0; i < nk; ++i)
-                            wb[g] |= load_scale_byte(p.X_scale, p.x_ue8m0, at + i, bad) << (8 * i);
-                    }
+                    const int r = half * 128 + g * 32 + lane;
+                    if (r < t.rows)
+                        wb[g] = load_scale_word(p.X_scale, p.x_ue8m0, (t.row0 + r) * blocks + k0, 1, nk, p.x_vec, bad);
                 }
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.sf_empty[q], qph ^ 1u, abort_flag, 64));
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.sf_empty[q], qph ^ 1u, abort_flag, 32));
                 if (!ok) break;
                 uint4 *slot = reinterpret_cast<uint4 *>(sf_ring + q * kScaleSlotBytes);
-                slot[lane] = make_uint4(wa, wa, wa, wa);
-                slot[32 + lane] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
-                slot[64 + lane] = make_uint4(wb[4], wb[5], wb[6], wb[7]);
+                if (half == 0) slot[lane] = make_uint4(wa, wa, wa, wa);
+                slot[32 + half * 32 + lane] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&tail.sf_full[q]);
@@ -458,6 +456,7 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t stream)
     p.transpose = a.transpose;
     p.x_ue8m0 = a.x_ue8m0;
     p.w_ue8m0 = a.w_ue8m0;
+    p.x_vec = (red / kBlk) % 4 == 0 && reinterpret_cast<uintptr_t>(a.X_scale) % (a.x_ue8m0 ? 4 : 16) == 0;
     p.m_tiles = (out + kTileM - 1) / kTileM;
     p.Y = a.Y;
     p.status = a.status;
