@@ -9,14 +9,17 @@
 // UE8M0 byte per row and K = 32 step): no partial sum leaves TMEM before the end
 // of the reduction, and the accumulation is fp32 throughout.
 //
-// The weights sit on the M side of the MMA (128 of their output features per
-// tile) and the tokens on the N side, whose size can be any multiple of 16: a
-// group of c rows is cut into ceil(c / 224) tiles of equal size, so that a ragged
-// group pays for at most 15 rows that it does not have.
+// The weights sit on the M side of the MMA and the tokens on the N side, whose size
+// can be any multiple of 16: a group of c rows is cut into ceil(c / 224) tiles of
+// equal size, so that a ragged group pays for at most 15 rows that it does not have.
 //
-// Persistent CTAs, one per SM; warp roles:
+// Persistent CTA pairs (cta_group::2): a tile is 256 output features x up to 224
+// tokens, each CTA holds the accumulators of 128 of the features and brings their
+// weights and half of the tokens, which halves the token bytes that an SM takes in.
+// Warp roles, in each CTA:
 //   warp 0      TMA producer (weights 128 x 128, tokens in boxes of 32 rows)
-//   warp 1      MMA issuer (one thread), copies the scales to TMEM (tcgen05.cp)
+//   warp 1      leader: MMA issuer (one thread), copies the scales to TMEM
+//               (tcgen05.cp); other CTA: tells the leader which stages have landed
 //   warps 2, 3  scale producers: gather the bytes of four 128-blocks per row; warp 3
 //               allocates TMEM
 //   warps 4..7  epilogue: TMEM -> registers -> bf16, transposed through shared memory
@@ -27,13 +30,14 @@
 namespace moe {
 namespace {
 
-constexpr int kTileM = 128;        // output features per tile
+constexpr int kTileM = 256;        // output features per tile, half of them in each CTA
+constexpr int kHalfM = 128;
 constexpr int kTileN = 224;        // most tokens per tile: two accumulators and the scales fit TMEM
 constexpr int kBlk = 128;          // reduction block of a scale, and of a ring stage
-constexpr int kStages = 4;
+constexpr int kStages = 6;
 constexpr int kScaleSlots = 4;
-constexpr int kABytes = kTileM * kBlk;
-constexpr int kBBytes = kTileN * kBlk;
+constexpr int kABytes = kHalfM * kBlk;
+constexpr int kBBytes = 128 * kBlk;             // half of the tokens, whole in boxes of 32
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kScaleSlotBytes = 512 + 1024;   // 128 feature words, 256 token words
 constexpr int kEpiBytes = 4 * 32 * 64;        // per epilogue warp 32 tokens x 32 features
@@ -43,7 +47,7 @@ constexpr uint32_t kSfCol = 2 * kTileN;       // scales behind the two accumulat
 constexpr int kMaxE = 256;
 
 struct Tail {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kStages], peer_full[kStages], empty[kStages];
     uint64_t sf_full[kScaleSlots], sf_empty[kScaleSlots];
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem_base;
@@ -63,13 +67,13 @@ struct Params {
     int64_t R;
     int E, out, red;              // output features, reduction length
     int transpose, x_ue8m0, w_ue8m0;
-    int x_vec;                    // a row's four scales can be loaded as one vector
+    int x_vec;                    // 1: a row's four scales are one aligned vector; 2: sixteen are (bytes)
     int m_tiles;
     void *Y;
     int32_t *status;
 };
 
-// One tile of a group: where its rows start, how many it holds.
+// One tile of a group: its features, where its rows start, how many it holds.
 struct Tile {
     int e, m0, rows;
     int64_t row0;
@@ -109,20 +113,61 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, u
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
 
-// 32 rows of 16 bytes from shared memory to 4 TMEM columns, repeated in the four lane quarters.
+// 32 rows of 16 bytes from shared memory to 4 TMEM columns, repeated in the four lane quarters; each
+// CTA of the pair from its own memory to its own TMEM.
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr)
 {
     const uint64_t desc = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
                           (1ull << 46);   // no swizzle, 8-row groups 128 B apart
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+// The scales of 16 blocks of the reduction from k0 on: a lane's words of four token rows, and the
+// feature block's scale of block k0 + lane.
+struct ScaleWords {
+    uint32_t tok[4][4], feat;
+
+    __device__ __forceinline__ void load(const Params &p, const Tile &t, int k0, int half, int lane, uint32_t rank,
+                                         int blocks, bool &bad)
+    {
+        const int n = blocks - k0;
+        if (half == 0) {
+            const int m_blocks = (p.out + kBlk - 1) / kBlk, mb = t.m0 / kBlk + rank;
+            feat = 0;
+            if (lane < 16 && lane < n && mb < m_blocks)
+                feat = load_scale_byte(p.W_scale, p.w_ue8m0,
+                                       p.transpose ? (static_cast<int64_t>(t.e) * blocks + k0 + lane) * m_blocks + mb
+                                                   : (static_cast<int64_t>(t.e) * m_blocks + mb) * blocks + k0 + lane,
+                                       bad);
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int r = half * 128 + g * 32 + lane;
+            const int64_t at = (t.row0 + r) * blocks + k0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tok[g][i] = 0;
+            if (r >= t.rows) continue;
+            if (p.x_vec == 2) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.X_scale) + at));
+                tok[g][0] = v.x;
+                tok[g][1] = v.y;
+                tok[g][2] = v.z;
+                tok[g][3] = v.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (4 * i < n) tok[g][i] = load_scale_word(p.X_scale, p.x_ue8m0, at + 4 * i, 1, n - 4 * i, p.x_vec, bad);
+            }
+        }
+    }
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expert_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Params p)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -132,19 +177,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     Tail &tail = *reinterpret_cast<Tail *>(epi + kEpiBytes);
     volatile int *abort_flag = &tail.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&tail.full[s], 1);
+            mbar_init(&tail.peer_full[s], 1);
             mbar_init(&tail.empty[s], 1);
         }
         for (int s = 0; s < kScaleSlots; ++s) {
-            mbar_init(&tail.sf_full[s], 2);
+            mbar_init(&tail.sf_full[s], 4);
             mbar_init(&tail.sf_empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tail.acc_full[b], 1);
-            mbar_init(&tail.acc_empty[b], 4);
+            mbar_init(&tail.acc_empty[b], 8);
         }
         mbar_init(&tail.drain, 1);
         tail.abort = tail.bad_index = tail.bad_scale = 0;
@@ -153,8 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmW);
     }
     if (warp == 3) {
-        tmem_alloc(&tail.tmem_base, kTmemCols);
-        tmem_relinquish();
+        tmem_alloc_pair(&tail.tmem_base, kTmemCols);
     }
     // the groups: rows and token tiles of each (a group outside [0, R] holds none)
     __syncthreads();
@@ -187,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (e == 0) tail.first[0] = 0;
     }
     tc_fence_before_sync();
-    __syncthreads();
+    cluster_sync();               // both CTAs' barriers stand, both hold TMEM
     tc_fence_after_sync();
     const uint32_t tmem = tail.tmem_base;
     const int tiles = tail.first[p.E] * p.m_tiles;
@@ -198,20 +245,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             // weights of a group are read by several CTAs at about the same time, tokens too
             const uint64_t keep = l2_policy_evict_normal();
             uint32_t s = 0, ph = 0, issued = 0;
-            for (int tile = blockIdx.x; tile < tiles && !*abort_flag; tile += gridDim.x) {
+            for (int tile = pair; tile < tiles && !*abort_flag; tile += pairs) {
                 const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
-                const int boxes = (t.rows + 31) >> 5;
+                const int half = ((t.rows + 15) & ~15) >> 1;        // tokens of each CTA
+                const int boxes = (half + 31) >> 5;
+                const int m0 = t.m0 + rank * kHalfM;
+                const int32_t row0 = static_cast<int32_t>(t.row0) + rank * half;
                 for (int kb = 0; kb < blocks; ++kb) {
                     if (!mbar_wait_bounded(&tail.empty[s], ph ^ 1u, abort_flag)) break;
                     uint8_t *a = ring + s * kStageBytes, *b = a + kABytes;
                     mbar_arrive_expect_tx(&tail.full[s], kABytes + boxes * 32 * kBlk);
                     if (p.transpose)
-                        tma_load_3d(a, &tmW, &tail.full[s], t.m0, kb * kBlk, t.e, keep);
+                        tma_load_3d(a, &tmW, &tail.full[s], m0, kb * kBlk, t.e, keep);
                     else
-                        tma_load_3d(a, &tmW, &tail.full[s], kb * kBlk, t.m0, t.e, keep);
+                        tma_load_3d(a, &tmW, &tail.full[s], kb * kBlk, m0, t.e, keep);
                     for (int i = 0; i < boxes; ++i)
-                        tma_load_2d(b + i * 32 * kBlk, &tmX, &tail.full[s], kb * kBlk,
-                                    static_cast<int32_t>(t.row0) + i * 32, keep);
+                        tma_load_2d(b + i * 32 * kBlk, &tmX, &tail.full[s], kb * kBlk, row0 + i * 32, keep);
                     ++issued;
                     if (++s == kStages) {
                         s = 0;
@@ -228,6 +277,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+    } else if (warp == 1 && rank != 0) {
+        if (lane == 0) {
+            uint32_t s = 0, ph = 0;
+            for (int tile = pair; tile < tiles && !*abort_flag; tile += pairs) {
+                for (int kb = 0; kb < blocks; ++kb) {
+                    if (!mbar_wait_bounded(&tail.full[s], ph, abort_flag)) break;
+                    mbar_arrive_at(&tail.peer_full[s], 0);
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+        }
     } else if (warp == 1) {
         if (lane == 0) {
             // A: the weights, K-major (128-byte rows of k) or, transposed, MN-major (rows of m); 8-row
@@ -238,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t s = 0, ph = 0, q = 0, qph = 0;
             int j = 0;
             bool stop = false;
-            for (int tile = blockIdx.x; tile < tiles && !stop; tile += gridDim.x) {
+            for (int tile = pair; tile < tiles && !stop; tile += pairs) {
                 const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
                 const int b = j & 1;
                 if (!mbar_wait_bounded(&tail.acc_empty[b], ((j >> 1) & 1) ^ 1, abort_flag)) break;
@@ -248,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t sfa = 0, sfb = 0;
                 for (int kb = 0; kb < blocks; ++kb) {
                     if ((kb & 3) == 0) {
-                        if (!mbar_wait_bounded(&tail.sf_full[q], qph, abort_flag)) {
+                        if (!mbar_wait_cluster(&tail.sf_full[q], qph, abort_flag)) {
                             stop = true;
                             break;
                         }
@@ -259,13 +322,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         copy_scales(sfa, src);
                         copy_scales(sfb, src + 512);
                         copy_scales(sfb + 4, src + 1024);
-                        tc_commit(&tail.sf_empty[q]);
+                        tc_commit_pair(&tail.sf_empty[q]);
                         if (++q == kScaleSlots) {
                             q = 0;
                             qph ^= 1u;
                         }
                     }
-                    if (!mbar_wait_bounded(&tail.full[s], ph, abort_flag)) {
+                    if (!mbar_wait_bounded(&tail.full[s], ph, abort_flag) ||
+                        !mbar_wait_bounded(&tail.peer_full[s], ph, abort_flag)) {
                         stop = true;
                         break;
                     }
@@ -275,61 +339,61 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kBlk / 32; ++i)
                         mma_scaled(d, a0 + at + i * a_step, b0 + at + i * 2, idesc, sfa, sfb, (kb | i) != 0);
-                    tc_commit(&tail.empty[s]);
+                    tc_commit_pair(&tail.empty[s]);
                     if (++s == kStages) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
                 if (stop) break;
-                tc_commit(&tail.acc_full[b]);
+                tc_commit_pair(&tail.acc_full[b]);
                 ++j;
             }
-            tc_commit(&tail.drain);
+            tc_commit_pair(&tail.drain);
             volatile int no_abort = 0;
             mbar_wait_bounded(&tail.drain, 0, &no_abort);
         }
     } else if (warp == 2 || warp == 3) {
         // Scale words: byte i of a row's word is the scale of 128-block 4 q + i.  Tokens: row r at
-        // lane r % 32, word r / 32 of a 128-row atom; features: one word for the whole 128.  A warp
-        // gathers one atom, all its loads in flight together and ahead of the ring's free slot.
-        const int m_blocks = (p.out + kBlk - 1) / kBlk;
+        // lane r % 32, word r / 32 of a 128-row atom; features: one word for the whole 128.  Each warp
+        // holds one atom's words of up to 16 blocks, and has those of the next 16 (or of the next tile)
+        // in flight while it hands these out: a load's latency is spread over as many ring stages.
         const int half = warp - 2;
         uint32_t q = 0, qph = 0;
-        bool bad = false;
-        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
-            const int mb = t.m0 / kBlk;
-            bool ok = true;
-            for (int k0 = 0; k0 < blocks; k0 += 4) {
-                const int nk = blocks - k0 < 4 ? blocks - k0 : 4;
-                uint32_t wa = 0, wb[4];
-                if (half == 0) {
-                    const int64_t at = p.transpose ? (static_cast<int64_t>(t.e) * blocks + k0) * m_blocks + mb
-                                                   : (static_cast<int64_t>(t.e) * m_blocks + mb) * blocks + k0;
-                    wa = load_scale_word(p.W_scale, p.w_ue8m0, at, p.transpose ? m_blocks : 1, nk, false, bad);
-                }
+        bool bad = false, ok = true;
+        ScaleWords cur, nxt;
+        int tile = pair, k0 = 0;
+        if (tile < tiles) cur.load(p, find_tile(tail, tile, p.m_tiles, p.E), k0, half, lane, rank, blocks, bad);
+        while (tile < tiles && ok) {
+            int tile2 = tile, k2 = k0 + 16;
+            if (k2 >= blocks) {
+                k2 = 0;
+                tile2 += pairs;
+            }
+            if (tile2 < tiles) nxt.load(p, find_tile(tail, tile2, p.m_tiles, p.E), k2, half, lane, rank, blocks, bad);
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    wb[g] = 0;
-                    const int r = half * 128 + g * 32 + lane;
-                    if (r < t.rows)
-                        wb[g] = load_scale_word(p.X_scale, p.x_ue8m0, (t.row0 + r) * blocks + k0, 1, nk, p.x_vec, bad);
-                }
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.sf_empty[q], qph ^ 1u, abort_flag, 32));
-                if (!ok) break;
+            for (int i = 0; i < 4; ++i) {
+                if (k0 + 4 * i >= blocks) break;
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&tail.sf_empty[q], qph ^ 1u, abort_flag, 32));
                 uint4 *slot = reinterpret_cast<uint4 *>(sf_ring + q * kScaleSlotBytes);
-                if (half == 0) slot[lane] = make_uint4(wa, wa, wa, wa);
-                slot[32 + half * 32 + lane] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+                if (half == 0) {
+                    uint32_t wa = 0;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) wa |= __shfl_sync(0xffffffffu, cur.feat, 4 * i + b) << (8 * b);
+                    slot[lane] = make_uint4(wa, wa, wa, wa);
+                }
+                slot[32 + half * 32 + lane] = make_uint4(cur.tok[0][i], cur.tok[1][i], cur.tok[2][i], cur.tok[3][i]);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&tail.sf_full[q]);
+                if (lane == 0) mbar_arrive_release_at(&tail.sf_full[q], 0);
                 if (++q == kScaleSlots) {
                     q = 0;
                     qph ^= 1u;
                 }
             }
-            if (!ok) break;
+            cur = nxt;
+            tile = tile2;
+            k0 = k2;
         }
         if (bad) tail.bad_scale = 1;
     } else if (warp >= 4) {
@@ -337,12 +401,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t *buf = epi + w * 32 * 64;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(w * 32) << 16);
         int j = 0;
-        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        for (int tile = pair; tile < tiles; tile += pairs) {
             const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
             const int b = j & 1;
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, abort_flag, 64))) break;
             tc_fence_after_sync();
-            const int m = t.m0 + w * 32;                 // this warp's features
+            const int m = t.m0 + rank * kHalfM + w * 32;  // this warp's features
             const int feats = p.out - m;                 // a multiple of 16, may be <= 0
             for (int c = 0; c < t.rows; c += 32) {
                 float v[32];
@@ -363,15 +427,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
             tc_fence_before_sync();
-            if (lane == 0) mbar_arrive(&tail.acc_empty[b]);
+            if (lane == 0) mbar_arrive_at(&tail.acc_empty[b], 0);
             ++j;
         }
     }
 
     tc_fence_before_sync();
-    __syncthreads();
+    cluster_sync();               // the leader's MMAs have read the other CTA's memory
     tc_fence_after_sync();
-    if (warp == 3) tmem_dealloc(tmem, kTmemCols);
+    if (warp == 3) tmem_dealloc_pair(tmem, kTmemCols);
     if (threadIdx.x == 0) {
         if (tail.abort) report_status(p.status, MOE_ERR_TIMEOUT);
         if (tail.bad_index) report_status(p.status, MOE_ERR_BAD_INDEX);
@@ -456,14 +520,16 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t stream)
     p.transpose = a.transpose;
     p.x_ue8m0 = a.x_ue8m0;
     p.w_ue8m0 = a.w_ue8m0;
-    p.x_vec = (red / kBlk) % 4 == 0 && reinterpret_cast<uintptr_t>(a.X_scale) % (a.x_ue8m0 ? 4 : 16) == 0;
+    const uintptr_t xs = reinterpret_cast<uintptr_t>(a.X_scale);
+    p.x_vec = (red / kBlk) % 4 == 0 && xs % (a.x_ue8m0 ? 4 : 16) == 0;
+    if (a.x_ue8m0 && (red / kBlk) % 16 == 0 && xs % 16 == 0) p.x_vec = 2;
     p.m_tiles = (out + kTileM - 1) / kTileM;
     p.Y = a.Y;
     p.status = a.status;
-    // the most tiles that R rows in E groups can make; no more CTAs than that
+    // the most tiles that R rows in E groups can make; no more pairs than that
     const int64_t most = (a.R / kTileN + (a.R < a.E ? a.R : a.E) + 1) * p.m_tiles;
-    const int sms = device_sm_count(dev);
-    const int grid = static_cast<int>(most < sms ? most : sms);
+    const int pairs = device_sm_count(dev) / 2;
+    const int grid = 2 * static_cast<int>(most < pairs ? most : pairs);
     expert_gemm_kernel<<<grid, kThreads, kSmemBytes, stream>>>(tmX, tmW, p);
     return cudaGetLastError();
 }
