@@ -176,7 +176,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t *epi = sf_ring + kScaleSlots * kScaleSlotBytes;
     Tail &tail = *reinterpret_cast<Tail *>(epi + kEpiBytes);
     volatile int *abort_flag = &tail.abort;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
@@ -241,118 +241,121 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int blocks = p.red / kBlk;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // weights of a group are read by several CTAs at about the same time, tokens too
-            const uint64_t keep = l2_policy_evict_normal();
-            uint32_t s = 0, ph = 0, issued = 0;
-            for (int tile = pair; tile < tiles && !*abort_flag; tile += pairs) {
-                const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
-                const int half = ((t.rows + 15) & ~15) >> 1;        // tokens of each CTA
-                const int boxes = (half + 31) >> 5;
-                const int m0 = t.m0 + rank * kHalfM;
-                const int32_t row0 = static_cast<int32_t>(t.row0) + rank * half;
-                for (int kb = 0; kb < blocks; ++kb) {
-                    if (!mbar_wait_bounded(&tail.empty[s], ph ^ 1u, abort_flag)) break;
-                    uint8_t *a = ring + s * kStageBytes, *b = a + kABytes;
+        // weights of a group are read by several CTAs at about the same time, tokens too
+        const uint64_t keep = l2_policy_evict_normal();
+        uint32_t s = 0, ph = 0, issued = 0;
+        bool ok = true;
+        for (int tile = pair; tile < tiles && ok; tile += pairs) {
+            const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
+            const int half = ((t.rows + 15) & ~15) >> 1;        // tokens of each CTA
+            const int boxes = (half + 31) >> 5;
+            const int m0 = t.m0 + rank * kHalfM;
+            const int32_t row0 = static_cast<int32_t>(t.row0) + rank * half;
+            for (int kb = 0; kb < blocks; ++kb) {
+                ok = warp_wait(&tail.empty[s], ph ^ 1u, abort_flag);
+                if (!ok) break;
+                uint8_t *a = ring + s * kStageBytes, *b = a + kABytes;
+                if (elect_one()) {
                     mbar_arrive_expect_tx(&tail.full[s], kABytes + boxes * 32 * kBlk);
-                    if (p.transpose)
-                        tma_load_3d(a, &tmW, &tail.full[s], m0, kb * kBlk, t.e, keep);
-                    else
-                        tma_load_3d(a, &tmW, &tail.full[s], kb * kBlk, m0, t.e, keep);
+                    tma_load_3d(a, &tmW, &tail.full[s], p.transpose ? m0 : kb * kBlk, p.transpose ? kb * kBlk : m0, t.e, keep);
                     for (int i = 0; i < boxes; ++i)
                         tma_load_2d(b + i * 32 * kBlk, &tmX, &tail.full[s], kb * kBlk, row0 + i * 32, keep);
-                    ++issued;
-                    if (++s == kStages) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
                 }
-            }
-            if (*abort_flag) {
-                // let the copies already issued land before the CTA ends
-                const uint32_t from = issued > kStages ? issued - kStages : 0u;
-                for (uint32_t x = from; x < issued; ++x) {
-                    volatile int no_abort = 0;
-                    mbar_wait_bounded(&tail.full[x % kStages], (x / kStages) & 1u, &no_abort);
+                __syncwarp();
+                ++issued;
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
         }
+        if (!ok) {
+            // let the copies already issued land before the CTA ends
+            const uint32_t from = issued > kStages ? issued - kStages : 0u;
+            for (uint32_t x = from; x < issued; ++x) {
+                volatile int no_abort = 0;
+                mbar_wait_bounded(&tail.full[x % kStages], (x / kStages) & 1u, &no_abort);
+            }
+        }
     } else if (warp == 1 && rank != 0) {
-        if (lane == 0) {
-            uint32_t s = 0, ph = 0;
-            for (int tile = pair; tile < tiles && !*abort_flag; tile += pairs) {
-                for (int kb = 0; kb < blocks; ++kb) {
-                    if (!mbar_wait_bounded(&tail.full[s], ph, abort_flag)) break;
-                    mbar_arrive_at(&tail.peer_full[s], 0);
-                    if (++s == kStages) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+        uint32_t s = 0, ph = 0;
+        bool ok = true;
+        for (int tile = pair; tile < tiles && ok; tile += pairs) {
+            for (int kb = 0; kb < blocks; ++kb) {
+                ok = warp_wait(&tail.full[s], ph, abort_flag);
+                if (!ok) break;
+                if (elect_one()) mbar_arrive_at(&tail.peer_full[s], 0);
+                __syncwarp();
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // A: the weights, K-major (128-byte rows of k) or, transposed, MN-major (rows of m); 8-row
-            // groups 1024 B apart either way.  A K = 32 step is 32 bytes of a row, or 32 rows.
-            const uint64_t a0 = make_smem_desc_sw128(smem_u32(ring), 16, 1024);
-            const uint64_t b0 = make_smem_desc_sw128(smem_u32(ring + kABytes), 16, 1024);
-            const uint32_t a_step = p.transpose ? 32 * 128 / 16 : 2;
-            uint32_t s = 0, ph = 0, q = 0, qph = 0;
-            int j = 0;
-            bool stop = false;
-            for (int tile = pair; tile < tiles && !stop; tile += pairs) {
-                const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
-                const int b = j & 1;
-                if (!mbar_wait_bounded(&tail.acc_empty[b], ((j >> 1) & 1) ^ 1, abort_flag)) break;
+        // A: the weights, K-major (128-byte rows of k) or, transposed, MN-major (rows of m); 8-row
+        // groups 1024 B apart either way.  A K = 32 step is 32 bytes of a row, or 32 rows.
+        const uint64_t a0 = make_smem_desc_sw128(smem_u32(ring), 16, 1024);
+        const uint64_t b0 = make_smem_desc_sw128(smem_u32(ring + kABytes), 16, 1024);
+        const uint32_t a_step = p.transpose ? 32 * 128 / 16 : 2;
+        uint32_t s = 0, ph = 0, q = 0, qph = 0;
+        int j = 0;
+        bool ok = true;
+        for (int tile = pair; tile < tiles; tile += pairs) {
+            const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
+            const int b = j & 1;
+            ok = warp_wait(&tail.acc_empty[b], ((j >> 1) & 1) ^ 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t d = tmem + b * kTileN;
+            const uint32_t idesc0 = make_idesc((t.rows + 15) & ~15, p.transpose, 0);
+            for (int k0 = 0; k0 < blocks && ok; k0 += 4) {
+                ok = warp_wait_cluster(&tail.sf_full[q], qph, abort_flag);
+                if (!ok) break;
                 tc_fence_after_sync();
-                const uint32_t d = tmem + b * kTileN;
-                const uint32_t N = (t.rows + 15) & ~15;
-                uint32_t sfa = 0, sfb = 0;
-                for (int kb = 0; kb < blocks; ++kb) {
-                    if ((kb & 3) == 0) {
-                        if (!mbar_wait_cluster(&tail.sf_full[q], qph, abort_flag)) {
-                            stop = true;
-                            break;
-                        }
-                        tc_fence_after_sync();
-                        const uint32_t src = smem_u32(sf_ring + q * kScaleSlotBytes);
-                        sfa = tmem + kSfCol + (q & 1) * 12;
-                        sfb = sfa + 4;
-                        copy_scales(sfa, src);
-                        copy_scales(sfb, src + 512);
-                        copy_scales(sfb + 4, src + 1024);
-                        tc_commit_pair(&tail.sf_empty[q]);
-                        if (++q == kScaleSlots) {
-                            q = 0;
-                            qph ^= 1u;
-                        }
-                    }
-                    if (!mbar_wait_bounded(&tail.full[s], ph, abort_flag) ||
-                        !mbar_wait_bounded(&tail.peer_full[s], ph, abort_flag)) {
-                        stop = true;
-                        break;
-                    }
+                const uint32_t src = smem_u32(sf_ring + q * kScaleSlotBytes);
+                const uint32_t sfa = tmem + kSfCol + (q & 1) * 12, sfb = sfa + 4;
+                if (elect_one()) {
+                    copy_scales(sfa, src);
+                    copy_scales(sfb, src + 512);
+                    copy_scales(sfb + 4, src + 1024);
+                    tc_commit_pair(&tail.sf_empty[q]);
+                }
+                __syncwarp();
+                if (++q == kScaleSlots) {
+                    q = 0;
+                    qph ^= 1u;
+                }
+#pragma unroll
+                for (uint32_t kk = 0; kk < 4; ++kk) {
+                    if (k0 + static_cast<int>(kk) >= blocks) break;
+                    ok = warp_wait(&tail.full[s], ph, abort_flag) && warp_wait(&tail.peer_full[s], ph, abort_flag);
+                    if (!ok) break;
                     tc_fence_after_sync();
                     const uint64_t at = (s * kStageBytes) >> 4;
-                    const uint32_t idesc = make_idesc(N, p.transpose, kb & 3);
+                    const uint32_t idesc = idesc0 | (kk << 4) | (kk << 29);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < kBlk / 32; ++i)
-                        mma_scaled(d, a0 + at + i * a_step, b0 + at + i * 2, idesc, sfa, sfb, (kb | i) != 0);
-                    tc_commit_pair(&tail.empty[s]);
+                        for (int i = 0; i < kBlk / 32; ++i)
+                            mma_scaled(d, a0 + at + i * a_step, b0 + at + i * 2, idesc, sfa, sfb, (k0 | kk | i) != 0);
+                        tc_commit_pair(&tail.empty[s]);
+                    }
+                    __syncwarp();
                     if (++s == kStages) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
-                if (stop) break;
-                tc_commit_pair(&tail.acc_full[b]);
-                ++j;
             }
-            tc_commit_pair(&tail.drain);
-            volatile int no_abort = 0;
-            mbar_wait_bounded(&tail.drain, 0, &no_abort);
+            if (!ok) break;
+            if (elect_one()) tc_commit_pair(&tail.acc_full[b]);
+            __syncwarp();
+            ++j;
         }
+        if (elect_one()) tc_commit_pair(&tail.drain);
+        __syncwarp();
+        volatile int no_abort = 0;
+        mbar_wait_bounded(&tail.drain, 0, &no_abort);
     } else if (warp == 2 || warp == 3) {
         // Scale words: byte i of a row's word is the scale of 128-block 4 q + i.  Tokens: row r at
         // lane r % 32, word r / 32 of a 128-row atom; features: one word for the whole 128.  Each warp

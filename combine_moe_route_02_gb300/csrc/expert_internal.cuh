@@ -158,6 +158,36 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
 }
 
+// A warp's waits, all lanes together: the warp's control flow stays uniform, which keeps the operands
+// of the TMA and tcgen05 instructions that follow in uniform registers (a single-lane branch around
+// the expert products' loops cost 70 cycles for each MMA issued).  The polling loop is out of line.
+static __device__ __noinline__ bool warp_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort));
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
+    return warp_wait_slow(bar, parity, abort);
+}
+// The same for a barrier that mbar_arrive_release_at arrives on.
+static __device__ __noinline__ bool warp_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort));
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst, uint32_t ncols)
 {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
