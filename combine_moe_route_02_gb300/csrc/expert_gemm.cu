@@ -35,11 +35,12 @@ constexpr int kHalfM = 128;
 constexpr int kTileN = 224;        // most tokens per tile: two accumulators and the scales fit TMEM
 constexpr int kBlk = 128;          // reduction block of a scale, and of a ring stage
 constexpr int kStages = 6;
-constexpr int kScaleSlots = 4;
+constexpr int kScaleSlots = 2;
 constexpr int kABytes = kHalfM * kBlk;
 constexpr int kBBytes = 128 * kBlk;             // half of the tokens, whole in boxes of 32
 constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kScaleSlotBytes = 512 + 1024;   // 128 feature words, 256 token words
+constexpr int kScaleQuadBytes = 512 + 1024;   // four blocks: 128 feature words, 256 token words
+constexpr int kScaleSlotBytes = 4 * kScaleQuadBytes;
 constexpr int kEpiBytes = 4 * 32 * 64;        // per epilogue warp 32 tokens x 32 features
 constexpr int kThreads = 256;
 constexpr uint32_t kTmemCols = 512;
@@ -47,7 +48,7 @@ constexpr uint32_t kSfCol = 2 * kTileN;       // scales behind the two accumulat
 constexpr int kMaxE = 256;
 
 struct Tail {
-    uint64_t full[kStages], peer_full[kStages], empty[kStages];
+    uint64_t full[kStages], empty[kStages];
     uint64_t sf_full[kScaleSlots], sf_empty[kScaleSlots];
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem_base;
@@ -182,8 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&tail.full[s], 1);
-            mbar_init(&tail.peer_full[s], 1);
+            mbar_init(&tail.full[s], rank == 0 ? 2 : 1);   // the leader's: its own stage and the other CTA's
             mbar_init(&tail.empty[s], 1);
         }
         for (int s = 0; s < kScaleSlots; ++s) {
@@ -284,7 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int kb = 0; kb < blocks; ++kb) {
                 ok = warp_wait(&tail.full[s], ph, abort_flag);
                 if (!ok) break;
-                if (elect_one()) mbar_arrive_at(&tail.peer_full[s], 0);
+                if (elect_one()) mbar_arrive_at(&tail.full[s], 0);
                 __syncwarp();
                 if (++s == kStages) {
                     s = 0;
@@ -310,26 +310,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t d = tmem + b * kTileN;
             const uint32_t idesc0 = make_idesc((t.rows + 15) & ~15, p.transpose, 0);
             for (int k0 = 0; k0 < blocks && ok; k0 += 4) {
-                ok = warp_wait_cluster(&tail.sf_full[q], qph, abort_flag);
-                if (!ok) break;
-                tc_fence_after_sync();
-                const uint32_t src = smem_u32(sf_ring + q * kScaleSlotBytes);
-                const uint32_t sfa = tmem + kSfCol + (q & 1) * 12, sfb = sfa + 4;
+                if ((k0 & 15) == 0) {
+                    ok = warp_wait_cluster(&tail.sf_full[q], qph, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                }
+                const uint32_t src = smem_u32(sf_ring + q * kScaleSlotBytes) + ((k0 >> 2) & 3) * kScaleQuadBytes;
+                const uint32_t sfa = tmem + kSfCol + ((k0 >> 2) & 1) * 12, sfb = sfa + 4;
+                const bool last = (k0 & 15) == 12 || k0 + 4 >= blocks;    // of the slot
                 if (elect_one()) {
                     copy_scales(sfa, src);
                     copy_scales(sfb, src + 512);
                     copy_scales(sfb + 4, src + 1024);
-                    tc_commit_pair(&tail.sf_empty[q]);
+                    if (last) tc_commit_pair(&tail.sf_empty[q]);
                 }
                 __syncwarp();
-                if (++q == kScaleSlots) {
-                    q = 0;
-                    qph ^= 1u;
+                if (last) {
+                    q ^= 1u;
+                    qph ^= q ^ 1u;
                 }
 #pragma unroll
                 for (uint32_t kk = 0; kk < 4; ++kk) {
                     if (k0 + static_cast<int>(kk) >= blocks) break;
-                    ok = warp_wait(&tail.full[s], ph, abort_flag) && warp_wait(&tail.peer_full[s], ph, abort_flag);
+                    ok = warp_wait(&tail.full[s], ph, abort_flag);
                     if (!ok) break;
                     tc_fence_after_sync();
                     const uint64_t at = (s * kStageBytes) >> 4;
@@ -374,26 +377,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tile2 += pairs;
             }
             if (tile2 < tiles) nxt.load(p, find_tile(tail, tile2, p.m_tiles, p.E), k2, half, lane, rank, blocks, bad);
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.sf_empty[q], qph ^ 1u, abort_flag, 32));
+            uint4 *slot = reinterpret_cast<uint4 *>(sf_ring + q * kScaleSlotBytes);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (k0 + 4 * i >= blocks) break;
-                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&tail.sf_empty[q], qph ^ 1u, abort_flag, 32));
-                uint4 *slot = reinterpret_cast<uint4 *>(sf_ring + q * kScaleSlotBytes);
                 if (half == 0) {
                     uint32_t wa = 0;
 #pragma unroll
                     for (int b = 0; b < 4; ++b) wa |= __shfl_sync(0xffffffffu, cur.feat, 4 * i + b) << (8 * b);
-                    slot[lane] = make_uint4(wa, wa, wa, wa);
+                    slot[i * (kScaleQuadBytes / 16) + lane] = make_uint4(wa, wa, wa, wa);
                 }
-                slot[32 + half * 32 + lane] = make_uint4(cur.tok[0][i], cur.tok[1][i], cur.tok[2][i], cur.tok[3][i]);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_release_at(&tail.sf_full[q], 0);
-                if (++q == kScaleSlots) {
-                    q = 0;
-                    qph ^= 1u;
-                }
+                slot[i * (kScaleQuadBytes / 16) + 32 + half * 32 + lane] =
+                    make_uint4(cur.tok[0][i], cur.tok[1][i], cur.tok[2][i], cur.tok[3][i]);
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_release_at(&tail.sf_full[q], 0);
+            q ^= 1u;
+            qph ^= q ^ 1u;
             cur = nxt;
             tile = tile2;
             k0 = k2;
