@@ -17,7 +17,7 @@
 // tokens, each CTA holds the accumulators of 128 of the features and brings their
 // weights and half of the tokens, which halves the token bytes that an SM takes in.
 // Warp roles, in each CTA:
-//   warp 0      TMA producer (weights 128 x 128, tokens in boxes of 32 rows)
+//   warp 0      TMA producer (weights 128 x 128, the tokens in one box)
 //   warp 1      leader: MMA issuer (one thread), copies the scales to TMEM
 //               (tcgen05.cp); other CTA: tells the leader which stages have landed
 //   warps 2, 3  scale producers: gather the bytes of four 128-blocks per row; warp 3
@@ -37,7 +37,7 @@ constexpr int kBlk = 128;          // reduction block of a scale, and of a ring 
 constexpr int kStages = 6;
 constexpr int kScaleSlots = 2;
 constexpr int kABytes = kHalfM * kBlk;
-constexpr int kBBytes = 128 * kBlk;             // half of the tokens, whole in boxes of 32
+constexpr int kBBytes = kTileN / 2 * kBlk;      // half of the tokens
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kScaleQuadBytes = 512 + 1024;   // four blocks: 128 feature words, 256 token words
 constexpr int kScaleSlotBytes = 4 * kScaleQuadBytes;
@@ -61,6 +61,14 @@ struct Tail {
 constexpr size_t kSmemBytes =
     1024 + kStages * kStageBytes + kScaleSlots * kScaleSlotBytes + kEpiBytes + sizeof(Tail);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// Boxes of token rows: a tile takes the smallest that holds its half, so that a stage is two copies
+// (issuing a copy took ~90 cycles: with one for every 32 rows the producer set the pace).
+constexpr int kBoxes = 5;
+__host__ __device__ constexpr int box_rows(int i) { return i == 0 ? 112 : i == 1 ? 96 : i == 2 ? 80 : i == 3 ? 64 : 32; }
+struct TokenMaps {
+    CUtensorMap map[kBoxes];
+};
 
 struct Params {
     const void *X_scale, *W_scale;
@@ -128,6 +136,48 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr)
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
+// 32 lanes x 32 columns of TMEM as fragments of 8x8: v[16 h + 4 c + 2 r + i] is row 16 h + 8 r + lane / 4,
+// column 8 c + 2 (lane % 4) + i.
+__device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, float (&v)[32])
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t r[16];
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr + (static_cast<uint32_t>(16 * h) << 16))
+            : "memory");
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[16 * h + i] = __uint_as_float(r[i]);
+    }
+}
+
+// Those fragments (rows features, columns tokens) as bf16 to shared memory with the tokens as rows of 64
+// bytes: stmatrix transposes each 8x8.  The 16-byte piece f of token t lies at place f ^ (t / 2 % 4).
+__device__ __forceinline__ void store_transposed(uint32_t buf, int lane, const float (&v)[32])
+{
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        // the four matrices: features 0..7, 8..15, 16..23, 24..31 of tokens 8 c .. 8 c + 7
+        uint32_t m[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            const int at = 16 * (f >> 1) + 4 * c + 2 * (f & 1);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[at], v[at + 1]);
+            m[f] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        // lane l gives the address of row l % 8 of matrix l / 8
+        const int tok = 8 * c + (lane & 7), f = lane >> 3;
+        const uint32_t addr = buf + tok * 64 + ((f ^ ((tok >> 1) & 3)) << 4);
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(m[0]),
+                     "r"(m[1]), "r"(m[2]), "r"(m[3])
+                     : "memory");
+    }
+}
+
 // The scales of 16 blocks of the reduction from k0 on: a lane's words of four token rows, and the
 // feature block's scale of block k0 + lane.
 struct ScaleWords {
@@ -169,7 +219,7 @@ struct ScaleWords {
 };
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    expert_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Params p)
+    expert_gemm_kernel(const __grid_constant__ TokenMaps tmX, const __grid_constant__ CUtensorMap tmW, const Params p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -197,7 +247,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(&tail.drain, 1);
         tail.abort = tail.bad_index = tail.bad_scale = 0;
         fence_mbarrier_init();
-        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmX.map[0]);
         tma_prefetch_desc(&tmW);
     }
     if (warp == 3) {
@@ -248,7 +298,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int tile = pair; tile < tiles && ok; tile += pairs) {
             const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
             const int half = ((t.rows + 15) & ~15) >> 1;        // tokens of each CTA
-            const int boxes = (half + 31) >> 5;
+            int box = kBoxes - 1;
+#pragma unroll
+            for (int i = 0; i < kBoxes - 1; ++i)
+                if (half > box_rows(i + 1)) {
+                    box = i;
+                    break;
+                }
+            const CUtensorMap *map = &tmX.map[box];
+            const uint32_t bytes = kABytes + box_rows(box) * kBlk;
             const int m0 = t.m0 + rank * kHalfM;
             const int32_t row0 = static_cast<int32_t>(t.row0) + rank * half;
             for (int kb = 0; kb < blocks; ++kb) {
@@ -256,10 +314,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 uint8_t *a = ring + s * kStageBytes, *b = a + kABytes;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&tail.full[s], kABytes + boxes * 32 * kBlk);
+                    mbar_arrive_expect_tx(&tail.full[s], bytes);
                     tma_load_3d(a, &tmW, &tail.full[s], p.transpose ? m0 : kb * kBlk, p.transpose ? kb * kBlk : m0, t.e, keep);
-                    for (int i = 0; i < boxes; ++i)
-                        tma_load_2d(b + i * 32 * kBlk, &tmX, &tail.full[s], kb * kBlk, row0 + i * 32, keep);
+                    tma_load_2d(b, map, &tail.full[s], kb * kBlk, row0, keep);
                 }
                 __syncwarp();
                 ++issued;
@@ -403,6 +460,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp >= 4) {
         const int w = warp - 4;
         uint8_t *buf = epi + w * 32 * 64;
+        const uint32_t buf_addr = smem_u32(buf);
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(w * 32) << 16);
         int j = 0;
         for (int tile = pair; tile < tiles; tile += pairs) {
@@ -412,21 +470,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             const int m = t.m0 + rank * kHalfM + w * 32;  // this warp's features
             const int feats = p.out - m;                 // a multiple of 16, may be <= 0
-            for (int c = 0; c < t.rows; c += 32) {
-                float v[32];
-                tmem_ld_32x32b_x32(lane_addr + b * kTileN + c, v);
+            // a lane's four 16-byte pieces of a chunk: tokens lane / 4 + 8 i, features 8 (lane % 4) on
+            const bool part_ok = (lane & 3) * 8 < feats;
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.Y) + (t.row0 + (lane >> 2)) * p.out + m + (lane & 3) * 8;
+            float v[2][32];
+            tmem_ld_fragments(lane_addr + b * kTileN, v[0]);
+#pragma unroll 2
+            for (int c = 0, x = 0; c < t.rows; c += 32, x ^= 1) {
                 tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    *reinterpret_cast<__nv_bfloat16 *>(buf + i * 64 + lane * 2) = __float2bfloat16(v[i]);
+                store_transposed(buf_addr, lane, v[x]);
+                if (c + 32 < t.rows) tmem_ld_fragments(lane_addr + b * kTileN + c + 32, v[x ^ 1]);
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int tok = i * 8 + (lane >> 2), part = lane & 3;
-                    const uint4 x = *reinterpret_cast<const uint4 *>(buf + tok * 64 + part * 16);
-                    if (c + tok < t.rows && part * 8 < feats)
-                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.Y) +
-                                                   (t.row0 + c + tok) * p.out + m + part * 8) = x;
+                    const int tok = i * 8 + (lane >> 2);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(buf + tok * 64 + (((lane & 3) ^ ((tok >> 1) & 3)) << 4));
+                    if (c + tok < t.rows && part_ok)
+                        *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(c + 8 * i) * p.out) = y;
                 }
                 __syncwarp();
             }
@@ -496,14 +556,16 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t stream)
     if (device_cc_major(dev) != 10) return cudaErrorNotSupported;
     const int red = a.transpose ? a.rows : a.cols, out = a.transpose ? a.cols : a.rows;
 
-    CUtensorMap tmX, tmW;
+    TokenMaps tmX;
+    CUtensorMap tmW;
     const uint64_t xd[2] = {static_cast<uint64_t>(red), static_cast<uint64_t>(a.R)};
-    const uint32_t xb[2] = {kBlk, 32};
     const uint64_t wd[3] = {static_cast<uint64_t>(a.cols), static_cast<uint64_t>(a.rows), static_cast<uint64_t>(a.E)};
     const uint32_t wb[3] = {128, 128, 1};
-    if (!encode_map_sw128(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.X, 2, xd, xb) ||
-        !encode_map_sw128(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.W, 3, wd, wb))
-        return cudaErrorInvalidValue;
+    for (int i = 0; i < kBoxes; ++i) {
+        const uint32_t xb[2] = {kBlk, static_cast<uint32_t>(box_rows(i))};
+        if (!encode_map_sw128(&tmX.map[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.X, 2, xd, xb)) return cudaErrorInvalidValue;
+    }
+    if (!encode_map_sw128(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.W, 3, wd, wb)) return cudaErrorInvalidValue;
 
     static std::atomic<uint64_t> done{0};
     const uint64_t bit = 1ull << (dev & 63);
