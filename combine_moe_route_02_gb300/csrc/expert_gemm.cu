@@ -20,7 +20,7 @@
 //   warp 0      TMA producer (weights 128 x 128, the tokens in one box)
 //   warp 1      leader: MMA issuer (one thread), copies the scales to TMEM
 //               (tcgen05.cp); other CTA: tells the leader which stages have landed
-//   warps 2, 3  scale producers: gather the bytes of four 128-blocks per row; warp 3
+//   warps 2, 3, 8, 9  scale producers: gather the bytes of 16 128-blocks per row; warp 3
 //               allocates TMEM
 //   warps 4..7  epilogue: TMEM -> registers -> bf16, transposed through shared memory
 #include <mutex>
@@ -42,7 +42,7 @@ constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kScaleQuadBytes = 512 + 1024;   // four blocks: 128 feature words, 256 token words
 constexpr int kScaleSlotBytes = 4 * kScaleQuadBytes;
 constexpr int kEpiBytes = 4 * 32 * 64;        // per epilogue warp 32 tokens x 32 features
-constexpr int kThreads = 256;
+constexpr int kThreads = 320;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSfCol = 2 * kTileN;       // scales behind the two accumulators: 2 x (4 + 8) columns
 constexpr int kMaxE = 256;
@@ -55,7 +55,7 @@ struct Tail {
     int abort, bad_index, bad_scale;
     int tiles;                    // token tiles of all groups
     int first[kMaxE + 1];         // first token tile of each group
-    int begin[kMaxE], count[kMaxE];
+    int begin[kMaxE], count[kMaxE], size[kMaxE];   // its rows, and the rows of its tiles but the last
 };
 
 constexpr size_t kSmemBytes =
@@ -88,27 +88,37 @@ struct Tile {
     int64_t row0;
 };
 
-__device__ __forceinline__ Tile find_tile(const Tail &t, int tile, int m_tiles, int E)
-{
-    const int j = tile / m_tiles;
-    int lo = 0, hi = E - 1;       // the last group whose first tile is <= j
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (t.first[mid] <= j)
-            lo = mid;
-        else
-            hi = mid - 1;
+// A role's walk over its CTA pair's tiles (pair, pair + pairs, ...; the features of a token tile
+// follow each other): the group only ever moves forward.
+struct Walk {
+    int tile, j, i, e;            // tile, its token tile and feature tile, the group reached
+
+    __device__ __forceinline__ Walk(int pair, int m_tiles) : tile(pair), j(pair / m_tiles), i(pair - j * m_tiles), e(0) {}
+
+    __device__ __forceinline__ void next(int pairs, int m_tiles)
+    {
+        tile += pairs;
+        i += pairs;
+        if (i >= m_tiles) {
+            const int n = i / m_tiles;
+            j += n;
+            i -= n * m_tiles;
+        }
     }
-    Tile r;
-    r.e = lo;
-    r.m0 = (tile - j * m_tiles) * kTileM;
-    const int c = t.count[lo], n = t.first[lo + 1] - t.first[lo], i = j - t.first[lo];
-    const int size = ((c + n - 1) / n + 15) & ~15;   // equal parts, whole in 16
-    r.row0 = static_cast<int64_t>(t.begin[lo]) + static_cast<int64_t>(i) * size;
-    const int left = c - i * size;
-    r.rows = left < size ? left : size;   // (never empty: size <= kTileN, and n - 1 tiles of that do not hold c)
-    return r;
-}
+
+    __device__ __forceinline__ Tile get(const Tail &t)
+    {
+        while (t.first[e + 1] <= j) ++e;
+        Tile r;
+        r.e = e;
+        r.m0 = i * kTileM;
+        const int size = t.size[e], at = (j - t.first[e]) * size;
+        r.row0 = static_cast<int64_t>(t.begin[e]) + at;
+        const int left = t.count[e] - at;
+        r.rows = left < size ? left : size;
+        return r;
+    }
+};
 
 // kind::mxf8f6f4, E4M3 x E4M3 -> fp32, UE8M0 scales; the scale byte of the word is `sf`.
 __device__ __forceinline__ uint32_t make_idesc(uint32_t N, uint32_t a_mn_major, uint32_t sf)
@@ -178,46 +188,6 @@ __device__ __forceinline__ void store_transposed(uint32_t buf, int lane, const f
     }
 }
 
-// The scales of 16 blocks of the reduction from k0 on: a lane's words of four token rows, and the
-// feature block's scale of block k0 + lane.
-struct ScaleWords {
-    uint32_t tok[4][4], feat;
-
-    __device__ __forceinline__ void load(const Params &p, const Tile &t, int k0, int half, int lane, uint32_t rank,
-                                         int blocks, bool &bad)
-    {
-        const int n = blocks - k0;
-        if (half == 0) {
-            const int m_blocks = (p.out + kBlk - 1) / kBlk, mb = t.m0 / kBlk + rank;
-            feat = 0;
-            if (lane < 16 && lane < n && mb < m_blocks)
-                feat = load_scale_byte(p.W_scale, p.w_ue8m0,
-                                       p.transpose ? (static_cast<int64_t>(t.e) * blocks + k0 + lane) * m_blocks + mb
-                                                   : (static_cast<int64_t>(t.e) * m_blocks + mb) * blocks + k0 + lane,
-                                       bad);
-        }
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int r = half * 128 + g * 32 + lane;
-            const int64_t at = (t.row0 + r) * blocks + k0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tok[g][i] = 0;
-            if (r >= t.rows) continue;
-            if (p.x_vec == 2) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.X_scale) + at));
-                tok[g][0] = v.x;
-                tok[g][1] = v.y;
-                tok[g][2] = v.z;
-                tok[g][3] = v.w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (4 * i < n) tok[g][i] = load_scale_word(p.X_scale, p.x_ue8m0, at + 4 * i, 1, n - 4 * i, p.x_vec, bad);
-            }
-        }
-    }
-};
-
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expert_gemm_kernel(const __grid_constant__ TokenMaps tmX, const __grid_constant__ CUtensorMap tmW, const Params p)
 {
@@ -255,7 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     // the groups: rows and token tiles of each (a group outside [0, R] holds none)
     __syncthreads();
-    {
+    if (threadIdx.x < kMaxE) {
         const int e = threadIdx.x;
         int64_t a = 0, b = 0;
         if (e < p.E) {
@@ -269,7 +239,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tail.count[e] = static_cast<int>(b - a);
         }
         int v = static_cast<int>((b - a + kTileN - 1) / kTileN);
-        // inclusive scan over the 256 threads
+        // a group's tiles are equal parts, whole in 16 (size <= kTileN, so that none is empty); inclusive
+        // scan of their number over the 256 threads
+        if (v > 0) tail.size[e] = (static_cast<int>((b - a + v - 1) / v) + 15) & ~15;
         int x = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -278,7 +250,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         int *part = reinterpret_cast<int *>(epi);
         if (lane == 31) part[warp] = x;
-        __syncthreads();
+        named_barrier_sync(1, kMaxE);
         for (int w = 0; w < warp; ++w) x += part[w];
         if (e < p.E) tail.first[e + 1] = x;
         if (e == 0) tail.first[0] = 0;
@@ -295,8 +267,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t keep = l2_policy_evict_normal();
         uint32_t s = 0, ph = 0, issued = 0;
         bool ok = true;
-        for (int tile = pair; tile < tiles && ok; tile += pairs) {
-            const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
+        for (Walk walk(pair, p.m_tiles); walk.tile < tiles && ok; walk.next(pairs, p.m_tiles)) {
+            const Tile t = walk.get(tail);
             const int half = ((t.rows + 15) & ~15) >> 1;        // tokens of each CTA
             int box = kBoxes - 1;
 #pragma unroll
@@ -337,7 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 1 && rank != 0) {
         uint32_t s = 0, ph = 0;
         bool ok = true;
-        for (int tile = pair; tile < tiles && ok; tile += pairs) {
+        for (Walk walk(pair, p.m_tiles); walk.tile < tiles && ok; walk.next(pairs, p.m_tiles)) {
             for (int kb = 0; kb < blocks; ++kb) {
                 ok = warp_wait(&tail.full[s], ph, abort_flag);
                 if (!ok) break;
@@ -358,8 +330,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t s = 0, ph = 0, q = 0, qph = 0;
         int j = 0;
         bool ok = true;
-        for (int tile = pair; tile < tiles; tile += pairs) {
-            const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
+        for (Walk walk(pair, p.m_tiles); walk.tile < tiles; walk.next(pairs, p.m_tiles)) {
+            const Tile t = walk.get(tail);
             const int b = j & 1;
             ok = warp_wait(&tail.acc_empty[b], ((j >> 1) & 1) ^ 1, abort_flag);
             if (!ok) break;
@@ -416,55 +388,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         volatile int no_abort = 0;
         mbar_wait_bounded(&tail.drain, 0, &no_abort);
-    } else if (warp == 2 || warp == 3) {
+    } else if (warp == 2 || warp == 3 || warp >= 8) {
         // Scale words: byte i of a row's word is the scale of 128-block 4 q + i.  Tokens: row r at
-        // lane r % 32, word r / 32 of a 128-row atom; features: one word for the whole 128.  Each warp
-        // holds one atom's words of up to 16 blocks, and has those of the next 16 (or of the next tile)
-        // in flight while it hands these out: a load's latency is spread over as many ring stages.
-        const int half = warp - 2;
-        uint32_t q = 0, qph = 0;
+        // lane r % 32, word r / 32 of a 128-row atom; features: one word for the whole 128.  Two warps,
+        // one for each atom, fill a slot with 16 blocks; two such teams take turns, so that a team has
+        // two tiles' time (16 blocks each) for the loads' latency and the hand-over.
+        const int team = warp >= 8, half = warp & 1;
+        const int m_blocks = (p.out + kBlk - 1) / kBlk;
+        uint32_t turn = 0, ph = 0;
         bool bad = false, ok = true;
-        ScaleWords cur, nxt;
-        int tile = pair, k0 = 0;
-        if (tile < tiles) cur.load(p, find_tile(tail, tile, p.m_tiles, p.E), k0, half, lane, rank, blocks, bad);
-        while (tile < tiles && ok) {
-            int tile2 = tile, k2 = k0 + 16;
-            if (k2 >= blocks) {
-                k2 = 0;
-                tile2 += pairs;
-            }
-            if (tile2 < tiles) nxt.load(p, find_tile(tail, tile2, p.m_tiles, p.E), k2, half, lane, rank, blocks, bad);
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.sf_empty[q], qph ^ 1u, abort_flag, 32));
-            uint4 *slot = reinterpret_cast<uint4 *>(sf_ring + q * kScaleSlotBytes);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (Walk walk(pair, p.m_tiles); walk.tile < tiles && ok; walk.next(pairs, p.m_tiles)) {
+            Tile t;
+            t.e = -1;
+            for (int k0 = 0; k0 < blocks && ok; k0 += 16, turn ^= 1u) {
+                if (turn != static_cast<uint32_t>(team)) continue;
+                if (t.e < 0) t = walk.get(tail);
+                const int n = blocks - k0;
+                uint32_t feat[4], tok[4][4];
                 if (half == 0) {
-                    uint32_t wa = 0;
+                    const int mb = t.m0 / kBlk + rank;
+                    const int64_t at = p.transpose ? (static_cast<int64_t>(t.e) * blocks + k0) * m_blocks + mb
+                                                   : (static_cast<int64_t>(t.e) * m_blocks + mb) * blocks + k0;
+                    const int step = p.transpose ? m_blocks : 1;
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) wa |= __shfl_sync(0xffffffffu, cur.feat, 4 * i + b) << (8 * b);
-                    slot[i * (kScaleQuadBytes / 16) + lane] = make_uint4(wa, wa, wa, wa);
+                    for (int i = 0; i < 4; ++i)
+                        feat[i] = mb < m_blocks && 4 * i < n
+                                      ? load_scale_word(p.W_scale, p.w_ue8m0, at + 4 * i * step, step, n - 4 * i, false, bad)
+                                      : 0u;
                 }
-                slot[i * (kScaleQuadBytes / 16) + 32 + half * 32 + lane] =
-                    make_uint4(cur.tok[0][i], cur.tok[1][i], cur.tok[2][i], cur.tok[3][i]);
+                const int64_t at0 = (t.row0 + half * 128 + lane) * blocks + k0;
+                if (p.x_vec == 2) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (half * 128 + g * 32 + lane < t.rows)
+                            v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.X_scale) + at0 +
+                                                                      static_cast<int64_t>(g) * 32 * blocks));
+                        tok[g][0] = v.x;
+                        tok[g][1] = v.y;
+                        tok[g][2] = v.z;
+                        tok[g][3] = v.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            tok[g][i] = half * 128 + g * 32 + lane < t.rows && 4 * i < n
+                                            ? load_scale_word(p.X_scale, p.x_ue8m0,
+                                                              at0 + static_cast<int64_t>(g) * 32 * blocks + 4 * i, 1,
+                                                              n - 4 * i, p.x_vec, bad)
+                                            : 0u;
+                }
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.sf_empty[team], ph ^ 1u, abort_flag, 32));
+                ph ^= 1u;
+                uint4 *slot = reinterpret_cast<uint4 *>(sf_ring + team * kScaleSlotBytes);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint4 *quad = slot + i * (kScaleQuadBytes / 16);
+                    if (half == 0) quad[lane] = make_uint4(feat[i], feat[i], feat[i], feat[i]);
+                    quad[32 + half * 32 + lane] = make_uint4(tok[0][i], tok[1][i], tok[2][i], tok[3][i]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_release_at(&tail.sf_full[team], 0);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_release_at(&tail.sf_full[q], 0);
-            q ^= 1u;
-            qph ^= q ^ 1u;
-            cur = nxt;
-            tile = tile2;
-            k0 = k2;
         }
         if (bad) tail.bad_scale = 1;
-    } else if (warp >= 4) {
+    } else {
         const int w = warp - 4;
         uint8_t *buf = epi + w * 32 * 64;
         const uint32_t buf_addr = smem_u32(buf);
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(w * 32) << 16);
         int j = 0;
-        for (int tile = pair; tile < tiles; tile += pairs) {
-            const Tile t = find_tile(tail, tile, p.m_tiles, p.E);
+        for (Walk walk(pair, p.m_tiles); walk.tile < tiles; walk.next(pairs, p.m_tiles)) {
+            const Tile t = walk.get(tail);
             const int b = j & 1;
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, abort_flag, 64))) break;
             tc_fence_after_sync();
