@@ -403,42 +403,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int k0 = 0; k0 < blocks && ok; k0 += 16, turn ^= 1u) {
                 if (turn != static_cast<uint32_t>(team)) continue;
                 if (t.e < 0) t = walk.get(tail);
+                // (blocks and rows that are not there read their neighbour's scale and are never used: the
+                // loads carry no condition and are all in flight together)
                 const int n = blocks - k0;
                 uint32_t feat[4], tok[4][4];
                 if (half == 0) {
-                    const int mb = t.m0 / kBlk + rank;
-                    const int64_t at = p.transpose ? (static_cast<int64_t>(t.e) * blocks + k0) * m_blocks + mb
-                                                   : (static_cast<int64_t>(t.e) * m_blocks + mb) * blocks + k0;
+                    const int mb = t.m0 / kBlk + rank < m_blocks ? t.m0 / kBlk + rank : m_blocks - 1;
                     const int step = p.transpose ? m_blocks : 1;
+                    const int64_t at = p.transpose ? static_cast<int64_t>(t.e) * blocks * m_blocks + mb
+                                                   : (static_cast<int64_t>(t.e) * m_blocks + mb) * blocks;
+                    uint32_t v[16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        feat[i] = mb < m_blocks && 4 * i < n
-                                      ? load_scale_word(p.W_scale, p.w_ue8m0, at + 4 * i * step, step, n - 4 * i, false, bad)
-                                      : 0u;
+                    for (int i = 0; i < 16; ++i)
+                        v[i] = load_scale_bits(p.W_scale, p.w_ue8m0, at + (k0 + (i < n ? i : n - 1)) * step);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = scale_bits_byte(v[i], p.w_ue8m0, bad);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) feat[i] = v[4 * i] | v[4 * i + 1] << 8 | v[4 * i + 2] << 16 | v[4 * i + 3] << 24;
                 }
-                const int64_t at0 = (t.row0 + half * 128 + lane) * blocks + k0;
+                int64_t at[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int r = half * 128 + g * 32 + lane;
+                    at[g] = (t.row0 + (r < t.rows ? r : t.rows - 1)) * blocks + k0;
+                }
                 if (p.x_vec == 2) {
+                    const uint8_t *xs = static_cast<const uint8_t *>(p.X_scale);
+                    uint4 v[4];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) v[g] = __ldg(reinterpret_cast<const uint4 *>(xs + at[g]));
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (half * 128 + g * 32 + lane < t.rows)
-                            v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.X_scale) + at0 +
-                                                                      static_cast<int64_t>(g) * 32 * blocks));
-                        tok[g][0] = v.x;
-                        tok[g][1] = v.y;
-                        tok[g][2] = v.z;
-                        tok[g][3] = v.w;
+                        tok[g][0] = v[g].x;
+                        tok[g][1] = v[g].y;
+                        tok[g][2] = v[g].z;
+                        tok[g][3] = v[g].w;
+                    }
+                } else if (p.x_vec == 1 && p.x_ue8m0) {
+                    const uint8_t *xs = static_cast<const uint8_t *>(p.X_scale);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            tok[g][i] = __ldg(reinterpret_cast<const uint32_t *>(xs + at[g] + (4 * i < n ? 4 * i : 0)));
+                } else if (p.x_vec == 1) {
+                    const float *xs = static_cast<const float *>(p.X_scale);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (4 * i >= n) break;
+                        uint4 v[4];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) v[g] = __ldg(reinterpret_cast<const uint4 *>(xs + at[g] + 4 * i));
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            tok[g][i] = scale_bits_byte(v[g].x, 0, bad) | scale_bits_byte(v[g].y, 0, bad) << 8 |
+                                        scale_bits_byte(v[g].z, 0, bad) << 16 | scale_bits_byte(v[g].w, 0, bad) << 24;
                     }
                 } else {
 #pragma unroll
-                    for (int g = 0; g < 4; ++g)
+                    for (int i = 0; i < 4; ++i) {
+                        if (4 * i >= n) break;
+                        uint32_t v[4][4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            tok[g][i] = half * 128 + g * 32 + lane < t.rows && 4 * i < n
-                                            ? load_scale_word(p.X_scale, p.x_ue8m0,
-                                                              at0 + static_cast<int64_t>(g) * 32 * blocks + 4 * i, 1,
-                                                              n - 4 * i, p.x_vec, bad)
-                                            : 0u;
+                        for (int g = 0; g < 4; ++g)
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                v[g][b] = load_scale_bits(p.X_scale, p.x_ue8m0, at[g] + (4 * i + b < n ? 4 * i + b : n - 1));
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            tok[g][i] = 0;
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) tok[g][i] |= scale_bits_byte(v[g][b], p.x_ue8m0, bad) << (8 * b);
+                        }
+                    }
                 }
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.sf_empty[team], ph ^ 1u, abort_flag, 32));
                 ph ^= 1u;

@@ -51,38 +51,21 @@ __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t q)
     return f;
 }
 
-// Reads scale `at` of an array in either format as its byte.  `bad` is raised
-// where a float is not a positive normal power of two.
-__device__ __forceinline__ uint32_t load_scale_byte(const void *p, int ue8m0, int64_t at, bool &bad)
+// Scale `at` of an array in either format, as stored; and its byte.  `bad` is raised where a float is
+// not a positive normal power of two.
+__device__ __forceinline__ uint32_t load_scale_bits(const void *p, int ue8m0, int64_t at)
 {
-    if (ue8m0) return __ldg(static_cast<const uint8_t *>(p) + at);
-    const uint32_t w = __float_as_uint(__ldg(static_cast<const float *>(p) + at));
+    return ue8m0 ? __ldg(static_cast<const uint8_t *>(p) + at) : __ldg(static_cast<const uint32_t *>(p) + at);
+}
+__device__ __forceinline__ uint32_t scale_bits_byte(uint32_t w, int ue8m0, bool &bad)
+{
+    if (ue8m0) return w;
     bad |= (w & 0x807FFFFFu) != 0 || w == 0;
     return (w >> 23) & 0xFFu;
 }
-
-// Four scales `step` apart from `at` on as one word of bytes, those from `n` on zero.  `vec`: n is 4,
-// the step 1 and the address whole in four elements.
-__device__ __forceinline__ uint32_t load_scale_word(const void *p, int ue8m0, int64_t at, int64_t step, int n, bool vec,
-                                                    bool &bad)
+__device__ __forceinline__ uint32_t load_scale_byte(const void *p, int ue8m0, int64_t at, bool &bad)
 {
-    if (vec) {
-        if (ue8m0) return __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(p) + at));
-        const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at));
-        const uint32_t w[4] = {__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z), __float_as_uint(f.w)};
-        uint32_t v = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            bad |= (w[i] & 0x807FFFFFu) != 0 || w[i] == 0;
-            v |= ((w[i] >> 23) & 0xFFu) << (8 * i);
-        }
-        return v;
-    }
-    uint32_t v = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < n) v |= load_scale_byte(p, ue8m0, at + i * step, bad) << (8 * i);
-    return v;
+    return scale_bits_byte(load_scale_bits(p, ue8m0, at), ue8m0, bad);
 }
 
 __device__ __forceinline__ void store_scale(void *p, int ue8m0, int64_t at, uint32_t byte)
