@@ -8,29 +8,34 @@
 // bf16 one with fp32 accumulation.  The E4M3 rows are read as they are (half the
 // bytes of bf16) and become bf16 on their way through shared memory.
 //
-// Both operands have the reduction on their slow axis (MN-major).  Persistent
-// CTAs; a tile is 128 weight rows x 256 weight columns of one expert, a ring
-// stage 64 rows of the group.  Warp roles:
-//   warp 0       TMA producer (dY 64 x 128 bf16, x 64 x 256 E4M3)
-//   warp 1       MMA issuer (one thread)
-//   warp 3       allocates TMEM
-//   warps 4..7   epilogue
-//   warps 8..15  converters E4M3 -> bf16; in a group's last stage they also clear
-//                the rows behind its end (the next group's, or none)
+// Both operands have the reduction on their slow axis (MN-major).  Persistent CTA
+// pairs (cta_group::2); a tile is 256 weight rows x 256 weight columns of one expert,
+// a ring stage 64 rows of the group.  Each CTA holds the accumulators of 128 of the
+// weight rows, and brings those columns of dY and half of the columns of x: it
+// converts 128 columns, one scale for each row, in the time of a 256 x 256 x 64 MMA.
+// Warp roles, in each CTA:
+//   warp 0        TMA producer (dY 64 x 128 bf16, x 64 x 128 E4M3)
+//   warp 1        MMA issuer (one thread of the leader)
+//   warp 3        allocates TMEM
+//   warps 4..11   epilogue, two warps to a quarter of the TMEM lanes
+//   warps 12..19  two teams of converters E4M3 -> bf16, which take the stages in turn;
+//                 in a group's last stage they also clear the rows behind its end
+//                 (the next group's, or none)
 #include "expert_internal.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTileM = 128, kTileN = 256, kRows = 64, kStages = 3;
-constexpr int kABytes = kRows * kTileM * 2;       // two boxes of 64 columns
-constexpr int kRawBytes = kRows * kTileN;         // two boxes of 128 columns
-constexpr int kBBytes = kRows * kTileN * 2;       // four boxes of 64 columns
-constexpr int kBox = kRows * 128;                 // bytes of a box
+constexpr int kTileM = 256, kTileN = 256, kRows = 64, kStages = 5;
+constexpr int kHalf = 128;                        // weight rows, and columns of x, of each CTA
+constexpr int kBox = kRows * 128;                 // bytes of a box: 64 rows of 128 bytes
+constexpr int kABytes = 2 * kBox;                 // two boxes of 64 columns
+constexpr int kRawBytes = kBox;                   // 128 columns
+constexpr int kBBytes = 2 * kBox;                 // two boxes of 64 columns
 constexpr int kStageBytes = kABytes + kRawBytes + kBBytes;
-constexpr int kEpiBytes = 4 * 32 * 128;
-constexpr int kThreads = 512;
-constexpr int kConvWarps = 8;
+constexpr int kEpiWarps = 8, kTeams = 2, kTeamWarps = 4;
+constexpr int kEpiBytes = kEpiWarps * 32 * 64;    // 32 rows x 16 fp32 each
+constexpr int kThreads = 32 * (4 + kEpiWarps + kTeams * kTeamWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxE = 256;
 
@@ -54,6 +59,34 @@ struct Params {
     int m_tiles, n_tiles;
     int32_t *status;
 };
+
+// Tile `tile` of the walk: expert-major, the columns of a row of tiles next to each other.
+struct Tile {
+    int e, m0, n0, count;
+    int64_t begin;
+};
+__device__ __forceinline__ Tile get_tile(const Tail &t, const Params &p, int tile)
+{
+    const int per = p.m_tiles * p.n_tiles;
+    Tile r;
+    r.e = tile / per;
+    const int i = tile - r.e * per, m = i / p.n_tiles;
+    r.m0 = m * kTileM;
+    r.n0 = (i - m * p.n_tiles) * kTileN;
+    r.count = t.count[r.e];
+    r.begin = t.begin[r.e];
+    return r;
+}
+
+__device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 
 // Two bf16 products per call; exact here (the factors are powers of two).
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
@@ -84,7 +117,33 @@ __device__ __forceinline__ uint32_t set_nan(uint32_t v, uint32_t w, int i)
     return v;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+// A chunk of 16 codes of a row -> 32 bytes of a 128-byte-swizzled row of 64 bf16 (`row8`: the row's place in
+// its group of eight).  Chunk c holds the 16-byte pieces 2 (c % 4) and the next; half of the lanes store the
+// second one first, so that a row's eight stores meet different banks.
+__device__ __forceinline__ void convert_chunk(const uint4 &w, uint32_t byte, uint8_t *dst, int row8, int c)
+{
+    // 2^120 * s as a bf16; beyond its range the rest goes into a second factor
+    const uint32_t ex = 120u + byte;
+    const uint32_t f = (ex < 254u ? ex : 254u) * 0x00800080u;
+    uint2 v[4] = {codes_to_bf16(w.x, f), codes_to_bf16(w.y, f), codes_to_bf16(w.z, f), codes_to_bf16(w.w, f)};
+    if (ex > 254u) {
+        const uint32_t f2 = (127u + ex - 254u) * 0x00800080u;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) v[y] = make_uint2(mul_bf16x2(v[y].x, f2), mul_bf16x2(v[y].y, f2));
+    }
+    if (nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w)) {
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) v[y] = make_uint2(set_nan(v[y].x, ww[y], 0), set_nan(v[y].y, ww[y], 2));
+    }
+    const int piece = (c & 3) * 2, first = c >> 2;
+    const uint4 lo = make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
+    const uint4 hi = make_uint4(v[2].x, v[2].y, v[3].x, v[3].y);
+    *reinterpret_cast<uint4 *>(dst + (((piece + first) ^ row8) << 4)) = first ? hi : lo;
+    *reinterpret_cast<uint4 *>(dst + (((piece + 1 - first) ^ row8) << 4)) = first ? lo : hi;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expert_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX, const Params p)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -92,17 +151,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *epi = ring + kStages * kStageBytes;
     Tail &tail = *reinterpret_cast<Tail *>(epi + kEpiBytes);
     volatile int *abort_flag = &tail.abort;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&tail.full[s], 1);
-            mbar_init(&tail.conv[s], kConvWarps);
+            mbar_init(&tail.conv[s], 2 * kTeamWarps);   // the leader's: both CTAs' converters
             mbar_init(&tail.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tail.acc_full[b], 1);
-            mbar_init(&tail.acc_empty[b], 4);
+            mbar_init(&tail.acc_empty[b], 2 * kEpiWarps);
         }
         mbar_init(&tail.drain, 1);
         tail.abort = tail.bad_index = tail.bad_scale = 0;
@@ -110,10 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmY);
         tma_prefetch_desc(&tmX);
     }
-    if (warp == 3) {
-        tmem_alloc(&tail.tmem_base, kTmemCols);
-        tmem_relinquish();
-    }
+    if (warp == 3) tmem_alloc_pair(&tail.tmem_base, kTmemCols);
     __syncthreads();
     if (static_cast<int>(threadIdx.x) < p.E) {
         const int e = threadIdx.x;
@@ -126,203 +184,202 @@ __global__ void __launch_bounds__(kThreads, 1)
         tail.count[e] = static_cast<int>(b - a);
     }
     tc_fence_before_sync();
-    __syncthreads();
+    cluster_sync();               // both CTAs' barriers stand, both hold TMEM
     tc_fence_after_sync();
     const uint32_t tmem = tail.tmem_base;
-    const int per = p.m_tiles * p.n_tiles;
-    const int tiles = p.E * per;
+    const int tiles = p.E * p.m_tiles * p.n_tiles;
 
     if (warp == 0) {
-        if (lane == 0) {
-            const uint64_t keep = l2_policy_evict_normal();
-            uint32_t s = 0, ph = 0, issued = 0;
-            for (int tile = blockIdx.x; tile < tiles && !*abort_flag; tile += gridDim.x) {
-                const int e = tile / per, i = tile - e * per, m0 = (i / p.n_tiles) * kTileM, n0 = (i % p.n_tiles) * kTileN;
-                const int count = tail.count[e], begin = tail.begin[e];
-                const int boxes = p.cols - n0 > 128 ? 2 : 1;
-                for (int r = 0; r < count; r += kRows) {
-                    if (!mbar_wait_bounded(&tail.empty[s], ph ^ 1u, abort_flag)) break;
-                    uint8_t *a = ring + s * kStageBytes, *raw = a + kABytes;
-                    mbar_arrive_expect_tx(&tail.full[s], kABytes + boxes * kBox);
-                    tma_load_2d(a, &tmY, &tail.full[s], m0, begin + r, keep);
-                    tma_load_2d(a + kBox, &tmY, &tail.full[s], m0 + 64, begin + r, keep);
-                    tma_load_2d(raw, &tmX, &tail.full[s], n0, begin + r, keep);
-                    if (boxes > 1) tma_load_2d(raw + kBox, &tmX, &tail.full[s], n0 + 128, begin + r, keep);
-                    ++issued;
-                    if (++s == kStages) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+        const uint64_t keep = l2_policy_evict_normal();
+        uint32_t s = 0, ph = 0, issued = 0;
+        bool ok = true;
+        for (int tile = pair; tile < tiles && ok; tile += pairs) {
+            const Tile t = get_tile(tail, p, tile);
+            const int m = t.m0 + rank * kHalf, n = t.n0 + rank * kHalf;
+            for (int r = 0; r < t.count; r += kRows) {
+                ok = warp_wait(&tail.empty[s], ph ^ 1u, abort_flag);
+                if (!ok) break;
+                uint8_t *a = ring + s * kStageBytes;
+                const int row = static_cast<int>(t.begin) + r;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&tail.full[s], kABytes + kRawBytes);
+                    tma_load_2d(a + kABytes, &tmX, &tail.full[s], n, row, keep);
+                    tma_load_2d(a, &tmY, &tail.full[s], m, row, keep);
+                    tma_load_2d(a + kBox, &tmY, &tail.full[s], m + 64, row, keep);
                 }
-            }
-            if (*abort_flag) {
-                const uint32_t from = issued > kStages ? issued - kStages : 0u;
-                for (uint32_t x = from; x < issued; ++x) {
-                    volatile int no_abort = 0;
-                    mbar_wait_bounded(&tail.full[x % kStages], (x / kStages) & 1u, &no_abort);
+                __syncwarp();
+                ++issued;
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            const uint64_t a0 = make_smem_desc_sw128(smem_u32(ring), kBox, 1024);
-            const uint64_t b0 = make_smem_desc_sw128(smem_u32(ring + kABytes + kRawBytes), kBox, 1024);
-            uint32_t s = 0, ph = 0;
-            int j = 0;
-            bool stop = false;
-            for (int tile = blockIdx.x; tile < tiles && !stop; tile += gridDim.x) {
-                const int e = tile / per, i = tile - e * per, n0 = (i % p.n_tiles) * kTileN;
-                const int count = tail.count[e];
-                if (count == 0) continue;
-                const uint32_t idesc = make_idesc_bf16_f32(kTileM, p.cols - n0 > 128 ? 256 : 128, 1, 1);
-                const int b = j & 1;
-                if (!mbar_wait_bounded(&tail.acc_empty[b], ((j >> 1) & 1) ^ 1, abort_flag)) break;
+        if (!ok) {
+            // let the copies already issued land before the CTA ends
+            const uint32_t from = issued > kStages ? issued - kStages : 0u;
+            for (uint32_t x = from; x < issued; ++x) {
+                volatile int no_abort = 0;
+                mbar_wait_bounded(&tail.full[x % kStages], (x / kStages) & 1u, &no_abort);
+            }
+        }
+    } else if (warp == 1 && rank == 0) {
+        const uint64_t a0 = make_smem_desc_sw128(smem_u32(ring), kBox, 1024);
+        const uint64_t b0 = make_smem_desc_sw128(smem_u32(ring + kABytes + kRawBytes), kBox, 1024);
+        const uint32_t idesc = make_idesc_bf16_f32(kTileM, kTileN, 1, 1);
+        uint32_t s = 0, ph = 0;
+        int j = 0;
+        bool ok = true;
+        for (int tile = pair; tile < tiles; tile += pairs) {
+            const int count = get_tile(tail, p, tile).count;
+            if (count == 0) continue;
+            const int b = j & 1;
+            ok = warp_wait(&tail.acc_empty[b], ((j >> 1) & 1) ^ 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t d = tmem + b * kTileN;
+            for (int r = 0; r < count; r += kRows) {
+                ok = warp_wait_cluster(&tail.conv[s], ph, abort_flag);
+                if (!ok) break;
                 tc_fence_after_sync();
-                const uint32_t d = tmem + b * kTileN;
-                for (int r = 0; r < count; r += kRows) {
-                    if (!mbar_wait_bounded(&tail.conv[s], ph, abort_flag)) {
-                        stop = true;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    const uint64_t at = (s * kStageBytes) >> 4;
+                const uint64_t at = (s * kStageBytes) >> 4;
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kRows / 16; ++k)
-                        tc_mma_f16(d, a0 + at + k * 128, b0 + at + k * 128, idesc, (r | k) != 0);
-                    tc_commit(&tail.empty[s]);
-                    if (++s == kStages) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                        mma_f16_pair(d, a0 + at + k * 128, b0 + at + k * 128, idesc, (r | k) != 0);
+                    tc_commit_pair(&tail.empty[s]);
                 }
-                if (stop) break;
-                tc_commit(&tail.acc_full[b]);
-                ++j;
-            }
-            tc_commit(&tail.drain);
-            volatile int no_abort = 0;
-            mbar_wait_bounded(&tail.drain, 0, &no_abort);
-        }
-    } else if (warp >= 8) {
-        const int t = threadIdx.x - 256, c = t & 7, r0 = t >> 3;   // 16-byte chunk of a row, first row
-        const int kblocks = p.cols >> 7;
-        uint32_t s = 0, ph = 0;
-        bool bad = false;
-        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            const int e = tile / per, i = tile - e * per, n0 = (i % p.n_tiles) * kTileN;
-            const int count = tail.count[e];
-            const int64_t begin = tail.begin[e];
-            const int boxes = p.cols - n0 > 128 ? 2 : 1;
-            bool ok = true;
-            for (int r = 0; r < count; r += kRows) {
-                const int valid = count - r;
-                uint32_t sb[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int row = r0 + 32 * (x & 1), kb = x >> 1;
-                    sb[x] = 127;
-                    if (row < valid && kb < boxes)
-                        sb[x] = load_scale_byte(p.X_scale, p.x_ue8m0, (begin + r + row) * kblocks + (n0 >> 7) + kb, bad);
-                }
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.full[s], ph, abort_flag, 32));
-                if (!ok) break;
-                uint8_t *a = ring + s * kStageBytes, *raw = a + kABytes, *b = raw + kRawBytes;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int row = r0 + 32 * (x & 1), kb = x >> 1;
-                    if (kb >= boxes) continue;
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (row < valid) w = *reinterpret_cast<const uint4 *>(raw + kb * kBox + row * 128 + ((c ^ (row & 7)) << 4));
-                    // 2^120 * s as a bf16; beyond its range the rest goes into a second factor
-                    const uint32_t ex = 120u + sb[x];
-                    const uint32_t f = (ex < 254u ? ex : 254u) * 0x00800080u;
-                    uint2 v[4] = {codes_to_bf16(w.x, f), codes_to_bf16(w.y, f), codes_to_bf16(w.z, f),
-                                  codes_to_bf16(w.w, f)};
-                    if (ex > 254u) {
-                        const uint32_t f2 = (127u + ex - 254u) * 0x00800080u;
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) v[y] = make_uint2(mul_bf16x2(v[y].x, f2), mul_bf16x2(v[y].y, f2));
-                    }
-                    if (nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w)) {
-                        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            v[y] = make_uint2(set_nan(v[y].x, ww[y], 0), set_nan(v[y].y, ww[y], 2));
-                    }
-                    // chunk c is bf16 columns 16 c .. 16 c + 15: two 16-byte chunks of box c / 4.  Half of
-                    // the lanes store the second one first, so that a row's eight stores meet eight banks
-                    uint8_t *dst = b + (kb * 2 + (c >> 2)) * kBox + row * 128;
-                    const int ch = (c & 3) * 2, first = c >> 2;
-                    const uint4 lo = make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
-                    const uint4 hi = make_uint4(v[2].x, v[2].y, v[3].x, v[3].y);
-                    *reinterpret_cast<uint4 *>(dst + (((ch + first) ^ (row & 7)) << 4)) = first ? hi : lo;
-                    *reinterpret_cast<uint4 *>(dst + (((ch + 1 - first) ^ (row & 7)) << 4)) = first ? lo : hi;
-                }
-                if (valid < kRows) {
-                    // rows behind the group's end: whatever dY holds there must not meet the zeros of x
-                    for (int x = t; x < (kRows - valid) * 16; x += kConvWarps * 32)
-                        *reinterpret_cast<uint4 *>(a + (x & 8 ? kBox : 0) + (valid + (x >> 4)) * 128 + ((x & 7) << 4)) =
-                            make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&tail.conv[s]);
                 if (++s == kStages) {
                     s = 0;
                     ph ^= 1u;
                 }
             }
             if (!ok) break;
+            if (elect_one()) tc_commit_pair(&tail.acc_full[b]);
+            __syncwarp();
+            ++j;
+        }
+        if (elect_one()) tc_commit_pair(&tail.drain);
+        __syncwarp();
+        volatile int no_abort = 0;
+        mbar_wait_bounded(&tail.drain, 0, &no_abort);
+    } else if (warp >= 4 + kEpiWarps) {
+        const int team = (warp - 4 - kEpiWarps) / kTeamWarps;
+        const int t = threadIdx.x - 32 * (4 + kEpiWarps + team * kTeamWarps);
+        const int c = t & 7, r0 = t >> 3;                       // 16-byte chunk of a row, first row of four
+        const int kblocks = p.cols >> 7;
+        uint32_t s = 0, ph = 0, turn = 0;
+        bool bad = false, ok = true;
+        for (int tile = pair; tile < tiles && ok; tile += pairs) {
+            const Tile w = get_tile(tail, p, tile);
+            const int kb = (w.n0 >> 7) + rank;
+            // (columns behind the edge: any scale will do for their zeros)
+            const int64_t col = kb < kblocks ? kb : kblocks - 1;
+            for (int r = 0; r < w.count && ok; r += kRows, turn ^= 1u) {
+                if (turn == static_cast<uint32_t>(team)) {
+                    const int valid = w.count - r;
+                    uint32_t sb[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int row = r0 + 16 * x < valid ? r0 + 16 * x : valid - 1;
+                        sb[x] = load_scale_bits(p.X_scale, p.x_ue8m0, (w.begin + r + row) * kblocks + col);
+                    }
+                    ok = warp_wait(&tail.full[s], ph, abort_flag);
+                    if (!ok) break;
+                    uint8_t *a = ring + s * kStageBytes, *raw = a + kABytes, *b = raw + kRawBytes;
+                    uint4 v[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int row = r0 + 16 * x;
+                        v[x] = *reinterpret_cast<const uint4 *>(raw + row * 128 + ((c ^ (row & 7)) << 4));
+                        if (row >= valid) v[x] = make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int row = r0 + 16 * x;
+                        convert_chunk(v[x], scale_bits_byte(sb[x], p.x_ue8m0, bad), b + (c >> 2) * kBox + row * 128, row & 7,
+                                      c);
+                    }
+                    if (valid < kRows) {
+                        // rows behind the group's end: whatever dY holds there must not meet the zeros of x
+                        for (int x = t; x < (kRows - valid) * 16; x += kTeamWarps * 32)
+                            *reinterpret_cast<uint4 *>(a + (x & 8 ? kBox : 0) + (valid + (x >> 4)) * 128 +
+                                                       ((x & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_release_at(&tail.conv[s], 0);
+                }
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
         }
         if (bad) tail.bad_scale = 1;
     } else if (warp >= 4) {
-        const int w = warp - 4;
-        uint8_t *buf = epi + w * 32 * 128;
-        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(w * 32) << 16);
+        const int w = warp - 4, quarter = w & 3, side = w >> 2;   // TMEM lanes, columns 128 side on
+        uint8_t *buf = epi + w * 32 * 64;
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + side * 128;
+        // of a chunk of 32 rows x 16 columns: this lane's 16 bytes of rows lane / 4 + 8 i
+        const int lrow = lane >> 2, lch = lane & 3;
         int j = 0;
-        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            const int e = tile / per, i = tile - e * per, m0 = (i / p.n_tiles) * kTileM, n0 = (i % p.n_tiles) * kTileN;
-            const bool some = tail.count[e] != 0;
+        for (int tile = pair; tile < tiles; tile += pairs) {
+            const Tile t = get_tile(tail, p, tile);
+            const bool some = t.count != 0;
+            const int m = t.m0 + rank * kHalf + quarter * 32, n = t.n0 + side * 128;
+            const bool inside = n < p.cols;                       // (columns come in whole 128)
+            const int64_t base = (static_cast<int64_t>(t.e) * p.rows + m + lrow) * p.cols + n + lch * 4;
+            const int64_t step = 8ll * p.cols;
+            float4 z[2][4];
+            auto fetch = [&](int c, float4 (&y)[4]) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    y[i] = p.add && inside && m + lrow + 8 * i < p.rows
+                               ? __ldcs(reinterpret_cast<const float4 *>(p.add + base + i * step + c))
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+            };
+            // what is added is on its way while the accumulators are waited for
+            fetch(0, z[0]);
             const int b = j & 1;
             if (some) {
                 if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, abort_flag, 64))) break;
                 tc_fence_after_sync();
                 ++j;
             }
-            const int width = p.cols - n0 > 128 ? 256 : 128;
-            const int64_t base = (static_cast<int64_t>(e) * p.rows + m0 + w * 32) * p.cols + n0;
-            for (int c = 0; c < width; c += 32) {
-                float v[32];
+#pragma unroll 2
+            for (int c = 0; c < kHalf; c += 16) {
+                if (c + 16 < kHalf) fetch(c + 16, z[((c >> 4) & 1) ^ 1]);
+                float v[16];
                 if (some) {
-                    tmem_ld_32x32b_x32(lane_addr + b * kTileN + c, v);
+                    tmem_ld_32x32b_x16(lane_addr + b * kTileN + c, v);
                     tmem_ld_wait();
                 } else {
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) v[x] = 0.f;
+                    for (int x = 0; x < 16; ++x) v[x] = 0.f;
                 }
-                // a row of 32 fp32 is eight 16-byte chunks, chunk x of row l at place x ^ (l & 7)
+                // a row's four 16-byte chunks: chunk x of row l at place x ^ (l / 2 % 4)
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    *reinterpret_cast<float4 *>(buf + lane * 128 + ((x ^ (lane & 7)) << 4)) =
+                for (int x = 0; x < 4; ++x)
+                    *reinterpret_cast<float4 *>(buf + lane * 64 + ((x ^ ((lane >> 1) & 3)) << 4)) =
                         make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
                 __syncwarp();
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    const int row = x * 4 + (lane >> 3), ch = lane & 7;
-                    float4 y = *reinterpret_cast<const float4 *>(buf + row * 128 + ((ch ^ (row & 7)) << 4));
-                    if (m0 + w * 32 + row < p.rows) {
-                        const int64_t at = base + static_cast<int64_t>(row) * p.cols + c + ch * 4;
-                        if (p.add) {
-                            const float4 z = __ldcs(reinterpret_cast<const float4 *>(p.add + at));
-                            y.x += z.x;
-                            y.y += z.y;
-                            y.z += z.z;
-                            y.w += z.w;
-                        }
+                for (int i = 0; i < 4; ++i) {
+                    const int row = lrow + 8 * i;
+                    float4 y = *reinterpret_cast<const float4 *>(buf + row * 64 + ((lch ^ ((row >> 1) & 3)) << 4));
+                    const float4 q = z[(c >> 4) & 1][i];
+                    y.x += q.x;
+                    y.y += q.y;
+                    y.z += q.z;
+                    y.w += q.w;
+                    if (inside && m + row < p.rows) {
+                        const int64_t at = base + i * step + c;
                         if (p.bf16_out) {
                             __nv_bfloat162 h[2] = {__floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
-                            __stcs(reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.dW) + at),
-                                   *reinterpret_cast<uint2 *>(h));
+                            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.dW) + at) =
+                                *reinterpret_cast<uint2 *>(h);
                         } else {
                             __stcs(reinterpret_cast<float4 *>(static_cast<float *>(p.dW) + at), y);
                         }
@@ -332,15 +389,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (some) {
                 tc_fence_before_sync();
-                if (lane == 0) mbar_arrive(&tail.acc_empty[b]);
+                if (lane == 0) mbar_arrive_at(&tail.acc_empty[b], 0);
             }
         }
     }
 
     tc_fence_before_sync();
-    __syncthreads();
+    cluster_sync();               // the leader's MMAs have read the other CTA's memory
     tc_fence_after_sync();
-    if (warp == 3) tmem_dealloc(tmem, kTmemCols);
+    if (warp == 3) tmem_dealloc_pair(tmem, kTmemCols);
     if (threadIdx.x == 0) {
         if (tail.abort) report_status(p.status, MOE_ERR_TIMEOUT);
         if (tail.bad_index) report_status(p.status, MOE_ERR_BAD_INDEX);
@@ -388,8 +445,8 @@ cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream)
     p.n_tiles = (a.cols + kTileN - 1) / kTileN;
     p.status = a.status;
     const int64_t tiles = static_cast<int64_t>(a.E) * p.m_tiles * p.n_tiles;
-    const int sms = device_sm_count(dev);
-    expert_wgrad_kernel<<<static_cast<int>(tiles < sms ? tiles : sms), kThreads, kSmemBytes, stream>>>(tmY, tmX, p);
+    const int pairs = device_sm_count(dev) / 2;
+    expert_wgrad_kernel<<<2 * static_cast<int>(tiles < pairs ? tiles : pairs), kThreads, kSmemBytes, stream>>>(tmY, tmX, p);
     return cudaGetLastError();
 }
 
