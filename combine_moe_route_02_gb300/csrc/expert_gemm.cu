@@ -340,7 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t idesc0 = make_idesc((t.rows + 15) & ~15, p.transpose, 0);
             for (int k0 = 0; k0 < blocks && ok; k0 += 4) {
                 if ((k0 & 15) == 0) {
-                    ok = warp_wait_cluster(&tail.sf_full[q], qph, abort_flag);
+                    ok = warp_wait(&tail.sf_full[q], qph, abort_flag);
                     if (!ok) break;
                     tc_fence_after_sync();
                 }
@@ -486,9 +486,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (half == 0) quad[lane] = make_uint4(feat[i], feat[i], feat[i], feat[i]);
                     quad[32 + half * 32 + lane] = make_uint4(tok[0][i], tok[1][i], tok[2][i], tok[3][i]);
                 }
+                // (each CTA's copy to TMEM reads these bytes from its own shared memory: once they are ordered
+                // before the async proxy, the arrival at the leader has no other memory to order)
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_release_at(&tail.sf_full[team], 0);
+                if (lane == 0) mbar_arrive_at(&tail.sf_full[team], 0);
             }
         }
         if (bad) tail.bad_scale = 1;

@@ -18,7 +18,7 @@
 //   warp 1        MMA issuer (one thread of the leader)
 //   warp 3        allocates TMEM
 //   warps 4..11   epilogue, two warps to a quarter of the TMEM lanes
-//   warps 12..19  two teams of converters E4M3 -> bf16, which take the stages in turn;
+//   warps 12..23  three teams of converters E4M3 -> bf16, which take the stages in turn;
 //                 in a group's last stage they also clear the rows behind its end
 //                 (the next group's, or none)
 #include "expert_internal.cuh"
@@ -33,7 +33,7 @@ constexpr int kABytes = 2 * kBox;                 // two boxes of 64 columns
 constexpr int kRawBytes = kBox;                   // 128 columns
 constexpr int kBBytes = 2 * kBox;                 // two boxes of 64 columns
 constexpr int kStageBytes = kABytes + kRawBytes + kBBytes;
-constexpr int kEpiWarps = 8, kTeams = 2, kTeamWarps = 4;
+constexpr int kEpiWarps = 8, kTeams = 3, kTeamWarps = 4;
 constexpr int kEpiBytes = kEpiWarps * 32 * 64;    // 32 rows x 16 fp32 each
 constexpr int kThreads = 32 * (4 + kEpiWarps + kTeams * kTeamWarps);
 constexpr uint32_t kTmemCols = 512;
@@ -78,6 +78,30 @@ __device__ __forceinline__ Tile get_tile(const Tail &t, const Params &p, int til
     return r;
 }
 
+// The ring stages of a CTA pair's walk, one after the other; groups without rows have none.
+struct Stages {
+    int tile, r;
+    Tile w;
+
+    __device__ __forceinline__ Stages(const Tail &t, const Params &p, int pair, int pairs, int tiles) : tile(pair), r(0)
+    {
+        if (tile < tiles) w = get_tile(t, p, tile);
+        while (tile < tiles && w.count == 0) {
+            tile += pairs;
+            if (tile < tiles) w = get_tile(t, p, tile);
+        }
+    }
+    __device__ __forceinline__ void next(const Tail &t, const Params &p, int pairs, int tiles)
+    {
+        r += kRows;
+        while (tile < tiles && r >= w.count) {
+            r = 0;
+            tile += pairs;
+            if (tile < tiles) w = get_tile(t, p, tile);
+        }
+    }
+};
+
 __device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
@@ -96,9 +120,9 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
     return d;
 }
 
-// Four E4M3 codes -> four bf16, times f (and f2 where it is not 1).  A code's bits
-// s eeee mmm, moved to s 0000 eeee mmm 0000, are the bf16 number code * 2^-120
-// (its subnormals included), so that 2^120 goes into f.
+// Four E4M3 codes -> four bf16, times f.  A code's bits s eeee mmm, moved to
+// s 0000 eeee mmm 0000, are the bf16 number code * 2^-120 (its subnormals included),
+// so that 2^120 goes into f.
 __device__ __forceinline__ uint2 codes_to_bf16(uint32_t w, uint32_t f)
 {
     uint32_t lo, hi;   // each code in the low byte of a half, its sign spread over the high byte
@@ -108,7 +132,7 @@ __device__ __forceinline__ uint2 codes_to_bf16(uint32_t w, uint32_t f)
 }
 
 // Whether one of four codes is a NaN (s 1111 111).
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }
 
 __device__ __forceinline__ uint32_t set_nan(uint32_t v, uint32_t w, int i)
 {
@@ -117,30 +141,25 @@ __device__ __forceinline__ uint32_t set_nan(uint32_t v, uint32_t w, int i)
     return v;
 }
 
-// A chunk of 16 codes of a row -> 32 bytes of a 128-byte-swizzled row of 64 bf16 (`row8`: the row's place in
-// its group of eight).  Chunk c holds the 16-byte pieces 2 (c % 4) and the next; half of the lanes store the
-// second one first, so that a row's eight stores meet different banks.
-__device__ __forceinline__ void convert_chunk(const uint4 &w, uint32_t byte, uint8_t *dst, int row8, int c)
+// Eight codes of one row -> 16 bytes, times f = 2^120 * s; NaN codes raise bits of `nan` (0x80808080).
+__device__ __forceinline__ uint4 convert_codes(const uint2 &w, uint32_t f, uint32_t &nan)
 {
-    // 2^120 * s as a bf16; beyond its range the rest goes into a second factor
-    const uint32_t ex = 120u + byte;
-    const uint32_t f = (ex < 254u ? ex : 254u) * 0x00800080u;
-    uint2 v[4] = {codes_to_bf16(w.x, f), codes_to_bf16(w.y, f), codes_to_bf16(w.z, f), codes_to_bf16(w.w, f)};
-    if (ex > 254u) {
-        const uint32_t f2 = (127u + ex - 254u) * 0x00800080u;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) v[y] = make_uint2(mul_bf16x2(v[y].x, f2), mul_bf16x2(v[y].y, f2));
-    }
-    if (nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w)) {
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int y = 0; y < 4; ++y) v[y] = make_uint2(set_nan(v[y].x, ww[y], 0), set_nan(v[y].y, ww[y], 2));
-    }
-    const int piece = (c & 3) * 2, first = c >> 2;
-    const uint4 lo = make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
-    const uint4 hi = make_uint4(v[2].x, v[2].y, v[3].x, v[3].y);
-    *reinterpret_cast<uint4 *>(dst + (((piece + first) ^ row8) << 4)) = first ? hi : lo;
-    *reinterpret_cast<uint4 *>(dst + (((piece + 1 - first) ^ row8) << 4)) = first ? lo : hi;
+    const uint2 a = codes_to_bf16(w.x, f), b = codes_to_bf16(w.y, f);
+    nan |= nan_codes(w.x) | nan_codes(w.y);
+    return make_uint4(a.x, a.y, b.x, b.y);
+}
+
+// The same with NaN codes, and where 2^120 * s (s = 2^(byte - 127)) is beyond bf16's range.
+__device__ __forceinline__ uint4 convert_codes_rare(const uint2 &w, uint32_t byte)
+{
+    const uint32_t ex = 120u + byte, ex1 = ex < 254u ? ex : 254u;
+    const uint32_t f = ex1 * 0x00800080u, f2 = (127u + ex - ex1) * 0x00800080u;
+    uint2 a = codes_to_bf16(w.x, f), b = codes_to_bf16(w.y, f);
+    a = make_uint2(mul_bf16x2(a.x, f2), mul_bf16x2(a.y, f2));
+    b = make_uint2(mul_bf16x2(b.x, f2), mul_bf16x2(b.y, f2));
+    a = make_uint2(set_nan(a.x, w.x, 0), set_nan(a.y, w.x, 2));
+    b = make_uint2(set_nan(b.x, w.y, 0), set_nan(b.y, w.y, 2));
+    return make_uint4(a.x, a.y, b.x, b.y);
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -239,7 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             const uint32_t d = tmem + b * kTileN;
             for (int r = 0; r < count; r += kRows) {
-                ok = warp_wait_cluster(&tail.conv[s], ph, abort_flag);
+                ok = warp_wait(&tail.conv[s], ph, abort_flag);
                 if (!ok) break;
                 tc_fence_after_sync();
                 const uint64_t at = (s * kStageBytes) >> 4;
@@ -267,55 +286,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp >= 4 + kEpiWarps) {
         const int team = (warp - 4 - kEpiWarps) / kTeamWarps;
         const int t = threadIdx.x - 32 * (4 + kEpiWarps + team * kTeamWarps);
-        const int c = t & 7, r0 = t >> 3;                       // 16-byte chunk of a row, first row of four
+        // eight codes of a row, and the first of eight rows, 8 apart: their places in the swizzled tiles
+        // differ by whole groups of eight rows
+        const int c = t & 15, r0 = t >> 4;
+        const int raw_at = r0 * 128 + (((c >> 1) ^ r0) << 4) + (c & 1) * 8;
+        const int dst_at = (c >> 3) * kBox + r0 * 128 + (((c & 7) ^ r0) << 4);
         const int kblocks = p.cols >> 7;
-        uint32_t s = 0, ph = 0, turn = 0;
         bool bad = false, ok = true;
-        for (int tile = pair; tile < tiles && ok; tile += pairs) {
-            const Tile w = get_tile(tail, p, tile);
-            const int kb = (w.n0 >> 7) + rank;
-            // (columns behind the edge: any scale will do for their zeros)
-            const int64_t col = kb < kblocks ? kb : kblocks - 1;
-            for (int r = 0; r < w.count && ok; r += kRows, turn ^= 1u) {
-                if (turn == static_cast<uint32_t>(team)) {
-                    const int valid = w.count - r;
-                    uint32_t sb[4];
+        Stages at(tail, p, pair, pairs, tiles);
+        for (int i = 0; i < team; ++i) at.next(tail, p, pairs, tiles);
+        uint32_t s = team, ph = 0;
+        // A warp converts 16 rows of a stage, two at a time: lane l (and l + 16) loads the scale of the row
+        // r0 of lanes 16 (l & 1) on, 8 (l / 2) further, and hands it out by shuffles
+        const int srow = 2 * (t >> 5) + (lane & 1) + 8 * ((lane & 15) >> 1);
+        auto fetch = [&](const Stages &g) {
+            const int kb = (g.w.n0 >> 7) + rank, valid = g.w.count - g.r;
+            // (columns behind the edge and rows behind the group's end: any scale will do for their zeros)
+            return load_scale_bits(p.X_scale, p.x_ue8m0,
+                                   (g.w.begin + g.r + (srow < valid ? srow : valid - 1)) * kblocks +
+                                       (kb < kblocks ? kb : kblocks - 1));
+        };
+        // `ahead` is the stage whose scales are on their way, one of this team's behind the one it converts
+        Stages ahead = at;
+        uint32_t sb = 0, sb2 = 0;
+        if (at.tile < tiles) {
+            sb = fetch(at);
+            for (int i = 0; i < kTeams; ++i) ahead.next(tail, p, pairs, tiles);
+            if (ahead.tile < tiles) sb2 = fetch(ahead);
+        }
+        while (at.tile < tiles) {
+            const int valid = at.w.count - at.r;
+            const uint32_t byte = scale_bits_byte(sb, p.x_ue8m0, bad);
+            const uint32_t factor = (120u + byte) * 0x00800080u;      // 2^120 * s as a bf16, twice
+            ok = warp_wait(&tail.full[s], ph, abort_flag);
+            if (!ok) break;
+            uint8_t *a = ring + s * kStageBytes, *raw = a + kABytes, *b = raw + kRawBytes;
+            // all eight rows' codes first, no branch between them
+            uint2 v[8];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int row = r0 + 16 * x < valid ? r0 + 16 * x : valid - 1;
-                        sb[x] = load_scale_bits(p.X_scale, p.x_ue8m0, (w.begin + r + row) * kblocks + col);
-                    }
-                    ok = warp_wait(&tail.full[s], ph, abort_flag);
-                    if (!ok) break;
-                    uint8_t *a = ring + s * kStageBytes, *raw = a + kABytes, *b = raw + kRawBytes;
-                    uint4 v[4];
+            for (int x = 0; x < 8; ++x) v[x] = *reinterpret_cast<const uint2 *>(raw + raw_at + x * 1024);
+            if (valid < kRows) {
+                // the group's last rows.  Behind them x is zero, and whatever dY holds there must not meet
+                // those zeros
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int row = r0 + 16 * x;
-                        v[x] = *reinterpret_cast<const uint4 *>(raw + row * 128 + ((c ^ (row & 7)) << 4));
-                        if (row >= valid) v[x] = make_uint4(0, 0, 0, 0);
-                    }
+                for (int x = 0; x < 8; ++x)
+                    if (r0 + 8 * x >= valid) v[x] = make_uint2(0, 0);
+                for (int x = t; x < (kRows - valid) * 16; x += kTeamWarps * 32)
+                    *reinterpret_cast<uint4 *>(a + (x & 8 ? kBox : 0) + (valid + (x >> 4)) * 128 + ((x & 7) << 4)) =
+                        make_uint4(0, 0, 0, 0);
+            }
+            uint32_t nan = 0;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int row = r0 + 16 * x;
-                        convert_chunk(v[x], scale_bits_byte(sb[x], p.x_ue8m0, bad), b + (c >> 2) * kBox + row * 128, row & 7,
-                                      c);
-                    }
-                    if (valid < kRows) {
-                        // rows behind the group's end: whatever dY holds there must not meet the zeros of x
-                        for (int x = t; x < (kRows - valid) * 16; x += kTeamWarps * 32)
-                            *reinterpret_cast<uint4 *>(a + (x & 8 ? kBox : 0) + (valid + (x >> 4)) * 128 +
-                                                       ((x & 7) << 4)) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_release_at(&tail.conv[s], 0);
-                }
-                if (++s == kStages) {
-                    s = 0;
-                    ph ^= 1u;
+            for (int x = 0; x < 8; ++x) {
+                const uint32_t f = __shfl_sync(0xffffffffu, factor, 2 * x + (r0 & 1));
+                *reinterpret_cast<uint4 *>(b + dst_at + x * 1024) = convert_codes(v[x], f, nan);
+            }
+            if (__any_sync(0xffffffffu, (nan & 0x80808080u) != 0 || byte > 134u)) {
+#pragma unroll 1
+                for (int x = 0; x < 8; ++x) {
+                    const uint32_t y = __shfl_sync(0xffffffffu, byte, 2 * x + (r0 & 1));
+                    uint2 w = *reinterpret_cast<const uint2 *>(raw + raw_at + x * 1024);
+                    if (r0 + 8 * x >= valid) w = make_uint2(0, 0);
+                    *reinterpret_cast<uint4 *>(b + dst_at + x * 1024) = convert_codes_rare(w, y);
                 }
             }
+            // (each CTA's tensor core reads these bytes from its own shared memory: once they are ordered
+            // before the async proxy, the arrival at the leader has no other memory to order)
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(&tail.conv[s], 0);
+            s += kTeams;
+            if (s >= kStages) {
+                s -= kStages;
+                ph ^= 1u;
+            }
+            // (loads in flight are waited for by the fence above: they are issued right behind it)
+            sb = sb2;
+            at = ahead;
+            for (int i = 0; i < kTeams; ++i) ahead.next(tail, p, pairs, tiles);
+            if (ahead.tile < tiles) sb2 = fetch(ahead);
         }
         if (bad) tail.bad_scale = 1;
     } else if (warp >= 4) {
