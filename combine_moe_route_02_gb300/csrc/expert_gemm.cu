@@ -565,8 +565,8 @@ EncodeTiledFn encode_tiled()
 
 }  // namespace
 
-bool encode_map_sw128(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes, const void *base, int rank,
-                      const uint64_t *dims, const uint32_t *box)
+bool encode_map(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes, const void *base, int rank,
+                const uint64_t *dims, const uint32_t *box, CUtensorMapSwizzle swizzle)
 {
     EncodeTiledFn fn = encode_tiled();
     if (!fn) return false;
@@ -581,8 +581,7 @@ bool encode_map_sw128(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes
         if (i + 1 < rank) strides[i] = bytes;
     }
     return fn(map, type, rank, const_cast<void *>(base), d, strides, b, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t stream)
@@ -600,9 +599,9 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t stream)
     const uint32_t wb[3] = {128, 128, 1};
     for (int i = 0; i < kBoxes; ++i) {
         const uint32_t xb[2] = {kBlk, static_cast<uint32_t>(box_rows(i))};
-        if (!encode_map_sw128(&tmX.map[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.X, 2, xd, xb)) return cudaErrorInvalidValue;
+        if (!encode_map(&tmX.map[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.X, 2, xd, xb)) return cudaErrorInvalidValue;
     }
-    if (!encode_map_sw128(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.W, 3, wd, wb)) return cudaErrorInvalidValue;
+    if (!encode_map(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.W, 3, wd, wb)) return cudaErrorInvalidValue;
 
     static std::atomic<uint64_t> done{0};
     const uint64_t bit = 1ull << (dev & 63);

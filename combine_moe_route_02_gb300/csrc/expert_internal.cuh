@@ -117,6 +117,22 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
     return warp_wait_slow(bar, parity, abort);
 }
+// TMA store of a box (what lies outside the tensor is left out), in this thread's bulk async-group.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *smem_src, int32_t c0, int32_t c1, int32_t c2)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(smem_src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// Until this thread's bulk stores have read their shared memory / are complete.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one()
 {
@@ -200,8 +216,8 @@ struct LayerArgs {
 size_t layer_workspace_bytes(int N, int H, int I, int E, int K);
 cudaError_t launch_layer(const LayerArgs &a, cudaStream_t stream);
 
-// A tiled tensor map with 128-byte swizzle; false if the driver refuses it.
-bool encode_map_sw128(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes, const void *base, int rank,
-                      const uint64_t *dims, const uint32_t *box);
+// A tiled tensor map, 128-byte swizzle unless told otherwise; false if the driver refuses it.
+bool encode_map(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes, const void *base, int rank,
+                const uint64_t *dims, const uint32_t *box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 }  // namespace moe

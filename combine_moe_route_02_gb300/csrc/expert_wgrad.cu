@@ -34,7 +34,7 @@ constexpr int kRawBytes = kBox;                   // 128 columns
 constexpr int kBBytes = 2 * kBox;                 // two boxes of 64 columns
 constexpr int kStageBytes = kABytes + kRawBytes + kBBytes;
 constexpr int kEpiWarps = 8, kTeams = 3, kTeamWarps = 4;
-constexpr int kEpiBytes = kEpiWarps * 32 * 64;    // 32 rows x 16 fp32 each
+constexpr int kEpiBytes = kEpiWarps * 32 * 64;    // 32 rows x 64 bytes each
 constexpr int kThreads = 32 * (4 + kEpiWarps + kTeams * kTeamWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxE = 256;
@@ -163,7 +163,8 @@ __device__ __forceinline__ uint4 convert_codes_rare(const uint2 &w, uint32_t byt
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    expert_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX, const Params p)
+    expert_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX,
+                        const __grid_constant__ CUtensorMap tmW, const Params p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -189,6 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_mbarrier_init();
         tma_prefetch_desc(&tmY);
         tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
     }
     if (warp == 3) tmem_alloc_pair(&tail.tmem_base, kTmemCols);
     __syncthreads();
@@ -368,29 +370,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (bad) tail.bad_scale = 1;
     } else if (warp >= 4) {
+        // 32 rows x 128 columns of a tile: 16 columns at a time from TMEM (a lane is a row), through 2 KiB of
+        // shared memory, out as TMA boxes of 64-byte rows
         const int w = warp - 4, quarter = w & 3, side = w >> 2;   // TMEM lanes, columns 128 side on
         uint8_t *buf = epi + w * 32 * 64;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + side * 128;
-        // of a chunk of 32 rows x 16 columns: this lane's 16 bytes of rows lane / 4 + 8 i
-        const int lrow = lane >> 2, lch = lane & 3;
+        uint8_t *row_buf = buf + lane * 64;
+        const int swz = (lane >> 1) & 3;
         int j = 0;
+        // what is added is brought to L2 a tile ahead, and to registers 16 columns ahead
+        auto add_row = [&](const Tile &t) {
+            const int m = t.m0 + rank * kHalf + quarter * 32, n = t.n0 + side * 128;
+            return p.add && n < p.cols && m + lane < p.rows
+                       ? p.add + (static_cast<int64_t>(t.e) * p.rows + m + lane) * p.cols + n
+                       : nullptr;
+        };
+        auto prefetch = [&](int tile) {
+            const float *src = tile < tiles ? add_row(get_tile(tail, p, tile)) : nullptr;
+            if (src)
+#pragma unroll
+                for (int i = 0; i < kHalf; i += 32) prefetch_l2(src + i);
+        };
+        prefetch(pair);
         for (int tile = pair; tile < tiles; tile += pairs) {
             const Tile t = get_tile(tail, p, tile);
             const bool some = t.count != 0;
             const int m = t.m0 + rank * kHalf + quarter * 32, n = t.n0 + side * 128;
-            const bool inside = n < p.cols;                       // (columns come in whole 128)
-            const int64_t base = (static_cast<int64_t>(t.e) * p.rows + m + lrow) * p.cols + n + lch * 4;
-            const int64_t step = 8ll * p.cols;
-            float4 z[2][4];
-            auto fetch = [&](int c, float4 (&y)[4]) {
+            const bool inside = n < p.cols && m < p.rows;         // (columns come in whole 128)
+            const float *src = add_row(t);
+            float4 z[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    y[i] = p.add && inside && m + lrow + 8 * i < p.rows
-                               ? __ldcs(reinterpret_cast<const float4 *>(p.add + base + i * step + c))
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
-            };
-            // what is added is on its way while the accumulators are waited for
-            fetch(0, z[0]);
+            for (int i = 0; i < 4; ++i) z[i] = src ? __ldcs(reinterpret_cast<const float4 *>(src) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            prefetch(tile + pairs);
             const int b = j & 1;
             if (some) {
                 if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, abort_flag, 64))) break;
@@ -399,7 +410,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
 #pragma unroll 2
             for (int c = 0; c < kHalf; c += 16) {
-                if (c + 16 < kHalf) fetch(c + 16, z[((c >> 4) & 1) ^ 1]);
                 float v[16];
                 if (some) {
                     tmem_ld_32x32b_x16(lane_addr + b * kTileN + c, v);
@@ -408,39 +418,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int x = 0; x < 16; ++x) v[x] = 0.f;
                 }
-                // a row's four 16-byte chunks: chunk x of row l at place x ^ (l / 2 % 4)
+                if (src) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    *reinterpret_cast<float4 *>(buf + lane * 64 + ((x ^ ((lane >> 1) & 3)) << 4)) =
-                        make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = lrow + 8 * i;
-                    float4 y = *reinterpret_cast<const float4 *>(buf + row * 64 + ((lch ^ ((row >> 1) & 3)) << 4));
-                    const float4 q = z[(c >> 4) & 1][i];
-                    y.x += q.x;
-                    y.y += q.y;
-                    y.z += q.z;
-                    y.w += q.w;
-                    if (inside && m + row < p.rows) {
-                        const int64_t at = base + i * step + c;
-                        if (p.bf16_out) {
-                            __nv_bfloat162 h[2] = {__floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
-                            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.dW) + at) =
-                                *reinterpret_cast<uint2 *>(h);
-                        } else {
-                            __stcs(reinterpret_cast<float4 *>(static_cast<float *>(p.dW) + at), y);
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        v[4 * i] += z[i].x;
+                        v[4 * i + 1] += z[i].y;
+                        v[4 * i + 2] += z[i].z;
+                        v[4 * i + 3] += z[i].w;
+                        if (c + 16 < kHalf) z[i] = __ldcs(reinterpret_cast<const float4 *>(src + c + 16) + i);
                     }
                 }
+                // a row's four 16-byte pieces: piece x of row l at place x ^ (l / 2 % 4)
+                if (p.bf16_out) {
+                    const int half = (c >> 4) & 1;
+                    if (half == 0) {
+                        bulk_wait_read();
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint4 h;
+                        __nv_bfloat162 *hp = reinterpret_cast<__nv_bfloat162 *>(&h);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) hp[i] = __floats2bfloat162_rn(v[8 * x + 2 * i], v[8 * x + 2 * i + 1]);
+                        *reinterpret_cast<uint4 *>(row_buf + (((2 * half + x) ^ swz) << 4)) = h;
+                    }
+                    if (half == 0) continue;
+                } else {
+                    bulk_wait_read();
+                    __syncwarp();
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        *reinterpret_cast<float4 *>(row_buf + ((x ^ swz) << 4)) =
+                            make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                }
+                fence_proxy_async_smem();
                 __syncwarp();
+                if (lane == 0 && inside) tma_store_3d(&tmW, buf, n + (p.bf16_out ? c - 16 : c), m, t.e);
             }
             if (some) {
                 tc_fence_before_sync();
                 if (lane == 0) mbar_arrive_at(&tail.acc_empty[b], 0);
             }
         }
+        bulk_wait_all();
     }
 
     tc_fence_before_sync();
@@ -462,14 +483,19 @@ cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream)
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (device_cc_major(dev) != 10) return cudaErrorNotSupported;
-    CUtensorMap tmY, tmX;
+    CUtensorMap tmY, tmX, tmW;
     const uint64_t R = a.R > 0 ? a.R : 1;   // (no rows: the maps are not used)
     const uint64_t yd[2] = {static_cast<uint64_t>(a.rows), R};
     const uint32_t yb[2] = {64, kRows};
     const uint64_t xd[2] = {static_cast<uint64_t>(a.cols), R};
     const uint32_t xb[2] = {128, kRows};
-    if (!encode_map_sw128(&tmY, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.R > 0 ? a.dY : a.dW, 2, yd, yb) ||
-        !encode_map_sw128(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.R > 0 ? a.X : a.dW, 2, xd, xb))
+    if (!encode_map(&tmY, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.R > 0 ? a.dY : a.dW, 2, yd, yb) ||
+        !encode_map(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.R > 0 ? a.X : a.dW, 2, xd, xb))
+        return cudaErrorInvalidValue;
+    const uint64_t wd[3] = {static_cast<uint64_t>(a.cols), static_cast<uint64_t>(a.rows), static_cast<uint64_t>(a.E)};
+    const uint32_t wb[3] = {a.bf16_out ? 32u : 16u, 32, 1};
+    if (!encode_map(&tmW, a.bf16_out ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                    a.bf16_out ? 2 : 4, a.dW, 3, wd, wb, CU_TENSOR_MAP_SWIZZLE_64B))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
     const uint64_t bit = 1ull << (dev & 63);
@@ -495,7 +521,8 @@ cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream)
     p.status = a.status;
     const int64_t tiles = static_cast<int64_t>(a.E) * p.m_tiles * p.n_tiles;
     const int pairs = device_sm_count(dev) / 2;
-    expert_wgrad_kernel<<<2 * static_cast<int>(tiles < pairs ? tiles : pairs), kThreads, kSmemBytes, stream>>>(tmY, tmX, p);
+    expert_wgrad_kernel<<<2 * static_cast<int>(tiles < pairs ? tiles : pairs), kThreads, kSmemBytes, stream>>>(tmY, tmX,
+                                                                                                   tmW, p);
     return cudaGetLastError();
 }
 
