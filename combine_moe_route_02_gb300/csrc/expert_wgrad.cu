@@ -78,28 +78,35 @@ __device__ __forceinline__ Tile get_tile(const Tail &t, const Params &p, int til
     return r;
 }
 
-// The ring stages of a CTA pair's walk, one after the other; groups without rows have none.
+// Every kTeams-th ring stage of a CTA pair's walk; groups without rows have none.
 struct Stages {
-    int tile, r;
+    int tile, i, n;               // the tile, the stage in it, its stages
     Tile w;
 
-    __device__ __forceinline__ Stages(const Tail &t, const Params &p, int pair, int pairs, int tiles) : tile(pair), r(0)
+    __device__ __forceinline__ Stages(const Tail &t, const Params &p, int pair, int pairs, int tiles, int team)
+        : tile(pair - pairs), i(team), n(0)
     {
-        if (tile < tiles) w = get_tile(t, p, tile);
-        while (tile < tiles && w.count == 0) {
-            tile += pairs;
-            if (tile < tiles) w = get_tile(t, p, tile);
-        }
+        settle(t, p, pairs, tiles);
     }
     __device__ __forceinline__ void next(const Tail &t, const Params &p, int pairs, int tiles)
     {
-        r += kRows;
-        while (tile < tiles && r >= w.count) {
-            r = 0;
+        i += kTeams;
+        settle(t, p, pairs, tiles);
+    }
+    __device__ __forceinline__ void settle(const Tail &t, const Params &p, int pairs, int tiles)
+    {
+        while (i >= n && tile < tiles) {
+            i -= n;
+            n = 0;
             tile += pairs;
-            if (tile < tiles) w = get_tile(t, p, tile);
+            if (tile < tiles) {
+                w = get_tile(t, p, tile);
+                n = (w.count + kRows - 1) / kRows;
+            }
         }
     }
+    __device__ __forceinline__ int row() const { return i * kRows; }
+    __device__ __forceinline__ int valid() const { return w.count - i * kRows; }
 };
 
 __device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
@@ -295,17 +302,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int dst_at = (c >> 3) * kBox + r0 * 128 + (((c & 7) ^ r0) << 4);
         const int kblocks = p.cols >> 7;
         bool bad = false, ok = true;
-        Stages at(tail, p, pair, pairs, tiles);
-        for (int i = 0; i < team; ++i) at.next(tail, p, pairs, tiles);
+        Stages at(tail, p, pair, pairs, tiles, team);
         uint32_t s = team, ph = 0;
         // A warp converts 16 rows of a stage, two at a time: lane l (and l + 16) loads the scale of the row
         // r0 of lanes 16 (l & 1) on, 8 (l / 2) further, and hands it out by shuffles
         const int srow = 2 * (t >> 5) + (lane & 1) + 8 * ((lane & 15) >> 1);
         auto fetch = [&](const Stages &g) {
-            const int kb = (g.w.n0 >> 7) + rank, valid = g.w.count - g.r;
+            const int kb = (g.w.n0 >> 7) + rank, valid = g.valid();
             // (columns behind the edge and rows behind the group's end: any scale will do for their zeros)
             return load_scale_bits(p.X_scale, p.x_ue8m0,
-                                   (g.w.begin + g.r + (srow < valid ? srow : valid - 1)) * kblocks +
+                                   (g.w.begin + g.row() + (srow < valid ? srow : valid - 1)) * kblocks +
                                        (kb < kblocks ? kb : kblocks - 1));
         };
         // `ahead` is the stage whose scales are on their way, one of this team's behind the one it converts
@@ -313,11 +319,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t sb = 0, sb2 = 0;
         if (at.tile < tiles) {
             sb = fetch(at);
-            for (int i = 0; i < kTeams; ++i) ahead.next(tail, p, pairs, tiles);
+            ahead.next(tail, p, pairs, tiles);
             if (ahead.tile < tiles) sb2 = fetch(ahead);
         }
         while (at.tile < tiles) {
-            const int valid = at.w.count - at.r;
+            const int valid = at.valid();
             const uint32_t byte = scale_bits_byte(sb, p.x_ue8m0, bad);
             const uint32_t factor = (120u + byte) * 0x00800080u;      // 2^120 * s as a bf16, twice
             ok = warp_wait(&tail.full[s], ph, abort_flag);
@@ -365,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // (loads in flight are waited for by the fence above: they are issued right behind it)
             sb = sb2;
             at = ahead;
-            for (int i = 0; i < kTeams; ++i) ahead.next(tail, p, pairs, tiles);
+            ahead.next(tail, p, pairs, tiles);
             if (ahead.tile < tiles) sb2 = fetch(ahead);
         }
         if (bad) tail.bad_scale = 1;
@@ -387,9 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         auto prefetch = [&](int tile) {
             const float *src = tile < tiles ? add_row(get_tile(tail, p, tile)) : nullptr;
-            if (src)
-#pragma unroll
-                for (int i = 0; i < kHalf; i += 32) prefetch_l2(src + i);
+            if (src) bulk_prefetch_l2(src, kHalf * 4);
         };
         prefetch(pair);
         for (int tile = pair; tile < tiles; tile += pairs) {
