@@ -127,15 +127,13 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void 
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// Until this thread's bulk stores have read their shared memory / are complete.
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
-// Brings `bytes` (a multiple of 16, from a 16-byte boundary) to L2.
-__device__ __forceinline__ void bulk_prefetch_l2(const void *p, uint32_t bytes)
+// Until all but the last N of this thread's bulk stores have read their shared memory / all are complete.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read()
 {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(p)), "r"(bytes) : "memory");
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one()

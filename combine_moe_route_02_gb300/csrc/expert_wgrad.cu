@@ -30,11 +30,12 @@ constexpr int kTileM = 256, kTileN = 256, kRows = 64, kStages = 5;
 constexpr int kHalf = 128;                        // weight rows, and columns of x, of each CTA
 constexpr int kBox = kRows * 128;                 // bytes of a box: 64 rows of 128 bytes
 constexpr int kABytes = 2 * kBox;                 // two boxes of 64 columns
-constexpr int kRawBytes = kBox;                   // 128 columns
+constexpr int kRawBytes = kBox;                   // 128 columns; a row lies where its second half will, of
 constexpr int kBBytes = 2 * kBox;                 // two boxes of 64 columns
-constexpr int kStageBytes = kABytes + kRawBytes + kBBytes;
+constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kEpiWarps = 8, kTeams = 3, kTeamWarps = 4;
-constexpr int kEpiBytes = kEpiWarps * 32 * 64;    // 32 rows x 64 bytes each
+constexpr int kBufs = 4, kBufBytes = 32 * 64;     // of an epilogue warp: 32 rows x 16 fp32 each
+constexpr int kEpiBytes = kEpiWarps * kBufs * kBufBytes;
 constexpr int kThreads = 32 * (4 + kEpiWarps + kTeams * kTeamWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxE = 256;
@@ -42,9 +43,11 @@ constexpr int kMaxE = 256;
 struct Tail {
     uint64_t full[kStages], conv[kStages], empty[kStages];
     uint64_t acc_full[2], acc_empty[2], drain;
+    uint64_t added[kEpiWarps][kBufs];
     uint32_t tmem_base;
     int abort, bad_index, bad_scale;
-    int begin[kMaxE], count[kMaxE];
+    uint32_t valid[kMaxE / 32];   // a bit for each group that lies inside [0, R]
+    int off[kMaxE + 1];
 };
 constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kEpiBytes + sizeof(Tail);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -52,10 +55,8 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 struct Params {
     const void *X_scale;
     const int32_t *offsets;
-    const float *add;
-    void *dW;
     int64_t R;
-    int E, rows, cols, x_ue8m0, bf16_out;
+    int E, rows, cols, x_ue8m0, bf16_out, has_add;
     int m_tiles, n_tiles;
     int32_t *status;
 };
@@ -73,8 +74,8 @@ __device__ __forceinline__ Tile get_tile(const Tail &t, const Params &p, int til
     const int i = tile - r.e * per, m = i / p.n_tiles;
     r.m0 = m * kTileM;
     r.n0 = (i - m * p.n_tiles) * kTileN;
-    r.count = t.count[r.e];
-    r.begin = t.begin[r.e];
+    r.begin = t.off[r.e];
+    r.count = (t.valid[r.e >> 5] >> (r.e & 31)) & 1u ? t.off[r.e + 1] - t.off[r.e] : 0;
     return r;
 }
 
@@ -138,7 +139,7 @@ __device__ __forceinline__ uint2 codes_to_bf16(uint32_t w, uint32_t f)
     return make_uint2(mul_bf16x2((lo << 4) & 0x87F087F0u, f), mul_bf16x2((hi << 4) & 0x87F087F0u, f));
 }
 
-// Whether one of four codes is a NaN (s 1111 111).
+// Bits 0x80808080 of the result: which of four codes are NaNs (s 1111 111).
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }
 
 __device__ __forceinline__ uint32_t set_nan(uint32_t v, uint32_t w, int i)
@@ -148,11 +149,10 @@ __device__ __forceinline__ uint32_t set_nan(uint32_t v, uint32_t w, int i)
     return v;
 }
 
-// Eight codes of one row -> 16 bytes, times f = 2^120 * s; NaN codes raise bits of `nan` (0x80808080).
-__device__ __forceinline__ uint4 convert_codes(const uint2 &w, uint32_t f, uint32_t &nan)
+// Eight codes of one row, none of them a NaN -> 16 bytes, times f = 2^120 * s.
+__device__ __forceinline__ uint4 convert_codes(const uint2 &w, uint32_t f)
 {
     const uint2 a = codes_to_bf16(w.x, f), b = codes_to_bf16(w.y, f);
-    nan |= nan_codes(w.x) | nan_codes(w.y);
     return make_uint4(a.x, a.y, b.x, b.y);
 }
 
@@ -171,7 +171,7 @@ __device__ __forceinline__ uint4 convert_codes_rare(const uint2 &w, uint32_t byt
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expert_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX,
-                        const __grid_constant__ CUtensorMap tmW, const Params p)
+                        const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmAdd, const Params p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -193,23 +193,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&tail.acc_empty[b], 2 * kEpiWarps);
         }
         mbar_init(&tail.drain, 1);
+        for (int i = 0; i < kEpiWarps * kBufs; ++i) mbar_init(&tail.added[0][0] + i, 1);
         tail.abort = tail.bad_index = tail.bad_scale = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&tmY);
         tma_prefetch_desc(&tmX);
         tma_prefetch_desc(&tmW);
+        if (p.has_add) tma_prefetch_desc(&tmAdd);
     }
     if (warp == 3) tmem_alloc_pair(&tail.tmem_base, kTmemCols);
     __syncthreads();
-    if (static_cast<int>(threadIdx.x) < p.E) {
+    if (threadIdx.x < kMaxE) {
         const int e = threadIdx.x;
-        int64_t a = p.offsets ? p.offsets[e] : 0, b = p.offsets ? p.offsets[e + 1] : p.R;
-        if (a < 0 || b < a || b > p.R) {
-            tail.bad_index = 1;
-            a = b = 0;
+        int a = 0, b = 0;
+        if (e < p.E) {
+            a = p.offsets ? p.offsets[e] : 0;
+            b = p.offsets ? p.offsets[e + 1] : static_cast<int>(p.R);
+            tail.off[e] = a;
+            if (e == p.E - 1) tail.off[p.E] = b;
         }
-        tail.begin[e] = static_cast<int>(a);
-        tail.count[e] = static_cast<int>(b - a);
+        const bool good = a >= 0 && a <= b && b <= p.R;
+        const uint32_t mask = __ballot_sync(0xffffffffu, good);
+        if (lane == 0) tail.valid[warp] = mask;
+        if (!good) tail.bad_index = 1;
     }
     tc_fence_before_sync();
     cluster_sync();               // both CTAs' barriers stand, both hold TMEM
@@ -231,7 +237,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int row = static_cast<int>(t.begin) + r;
                 if (elect_one()) {
                     mbar_arrive_expect_tx(&tail.full[s], kABytes + kRawBytes);
-                    tma_load_2d(a + kABytes, &tmX, &tail.full[s], n, row, keep);
+                    tma_load_2d(a + kABytes + kBBytes - kRawBytes, &tmX, &tail.full[s], n, row, keep);
                     tma_load_2d(a, &tmY, &tail.full[s], m, row, keep);
                     tma_load_2d(a + kBox, &tmY, &tail.full[s], m + 64, row, keep);
                 }
@@ -253,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1 && rank == 0) {
         const uint64_t a0 = make_smem_desc_sw128(smem_u32(ring), kBox, 1024);
-        const uint64_t b0 = make_smem_desc_sw128(smem_u32(ring + kABytes + kRawBytes), kBox, 1024);
+        const uint64_t b0 = make_smem_desc_sw128(smem_u32(ring + kABytes), kBox, 1024);
         const uint32_t idesc = make_idesc_bf16_f32(kTileM, kTileN, 1, 1);
         uint32_t s = 0, ph = 0;
         int j = 0;
@@ -328,8 +334,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t factor = (120u + byte) * 0x00800080u;      // 2^120 * s as a bf16, twice
             ok = warp_wait(&tail.full[s], ph, abort_flag);
             if (!ok) break;
-            uint8_t *a = ring + s * kStageBytes, *raw = a + kABytes, *b = raw + kRawBytes;
-            // all eight rows' codes first, no branch between them
+            uint8_t *a = ring + s * kStageBytes, *b = a + kABytes, *raw = b + kBBytes - kRawBytes;
+            // a warp's rows are in registers before their bf16 forms overwrite them
             uint2 v[8];
 #pragma unroll
             for (int x = 0; x < 8; ++x) v[x] = *reinterpret_cast<const uint2 *>(raw + raw_at + x * 1024);
@@ -343,20 +349,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     *reinterpret_cast<uint4 *>(a + (x & 8 ? kBox : 0) + (valid + (x >> 4)) * 128 + ((x & 7) << 4)) =
                         make_uint4(0, 0, 0, 0);
             }
+            __syncwarp();
             uint32_t nan = 0;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const uint32_t f = __shfl_sync(0xffffffffu, factor, 2 * x + (r0 & 1));
-                *reinterpret_cast<uint4 *>(b + dst_at + x * 1024) = convert_codes(v[x], f, nan);
-            }
-            if (__any_sync(0xffffffffu, (nan & 0x80808080u) != 0 || byte > 134u)) {
-#pragma unroll 1
-                for (int x = 0; x < 8; ++x) {
-                    const uint32_t y = __shfl_sync(0xffffffffu, byte, 2 * x + (r0 & 1));
-                    uint2 w = *reinterpret_cast<const uint2 *>(raw + raw_at + x * 1024);
-                    if (r0 + 8 * x >= valid) w = make_uint2(0, 0);
-                    *reinterpret_cast<uint4 *>(b + dst_at + x * 1024) = convert_codes_rare(w, y);
-                }
+            for (int x = 0; x < 8; ++x) nan |= nan_codes(v[x].x) | nan_codes(v[x].y);
+            if (!__any_sync(0xffffffffu, (nan & 0x80808080u) != 0 || byte > 134u)) {
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    *reinterpret_cast<uint4 *>(b + dst_at + x * 1024) =
+                        convert_codes(v[x], __shfl_sync(0xffffffffu, factor, 2 * x + (r0 & 1)));
+            } else {
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    *reinterpret_cast<uint4 *>(b + dst_at + x * 1024) =
+                        convert_codes_rare(v[x], __shfl_sync(0xffffffffu, byte, 2 * x + (r0 & 1)));
             }
             // (each CTA's tensor core reads these bytes from its own shared memory: once they are ordered
             // before the async proxy, the arrival at the leader has no other memory to order)
@@ -376,44 +382,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (bad) tail.bad_scale = 1;
     } else if (warp >= 4) {
-        // 32 rows x 128 columns of a tile: 16 columns at a time from TMEM (a lane is a row), through 2 KiB of
-        // shared memory, out as TMA boxes of 64-byte rows
+        // 32 rows x 128 columns of a tile: 16 columns at a time from TMEM (a lane is a row), through one of
+        // four buffers of shared memory, out as a TMA box.  What is added comes in the same way, up to
+        // three boxes ahead (by loads to registers, 16 KiB in flight per SM, it took twice the time).
         const int w = warp - 4, quarter = w & 3, side = w >> 2;   // TMEM lanes, columns 128 side on
-        uint8_t *buf = epi + w * 32 * 64;
+        uint8_t *bufs = epi + w * kBufs * kBufBytes;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + side * 128;
-        uint8_t *row_buf = buf + lane * 64;
-        const int swz = (lane >> 1) & 3;
+        const int dm = rank * kHalf + quarter * 32, dn = side * 128;
+        // place of a lane's 16-byte piece x: its row's bytes, swizzled as the boxes are (64- or 32-byte rows)
+        const int row64 = lane * 64, swz64 = (lane >> 1) & 3, row32 = lane * 32, swz32 = (lane >> 2) & 1;
+        // the boxes that are to be added: of which tile, which columns, how many have been asked for
+        int a_tile = pair, a_c = 0;
+        uint32_t asked = 0, q = 0;                                // q: boxes done
+        auto ask = [&]() {
+            Tile t;
+            while (a_tile < tiles) {
+                t = get_tile(tail, p, a_tile);
+                if (t.m0 + dm < p.rows && t.n0 + dn < p.cols) break;
+                a_tile += pairs;
+            }
+            if (a_tile >= tiles) return;
+            if (lane == 0) {
+                uint64_t *bar = &tail.added[w][asked % kBufs];
+                mbar_arrive_expect_tx(bar, kBufBytes);
+                tma_load_3d(bufs + (asked % kBufs) * kBufBytes, &tmAdd, bar, t.n0 + dn + a_c, t.m0 + dm, t.e,
+                            l2_policy_evict_first());
+            }
+            __syncwarp();
+            ++asked;
+            a_c += 16;
+            if (a_c == kHalf) {
+                a_c = 0;
+                a_tile += pairs;
+            }
+        };
+        if (p.has_add)
+            for (int i = 0; i < kBufs - 1; ++i) ask();
         int j = 0;
-        // what is added is brought to L2 a tile ahead, and to registers 16 columns ahead
-        auto add_row = [&](const Tile &t) {
-            const int m = t.m0 + rank * kHalf + quarter * 32, n = t.n0 + side * 128;
-            return p.add && n < p.cols && m + lane < p.rows
-                       ? p.add + (static_cast<int64_t>(t.e) * p.rows + m + lane) * p.cols + n
-                       : nullptr;
-        };
-        auto prefetch = [&](int tile) {
-            const float *src = tile < tiles ? add_row(get_tile(tail, p, tile)) : nullptr;
-            if (src) bulk_prefetch_l2(src, kHalf * 4);
-        };
-        prefetch(pair);
+        bool ok = true;
         for (int tile = pair; tile < tiles; tile += pairs) {
             const Tile t = get_tile(tail, p, tile);
             const bool some = t.count != 0;
-            const int m = t.m0 + rank * kHalf + quarter * 32, n = t.n0 + side * 128;
+            const int m = t.m0 + dm, n = t.n0 + dn;
             const bool inside = n < p.cols && m < p.rows;         // (columns come in whole 128)
-            const float *src = add_row(t);
-            float4 z[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z[i] = src ? __ldcs(reinterpret_cast<const float4 *>(src) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-            prefetch(tile + pairs);
             const int b = j & 1;
             if (some) {
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, abort_flag, 64))) break;
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, abort_flag, 64));
+                if (!ok) break;
                 tc_fence_after_sync();
                 ++j;
             }
-#pragma unroll 2
-            for (int c = 0; c < kHalf; c += 16) {
+            for (int c = 0; c < kHalf && inside; c += 16, ++q) {
+                uint8_t *buf = bufs + (q % kBufs) * kBufBytes;
+                if (p.has_add) {
+                    // the buffer of the box before this one is free again once it has been read
+                    bulk_wait_read<0>();
+                    __syncwarp();
+                    ask();
+                } else {
+                    bulk_wait_read<kBufs - 1>();
+                    __syncwarp();
+                }
                 float v[16];
                 if (some) {
                     tmem_ld_32x32b_x16(lane_addr + b * kTileN + c, v);
@@ -422,48 +451,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int x = 0; x < 16; ++x) v[x] = 0.f;
                 }
-                if (src) {
+                if (p.has_add) {
+                    ok = warp_wait(&tail.added[w][q % kBufs], (q / kBufs) & 1u, abort_flag);
+                    if (!ok) break;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        v[4 * i] += z[i].x;
-                        v[4 * i + 1] += z[i].y;
-                        v[4 * i + 2] += z[i].z;
-                        v[4 * i + 3] += z[i].w;
-                        if (c + 16 < kHalf) z[i] = __ldcs(reinterpret_cast<const float4 *>(src + c + 16) + i);
+                    for (int x = 0; x < 4; ++x) {
+                        const float4 z = *reinterpret_cast<const float4 *>(buf + row64 + ((x ^ swz64) << 4));
+                        v[4 * x] += z.x;
+                        v[4 * x + 1] += z.y;
+                        v[4 * x + 2] += z.z;
+                        v[4 * x + 3] += z.w;
                     }
+                    if (p.bf16_out) __syncwarp();                 // (other lanes' rows lie where this one writes)
                 }
-                // a row's four 16-byte pieces: piece x of row l at place x ^ (l / 2 % 4)
                 if (p.bf16_out) {
-                    const int half = (c >> 4) & 1;
-                    if (half == 0) {
-                        bulk_wait_read();
-                        __syncwarp();
-                    }
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         uint4 h;
                         __nv_bfloat162 *hp = reinterpret_cast<__nv_bfloat162 *>(&h);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) hp[i] = __floats2bfloat162_rn(v[8 * x + 2 * i], v[8 * x + 2 * i + 1]);
-                        *reinterpret_cast<uint4 *>(row_buf + (((2 * half + x) ^ swz) << 4)) = h;
+                        *reinterpret_cast<uint4 *>(buf + row32 + ((x ^ swz32) << 4)) = h;
                     }
-                    if (half == 0) continue;
                 } else {
-                    bulk_wait_read();
-                    __syncwarp();
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        *reinterpret_cast<float4 *>(row_buf + ((x ^ swz) << 4)) =
+                        *reinterpret_cast<float4 *>(buf + row64 + ((x ^ swz64) << 4)) =
                             make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0 && inside) tma_store_3d(&tmW, buf, n + (p.bf16_out ? c - 16 : c), m, t.e);
+                if (lane == 0) tma_store_3d(&tmW, buf, n + c, m, t.e);
             }
+            if (!ok) break;
             if (some) {
                 tc_fence_before_sync();
                 if (lane == 0) mbar_arrive_at(&tail.acc_empty[b], 0);
             }
+        }
+        for (; q < asked; ++q) {                                  // (given up: what was asked for still lands here)
+            volatile int no_abort = 0;
+            mbar_wait_bounded(&tail.added[w][q % kBufs], (q / kBufs) & 1u, &no_abort);
         }
         bulk_wait_all();
     }
@@ -487,7 +515,7 @@ cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream)
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (device_cc_major(dev) != 10) return cudaErrorNotSupported;
-    CUtensorMap tmY, tmX, tmW;
+    CUtensorMap tmY, tmX, tmW, tmAdd;
     const uint64_t R = a.R > 0 ? a.R : 1;   // (no rows: the maps are not used)
     const uint64_t yd[2] = {static_cast<uint64_t>(a.rows), R};
     const uint32_t yb[2] = {64, kRows};
@@ -496,10 +524,16 @@ cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream)
     if (!encode_map(&tmY, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.R > 0 ? a.dY : a.dW, 2, yd, yb) ||
         !encode_map(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.R > 0 ? a.X : a.dW, 2, xd, xb))
         return cudaErrorInvalidValue;
+    // boxes of 16 columns x 32 rows
     const uint64_t wd[3] = {static_cast<uint64_t>(a.cols), static_cast<uint64_t>(a.rows), static_cast<uint64_t>(a.E)};
-    const uint32_t wb[3] = {a.bf16_out ? 32u : 16u, 32, 1};
-    if (!encode_map(&tmW, a.bf16_out ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                    a.bf16_out ? 2 : 4, a.dW, 3, wd, wb, CU_TENSOR_MAP_SWIZZLE_64B))
+    const uint32_t wb[3] = {16, 32, 1};
+    const bool out_ok = a.bf16_out ? encode_map(&tmW, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.dW, 3, wd, wb,
+                                                CU_TENSOR_MAP_SWIZZLE_32B)
+                                   : encode_map(&tmW, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.dW, 3, wd, wb,
+                                                CU_TENSOR_MAP_SWIZZLE_64B);
+    // (nothing to add: the map is not used)
+    if (!out_ok || !encode_map(&tmAdd, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.add ? a.add : a.dW, 3, wd, wb,
+                               CU_TENSOR_MAP_SWIZZLE_64B))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
     const uint64_t bit = 1ull << (dev & 63);
@@ -512,8 +546,7 @@ cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream)
     Params p;
     p.X_scale = a.X_scale;
     p.offsets = a.offsets;
-    p.add = a.add;
-    p.dW = a.dW;
+    p.has_add = a.add != nullptr;
     p.R = a.R;
     p.E = a.E;
     p.rows = a.rows;
@@ -525,8 +558,7 @@ cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream)
     p.status = a.status;
     const int64_t tiles = static_cast<int64_t>(a.E) * p.m_tiles * p.n_tiles;
     const int pairs = device_sm_count(dev) / 2;
-    expert_wgrad_kernel<<<2 * static_cast<int>(tiles < pairs ? tiles : pairs), kThreads, kSmemBytes, stream>>>(tmY, tmX,
-                                                                                                   tmW, p);
+    expert_wgrad_kernel<<<2 * static_cast<int>(tiles < pairs ? tiles : pairs), kThreads, kSmemBytes, stream>>>(tmY, tmX, tmW, tmAdd, p);
     return cudaGetLastError();
 }
 
