@@ -26,7 +26,7 @@
 namespace moe {
 namespace {
 
-constexpr int kTileM = 256, kTileN = 256, kRows = 64, kStages = 5;
+constexpr int kTileM = 256, kTileN = 256, kRows = 64;
 constexpr int kHalf = 128;                        // weight rows, and columns of x, of each CTA
 constexpr int kBox = kRows * 128;                 // bytes of a box: 64 rows of 128 bytes
 constexpr int kABytes = 2 * kBox;                 // two boxes of 64 columns
@@ -34,29 +34,41 @@ constexpr int kRawBytes = kBox;                   // 128 columns; a row lies whe
 constexpr int kBBytes = 2 * kBox;                 // two boxes of 64 columns
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kEpiWarps = 8, kTeams = 3, kTeamWarps = 4;
-constexpr int kBufs = 4, kBufBytes = 32 * 64;     // of an epilogue warp: 32 rows x 16 fp32 each
-constexpr int kEpiBytes = kEpiWarps * kBufs * kBufBytes;
+constexpr int kBufBytes = 32 * 64;                // a buffer of an epilogue warp: 32 rows x 16 fp32
+// Shared memory goes to ring stages or to the epilogue's buffers.  With something to add, small groups are
+// bound by its way in: four buffers keep three boxes of it in flight for each of the eight warps (64 experts
+// of 512 x 1024 with 32 rows each: 65 us, 82 us with two thirds of that in flight).  Without, a sixth stage
+// covers more of the ring's latency (128 experts of 2048 x 2048, 1024 rows each: 683 us, 724 us with five).
+template <bool kAdd>
+struct Split {
+    static constexpr int kStages = kAdd ? 5 : 6, kBufs = kAdd ? 4 : 2;
+};
+constexpr int kMostStages = 6, kMostBufs = 4;
 constexpr int kThreads = 32 * (4 + kEpiWarps + kTeams * kTeamWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxE = 256;
 
 struct Tail {
-    uint64_t full[kStages], conv[kStages], empty[kStages];
+    uint64_t full[kMostStages], conv[kMostStages], empty[kMostStages];
     uint64_t acc_full[2], acc_empty[2], drain;
-    uint64_t added[kEpiWarps][kBufs];
+    uint64_t added[kEpiWarps][kMostBufs];
     uint32_t tmem_base;
     int abort, bad_index, bad_scale;
     uint32_t valid[kMaxE / 32];   // a bit for each group that lies inside [0, R]
     int off[kMaxE + 1];
 };
-constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kEpiBytes + sizeof(Tail);
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+template <bool kAdd>
+constexpr size_t smem_bytes()
+{
+    return 1024 + Split<kAdd>::kStages * kStageBytes + Split<kAdd>::kBufs * kEpiWarps * kBufBytes + sizeof(Tail);
+}
+static_assert(smem_bytes<false>() <= 227 * 1024 && smem_bytes<true>() <= 227 * 1024, "shared memory");
 
 struct Params {
     const void *X_scale;
     const int32_t *offsets;
     int64_t R;
-    int E, rows, cols, x_ue8m0, bf16_out, has_add;
+    int E, rows, cols, x_ue8m0, bf16_out;
     int m_tiles, n_tiles;
     int32_t *status;
 };
@@ -79,35 +91,39 @@ __device__ __forceinline__ Tile get_tile(const Tail &t, const Params &p, int til
     return r;
 }
 
-// Every kTeams-th ring stage of a CTA pair's walk; groups without rows have none.
+// Every kTeams-th ring stage of a CTA pair's walk (groups without rows have none), as a converter needs
+// it: how many rows of the group from its first on there are, and where their scales of this CTA's
+// columns are.
 struct Stages {
-    int tile, i, n;               // the tile, the stage in it, its stages
-    Tile w;
+    int tile, i, count;           // the tile, the first row in its group, the group's rows
+    int64_t scales;               // of the group's first row
 
-    __device__ __forceinline__ Stages(const Tail &t, const Params &p, int pair, int pairs, int tiles, int team)
-        : tile(pair - pairs), i(team), n(0)
+    __device__ __forceinline__ Stages(const Tail &t, const Params &p, int pair, int pairs, int tiles, int team, int rank)
+        : tile(pair - pairs), i(team * kRows), count(0)
     {
-        settle(t, p, pairs, tiles);
+        settle(t, p, pairs, tiles, rank);
     }
-    __device__ __forceinline__ void next(const Tail &t, const Params &p, int pairs, int tiles)
+    __device__ __forceinline__ void next(const Tail &t, const Params &p, int pairs, int tiles, int rank)
     {
-        i += kTeams;
-        settle(t, p, pairs, tiles);
+        i += kTeams * kRows;
+        if (i >= count) settle(t, p, pairs, tiles, rank);
     }
-    __device__ __forceinline__ void settle(const Tail &t, const Params &p, int pairs, int tiles)
+    __device__ __forceinline__ void settle(const Tail &t, const Params &p, int pairs, int tiles, int rank)
     {
-        while (i >= n && tile < tiles) {
-            i -= n;
-            n = 0;
+        while (i >= count && tile < tiles) {
+            i -= (count + kRows - 1) / kRows * kRows;
+            count = 0;
             tile += pairs;
             if (tile < tiles) {
-                w = get_tile(t, p, tile);
-                n = (w.count + kRows - 1) / kRows;
+                const Tile w = get_tile(t, p, tile);
+                const int kblocks = p.cols >> 7, kb = (w.n0 >> 7) + rank;
+                // (columns behind the edge: any scale will do for their zeros)
+                scales = w.begin * kblocks + (kb < kblocks ? kb : kblocks - 1);
+                count = w.count;
             }
         }
     }
-    __device__ __forceinline__ int row() const { return i * kRows; }
-    __device__ __forceinline__ int valid() const { return w.count - i * kRows; }
+    __device__ __forceinline__ int valid() const { return count - i; }
 };
 
 __device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
@@ -169,14 +185,16 @@ __device__ __forceinline__ uint4 convert_codes_rare(const uint2 &w, uint32_t byt
     return make_uint4(a.x, a.y, b.x, b.y);
 }
 
+template <bool kAdd>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expert_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX,
                         const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmAdd, const Params p)
 {
+    constexpr int kStages = Split<kAdd>::kStages, kBufs = Split<kAdd>::kBufs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *epi = ring + kStages * kStageBytes;
-    Tail &tail = *reinterpret_cast<Tail *>(epi + kEpiBytes);
+    Tail &tail = *reinterpret_cast<Tail *>(epi + kBufs * kEpiWarps * kBufBytes);
     volatile int *abort_flag = &tail.abort;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -193,13 +211,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&tail.acc_empty[b], 2 * kEpiWarps);
         }
         mbar_init(&tail.drain, 1);
-        for (int i = 0; i < kEpiWarps * kBufs; ++i) mbar_init(&tail.added[0][0] + i, 1);
+        for (int i = 0; i < kEpiWarps * kMostBufs; ++i) mbar_init(&tail.added[0][0] + i, 1);
         tail.abort = tail.bad_index = tail.bad_scale = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&tmY);
         tma_prefetch_desc(&tmX);
         tma_prefetch_desc(&tmW);
-        if (p.has_add) tma_prefetch_desc(&tmAdd);
+        if (kAdd) tma_prefetch_desc(&tmAdd);
     }
     if (warp == 3) tmem_alloc_pair(&tail.tmem_base, kTmemCols);
     __syncthreads();
@@ -308,28 +326,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int dst_at = (c >> 3) * kBox + r0 * 128 + (((c & 7) ^ r0) << 4);
         const int kblocks = p.cols >> 7;
         bool bad = false, ok = true;
-        Stages at(tail, p, pair, pairs, tiles, team);
         uint32_t s = team, ph = 0;
         // A warp converts 16 rows of a stage, two at a time: lane l (and l + 16) loads the scale of the row
         // r0 of lanes 16 (l & 1) on, 8 (l / 2) further, and hands it out by shuffles
         const int srow = 2 * (t >> 5) + (lane & 1) + 8 * ((lane & 15) >> 1);
         auto fetch = [&](const Stages &g) {
-            const int kb = (g.w.n0 >> 7) + rank, valid = g.valid();
-            // (columns behind the edge and rows behind the group's end: any scale will do for their zeros)
-            return load_scale_bits(p.X_scale, p.x_ue8m0,
-                                   (g.w.begin + g.row() + (srow < valid ? srow : valid - 1)) * kblocks +
-                                       (kb < kblocks ? kb : kblocks - 1));
+            // (rows behind the group's end: any scale will do for their zeros)
+            const int row = g.i + srow < g.count ? g.i + srow : g.count - 1;
+            return load_scale_bits(p.X_scale, p.x_ue8m0, g.scales + static_cast<int64_t>(row) * kblocks);
         };
-        // `ahead` is the stage whose scales are on their way, one of this team's behind the one it converts
-        Stages ahead = at;
-        uint32_t sb = 0, sb2 = 0;
-        if (at.tile < tiles) {
-            sb = fetch(at);
-            ahead.next(tail, p, pairs, tiles);
-            if (ahead.tile < tiles) sb2 = fetch(ahead);
-        }
-        while (at.tile < tiles) {
-            const int valid = at.valid();
+        // The scales of this team's next two stages are on their way while it converts one (with one, the
+        // wait for them was a third of the team's time).  rows: of the stage; 0: there is none.
+        Stages ahead(tail, p, pair, pairs, tiles, team, rank);
+        auto take = [&](uint32_t &scale, int &rows) {
+            rows = 0;
+            if (ahead.tile < tiles) {
+                scale = fetch(ahead);
+                rows = ahead.valid();
+                ahead.next(tail, p, pairs, tiles, rank);
+            }
+        };
+        uint32_t sb = 0, sb1 = 0, sb2 = 0;
+        int valid, valid1, valid2;
+        take(sb, valid);
+        take(sb1, valid1);
+        take(sb2, valid2);
+        while (valid > 0) {
             const uint32_t byte = scale_bits_byte(sb, p.x_ue8m0, bad);
             const uint32_t factor = (120u + byte) * 0x00800080u;      // 2^120 * s as a bf16, twice
             ok = warp_wait(&tail.full[s], ph, abort_flag);
@@ -375,10 +397,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ph ^= 1u;
             }
             // (loads in flight are waited for by the fence above: they are issued right behind it)
-            sb = sb2;
-            at = ahead;
-            ahead.next(tail, p, pairs, tiles);
-            if (ahead.tile < tiles) sb2 = fetch(ahead);
+            sb = sb1;
+            valid = valid1;
+            sb1 = sb2;
+            valid1 = valid2;
+            take(sb2, valid2);
         }
         if (bad) tail.bad_scale = 1;
     } else if (warp >= 4) {
@@ -416,7 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 a_tile += pairs;
             }
         };
-        if (p.has_add)
+        if (kAdd)
             for (int i = 0; i < kBufs - 1; ++i) ask();
         int j = 0;
         bool ok = true;
@@ -434,7 +457,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             for (int c = 0; c < kHalf && inside; c += 16, ++q) {
                 uint8_t *buf = bufs + (q % kBufs) * kBufBytes;
-                if (p.has_add) {
+                if (kAdd) {
                     // the buffer of the box before this one is free again once it has been read
                     bulk_wait_read<0>();
                     __syncwarp();
@@ -451,7 +474,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int x = 0; x < 16; ++x) v[x] = 0.f;
                 }
-                if (p.has_add) {
+                if (kAdd) {
                     ok = warp_wait(&tail.added[w][q % kBufs], (q / kBufs) & 1u, abort_flag);
                     if (!ok) break;
 #pragma unroll
@@ -507,6 +530,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
+template <bool kAdd>
+cudaError_t launch(int dev, dim3 grid, cudaStream_t stream, const CUtensorMap &tmY, const CUtensorMap &tmX,
+                   const CUtensorMap &tmW, const CUtensorMap &tmAdd, const Params &p)
+{
+    constexpr size_t bytes = smem_bytes<kAdd>();
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        const cudaError_t err = cudaFuncSetAttribute(expert_wgrad_kernel<kAdd>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     static_cast<int>(bytes));
+        if (err != cudaSuccess) return err;
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    expert_wgrad_kernel<kAdd><<<grid, kThreads, bytes, stream>>>(tmY, tmX, tmW, tmAdd, p);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream)
@@ -535,18 +575,9 @@ cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream)
     if (!out_ok || !encode_map(&tmAdd, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.add ? a.add : a.dW, 3, wd, wb,
                                CU_TENSOR_MAP_SWIZZLE_64B))
         return cudaErrorInvalidValue;
-    static std::atomic<uint64_t> done{0};
-    const uint64_t bit = 1ull << (dev & 63);
-    if (!(done.load(std::memory_order_relaxed) & bit)) {
-        err = cudaFuncSetAttribute(expert_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(kSmemBytes));
-        if (err != cudaSuccess) return err;
-        done.fetch_or(bit, std::memory_order_relaxed);
-    }
     Params p;
     p.X_scale = a.X_scale;
     p.offsets = a.offsets;
-    p.has_add = a.add != nullptr;
     p.R = a.R;
     p.E = a.E;
     p.rows = a.rows;
@@ -558,8 +589,9 @@ cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream)
     p.status = a.status;
     const int64_t tiles = static_cast<int64_t>(a.E) * p.m_tiles * p.n_tiles;
     const int pairs = device_sm_count(dev) / 2;
-    expert_wgrad_kernel<<<2 * static_cast<int>(tiles < pairs ? tiles : pairs), kThreads, kSmemBytes, stream>>>(tmY, tmX, tmW, tmAdd, p);
-    return cudaGetLastError();
+    const dim3 grid(2 * static_cast<unsigned>(tiles < pairs ? tiles : pairs));
+    return a.add ? launch<true>(dev, grid, stream, tmY, tmX, tmW, tmAdd, p)
+                 : launch<false>(dev, grid, stream, tmY, tmX, tmW, tmAdd, p);
 }
 
 }  // namespace moe

@@ -8,14 +8,15 @@
 // With N <= 64 tokens the time is the weights of the experts that are touched, read
 // once; everything else is arranged around that stream.  One CTA per SM.  A unit of
 // work is 16 weight rows of one expert (8 gate and 8 up rows of W1, or 16 rows of
-// W2); the units of all touched experts are split evenly and in order over the CTAs.
-// One warp streams its CTA's units through a shared-memory ring with bulk copies, W1's
-// and then W2's without a pause between; it needs only the routing, so that W2 is in
-// flight while the CTAs wait for each other between the two products.  Sixteen warps
-// consume: each takes 128-wide reduction blocks of a unit, multiplies them by the
-// tokens of the expert (mma.sync, 16 rows x 8 tokens x 32: the tensor work is far
-// below the stream's time, so the registers' path costs nothing), applies the block's
-// scales in fp32, and the sixteen partial sums are added in a fixed order.
+// W2); the units of all touched experts are split evenly and in order over the CTAs,
+// and a CTA's over its eight streaming warps.  Each of those is on its own: it copies
+// its units in pieces of 16 rows x 512 bytes to a ring of three in shared memory (bulk
+// copies, W1's and then W2's without a pause between: they need only the routing, so
+// that W2 is in flight while the CTAs wait for each other between the products),
+// multiplies a piece by the tokens of its expert (mma.sync, 16 rows x 8 tokens x 32:
+// the tensor work is far below the stream's time, so the registers' path costs
+// nothing), applies each 128-block's scales in fp32, and holds a unit's whole
+// reduction in its registers: no sum crosses warps, and none depends on an order.
 //
 // Phases, with grid barriers where marked:
 //   logits of row slices of W_gate, x to E4M3 | top-K, one CTA per token | lists of
@@ -27,29 +28,33 @@ namespace moe {
 namespace {
 
 constexpr int kMaxN = 64, kMaxE = 256, kMaxK = 16;
-constexpr int kConsumers = 512, kThreads = kConsumers + 32;
-constexpr int kConsWarps = kConsumers / 32;
-constexpr int kWide = 2048;                   // reduction bytes of a row in one ring stage
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kStreams = 8;                   // streaming warps
+constexpr int kWide = 512;                    // reduction bytes of a row in one ring stage: four 128-blocks
 constexpr int kRowBytes = kWide + 64;         // 64: eight rows at one offset meet different banks
-constexpr int kStages = 5;
+constexpr int kStages = 3;                    // of each streaming warp
 constexpr int kStageBytes = 16 * kRowBytes;
-constexpr int kRedBytes = kConsWarps * 128 * 4;   // a group of 8 tokens x 16 rows from each warp
+constexpr int kRingBytes = kStreams * kStages * kStageBytes;
+constexpr int kMostBlocks = 256;              // 128-blocks of the activation that a CTA counts for itself
 
 struct Header {                               // zero before the first call, left zero by every call
     unsigned barrier[4], done, aborted;
 };
 
 struct Smem {
-    uint64_t full[kStages], empty[kStages];
-    int abort, last;
+    uint64_t full[kStreams][kStages];
+    int abort;
     int active;                               // touched experts
     uint32_t mask[kMaxE][2];                  // tokens of each expert
     int16_t expert[kMaxE];                    // the touched ones, ascending
     int16_t first[kMaxE + 1];                 // where each touched expert's slots start
     int16_t slot[kMaxN * kMaxK];              // slots n * K + k by expert, then token
+    int16_t token[kMaxN * kMaxK];             // their n
     float logit[kMaxE];
+    int done[kMostBlocks];                    // units that this CTA has done of its 128-blocks
 };
-constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + 2 * kRedBytes + sizeof(Smem);
+constexpr size_t kSmemBytes = 1024 + kRingBytes + sizeof(Smem);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 struct Layout {                               // byte offsets into the workspace
@@ -61,6 +66,9 @@ __host__ __device__ inline size_t up256(size_t v) { return (v + 255) & ~size_t(2
 // Rows of a slice of W_gate: at most 128 slices.
 __host__ __device__ inline int slice_rows(int H) { return (((H + 127) / 128) + 7) & ~7; }
 
+// Bytes of a row's scales in the workspace: whole words, one for each ring stage.
+__host__ __device__ inline int scale_stride(int n) { return ((n / 128) + 3) & ~3; }
+
 Layout make_layout(int N, int H, int I, int E, int K)
 {
     const size_t S = (H + slice_rows(H) - 1) / slice_rows(H), slots = static_cast<size_t>(N) * K;
@@ -68,11 +76,11 @@ Layout make_layout(int N, int H, int I, int E, int K)
     l.counters = 256;
     l.x8 = up256(l.counters + static_cast<size_t>(E) * (I / 128) * 4);
     l.xs = up256(l.x8 + static_cast<size_t>(N) * H);
-    l.part = up256(l.xs + static_cast<size_t>(N) * (H / 128));
+    l.part = up256(l.xs + static_cast<size_t>(N) * scale_stride(H));
     l.a = up256(l.part + S * N * E * 4);
     l.a8 = up256(l.a + slots * I * 4);
     l.as = up256(l.a8 + slots * I);
-    l.y = up256(l.as + slots * (I / 128));
+    l.y = up256(l.as + slots * scale_stride(I));
     l.total = up256(l.y + slots * H * 4);
     return l;
 }
@@ -89,15 +97,13 @@ __device__ __forceinline__ void my_units(int total, int &from, int &to)
     to = static_cast<int>(static_cast<int64_t>(total) * (blockIdx.x + 1) / gridDim.x);
 }
 
-__device__ __forceinline__ void consumers_sync() { named_barrier_sync(1, kConsumers); }
-
-// All CTAs' consumer threads; what they wrote before is visible to all after.  A CTA that gives up
+// All CTAs' threads; what they wrote before is visible to all after.  A CTA that gives up
 // goes on through the remaining phases (each wait then ends at once), so that every thread meets
 // every barrier and the counters always end complete; its results are then worthless, and the
 // status word says so.
 __device__ void grid_barrier(Header *h, int which, Smem &sm)
 {
-    consumers_sync();
+    __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
         red_add_release_gpu(&h->barrier[which], 1);
@@ -111,7 +117,7 @@ __device__ void grid_barrier(Header *h, int which, Smem &sm)
         }
         __threadfence();
     }
-    consumers_sync();
+    __syncthreads();
 }
 
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -143,16 +149,16 @@ __device__ void partial_logits(const Params &p, float *xs)
     const int hc = slice_rows(H);
     const int slices = (H + hc - 1) / hc;
     float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(p.a.workspace) + p.l.part);
-    const int Er = (E + 31) & ~31, groups = kConsumers / Er;
+    const int Er = (E + 31) & ~31, groups = kThreads / Er;
     const int e = t % Er, tg = t / Er;
     for (int s = blockIdx.x; s < slices; s += gridDim.x) {
         const int from = s * hc, rows = H - from < hc ? H - from : hc;   // a multiple of 8
-        consumers_sync();
-        for (int i = t; i < N * rows; i += kConsumers) {
+        __syncthreads();
+        for (int i = t; i < N * rows; i += kThreads) {
             const int n = i / rows, h = i - n * rows;
             xs[n * hc + h] = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.a.X)[static_cast<int64_t>(n) * H + from + h]);
         }
-        consumers_sync();
+        __syncthreads();
         if (e >= E || tg >= groups) continue;
         float acc[32];
 #pragma unroll
@@ -194,7 +200,8 @@ __device__ void quantise_x(const Params &p)
     const int H = p.a.H, blocks = H / 128, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *x8 = static_cast<uint8_t *>(p.a.workspace) + p.l.x8, *xs = static_cast<uint8_t *>(p.a.workspace) + p.l.xs;
     const int me = gridDim.x - 1 - blockIdx.x;
-    for (int i = me * kConsWarps + warp; i < p.a.N * blocks; i += gridDim.x * kConsWarps) {
+    const int stride = scale_stride(H);
+    for (int i = me * kWarps + warp; i < p.a.N * blocks; i += gridDim.x * kWarps) {
         const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.a.X) +
                                                          static_cast<int64_t>(i) * 128 + lane * 4);
         const float f[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
@@ -202,7 +209,7 @@ __device__ void quantise_x(const Params &p)
         uint32_t byte;
         const uint32_t q = quant_warp_block(f, byte);
         reinterpret_cast<uint32_t *>(x8)[static_cast<int64_t>(i) * 32 + lane] = q;
-        if (lane == 0) xs[i] = static_cast<uint8_t>(byte);
+        if (lane == 0) xs[(i / blocks) * stride + i % blocks] = static_cast<uint8_t>(byte);
     }
 }
 
@@ -214,7 +221,7 @@ __device__ void select(const Params &p, int n, Smem &sm, float *scratch)
     const int E = p.a.E, N = p.a.N, K = p.a.K, t = threadIdx.x, lane = t & 31;
     const int hc = slice_rows(p.a.H), slices = (p.a.H + hc - 1) / hc;
     const float *part = reinterpret_cast<const float *>(static_cast<const uint8_t *>(p.a.workspace) + p.l.part);
-    const int Er = (E + 31) & ~31, groups = kConsumers / Er;
+    const int Er = (E + 31) & ~31, groups = kThreads / Er;
     const int e = t % Er, tg = t / Er;
     if (e < E && tg < groups) {
         float s = 0.f;
@@ -222,14 +229,14 @@ __device__ void select(const Params &p, int n, Smem &sm, float *scratch)
         for (int i = tg; i < slices; i += groups) s += __ldcg(part + (static_cast<int64_t>(i) * N + n) * E + e);
         scratch[tg * Er + e] = s;
     }
-    consumers_sync();
+    __syncthreads();
     if (t < E) {
         float s = 0.f;
         for (int g = 0; g < groups; ++g) s += scratch[g * Er + t];
         if (p.a.bias) s += p.a.bias[t];
         sm.logit[t] = isnan(s) ? -INFINITY : s;
     }
-    consumers_sync();
+    __syncthreads();
     if (t < 32) {
         float v[kMaxE / 32];
 #pragma unroll
@@ -285,12 +292,12 @@ __device__ void select(const Params &p, int n, Smem &sm, float *scratch)
 __device__ void make_lists(const Params &p, Smem &sm)
 {
     const int t = threadIdx.x, lane = t & 31, E = p.a.E, K = p.a.K, slots = p.a.N * K;
-    for (int i = t; i < 2 * E; i += kConsumers) sm.mask[i >> 1][i & 1] = 0;
-    consumers_sync();
+    for (int i = t; i < 2 * E; i += kThreads) sm.mask[i >> 1][i & 1] = 0;
+    __syncthreads();
     int e[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int s = t + i * kConsumers;
+        const int s = t + i * kThreads;
         e[i] = s < slots ? __ldcg(p.a.topk_idx + s) : -1;
         if (e[i] < 0 || e[i] >= E) {
             e[i] = -1;   // (ids that are not there: only after a barrier that gave up)
@@ -299,7 +306,7 @@ __device__ void make_lists(const Params &p, Smem &sm)
         const int n = s / K;
         atomicOr(&sm.mask[e[i]][n >> 5], 1u << (n & 31));
     }
-    consumers_sync();
+    __syncthreads();
     if (t < 32) {
         int active = 0, before = 0;
         for (int b = 0; b < E; b += 32) {
@@ -326,175 +333,221 @@ __device__ void make_lists(const Params &p, Smem &sm)
             sm.first[active] = static_cast<int16_t>(before);
         }
     }
-    consumers_sync();
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         if (e[i] < 0) continue;
-        const int s = t + i * kConsumers, n = s / K;
+        const int s = t + i * kThreads, n = s / K;
         const uint32_t m0 = sm.mask[e[i]][0], m1 = sm.mask[e[i]][1];
         const uint32_t below = (1u << (n & 31)) - 1u;
         const int rank = n < 32 ? __popc(m0 & below) : __popc(m0) + __popc(m1 & below);
-        sm.slot[__float_as_int(sm.logit[e[i]]) + rank] = static_cast<int16_t>(s);
+        const int at = __float_as_int(sm.logit[e[i]]) + rank;
+        sm.slot[at] = static_cast<int16_t>(s);
+        sm.token[at] = static_cast<int16_t>(n);
     }
+    __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
 // The products.  FIRST: units of 8 gate + 8 up rows of W1, tokens from x8; else 16
 // rows of W2, slots from a8.
 // ---------------------------------------------------------------------------
+// A streaming warp's walk over the pieces of its units, first W1's, then W2's.
+struct Pieces {
+    int product, u, to, k;        // (product 2: the end)
+
+    __device__ __forceinline__ void enter(const Params &p, const Smem &sm, int warp)
+    {
+        for (; product < 2; ++product) {
+            int from;
+            my_units(sm.active * (product == 0 ? p.a.I / 8 : p.a.H / 16), from, to);
+            u = from + warp;
+            k = 0;
+            if (u < to) break;
+        }
+    }
+    __device__ __forceinline__ void next(const Params &p, const Smem &sm, int warp)
+    {
+        k += kWide;
+        if (k < (product == 0 ? p.a.H : p.a.I)) return;
+        k = 0;
+        u += kStreams;
+        if (u < to) return;
+        ++product;
+        enter(p, sm, warp);
+    }
+    // Asks for the piece: lane r < 16 its row r.
+    __device__ __forceinline__ void copy(const Params &p, const Smem &sm, uint8_t *stage, uint64_t *full, int lane) const
+    {
+        const LayerArgs &a = p.a;
+        const int red = product == 0 ? a.H : a.I, per = product == 0 ? a.I / 8 : a.H / 16;
+        const int ai = u / per, i = u - ai * per;
+        const int64_t e = sm.expert[ai];
+        const int width = red - k < kWide ? red - k : kWide;
+        if (lane == 0) mbar_arrive_expect_tx(full, 16 * width);
+        __syncwarp();
+        if (lane < 16) {
+            const uint8_t *row =
+                product == 0 ? static_cast<const uint8_t *>(a.W1) + (e * 2 * a.I + (lane & 8 ? a.I : 0) + i * 8 + (lane & 7)) * a.H
+                             : static_cast<const uint8_t *>(a.W2) + (e * a.H + i * 16 + lane) * a.I;
+            bulk_load(stage + lane * kRowBytes, row + k, width, full);
+        }
+    }
+};
+
+struct Stream {
+    uint8_t *ring;
+    uint64_t *full;
+    Pieces ahead;                 // the next piece to ask for
+    uint32_t asked, done;
+
+    __device__ __forceinline__ void ask(const Params &p, const Smem &sm, int warp, int lane)
+    {
+        if (ahead.product == 2) return;
+        const uint32_t s = asked % kStages;
+        ahead.copy(p, sm, ring + s * kStageBytes, full + s, lane);
+        ahead.next(p, sm, warp);
+        ++asked;
+    }
+};
+
 template <bool FIRST>
-__device__ void product(const Params &p, Smem &sm, const uint8_t *ring, float *red, uint32_t &stage, uint32_t &phase)
+__device__ void product(const Params &p, Smem &sm, Stream &st)
 {
     const LayerArgs &a = p.a;
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
-    const int red_len = FIRST ? a.H : a.I, rblocks = red_len / 128;
+    const int red = FIRST ? a.H : a.I, rblocks = red / 128, stride = scale_stride(red);
     const int per = FIRST ? a.I / 8 : a.H / 16;      // units of an expert
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const uint8_t *src = ws + (FIRST ? p.l.x8 : p.l.a8), *src_scale = ws + (FIRST ? p.l.xs : p.l.as);
+    const void *W_scale = FIRST ? a.W1_scale : a.W2_scale;
     float *act = reinterpret_cast<float *>(ws + p.l.a);
     float *y = reinterpret_cast<float *>(ws + p.l.y);
-    unsigned *counters = reinterpret_cast<unsigned *>(ws + p.l.counters);
-    const int chunks = (red_len + kWide - 1) / kWide;
     int from, to;
     my_units(sm.active * per, from, to);
     bool bad = false;
-    int buf = 0;
-    int in_block = 0;          // units of the current 128-block that this CTA has done
-    for (int u = from; u < to; ++u) {
+    for (int u = from + warp; u < to; u += kStreams) {
         const int ai = u / per, i = u - ai * per, e = sm.expert[ai];
         const int s0 = sm.first[ai], T = sm.first[ai + 1] - s0, groups = (T + 7) >> 3;
+        const int16_t *who = (FIRST ? sm.token : sm.slot) + s0;
+        // where the scales of the unit's rows start; gate and up rows lie in different blocks
+        const int64_t sc0 = FIRST ? (static_cast<int64_t>(e) * (2 * a.I / 128) + i / 16) * rblocks
+                                  : (static_cast<int64_t>(e) * (a.H / 128) + i / 8) * rblocks;
+        const int64_t sc1 = FIRST ? sc0 + static_cast<int64_t>(a.I / 128) * rblocks : sc0;
         float acc[8][4];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int x = 0; x < 4; ++x) acc[j][x] = 0.f;
-        for (int c = 0; c < chunks; ++c) {
-            const int kb = c * (kWide / 128) + warp;
-            const bool mine = kb < rblocks;
-            // scales of the weight block; gate and up rows lie in different ones
-            float sw0 = 0.f, sw1 = 0.f;
-            if (mine) {
-                if (FIRST) {
-                    const int64_t at = (static_cast<int64_t>(e) * ((2 * a.I) / 128) + i / 16) * rblocks + kb;
-                    sw0 = scale_value(load_scale_byte(a.W1_scale, a.ue8m0, at, bad));
-                    sw1 = scale_value(load_scale_byte(a.W1_scale, a.ue8m0, at + static_cast<int64_t>(a.I / 128) * rblocks, bad));
-                } else {
-                    const int64_t at = (static_cast<int64_t>(e) * (a.H / 128) + i / 8) * rblocks + kb;
-                    sw0 = sw1 = scale_value(load_scale_byte(a.W2_scale, a.ue8m0, at, bad));
-                }
+        float sw0 = 0.f, sw1 = 0.f;                  // of block (32 at a time) + lane
+        for (int k0 = 0; k0 < rblocks; k0 += kWide / 128) {
+            if ((k0 & 31) == 0) {
+                const int b = k0 + lane < rblocks ? k0 + lane : rblocks - 1;
+                sw0 = scale_value(load_scale_byte(W_scale, a.ue8m0, sc0 + b, bad));
+                sw1 = FIRST ? scale_value(load_scale_byte(W_scale, a.ue8m0, sc1 + b, bad)) : sw0;
             }
-            mbar_wait_bounded(&sm.full[stage], phase, &sm.abort);
-            __syncwarp();
-            if (mine) {
-                const uint8_t *row = ring + stage * kStageBytes + g * kRowBytes + warp * 128 + t4 * 16;
-                const uint4 lo0 = *reinterpret_cast<const uint4 *>(row);
-                const uint4 lo1 = *reinterpret_cast<const uint4 *>(row + 64);
-                const uint4 hi0 = *reinterpret_cast<const uint4 *>(row + 8 * kRowBytes);
-                const uint4 hi1 = *reinterpret_cast<const uint4 *>(row + 8 * kRowBytes + 64);
+            const uint32_t s = st.done % kStages;
+            warp_wait(st.full + s, (st.done / kStages) & 1u, &sm.abort);
+            const uint8_t *row = st.ring + s * kStageBytes + g * kRowBytes + t4 * 16;
+            const int nb = rblocks - k0 < 4 ? rblocks - k0 : 4;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (j >= groups) break;
-                    uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
-                    if (j * 8 + g < T) {
-                        const int s = sm.slot[s0 + j * 8 + g];
-                        const uint8_t *tok = src + static_cast<int64_t>(FIRST ? s / a.K : s) * red_len + kb * 128 + t4 * 16;
-                        b0 = __ldcg(reinterpret_cast<const uint4 *>(tok));
-                        b1 = __ldcg(reinterpret_cast<const uint4 *>(tok + 64));
-                    }
-                    // scales of the two tokens whose sums this lane holds
-                    float st[2];
+            for (int j = 0; j < 8; ++j) {
+                if (j >= groups) break;
+                // the tokens' side: eight of them, one a lane group; the scales of the two whose sums this
+                // lane holds
+                const bool mine = j * 8 + g < T;
+                const uint8_t *tok = src + static_cast<int64_t>(mine ? who[j * 8 + g] : who[0]) * red + k0 * 128 + t4 * 16;
+                uint4 b0[4], b1[4];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int col = j * 8 + t4 * 2 + x;
-                        st[x] = 0.f;
-                        if (col < T) {
-                            const int s = sm.slot[s0 + col];
-                            st[x] = scale_value(__ldcg(src_scale + static_cast<int64_t>(FIRST ? s / a.K : s) * rblocks + kb));
-                        }
+                for (int b = 0; b < 4; ++b) {
+                    b0[b] = b1[b] = make_uint4(0, 0, 0, 0);
+                    if (mine && b < nb) {
+                        b0[b] = *reinterpret_cast<const uint4 *>(tok + b * 128);
+                        b1[b] = *reinterpret_cast<const uint4 *>(tok + b * 128 + 64);
                     }
+                }
+                uint32_t st0 = 0, st1 = 0;
+                if (j * 8 + t4 * 2 < T)
+                    st0 = *reinterpret_cast<const uint32_t *>(src_scale + who[j * 8 + t4 * 2] * stride + k0);
+                if (j * 8 + t4 * 2 + 1 < T)
+                    st1 = *reinterpret_cast<const uint32_t *>(src_scale + who[j * 8 + t4 * 2 + 1] * stride + k0);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    if (b >= nb) break;
+                    const uint4 lo0 = *reinterpret_cast<const uint4 *>(row + b * 128);
+                    const uint4 lo1 = *reinterpret_cast<const uint4 *>(row + b * 128 + 64);
+                    const uint4 hi0 = *reinterpret_cast<const uint4 *>(row + 8 * kRowBytes + b * 128);
+                    const uint4 hi1 = *reinterpret_cast<const uint4 *>(row + 8 * kRowBytes + b * 128 + 64);
                     float d[4] = {0.f, 0.f, 0.f, 0.f};
                     // four K = 32 steps; which k a lane's bytes stand for is the same on both sides
-                    mma_e4m3(d, lo0.x, hi0.x, lo0.y, hi0.y, b0.x, b0.y);
-                    mma_e4m3(d, lo0.z, hi0.z, lo0.w, hi0.w, b0.z, b0.w);
-                    mma_e4m3(d, lo1.x, hi1.x, lo1.y, hi1.y, b1.x, b1.y);
-                    mma_e4m3(d, lo1.z, hi1.z, lo1.w, hi1.w, b1.z, b1.w);
-                    acc[j][0] = fmaf(d[0], sw0 * st[0], acc[j][0]);
-                    acc[j][1] = fmaf(d[1], sw0 * st[1], acc[j][1]);
-                    acc[j][2] = fmaf(d[2], sw1 * st[0], acc[j][2]);
-                    acc[j][3] = fmaf(d[3], sw1 * st[1], acc[j][3]);
+                    mma_e4m3(d, lo0.x, hi0.x, lo0.y, hi0.y, b0[b].x, b0[b].y);
+                    mma_e4m3(d, lo0.z, hi0.z, lo0.w, hi0.w, b0[b].z, b0[b].w);
+                    mma_e4m3(d, lo1.x, hi1.x, lo1.y, hi1.y, b1[b].x, b1[b].y);
+                    mma_e4m3(d, lo1.z, hi1.z, lo1.w, hi1.w, b1[b].z, b1[b].w);
+                    const float w0 = __shfl_sync(0xffffffffu, sw0, (k0 + b) & 31);
+                    const float w1 = FIRST ? __shfl_sync(0xffffffffu, sw1, (k0 + b) & 31) : w0;
+                    const float x0 = scale_value((st0 >> (8 * b)) & 0xFFu), x1 = scale_value((st1 >> (8 * b)) & 0xFFu);
+                    acc[j][0] = fmaf(d[0], w0 * x0, acc[j][0]);
+                    acc[j][1] = fmaf(d[1], w0 * x1, acc[j][1]);
+                    acc[j][2] = fmaf(d[2], w1 * x0, acc[j][2]);
+                    acc[j][3] = fmaf(d[3], w1 * x1, acc[j][3]);
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.empty[stage]);
-            if (++stage == kStages) {
-                stage = 0;
-                phase ^= 1u;
-            }
+            __syncwarp();                            // all lanes have read the stage
+            ++st.done;
+            st.ask(p, sm, warp, lane);
         }
-        // the warps' partial sums, added in the order of the warps
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             if (j >= groups) break;
-            float *r = red + buf * (kRedBytes / 4);
-            // [warp][row 16][token 8]
-            *reinterpret_cast<float2 *>(r + warp * 128 + g * 8 + t4 * 2) = make_float2(acc[j][0], acc[j][1]);
-            *reinterpret_cast<float2 *>(r + warp * 128 + (g + 8) * 8 + t4 * 2) = make_float2(acc[j][2], acc[j][3]);
-            consumers_sync();
-            if (threadIdx.x < 128) {
-                float s = 0.f;
 #pragma unroll
-                for (int w = 0; w < kConsWarps; ++w) s += r[w * 128 + threadIdx.x];
-                const int rr = threadIdx.x >> 3, tok = threadIdx.x & 7;
+            for (int x = 0; x < 2; ++x) {
+                const int col = j * 8 + t4 * 2 + x;
+                if (col >= T) continue;
+                const int64_t slot = sm.slot[s0 + col];
                 if (FIRST) {
-                    // rows 0..7 the gate, 8..15 the up half: through shared memory once more
-                    r[threadIdx.x] = s;
-                    named_barrier_sync(2, 128);
-                    if (threadIdx.x < 64) {
-                        const int f = threadIdx.x & 7, n = threadIdx.x >> 3;
-                        if (j * 8 + n < T) {
-                            const float gate = r[f * 8 + n], up = r[(f + 8) * 8 + n];
-                            __stcg(act + static_cast<int64_t>(sm.slot[s0 + j * 8 + n]) * a.I + i * 8 + f,
-                                   gate / (1.f + __expf(-gate)) * up);
-                        }
-                    }
+                    const float gate = acc[j][x], up = acc[j][2 + x];
+                    __stcg(act + slot * a.I + i * 8 + g, gate / (1.f + __expf(-gate)) * up);
                 } else {
-                    if (j * 8 + tok < T)
-                        __stcg(y + static_cast<int64_t>(sm.slot[s0 + j * 8 + tok]) * a.H + i * 16 + rr, s);
+                    __stcg(y + slot * a.H + i * 16 + g, acc[j][x]);
+                    __stcg(y + slot * a.H + i * 16 + 8 + g, acc[j][2 + x]);
                 }
             }
-            buf ^= 1;
         }
         if (FIRST) {
-            ++in_block;
-            if ((i & 15) == 15 || u + 1 == to) {
-                // the end of what this CTA does of a 128-block of the activation: whoever completes its
-                // sixteen units turns it into E4M3
+            // Whoever completes the sixteen units of a 128-block of the activation turns it into E4M3.  The
+            // units that this CTA has of it are counted here, CTAs that share one meet in the workspace.
+            const int b0 = u & ~15, b1 = b0 + 16;    // (an expert's units are whole blocks)
+            const int ours = (b1 < to ? b1 : to) - (b0 > from ? b0 : from);
+            const int at = (u >> 4) - (from >> 4);
+            const bool count_here = ((to - 1) >> 4) - (from >> 4) < kMostBlocks;
+            int last = 0;
+            __threadfence_block();
+            __syncwarp();
+            if (lane == 0) {
+                const int n = count_here ? ours : 1;
+                last = !count_here || atomicAdd(&sm.done[at], 1) == ours - 1;
+                if (last && n != 16) {
+                    unsigned *counter = reinterpret_cast<unsigned *>(ws + p.l.counters) + (u >> 4);
+                    __threadfence();
+                    last = atomicAdd(counter, n) + n == 16;
+                    if (last) *counter = 0;
+                    __threadfence();
+                }
+                __threadfence_block();
+            }
+            __syncwarp();
+            if (__shfl_sync(0xffffffffu, last, 0)) {
                 const int b = i >> 4;
-                bool last = in_block == 16;
-                consumers_sync();
-                if (!last) {
-                    if (threadIdx.x == 0) {
-                        __threadfence();
-                        const unsigned before = atomicAdd(&counters[ai * (a.I / 128) + b], in_block);
-                        sm.last = before + in_block == 16;
-                        if (sm.last) counters[ai * (a.I / 128) + b] = 0;
-                        __threadfence();
-                    }
-                    consumers_sync();
-                    last = sm.last;
+                for (int n = 0; n < T; ++n) {
+                    const int64_t slot = sm.slot[s0 + n];
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(act + slot * a.I + b * 128) + lane);
+                    const float f[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t byte;
+                    const uint32_t q = quant_warp_block(f, byte);
+                    __stcg(reinterpret_cast<uint32_t *>(ws + p.l.a8 + slot * a.I + b * 128) + lane, q);
+                    if (lane == 0) ws[p.l.as + slot * scale_stride(a.I) + b] = static_cast<uint8_t>(byte);
                 }
-                if (last) {
-                    for (int n = warp; n < T; n += kConsWarps) {
-                        const int64_t s = sm.slot[s0 + n];
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(act + s * a.I + b * 128) + lane);
-                        const float f[4] = {v.x, v.y, v.z, v.w};
-                        uint32_t byte;
-                        const uint32_t q = quant_warp_block(f, byte);
-                        __stcg(reinterpret_cast<uint32_t *>(ws + p.l.a8 + s * a.I + b * 128) + lane, q);
-                        if (lane == 0) ws[p.l.as + s * (a.I / 128) + b] = static_cast<uint8_t>(byte);
-                    }
-                }
-                in_block = 0;
             }
         }
     }
@@ -507,7 +560,7 @@ __device__ void combine(const Params &p)
     const float *y = reinterpret_cast<const float *>(static_cast<const uint8_t *>(a.workspace) + p.l.y);
     const int quads = a.H / 4;
     const int total = a.N * quads;
-    for (int i = blockIdx.x * kConsumers + threadIdx.x; i < total; i += gridDim.x * kConsumers) {
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < total; i += gridDim.x * kThreads) {
         const int n = i / quads, h = (i - n * quads) * 4;
         float s[4] = {0.f, 0.f, 0.f, 0.f};
         for (int k = 0; k < a.K; ++k) {
@@ -531,87 +584,52 @@ __device__ void combine(const Params &p)
     }
 }
 
-// The stream of this CTA's units of one product; `g` counts the stages issued.
-template <bool FIRST>
-__device__ bool stream_units(const Params &p, Smem &sm, uint8_t *ring, uint32_t &g)
-{
-    const LayerArgs &a = p.a;
-    const int lane = threadIdx.x & 31;
-    const int red_len = FIRST ? a.H : a.I, per = FIRST ? a.I / 8 : a.H / 16;
-    int from, to;
-    my_units(sm.active * per, from, to);
-    for (int u = from; u < to; ++u) {
-        const int ai = u / per, i = u - ai * per;
-        const int64_t e = sm.expert[ai];
-        // lane r < 16: row r of the unit
-        const uint8_t *row;
-        if (FIRST)
-            row = static_cast<const uint8_t *>(a.W1) + (e * 2 * a.I + (lane & 8 ? a.I : 0) + i * 8 + (lane & 7)) * a.H;
-        else
-            row = static_cast<const uint8_t *>(a.W2) + (e * a.H + i * 16 + (lane & 15)) * a.I;
-        for (int k = 0; k < red_len; k += kWide) {
-            const int width = red_len - k < kWide ? red_len - k : kWide;
-            const uint32_t s = g % kStages, ph = (g / kStages) & 1u;
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&sm.empty[s], ph ^ 1u, &sm.abort))) return false;
-            if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], 16 * width);
-            __syncwarp();
-            if (lane < 16) bulk_load(ring + s * kStageBytes + lane * kRowBytes, row + k, width, &sm.full[s]);
-            ++g;
-        }
-    }
-    return true;
-}
-
 __global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const Params p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *red = reinterpret_cast<float *>(ring + kStages * kStageBytes);
-    Smem &sm = *reinterpret_cast<Smem *>(ring + kStages * kStageBytes + 2 * kRedBytes);
+    Smem &sm = *reinterpret_cast<Smem *>(ring + kRingBytes);
     Header *hdr = static_cast<Header *>(p.a.workspace);
-    const int warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sm.full[s], 1);
-            mbar_init(&sm.empty[s], kConsWarps);
-        }
+        for (int i = 0; i < kStreams * kStages; ++i) mbar_init(&sm.full[0][0] + i, 1);
         sm.abort = 0;
         fence_mbarrier_init();
     }
+    for (int i = threadIdx.x; i < kMostBlocks; i += kThreads) sm.done[i] = 0;
     __syncthreads();
 
-    if (warp < kConsWarps) {
-        float *scratch = reinterpret_cast<float *>(ring);   // the ring is not in use yet
-        partial_logits(p, scratch);
-        quantise_x(p);
-        grid_barrier(hdr, 0, sm);
-        for (int n = blockIdx.x; n < p.a.N; n += gridDim.x) {
-            consumers_sync();
-            select(p, n, sm, scratch);
-        }
-        grid_barrier(hdr, 1, sm);
-        make_lists(p, sm);
-        fence_proxy_async_smem();   // the ring's memory passes from these threads to the copies
-        __syncthreads();            // with the streaming warp: the lists stand
-        uint32_t stage = 0, phase = 0;
-        product<true>(p, sm, ring, red, stage, phase);
-        grid_barrier(hdr, 2, sm);
-        product<false>(p, sm, ring, red, stage, phase);
-        grid_barrier(hdr, 3, sm);
-        combine(p);
-    } else {
+    float *scratch = reinterpret_cast<float *>(ring);   // the ring is not in use yet
+    partial_logits(p, scratch);
+    quantise_x(p);
+    grid_barrier(hdr, 0, sm);
+    for (int n = blockIdx.x; n < p.a.N; n += gridDim.x) {
         __syncthreads();
-        uint32_t g = 0;
-        if (*const_cast<volatile int *>(&sm.abort) == 0) {
-            if (stream_units<true>(p, sm, ring, g)) stream_units<false>(p, sm, ring, g);
-        }
-        if (*const_cast<volatile int *>(&sm.abort) != 0) {
-            // let the copies in flight land before the CTA ends
-            for (uint32_t x = g > kStages ? g - kStages : 0u; x < g; ++x) {
-                volatile int no_abort = 0;
-                mbar_wait_bounded(&sm.full[x % kStages], (x / kStages) & 1u, &no_abort);
-            }
+        select(p, n, sm, scratch);
+    }
+    grid_barrier(hdr, 1, sm);
+    fence_proxy_async_smem();   // the ring's memory passes from these threads to the copies
+    make_lists(p, sm);
+    Stream st;
+    st.asked = st.done = 0;
+    if (warp < kStreams) {
+        st.ring = ring + warp * kStages * kStageBytes;
+        st.full = sm.full[warp];
+        st.ahead.product = 0;
+        st.ahead.enter(p, sm, warp);
+        for (int i = 0; i < kStages; ++i) st.ask(p, sm, warp, lane);
+        product<true>(p, sm, st);
+    }
+    grid_barrier(hdr, 2, sm);
+    if (warp < kStreams) product<false>(p, sm, st);
+    grid_barrier(hdr, 3, sm);
+    combine(p);
+    if (*const_cast<volatile int *>(&sm.abort) != 0 && warp < kStreams) {
+        // let the copies in flight land before the CTA ends
+        for (uint32_t x = st.asked > kStages ? st.asked - kStages : 0u; x < st.asked; ++x) {
+            volatile int no_abort = 0;
+            mbar_wait_bounded(st.full + x % kStages, (x / kStages) & 1u, &no_abort);
         }
     }
     __syncthreads();
