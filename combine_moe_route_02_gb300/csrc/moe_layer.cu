@@ -9,8 +9,8 @@
 // once; everything else is arranged around that stream.  One CTA per SM.  A unit of
 // work is 16 weight rows of one expert (8 gate and 8 up rows of W1, or 16 rows of
 // W2); the units of all touched experts are split evenly and in order over the CTAs,
-// and a CTA's over its eight streaming warps.  Each of those is on its own: it copies
-// its units in pieces of 16 rows x 512 bytes to a ring of three in shared memory (bulk
+// and a CTA's over its sixteen warps.  Each of those is on its own: it copies its
+// units in pieces of 16 rows x 256 bytes to a ring of three in shared memory (bulk
 // copies, W1's and then W2's without a pause between: they need only the routing, so
 // that W2 is in flight while the CTAs wait for each other between the products),
 // multiplies a piece by the tokens of its expert (mma.sync, 16 rows x 8 tokens x 32:
@@ -30,13 +30,22 @@ namespace {
 constexpr int kMaxN = 64, kMaxE = 256, kMaxK = 16;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kStreams = 8;                   // streaming warps
-constexpr int kWide = 512;                    // reduction bytes of a row in one ring stage: four 128-blocks
-constexpr int kRowBytes = kWide + 64;         // 64: eight rows at one offset meet different banks
+constexpr int kStreams = 16;                  // streaming warps
+constexpr int kWide = 256;                    // reduction bytes of a row in one ring stage: two 128-blocks
+constexpr int kPieceBlocks = kWide / 128;
 constexpr int kStages = 3;                    // of each streaming warp
-constexpr int kStageBytes = 16 * kRowBytes;
+// Rows in pairs, the second 64 bytes further on than it would be: eight lanes read two rows' 64 bytes at a
+// time, and meet different banks.
+constexpr int kPairBytes = 2 * kWide + 64;
+constexpr int kStageBytes = 8 * kPairBytes;
+__device__ __forceinline__ int row_at(int r) { return (r >> 1) * kPairBytes + (r & 1) * (kWide + 64); }
 constexpr int kRingBytes = kStreams * kStages * kStageBytes;
 constexpr int kMostBlocks = 256;              // 128-blocks of the activation that a CTA counts for itself
+// An expert's tokens are taken 16 at a time, each lot as an entry of its own: one with more reads the
+// expert's weights again, from L2.
+constexpr int kLot = 16;
+constexpr int kMostLots = kMaxE + kMaxN * kMaxK / kLot;
+constexpr int kRedundant = 2;                 // up to this many tokens every CTA finds their top-K itself
 
 struct Header {                               // zero before the first call, left zero by every call
     unsigned barrier[4], done, aborted;
@@ -45,10 +54,11 @@ struct Header {                               // zero before the first call, lef
 struct Smem {
     uint64_t full[kStreams][kStages];
     int abort;
-    int active;                               // touched experts
+    int active;                               // lots of all touched experts
     uint32_t mask[kMaxE][2];                  // tokens of each expert
-    int16_t expert[kMaxE];                    // the touched ones, ascending
-    int16_t first[kMaxE + 1];                 // where each touched expert's slots start
+    int16_t expert[kMostLots];                // of each lot, ascending
+    int16_t first[kMostLots + 1];             // where its slots start
+    int16_t idx[kRedundant * kMaxK];          // the top-K ids where every CTA has found them
     int16_t slot[kMaxN * kMaxK];              // slots n * K + k by expert, then token
     int16_t token[kMaxN * kMaxK];             // their n
     float logit[kMaxE];
@@ -66,15 +76,15 @@ __host__ __device__ inline size_t up256(size_t v) { return (v + 255) & ~size_t(2
 // Rows of a slice of W_gate: at most 128 slices.
 __host__ __device__ inline int slice_rows(int H) { return (((H + 127) / 128) + 7) & ~7; }
 
-// Bytes of a row's scales in the workspace: whole words, one for each ring stage.
-__host__ __device__ inline int scale_stride(int n) { return ((n / 128) + 3) & ~3; }
+// Bytes of a row's scales in the workspace: whole pairs, one for each ring stage.
+__host__ __device__ inline int scale_stride(int n) { return ((n / 128) + 1) & ~1; }
 
 Layout make_layout(int N, int H, int I, int E, int K)
 {
     const size_t S = (H + slice_rows(H) - 1) / slice_rows(H), slots = static_cast<size_t>(N) * K;
     Layout l;
     l.counters = 256;
-    l.x8 = up256(l.counters + static_cast<size_t>(E) * (I / 128) * 4);
+    l.x8 = up256(l.counters + static_cast<size_t>(E + kMaxN * kMaxK / kLot) * (I / 128) * 4);
     l.xs = up256(l.x8 + static_cast<size_t>(N) * H);
     l.part = up256(l.xs + static_cast<size_t>(N) * scale_stride(H));
     l.a = up256(l.part + S * N * E * 4);
@@ -123,8 +133,7 @@ __device__ void grid_barrier(Header *h, int which, Smem &sm)
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -147,6 +156,7 @@ __device__ void partial_logits(const Params &p, float *xs)
 {
     const int H = p.a.H, E = p.a.E, N = p.a.N, t = threadIdx.x;
     const int hc = slice_rows(H);
+    const int hx = (hc + 15) & ~15;              // of x in shared memory: whole sixteens
     const int slices = (H + hc - 1) / hc;
     float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(p.a.workspace) + p.l.part);
     const int Er = (E + 31) & ~31, groups = kThreads / Er;
@@ -154,35 +164,35 @@ __device__ void partial_logits(const Params &p, float *xs)
     for (int s = blockIdx.x; s < slices; s += gridDim.x) {
         const int from = s * hc, rows = H - from < hc ? H - from : hc;   // a multiple of 8
         __syncthreads();
-        for (int i = t; i < N * rows; i += kThreads) {
-            const int n = i / rows, h = i - n * rows;
-            xs[n * hc + h] = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.a.X)[static_cast<int64_t>(n) * H + from + h]);
+        for (int i = t; i < N * hx; i += kThreads) {
+            const int n = i / hx, h = i - n * hx;
+            xs[i] = h < rows ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.a.X)[static_cast<int64_t>(n) * H + from + h])
+                             : 0.f;
         }
         __syncthreads();
         if (e >= E || tg >= groups) continue;
         float acc[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-        for (int h = 0; h < rows; h += 8) {
-            float w[8];
+        for (int h = 0; h < rows; h += 16) {
+            // (rows come in eights: those that are not there read the last one, against zeros of x)
+            float w[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                w[i] = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.a.W_gate)[static_cast<int64_t>(from + h + i) * E + e]);
+            for (int i = 0; i < 16; ++i)
+                w[i] = __bfloat162float(
+                    static_cast<const __nv_bfloat16 *>(p.a.W_gate)[static_cast<int64_t>(from + (h + i < rows ? h + i : rows - 1)) * E + e]);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
                 const int n = tg + i * groups;
                 if (n >= N) break;
-                const float4 x0 = *reinterpret_cast<const float4 *>(xs + n * hc + h);
-                const float4 x1 = *reinterpret_cast<const float4 *>(xs + n * hc + h + 4);
-                float v = acc[i];
-                v = fmaf(x0.x, w[0], v);
-                v = fmaf(x0.y, w[1], v);
-                v = fmaf(x0.z, w[2], v);
-                v = fmaf(x0.w, w[3], v);
-                v = fmaf(x1.x, w[4], v);
-                v = fmaf(x1.y, w[5], v);
-                v = fmaf(x1.z, w[6], v);
-                acc[i] = fmaf(x1.w, w[7], v);
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(xs + n * hx + h + j);
+                    acc[i] = fmaf(x.x, w[j], acc[i]);
+                    acc[i] = fmaf(x.y, w[j + 1], acc[i]);
+                    acc[i] = fmaf(x.z, w[j + 2], acc[i]);
+                    acc[i] = fmaf(x.w, w[j + 3], acc[i]);
+                }
             }
         }
 #pragma unroll
@@ -224,9 +234,19 @@ __device__ void select(const Params &p, int n, Smem &sm, float *scratch)
     const int Er = (E + 31) & ~31, groups = kThreads / Er;
     const int e = t % Er, tg = t / Er;
     if (e < E && tg < groups) {
+        // sixteen loads in flight, added in order
         float s = 0.f;
-#pragma unroll 8
-        for (int i = tg; i < slices; i += groups) s += __ldcg(part + (static_cast<int64_t>(i) * N + n) * E + e);
+        const float *src = part + static_cast<int64_t>(n) * E + e;
+        for (int i = tg; i < slices; i += 16 * groups) {
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int at = i + j * groups;
+                v[j] = __ldcg(src + static_cast<int64_t>(at < slices ? at : slices - 1) * N * E);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s += i + j * groups < slices ? v[j] : 0.f;
+        }
         scratch[tg * Er + e] = s;
     }
     __syncthreads();
@@ -282,8 +302,11 @@ __device__ void select(const Params &p, int n, Smem &sm, float *scratch)
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
         if (lane < K) {
-            p.a.topk_idx[n * K + lane] = my_i;
-            p.a.topk_w[n * K + lane] = my_p / sum;
+            if (N <= kRedundant) sm.idx[n * K + lane] = static_cast<int16_t>(my_i);
+            if (N > kRedundant || blockIdx.x == 0) {
+                p.a.topk_idx[n * K + lane] = my_i;
+                p.a.topk_w[n * K + lane] = my_p / sum;
+            }
         }
     }
 }
@@ -298,7 +321,7 @@ __device__ void make_lists(const Params &p, Smem &sm)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int s = t + i * kThreads;
-        e[i] = s < slots ? __ldcg(p.a.topk_idx + s) : -1;
+        e[i] = s >= slots ? -1 : p.a.N <= kRedundant ? sm.idx[s] : __ldcg(p.a.topk_idx + s);
         if (e[i] < 0 || e[i] >= E) {
             e[i] = -1;   // (ids that are not there: only after a barrier that gave up)
             continue;
@@ -312,21 +335,22 @@ __device__ void make_lists(const Params &p, Smem &sm)
         for (int b = 0; b < E; b += 32) {
             const int x = b + lane;
             const int c = x < E ? __popc(sm.mask[x][0]) + __popc(sm.mask[x][1]) : 0;
-            const uint32_t some = __ballot_sync(0xffffffffu, c > 0);
-            int sum = c;
+            const int lots = (c + kLot - 1) / kLot;
+            int sum = c | lots << 16;               // both scans in one
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, sum, o);
                 if (lane >= o) sum += y;
             }
-            if (c > 0) {
-                const int at = active + __popc(some & ((1u << lane) - 1u));
-                sm.expert[at] = static_cast<int16_t>(x);
-                sm.first[at] = static_cast<int16_t>(before + sum - c);
+            const int start = before + (sum & 0xFFFF) - c, at = active + (sum >> 16) - lots;
+            for (int i = 0; i < lots; ++i) {
+                sm.expert[at + i] = static_cast<int16_t>(x);
+                sm.first[at + i] = static_cast<int16_t>(start + i * kLot);
             }
-            if (x < E) sm.logit[x] = __int_as_float(before + sum - c);   // where this expert's slots start
-            active += __popc(some);
-            before += __shfl_sync(0xffffffffu, sum, 31);
+            if (x < E) sm.logit[x] = __int_as_float(start);   // where this expert's slots start
+            sum = __shfl_sync(0xffffffffu, sum, 31);
+            active += sum >> 16;
+            before += sum & 0xFFFF;
         }
         if (lane == 0) {
             sm.active = active;
@@ -352,174 +376,228 @@ __device__ void make_lists(const Params &p, Smem &sm)
 // The products.  FIRST: units of 8 gate + 8 up rows of W1, tokens from x8; else 16
 // rows of W2, slots from a8.
 // ---------------------------------------------------------------------------
-// A streaming warp's walk over the pieces of its units, first W1's, then W2's.
-struct Pieces {
-    int product, u, to, k;        // (product 2: the end)
+// A streaming warp's walk over its units, u0, u0 + kStreams, ... of the CTA's: the lot of each and its place
+// in the lot.
+struct Units {
+    int u, to, lot, i;
 
-    __device__ __forceinline__ void enter(const Params &p, const Smem &sm, int warp)
+    __device__ __forceinline__ void start(int active, int per, int warp)
     {
-        for (; product < 2; ++product) {
-            int from;
-            my_units(sm.active * (product == 0 ? p.a.I / 8 : p.a.H / 16), from, to);
-            u = from + warp;
-            k = 0;
-            if (u < to) break;
-        }
+        my_units(active * per, u, to);
+        u += warp;
+        lot = u / per;
+        i = u - lot * per;
     }
-    __device__ __forceinline__ void next(const Params &p, const Smem &sm, int warp)
+    __device__ __forceinline__ void next(int per)
     {
-        k += kWide;
-        if (k < (product == 0 ? p.a.H : p.a.I)) return;
-        k = 0;
         u += kStreams;
-        if (u < to) return;
-        ++product;
-        enter(p, sm, warp);
-    }
-    // Asks for the piece: lane r < 16 its row r.
-    __device__ __forceinline__ void copy(const Params &p, const Smem &sm, uint8_t *stage, uint64_t *full, int lane) const
-    {
-        const LayerArgs &a = p.a;
-        const int red = product == 0 ? a.H : a.I, per = product == 0 ? a.I / 8 : a.H / 16;
-        const int ai = u / per, i = u - ai * per;
-        const int64_t e = sm.expert[ai];
-        const int width = red - k < kWide ? red - k : kWide;
-        if (lane == 0) mbar_arrive_expect_tx(full, 16 * width);
-        __syncwarp();
-        if (lane < 16) {
-            const uint8_t *row =
-                product == 0 ? static_cast<const uint8_t *>(a.W1) + (e * 2 * a.I + (lane & 8 ? a.I : 0) + i * 8 + (lane & 7)) * a.H
-                             : static_cast<const uint8_t *>(a.W2) + (e * a.H + i * 16 + lane) * a.I;
-            bulk_load(stage + lane * kRowBytes, row + k, width, full);
+        i += kStreams;
+        while (i >= per) {
+            i -= per;
+            ++lot;
         }
     }
 };
 
+// What the warp asks for next: first W1's pieces, then W2's.  Lane r < 16 copies row r of a piece.
 struct Stream {
     uint8_t *ring;
     uint64_t *full;
-    Pieces ahead;                 // the next piece to ask for
     uint32_t asked, done;
+    int product, k, red, per;
+    Units unit;
+    const uint8_t *row;
 
+    __device__ __forceinline__ void enter(const Params &p, const Smem &sm, int warp, int lane)
+    {
+        for (; product < 2; ++product) {
+            red = product == 0 ? p.a.H : p.a.I;
+            per = product == 0 ? p.a.I / 8 : p.a.H / 16;
+            unit.start(sm.active, per, warp);
+            if (unit.u < unit.to) break;
+        }
+        k = 0;
+        if (product < 2) find_row(p, sm, lane);
+    }
+    __device__ __forceinline__ void find_row(const Params &p, const Smem &sm, int lane)
+    {
+        const int64_t e = sm.expert[unit.lot];
+        row = product == 0 ? static_cast<const uint8_t *>(p.a.W1) +
+                                 (e * 2 * p.a.I + (lane & 8 ? p.a.I : 0) + unit.i * 8 + (lane & 7)) * p.a.H
+                           : static_cast<const uint8_t *>(p.a.W2) + (e * p.a.H + unit.i * 16 + (lane & 15)) * p.a.I;
+    }
     __device__ __forceinline__ void ask(const Params &p, const Smem &sm, int warp, int lane)
     {
-        if (ahead.product == 2) return;
+        if (product == 2) return;
         const uint32_t s = asked % kStages;
-        ahead.copy(p, sm, ring + s * kStageBytes, full + s, lane);
-        ahead.next(p, sm, warp);
+        const int width = red - k < kWide ? red - k : kWide;
+        if (lane == 0) mbar_arrive_expect_tx(full + s, 16 * width);
+        __syncwarp();
+        if (lane < 16) bulk_load(ring + s * kStageBytes + row_at(lane), row + k, width, full + s);
         ++asked;
+        k += kWide;
+        if (k < red) return;
+        k = 0;
+        unit.next(per);
+        if (unit.u < unit.to) {
+            find_row(p, sm, lane);
+        } else {
+            ++product;
+            enter(p, sm, warp, lane);
+        }
     }
 };
 
+// Eight tokens' side of a piece: a lane's bytes of one of them, the scales of the two whose sums it holds.
+struct Tokens {
+    uint4 b0[kPieceBlocks], b1[kPieceBlocks];
+    uint32_t s0, s1;
+
+    __device__ __forceinline__ void load(const uint8_t *src, const uint8_t *sc0, const uint8_t *sc1, int k0, int nb)
+    {
+#pragma unroll
+        for (int b = 0; b < kPieceBlocks; ++b) {
+            b0[b] = b1[b] = make_uint4(0, 0, 0, 0);
+            if (src && b < nb) {
+                b0[b] = *reinterpret_cast<const uint4 *>(src + (k0 + b) * 128);
+                b1[b] = *reinterpret_cast<const uint4 *>(src + (k0 + b) * 128 + 64);
+            }
+        }
+        s0 = sc0 ? *reinterpret_cast<const uint16_t *>(sc0 + k0) : 0u;
+        s1 = sc1 ? *reinterpret_cast<const uint16_t *>(sc1 + k0) : 0u;
+    }
+};
+
+template <bool FIRST, int GROUPS>
+__device__ __forceinline__ void unit_sums(const LayerArgs &a, Smem &sm, Stream &st, const Params &p, int warp, int lane,
+                                          const uint8_t *src, const uint8_t *src_scale, int lot, int T, int64_t sc0,
+                                          int64_t sc1, bool &bad, float (&acc)[GROUPS][4])
+{
+    const int red = FIRST ? a.H : a.I, rblocks = red / 128, stride = scale_stride(red);
+    const int g = lane >> 2, t4 = lane & 3;
+    const void *W_scale = FIRST ? a.W1_scale : a.W2_scale;
+    const int16_t *who = (FIRST ? sm.token : sm.slot) + sm.first[lot];
+    const uint8_t *tok[GROUPS], *ts[GROUPS][2];
+#pragma unroll
+    for (int j = 0; j < GROUPS; ++j) {
+        tok[j] = j * 8 + g < T ? src + static_cast<int64_t>(who[j * 8 + g]) * red + t4 * 16 : nullptr;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int col = j * 8 + t4 * 2 + x;
+            ts[j][x] = col < T ? src_scale + who[col] * stride : nullptr;
+            acc[j][x] = acc[j][2 + x] = 0.f;
+        }
+    }
+    // the tokens' next piece is on its way while this one is worked on
+    Tokens x[GROUPS];
+#pragma unroll
+    for (int j = 0; j < GROUPS; ++j) x[j].load(tok[j], ts[j][0], ts[j][1], 0, rblocks);
+    uint32_t sw0 = 0, sw1 = 0;                       // bytes of block (32 at a time) + lane
+    const int lo_at = row_at(g) + t4 * 16, hi_at = row_at(g + 8) + t4 * 16;
+    for (int k0 = 0; k0 < rblocks; k0 += kPieceBlocks) {
+        if ((k0 & 31) == 0) {
+            const int b = k0 + lane < rblocks ? k0 + lane : rblocks - 1;
+            sw0 = load_scale_byte(W_scale, a.ue8m0, sc0 + b, bad);
+            sw1 = FIRST ? load_scale_byte(W_scale, a.ue8m0, sc1 + b, bad) : sw0;
+        }
+        const uint32_t s = st.done % kStages;
+        warp_wait(st.full + s, (st.done / kStages) & 1u, &sm.abort);
+        const uint8_t *stage = st.ring + s * kStageBytes;
+        const int nb = rblocks - k0;
+#pragma unroll
+        for (int b = 0; b < kPieceBlocks; ++b) {
+            if (b >= nb) break;
+            const uint4 lo0 = *reinterpret_cast<const uint4 *>(stage + lo_at + b * 128);
+            const uint4 lo1 = *reinterpret_cast<const uint4 *>(stage + lo_at + b * 128 + 64);
+            const uint4 hi0 = *reinterpret_cast<const uint4 *>(stage + hi_at + b * 128);
+            const uint4 hi1 = *reinterpret_cast<const uint4 *>(stage + hi_at + b * 128 + 64);
+            const float w0 = scale_value(__shfl_sync(0xffffffffu, sw0, (k0 + b) & 31));
+            const float w1 = FIRST ? scale_value(__shfl_sync(0xffffffffu, sw1, (k0 + b) & 31)) : w0;
+#pragma unroll
+            for (int j = 0; j < GROUPS; ++j) {
+                // four K = 32 steps in two chains; which k a lane's bytes stand for is the same on both sides
+                float d[4] = {0.f, 0.f, 0.f, 0.f}, f[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_e4m3(d, lo0.x, hi0.x, lo0.y, hi0.y, x[j].b0[b].x, x[j].b0[b].y);
+                mma_e4m3(f, lo1.x, hi1.x, lo1.y, hi1.y, x[j].b1[b].x, x[j].b1[b].y);
+                mma_e4m3(d, lo0.z, hi0.z, lo0.w, hi0.w, x[j].b0[b].z, x[j].b0[b].w);
+                mma_e4m3(f, lo1.z, hi1.z, lo1.w, hi1.w, x[j].b1[b].z, x[j].b1[b].w);
+                const float x0 = scale_value((x[j].s0 >> (8 * b)) & 0xFFu), x1 = scale_value((x[j].s1 >> (8 * b)) & 0xFFu);
+                acc[j][0] = fmaf(d[0] + f[0], w0 * x0, acc[j][0]);
+                acc[j][1] = fmaf(d[1] + f[1], w0 * x1, acc[j][1]);
+                acc[j][2] = fmaf(d[2] + f[2], w1 * x0, acc[j][2]);
+                acc[j][3] = fmaf(d[3] + f[3], w1 * x1, acc[j][3]);
+            }
+        }
+        __syncwarp();                                // all lanes have read the stage
+        ++st.done;
+        st.ask(p, sm, warp, lane);
+        if (k0 + kPieceBlocks < rblocks)
+#pragma unroll
+            for (int j = 0; j < GROUPS; ++j) x[j].load(tok[j], ts[j][0], ts[j][1], k0 + kPieceBlocks, nb - kPieceBlocks);
+    }
+}
+
+// A unit's sums to where they go: the activation of its 8 features, or 16 elements of y.
+template <bool FIRST, int GROUPS>
+__device__ __forceinline__ void unit_out(const LayerArgs &a, const Smem &sm, float *dst, int lot, int i, int T, int lane,
+                                         const float (&acc)[GROUPS][4])
+{
+    const int g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+    for (int j = 0; j < GROUPS; ++j) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int col = j * 8 + t4 * 2 + x;
+            if (col >= T) continue;
+            const int64_t slot = sm.slot[sm.first[lot] + col];
+            if (FIRST) {
+                const float gate = acc[j][x], up = acc[j][2 + x];
+                __stcg(dst + slot * a.I + i * 8 + g, gate / (1.f + __expf(-gate)) * up);
+            } else {
+                __stcg(dst + slot * a.H + i * 16 + g, acc[j][x]);
+                __stcg(dst + slot * a.H + i * 16 + 8 + g, acc[j][2 + x]);
+            }
+        }
+    }
+}
+
 template <bool FIRST>
-__device__ void product(const Params &p, Smem &sm, Stream &st)
+__device__ __forceinline__ void product(const Params &p, Smem &sm, Stream &st)
 {
     const LayerArgs &a = p.a;
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
-    const int red = FIRST ? a.H : a.I, rblocks = red / 128, stride = scale_stride(red);
-    const int per = FIRST ? a.I / 8 : a.H / 16;      // units of an expert
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const int rblocks = (FIRST ? a.H : a.I) / 128;
+    const int per = FIRST ? a.I / 8 : a.H / 16;      // units of a lot
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint8_t *src = ws + (FIRST ? p.l.x8 : p.l.a8), *src_scale = ws + (FIRST ? p.l.xs : p.l.as);
-    const void *W_scale = FIRST ? a.W1_scale : a.W2_scale;
     float *act = reinterpret_cast<float *>(ws + p.l.a);
-    float *y = reinterpret_cast<float *>(ws + p.l.y);
+    float *dst = FIRST ? act : reinterpret_cast<float *>(ws + p.l.y);
     int from, to;
     my_units(sm.active * per, from, to);
     bool bad = false;
-    for (int u = from + warp; u < to; u += kStreams) {
-        const int ai = u / per, i = u - ai * per, e = sm.expert[ai];
-        const int s0 = sm.first[ai], T = sm.first[ai + 1] - s0, groups = (T + 7) >> 3;
-        const int16_t *who = (FIRST ? sm.token : sm.slot) + s0;
+    Units un;
+    un.start(sm.active, per, warp);
+    for (; un.u < to; un.next(per)) {
+        const int lot = un.lot, i = un.i, e = sm.expert[lot], T = sm.first[lot + 1] - sm.first[lot];
         // where the scales of the unit's rows start; gate and up rows lie in different blocks
         const int64_t sc0 = FIRST ? (static_cast<int64_t>(e) * (2 * a.I / 128) + i / 16) * rblocks
                                   : (static_cast<int64_t>(e) * (a.H / 128) + i / 8) * rblocks;
         const int64_t sc1 = FIRST ? sc0 + static_cast<int64_t>(a.I / 128) * rblocks : sc0;
-        float acc[8][4];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) acc[j][x] = 0.f;
-        float sw0 = 0.f, sw1 = 0.f;                  // of block (32 at a time) + lane
-        for (int k0 = 0; k0 < rblocks; k0 += kWide / 128) {
-            if ((k0 & 31) == 0) {
-                const int b = k0 + lane < rblocks ? k0 + lane : rblocks - 1;
-                sw0 = scale_value(load_scale_byte(W_scale, a.ue8m0, sc0 + b, bad));
-                sw1 = FIRST ? scale_value(load_scale_byte(W_scale, a.ue8m0, sc1 + b, bad)) : sw0;
-            }
-            const uint32_t s = st.done % kStages;
-            warp_wait(st.full + s, (st.done / kStages) & 1u, &sm.abort);
-            const uint8_t *row = st.ring + s * kStageBytes + g * kRowBytes + t4 * 16;
-            const int nb = rblocks - k0 < 4 ? rblocks - k0 : 4;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (j >= groups) break;
-                // the tokens' side: eight of them, one a lane group; the scales of the two whose sums this
-                // lane holds
-                const bool mine = j * 8 + g < T;
-                const uint8_t *tok = src + static_cast<int64_t>(mine ? who[j * 8 + g] : who[0]) * red + k0 * 128 + t4 * 16;
-                uint4 b0[4], b1[4];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    b0[b] = b1[b] = make_uint4(0, 0, 0, 0);
-                    if (mine && b < nb) {
-                        b0[b] = *reinterpret_cast<const uint4 *>(tok + b * 128);
-                        b1[b] = *reinterpret_cast<const uint4 *>(tok + b * 128 + 64);
-                    }
-                }
-                uint32_t st0 = 0, st1 = 0;
-                if (j * 8 + t4 * 2 < T)
-                    st0 = *reinterpret_cast<const uint32_t *>(src_scale + who[j * 8 + t4 * 2] * stride + k0);
-                if (j * 8 + t4 * 2 + 1 < T)
-                    st1 = *reinterpret_cast<const uint32_t *>(src_scale + who[j * 8 + t4 * 2 + 1] * stride + k0);
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (b >= nb) break;
-                    const uint4 lo0 = *reinterpret_cast<const uint4 *>(row + b * 128);
-                    const uint4 lo1 = *reinterpret_cast<const uint4 *>(row + b * 128 + 64);
-                    const uint4 hi0 = *reinterpret_cast<const uint4 *>(row + 8 * kRowBytes + b * 128);
-                    const uint4 hi1 = *reinterpret_cast<const uint4 *>(row + 8 * kRowBytes + b * 128 + 64);
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    // four K = 32 steps; which k a lane's bytes stand for is the same on both sides
-                    mma_e4m3(d, lo0.x, hi0.x, lo0.y, hi0.y, b0[b].x, b0[b].y);
-                    mma_e4m3(d, lo0.z, hi0.z, lo0.w, hi0.w, b0[b].z, b0[b].w);
-                    mma_e4m3(d, lo1.x, hi1.x, lo1.y, hi1.y, b1[b].x, b1[b].y);
-                    mma_e4m3(d, lo1.z, hi1.z, lo1.w, hi1.w, b1[b].z, b1[b].w);
-                    const float w0 = __shfl_sync(0xffffffffu, sw0, (k0 + b) & 31);
-                    const float w1 = FIRST ? __shfl_sync(0xffffffffu, sw1, (k0 + b) & 31) : w0;
-                    const float x0 = scale_value((st0 >> (8 * b)) & 0xFFu), x1 = scale_value((st1 >> (8 * b)) & 0xFFu);
-                    acc[j][0] = fmaf(d[0], w0 * x0, acc[j][0]);
-                    acc[j][1] = fmaf(d[1], w0 * x1, acc[j][1]);
-                    acc[j][2] = fmaf(d[2], w1 * x0, acc[j][2]);
-                    acc[j][3] = fmaf(d[3], w1 * x1, acc[j][3]);
-                }
-            }
-            __syncwarp();                            // all lanes have read the stage
-            ++st.done;
-            st.ask(p, sm, warp, lane);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j >= groups) break;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int col = j * 8 + t4 * 2 + x;
-                if (col >= T) continue;
-                const int64_t slot = sm.slot[s0 + col];
-                if (FIRST) {
-                    const float gate = acc[j][x], up = acc[j][2 + x];
-                    __stcg(act + slot * a.I + i * 8 + g, gate / (1.f + __expf(-gate)) * up);
-                } else {
-                    __stcg(y + slot * a.H + i * 16 + g, acc[j][x]);
-                    __stcg(y + slot * a.H + i * 16 + 8 + g, acc[j][2 + x]);
-                }
-            }
+        if (T <= 8) {
+            float acc[1][4];
+            unit_sums<FIRST, 1>(a, sm, st, p, warp, lane, src, src_scale, lot, T, sc0, sc1, bad, acc);
+            unit_out<FIRST, 1>(a, sm, dst, lot, i, T, lane, acc);
+        } else {
+            float acc[2][4];
+            unit_sums<FIRST, 2>(a, sm, st, p, warp, lane, src, src_scale, lot, T, sc0, sc1, bad, acc);
+            unit_out<FIRST, 2>(a, sm, dst, lot, i, T, lane, acc);
         }
         if (FIRST) {
             // Whoever completes the sixteen units of a 128-block of the activation turns it into E4M3.  The
             // units that this CTA has of it are counted here, CTAs that share one meet in the workspace.
-            const int b0 = u & ~15, b1 = b0 + 16;    // (an expert's units are whole blocks)
+            const int b0 = un.u & ~15, b1 = b0 + 16;   // (a lot's units are whole blocks)
             const int ours = (b1 < to ? b1 : to) - (b0 > from ? b0 : from);
-            const int at = (u >> 4) - (from >> 4);
+            const int at = (un.u >> 4) - (from >> 4);
             const bool count_here = ((to - 1) >> 4) - (from >> 4) < kMostBlocks;
             int last = 0;
             __threadfence_block();
@@ -528,7 +606,7 @@ __device__ void product(const Params &p, Smem &sm, Stream &st)
                 const int n = count_here ? ours : 1;
                 last = !count_here || atomicAdd(&sm.done[at], 1) == ours - 1;
                 if (last && n != 16) {
-                    unsigned *counter = reinterpret_cast<unsigned *>(ws + p.l.counters) + (u >> 4);
+                    unsigned *counter = reinterpret_cast<unsigned *>(ws + p.l.counters) + (un.u >> 4);
                     __threadfence();
                     last = atomicAdd(counter, n) + n == 16;
                     if (last) *counter = 0;
@@ -540,7 +618,7 @@ __device__ void product(const Params &p, Smem &sm, Stream &st)
             if (__shfl_sync(0xffffffffu, last, 0)) {
                 const int b = i >> 4;
                 for (int n = 0; n < T; ++n) {
-                    const int64_t slot = sm.slot[s0 + n];
+                    const int64_t slot = sm.slot[sm.first[lot] + n];
                     const float4 v = __ldcg(reinterpret_cast<const float4 *>(act + slot * a.I + b * 128) + lane);
                     const float f[4] = {v.x, v.y, v.z, v.w};
                     uint32_t byte;
@@ -604,11 +682,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const Params p)
     partial_logits(p, scratch);
     quantise_x(p);
     grid_barrier(hdr, 0, sm);
-    for (int n = blockIdx.x; n < p.a.N; n += gridDim.x) {
+    // (with few tokens every CTA does what one would, and no barrier is needed behind it)
+    const bool redundant = p.a.N <= kRedundant;
+    for (int n = redundant ? 0 : blockIdx.x; n < p.a.N; n += redundant ? 1 : gridDim.x) {
         __syncthreads();
         select(p, n, sm, scratch);
     }
-    grid_barrier(hdr, 1, sm);
+    if (redundant)
+        __syncthreads();
+    else
+        grid_barrier(hdr, 1, sm);
     fence_proxy_async_smem();   // the ring's memory passes from these threads to the copies
     make_lists(p, sm);
     Stream st;
@@ -616,8 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const Params p)
     if (warp < kStreams) {
         st.ring = ring + warp * kStages * kStageBytes;
         st.full = sm.full[warp];
-        st.ahead.product = 0;
-        st.ahead.enter(p, sm, warp);
+        st.product = 0;
+        st.enter(p, sm, warp, lane);
         for (int i = 0; i < kStages; ++i) st.ask(p, sm, warp, lane);
         product<true>(p, sm, st);
     }
@@ -641,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const Params p)
             __threadfence();
             if (atomicExch(&hdr->aborted, 0u)) {
                 unsigned *counters = reinterpret_cast<unsigned *>(static_cast<uint8_t *>(p.a.workspace) + p.l.counters);
-                for (int i = 0; i < p.a.E * (p.a.I / 128); ++i) counters[i] = 0;
+                for (int i = 0; i < (p.a.E + kMaxN * kMaxK / kLot) * (p.a.I / 128); ++i) counters[i] = 0;
             }
             for (int i = 0; i < 4; ++i) hdr->barrier[i] = 0;
             hdr->done = 0;
