@@ -10,7 +10,7 @@
 // work is 16 weight rows of one expert (8 gate and 8 up rows of W1, or 16 rows of
 // W2); the units of all touched experts are split evenly and in order over the CTAs,
 // and a CTA's over its sixteen warps.  Each of those is on its own: it copies its
-// units in pieces of 16 rows x 256 bytes to a ring of three in shared memory (bulk
+// units in pieces of 16 rows x 256 bytes to a ring of three in shared memory (asynchronous
 // copies, W1's and then W2's without a pause between: they need only the routing, so
 // that W2 is in flight while the CTAs wait for each other between the products),
 // multiplies a piece by the tokens of its expert (mma.sync, 16 rows x 8 tokens x 32:
@@ -30,7 +30,6 @@ namespace {
 constexpr int kMaxN = 64, kMaxE = 256, kMaxK = 16;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kStreams = 16;                  // streaming warps
 constexpr int kWide = 256;                    // reduction bytes of a row in one ring stage: two 128-blocks
 constexpr int kPieceBlocks = kWide / 128;
 constexpr int kStages = 3;                    // of each streaming warp
@@ -39,11 +38,12 @@ constexpr int kStages = 3;                    // of each streaming warp
 constexpr int kPairBytes = 2 * kWide + 64;
 constexpr int kStageBytes = 8 * kPairBytes;
 __device__ __forceinline__ int row_at(int r) { return (r >> 1) * kPairBytes + (r & 1) * (kWide + 64); }
-constexpr int kRingBytes = kStreams * kStages * kStageBytes;
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kMostBlocks = 256;              // 128-blocks of the activation that a CTA counts for itself
-// An expert's tokens are taken 16 at a time, each lot as an entry of its own: one with more reads the
-// expert's weights again, from L2.
-constexpr int kLot = 16;
+// An expert's tokens are taken 8 at a time, each lot as an entry of its own: a second one reads the expert's
+// weights again, from L2.  (Lots of 16 made some units twice as long as others: 299 us where this takes XX
+// for 64 tokens on 128 experts, top 8.)
+constexpr int kLot = 8;
 constexpr int kMostLots = kMaxE + kMaxN * kMaxK / kLot;
 constexpr int kRedundant = 2;                 // up to this many tokens every CTA finds their top-K itself
 
@@ -52,7 +52,6 @@ struct Header {                               // zero before the first call, lef
 };
 
 struct Smem {
-    uint64_t full[kStreams][kStages];
     int abort;
     int active;                               // lots of all touched experts
     uint32_t mask[kMaxE][2];                  // tokens of each expert
@@ -376,7 +375,7 @@ __device__ void make_lists(const Params &p, Smem &sm)
 // The products.  FIRST: units of 8 gate + 8 up rows of W1, tokens from x8; else 16
 // rows of W2, slots from a8.
 // ---------------------------------------------------------------------------
-// A streaming warp's walk over its units, u0, u0 + kStreams, ... of the CTA's: the lot of each and its place
+// A streaming warp's walk over its units, u0, u0 + kWarps, ... of the CTA's: the lot of each and its place
 // in the lot.
 struct Units {
     int u, to, lot, i;
@@ -390,8 +389,8 @@ struct Units {
     }
     __device__ __forceinline__ void next(int per)
     {
-        u += kStreams;
-        i += kStreams;
+        u += kWarps;
+        i += kWarps;
         while (i >= per) {
             i -= per;
             ++lot;
@@ -399,14 +398,16 @@ struct Units {
     }
 };
 
-// What the warp asks for next: first W1's pieces, then W2's.  Lane r < 16 copies row r of a piece.
+// What the warp asks for next: first W1's pieces, then W2's.  A piece is eight asynchronous copies of 16
+// bytes per lane, two rows each: lanes 0..15 the even one, 16..31 the odd one.  (As one bulk copy per row,
+// issued by sixteen lanes, asking took 1300 cycles a piece, more than the rest of the work on it.)
 struct Stream {
-    uint8_t *ring;
-    uint64_t *full;
-    uint32_t asked, done;
+    uint32_t ring;                // shared-memory address of this lane's place in stage 0, row 0 or 1
+    uint32_t asked, done;         // (asked counts every turn, also those with nothing left to ask for)
     int product, k, red, per;
     Units unit;
-    const uint8_t *row;
+    const uint8_t *row;           // this lane's bytes of row 0 or 1 of the unit
+    int64_t second;               // how far the ninth row lies behind the first
 
     __device__ __forceinline__ void enter(const Params &p, const Smem &sm, int warp, int lane)
     {
@@ -422,29 +423,42 @@ struct Stream {
     __device__ __forceinline__ void find_row(const Params &p, const Smem &sm, int lane)
     {
         const int64_t e = sm.expert[unit.lot];
-        row = product == 0 ? static_cast<const uint8_t *>(p.a.W1) +
-                                 (e * 2 * p.a.I + (lane & 8 ? p.a.I : 0) + unit.i * 8 + (lane & 7)) * p.a.H
-                           : static_cast<const uint8_t *>(p.a.W2) + (e * p.a.H + unit.i * 16 + (lane & 15)) * p.a.I;
+        const uint8_t *W = static_cast<const uint8_t *>(product == 0 ? p.a.W1 : p.a.W2);
+        const int64_t first = product == 0 ? e * 2 * p.a.I + unit.i * 8 : e * p.a.H + unit.i * 16;
+        row = W + (first + (lane >> 4)) * red + (lane & 15) * 16;
+        second = static_cast<int64_t>(product == 0 ? p.a.I : 8) * red;
     }
     __device__ __forceinline__ void ask(const Params &p, const Smem &sm, int warp, int lane)
     {
-        if (product == 2) return;
-        const uint32_t s = asked % kStages;
-        const int width = red - k < kWide ? red - k : kWide;
-        if (lane == 0) mbar_arrive_expect_tx(full + s, 16 * width);
-        __syncwarp();
-        if (lane < 16) bulk_load(ring + s * kStageBytes + row_at(lane), row + k, width, full + s);
-        ++asked;
-        k += kWide;
-        if (k < red) return;
-        k = 0;
-        unit.next(per);
-        if (unit.u < unit.to) {
-            find_row(p, sm, lane);
-        } else {
-            ++product;
-            enter(p, sm, warp, lane);
+        if (product < 2) {
+            const uint32_t dst = ring + asked % kStages * kStageBytes;
+            if ((lane & 15) * 16 < red - k) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * kPairBytes),
+                                 "l"(row + k + (i < 4 ? 0 : second) + static_cast<int64_t>(2 * (i & 3)) * red)
+                                 : "memory");
+            }
+            k += kWide;
+            if (k >= red) {
+                k = 0;
+                unit.next(per);
+                if (unit.u < unit.to) {
+                    find_row(p, sm, lane);
+                } else {
+                    ++product;
+                    enter(p, sm, warp, lane);
+                }
+            }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ++asked;
+    }
+    // Until the oldest piece that is not done has landed, for the whole warp.
+    __device__ __forceinline__ void wait() const
+    {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        __syncwarp();
     }
 };
 
@@ -468,42 +482,34 @@ struct Tokens {
     }
 };
 
-template <bool FIRST, int GROUPS>
-__device__ __forceinline__ void unit_sums(const LayerArgs &a, Smem &sm, Stream &st, const Params &p, int warp, int lane,
-                                          const uint8_t *src, const uint8_t *src_scale, int lot, int T, int64_t sc0,
-                                          int64_t sc1, bool &bad, float (&acc)[GROUPS][4])
+template <bool FIRST>
+__device__ __forceinline__ void unit_sums(const LayerArgs &a, const Smem &sm, const uint8_t *ring, Stream &st,
+                                          const Params &p, int warp, int lane, const uint8_t *src,
+                                          const uint8_t *src_scale, int lot, int T, int64_t sc0, int64_t sc1, bool &bad,
+                                          float (&acc)[4])
 {
     const int red = FIRST ? a.H : a.I, rblocks = red / 128, stride = scale_stride(red);
     const int g = lane >> 2, t4 = lane & 3;
     const void *W_scale = FIRST ? a.W1_scale : a.W2_scale;
     const int16_t *who = (FIRST ? sm.token : sm.slot) + sm.first[lot];
-    const uint8_t *tok[GROUPS], *ts[GROUPS][2];
+    const uint8_t *tok = g < T ? src + static_cast<int64_t>(who[g]) * red + t4 * 16 : nullptr;
+    const uint8_t *ts0 = t4 * 2 < T ? src_scale + who[t4 * 2] * stride : nullptr;
+    const uint8_t *ts1 = t4 * 2 + 1 < T ? src_scale + who[t4 * 2 + 1] * stride : nullptr;
 #pragma unroll
-    for (int j = 0; j < GROUPS; ++j) {
-        tok[j] = j * 8 + g < T ? src + static_cast<int64_t>(who[j * 8 + g]) * red + t4 * 16 : nullptr;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int col = j * 8 + t4 * 2 + x;
-            ts[j][x] = col < T ? src_scale + who[col] * stride : nullptr;
-            acc[j][x] = acc[j][2 + x] = 0.f;
-        }
-    }
-    // the tokens' next piece is on its way while this one is worked on
-    Tokens x[GROUPS];
-#pragma unroll
-    for (int j = 0; j < GROUPS; ++j) x[j].load(tok[j], ts[j][0], ts[j][1], 0, rblocks);
+    for (int x = 0; x < 4; ++x) acc[x] = 0.f;
     uint32_t sw0 = 0, sw1 = 0;                       // bytes of block (32 at a time) + lane
     const int lo_at = row_at(g) + t4 * 16, hi_at = row_at(g + 8) + t4 * 16;
-    for (int k0 = 0; k0 < rblocks; k0 += kPieceBlocks) {
+    // one piece, blocks k0 on, by the tokens `x`; those of the next piece are on their way meanwhile
+    auto step = [&](const Tokens &x, Tokens &next, int k0) {
+        const int nb = rblocks - k0;
+        if (nb > kPieceBlocks) next.load(tok, ts0, ts1, k0 + kPieceBlocks, nb - kPieceBlocks);
         if ((k0 & 31) == 0) {
             const int b = k0 + lane < rblocks ? k0 + lane : rblocks - 1;
             sw0 = load_scale_byte(W_scale, a.ue8m0, sc0 + b, bad);
             sw1 = FIRST ? load_scale_byte(W_scale, a.ue8m0, sc1 + b, bad) : sw0;
         }
-        const uint32_t s = st.done % kStages;
-        warp_wait(st.full + s, (st.done / kStages) & 1u, &sm.abort);
-        const uint8_t *stage = st.ring + s * kStageBytes;
-        const int nb = rblocks - k0;
+        st.wait();
+        const uint8_t *stage = ring + st.done % kStages * kStageBytes;
 #pragma unroll
         for (int b = 0; b < kPieceBlocks; ++b) {
             if (b >= nb) break;
@@ -513,56 +519,53 @@ __device__ __forceinline__ void unit_sums(const LayerArgs &a, Smem &sm, Stream &
             const uint4 hi1 = *reinterpret_cast<const uint4 *>(stage + hi_at + b * 128 + 64);
             const float w0 = scale_value(__shfl_sync(0xffffffffu, sw0, (k0 + b) & 31));
             const float w1 = FIRST ? scale_value(__shfl_sync(0xffffffffu, sw1, (k0 + b) & 31)) : w0;
-#pragma unroll
-            for (int j = 0; j < GROUPS; ++j) {
-                // four K = 32 steps in two chains; which k a lane's bytes stand for is the same on both sides
-                float d[4] = {0.f, 0.f, 0.f, 0.f}, f[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_e4m3(d, lo0.x, hi0.x, lo0.y, hi0.y, x[j].b0[b].x, x[j].b0[b].y);
-                mma_e4m3(f, lo1.x, hi1.x, lo1.y, hi1.y, x[j].b1[b].x, x[j].b1[b].y);
-                mma_e4m3(d, lo0.z, hi0.z, lo0.w, hi0.w, x[j].b0[b].z, x[j].b0[b].w);
-                mma_e4m3(f, lo1.z, hi1.z, lo1.w, hi1.w, x[j].b1[b].z, x[j].b1[b].w);
-                const float x0 = scale_value((x[j].s0 >> (8 * b)) & 0xFFu), x1 = scale_value((x[j].s1 >> (8 * b)) & 0xFFu);
-                acc[j][0] = fmaf(d[0] + f[0], w0 * x0, acc[j][0]);
-                acc[j][1] = fmaf(d[1] + f[1], w0 * x1, acc[j][1]);
-                acc[j][2] = fmaf(d[2] + f[2], w1 * x0, acc[j][2]);
-                acc[j][3] = fmaf(d[3] + f[3], w1 * x1, acc[j][3]);
-            }
+            // four K = 32 steps in two chains; which k a lane's bytes stand for is the same on both sides
+            float d[4] = {0.f, 0.f, 0.f, 0.f}, f[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_e4m3(d, lo0.x, hi0.x, lo0.y, hi0.y, x.b0[b].x, x.b0[b].y);
+            mma_e4m3(f, lo1.x, hi1.x, lo1.y, hi1.y, x.b1[b].x, x.b1[b].y);
+            mma_e4m3(d, lo0.z, hi0.z, lo0.w, hi0.w, x.b0[b].z, x.b0[b].w);
+            mma_e4m3(f, lo1.z, hi1.z, lo1.w, hi1.w, x.b1[b].z, x.b1[b].w);
+            const float x0 = scale_value((x.s0 >> (8 * b)) & 0xFFu), x1 = scale_value((x.s1 >> (8 * b)) & 0xFFu);
+            acc[0] = fmaf(d[0] + f[0], w0 * x0, acc[0]);
+            acc[1] = fmaf(d[1] + f[1], w0 * x1, acc[1]);
+            acc[2] = fmaf(d[2] + f[2], w1 * x0, acc[2]);
+            acc[3] = fmaf(d[3] + f[3], w1 * x1, acc[3]);
         }
         __syncwarp();                                // all lanes have read the stage
         ++st.done;
         st.ask(p, sm, warp, lane);
-        if (k0 + kPieceBlocks < rblocks)
-#pragma unroll
-            for (int j = 0; j < GROUPS; ++j) x[j].load(tok[j], ts[j][0], ts[j][1], k0 + kPieceBlocks, nb - kPieceBlocks);
+    };
+    Tokens x, y;
+    x.load(tok, ts0, ts1, 0, rblocks);
+    for (int k0 = 0; k0 < rblocks; k0 += 2 * kPieceBlocks) {
+        step(x, y, k0);
+        if (k0 + kPieceBlocks < rblocks) step(y, x, k0 + kPieceBlocks);
     }
 }
 
 // A unit's sums to where they go: the activation of its 8 features, or 16 elements of y.
-template <bool FIRST, int GROUPS>
+template <bool FIRST>
 __device__ __forceinline__ void unit_out(const LayerArgs &a, const Smem &sm, float *dst, int lot, int i, int T, int lane,
-                                         const float (&acc)[GROUPS][4])
+                                         const float (&acc)[4])
 {
     const int g = lane >> 2, t4 = lane & 3;
 #pragma unroll
-    for (int j = 0; j < GROUPS; ++j) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int col = j * 8 + t4 * 2 + x;
-            if (col >= T) continue;
-            const int64_t slot = sm.slot[sm.first[lot] + col];
-            if (FIRST) {
-                const float gate = acc[j][x], up = acc[j][2 + x];
-                __stcg(dst + slot * a.I + i * 8 + g, gate / (1.f + __expf(-gate)) * up);
-            } else {
-                __stcg(dst + slot * a.H + i * 16 + g, acc[j][x]);
-                __stcg(dst + slot * a.H + i * 16 + 8 + g, acc[j][2 + x]);
-            }
+    for (int x = 0; x < 2; ++x) {
+        const int col = t4 * 2 + x;
+        if (col >= T) continue;
+        const int64_t slot = sm.slot[sm.first[lot] + col];
+        if (FIRST) {
+            const float gate = acc[x], up = acc[2 + x];
+            __stcg(dst + slot * a.I + i * 8 + g, gate / (1.f + __expf(-gate)) * up);
+        } else {
+            __stcg(dst + slot * a.H + i * 16 + g, acc[x]);
+            __stcg(dst + slot * a.H + i * 16 + 8 + g, acc[2 + x]);
         }
     }
 }
 
 template <bool FIRST>
-__device__ __forceinline__ void product(const Params &p, Smem &sm, Stream &st)
+__device__ __forceinline__ void product(const Params &p, Smem &sm, const uint8_t *ring, Stream &st)
 {
     const LayerArgs &a = p.a;
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
@@ -583,15 +586,9 @@ __device__ __forceinline__ void product(const Params &p, Smem &sm, Stream &st)
         const int64_t sc0 = FIRST ? (static_cast<int64_t>(e) * (2 * a.I / 128) + i / 16) * rblocks
                                   : (static_cast<int64_t>(e) * (a.H / 128) + i / 8) * rblocks;
         const int64_t sc1 = FIRST ? sc0 + static_cast<int64_t>(a.I / 128) * rblocks : sc0;
-        if (T <= 8) {
-            float acc[1][4];
-            unit_sums<FIRST, 1>(a, sm, st, p, warp, lane, src, src_scale, lot, T, sc0, sc1, bad, acc);
-            unit_out<FIRST, 1>(a, sm, dst, lot, i, T, lane, acc);
-        } else {
-            float acc[2][4];
-            unit_sums<FIRST, 2>(a, sm, st, p, warp, lane, src, src_scale, lot, T, sc0, sc1, bad, acc);
-            unit_out<FIRST, 2>(a, sm, dst, lot, i, T, lane, acc);
-        }
+        float acc[4];
+        unit_sums<FIRST>(a, sm, ring, st, p, warp, lane, src, src_scale, lot, T, sc0, sc1, bad, acc);
+        unit_out<FIRST>(a, sm, dst, lot, i, T, lane, acc);
         if (FIRST) {
             // Whoever completes the sixteen units of a 128-block of the activation turns it into E4M3.  The
             // units that this CTA has of it are counted here, CTAs that share one meet in the workspace.
@@ -671,9 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const Params p)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStreams * kStages; ++i) mbar_init(&sm.full[0][0] + i, 1);
         sm.abort = 0;
-        fence_mbarrier_init();
     }
     for (int i = threadIdx.x; i < kMostBlocks; i += kThreads) sm.done[i] = 0;
     __syncthreads();
@@ -692,29 +687,20 @@ __global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const Params p)
         __syncthreads();
     else
         grid_barrier(hdr, 1, sm);
-    fence_proxy_async_smem();   // the ring's memory passes from these threads to the copies
     make_lists(p, sm);
     Stream st;
     st.asked = st.done = 0;
-    if (warp < kStreams) {
-        st.ring = ring + warp * kStages * kStageBytes;
-        st.full = sm.full[warp];
-        st.product = 0;
-        st.enter(p, sm, warp, lane);
-        for (int i = 0; i < kStages; ++i) st.ask(p, sm, warp, lane);
-        product<true>(p, sm, st);
-    }
+    uint8_t *mine = ring + warp * kStages * kStageBytes;
+    st.ring = smem_u32(mine) + (lane >> 4) * (kWide + 64) + (lane & 15) * 16;
+    st.product = 0;
+    st.enter(p, sm, warp, lane);
+    for (int i = 0; i < kStages; ++i) st.ask(p, sm, warp, lane);
+    product<true>(p, sm, mine, st);
     grid_barrier(hdr, 2, sm);
-    if (warp < kStreams) product<false>(p, sm, st);
+    product<false>(p, sm, mine, st);
+    asm volatile("cp.async.wait_all;" ::: "memory");   // (given up or not, none is in flight at the end)
     grid_barrier(hdr, 3, sm);
     combine(p);
-    if (*const_cast<volatile int *>(&sm.abort) != 0 && warp < kStreams) {
-        // let the copies in flight land before the CTA ends
-        for (uint32_t x = st.asked > kStages ? st.asked - kStages : 0u; x < st.asked; ++x) {
-            volatile int no_abort = 0;
-            mbar_wait_bounded(st.full + x % kStages, (x / kStages) & 1u, &no_abort);
-        }
-    }
     __syncthreads();
     if (threadIdx.x == 0) {
         if (sm.abort) report_status(p.a.status, MOE_ERR_TIMEOUT);

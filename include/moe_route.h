@@ -484,7 +484,7 @@ MOE_API size_t moe_layer_workspace_size(int N, int H, int I, int E, int K);
  *   residual bf16 [N,H] or NULL (may be out)
  *   topk_idx int32 [N,K], topk_w fp32 [N,K], out bf16 [N,H]: outputs
  *   workspace  moe_layer_workspace_size() bytes, 256-byte aligned; its first
- *              256 + 4 * (E + 64) * (I/128) bytes zero before the first call with these E and I
+ *              256 + 4 * (E + 128) * (I/128) bytes zero before the first call with these E and I
  *              (every call leaves them zero).  Calls that may overlap need their own.
  * H % 128 == 0, I % 128 == 0, both <= 65536, 1 <= K <= min(E, 16), E <= 256.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_MISALIGNED, MOE_ERR_WORKSPACE,

@@ -609,7 +609,7 @@ def test_moe_layer_repeats_on_one_workspace_and_as_a_graph(dev):
             else:
                 assert torch.equal(r.out.view(torch.int16), first[n].out.view(torch.int16))
                 assert torch.equal(r.topk_w, first[n].topk_w)
-    assert bool((big[:256 + 4 * (E + 64) * (I // 128)] == 0).all())
+    assert bool((big[:256 + 4 * (E + 128) * (I // 128)] == 0).all())
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     x = t[0][:7].contiguous()
