@@ -13,9 +13,8 @@
 // units in pieces of 16 rows x 256 bytes to a ring of three in shared memory (asynchronous
 // copies, W1's and then W2's without a pause between: they need only the routing, so
 // that W2 is in flight while the CTAs wait for each other between the products),
-// multiplies a piece by the tokens of its expert (mma.sync, 16 rows x 8 tokens x 32:
-// the tensor work is far below the stream's time, so the registers' path costs
-// nothing), applies each 128-block's scales in fp32, and holds a unit's whole
+// multiplies a piece by the tokens of its expert (mma.sync, 16 rows x 8 tokens, the
+// codes as f16: the tensor work is far below the stream's time), applies each 128-block's scales in fp32, and holds a unit's whole
 // reduction in its registers: no sum crosses warps, and none depends on an order.
 //
 // Phases, with grid barriers where marked:
@@ -129,12 +128,25 @@ __device__ void grid_barrier(Header *h, int which, Smem &sm)
     __syncthreads();
 }
 
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1)
+// d += 16 rows x 8 tokens over 64 of the reduction: a lane's 16 codes of rows g and g + 8 and of token g, as
+// f16, which holds every E4M3 value, four at a time.  Which k a lane's codes stand for is the same on both
+// sides.  (mma.sync on the codes themselves took 150 cycles for each 32 of k, three times as long.)
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&h)[2])
 {
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(h[0]), "=r"(h[1])
+        : "r"(w));
+}
+__device__ __forceinline__ void mma_codes(float (&d)[4], uint32_t lo, uint32_t hi, uint32_t tok)
+{
+    uint32_t a[2], b[2], t[2];
+    codes_to_f16(lo, a);
+    codes_to_f16(hi, b);
+    codes_to_f16(tok, t);
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(b[0]), "r"(a[1]), "r"(b[1]), "r"(t[0]), "r"(t[1]));
 }
 
 // Four values of a 128-block per lane of a warp -> codes; the block's scale byte in every lane.
@@ -467,18 +479,17 @@ struct Tokens {
     uint4 b0[kPieceBlocks], b1[kPieceBlocks];
     uint32_t s0, s1;
 
+    // (no condition on the loads: a block behind the last reads the one before it and is not used)
     __device__ __forceinline__ void load(const uint8_t *src, const uint8_t *sc0, const uint8_t *sc1, int k0, int nb)
     {
 #pragma unroll
         for (int b = 0; b < kPieceBlocks; ++b) {
-            b0[b] = b1[b] = make_uint4(0, 0, 0, 0);
-            if (src && b < nb) {
-                b0[b] = *reinterpret_cast<const uint4 *>(src + (k0 + b) * 128);
-                b1[b] = *reinterpret_cast<const uint4 *>(src + (k0 + b) * 128 + 64);
-            }
+            const uint8_t *at = src + (k0 + (b < nb ? b : 0)) * 128;
+            b0[b] = *reinterpret_cast<const uint4 *>(at);
+            b1[b] = *reinterpret_cast<const uint4 *>(at + 64);
         }
-        s0 = sc0 ? *reinterpret_cast<const uint16_t *>(sc0 + k0) : 0u;
-        s1 = sc1 ? *reinterpret_cast<const uint16_t *>(sc1 + k0) : 0u;
+        s0 = *reinterpret_cast<const uint16_t *>(sc0 + k0);
+        s1 = *reinterpret_cast<const uint16_t *>(sc1 + k0);
     }
 };
 
@@ -492,9 +503,10 @@ __device__ __forceinline__ void unit_sums(const LayerArgs &a, const Smem &sm, co
     const int g = lane >> 2, t4 = lane & 3;
     const void *W_scale = FIRST ? a.W1_scale : a.W2_scale;
     const int16_t *who = (FIRST ? sm.token : sm.slot) + sm.first[lot];
-    const uint8_t *tok = g < T ? src + static_cast<int64_t>(who[g]) * red + t4 * 16 : nullptr;
-    const uint8_t *ts0 = t4 * 2 < T ? src_scale + who[t4 * 2] * stride : nullptr;
-    const uint8_t *ts1 = t4 * 2 + 1 < T ? src_scale + who[t4 * 2 + 1] * stride : nullptr;
+    // (places without a token take the lot's first one's: no sum crosses columns, and theirs goes nowhere)
+    const uint8_t *tok = src + static_cast<int64_t>(who[g < T ? g : 0]) * red + t4 * 16;
+    const uint8_t *ts0 = src_scale + who[t4 * 2 < T ? t4 * 2 : 0] * stride;
+    const uint8_t *ts1 = src_scale + who[t4 * 2 + 1 < T ? t4 * 2 + 1 : 0] * stride;
 #pragma unroll
     for (int x = 0; x < 4; ++x) acc[x] = 0.f;
     uint32_t sw0 = 0, sw1 = 0;                       // bytes of block (32 at a time) + lane
@@ -519,12 +531,16 @@ __device__ __forceinline__ void unit_sums(const LayerArgs &a, const Smem &sm, co
             const uint4 hi1 = *reinterpret_cast<const uint4 *>(stage + hi_at + b * 128 + 64);
             const float w0 = scale_value(__shfl_sync(0xffffffffu, sw0, (k0 + b) & 31));
             const float w1 = FIRST ? scale_value(__shfl_sync(0xffffffffu, sw1, (k0 + b) & 31)) : w0;
-            // four K = 32 steps in two chains; which k a lane's bytes stand for is the same on both sides
+            // eight K = 16 steps in two chains
             float d[4] = {0.f, 0.f, 0.f, 0.f}, f[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_e4m3(d, lo0.x, hi0.x, lo0.y, hi0.y, x.b0[b].x, x.b0[b].y);
-            mma_e4m3(f, lo1.x, hi1.x, lo1.y, hi1.y, x.b1[b].x, x.b1[b].y);
-            mma_e4m3(d, lo0.z, hi0.z, lo0.w, hi0.w, x.b0[b].z, x.b0[b].w);
-            mma_e4m3(f, lo1.z, hi1.z, lo1.w, hi1.w, x.b1[b].z, x.b1[b].w);
+            mma_codes(d, lo0.x, hi0.x, x.b0[b].x);
+            mma_codes(f, lo1.x, hi1.x, x.b1[b].x);
+            mma_codes(d, lo0.y, hi0.y, x.b0[b].y);
+            mma_codes(f, lo1.y, hi1.y, x.b1[b].y);
+            mma_codes(d, lo0.z, hi0.z, x.b0[b].z);
+            mma_codes(f, lo1.z, hi1.z, x.b1[b].z);
+            mma_codes(d, lo0.w, hi0.w, x.b0[b].w);
+            mma_codes(f, lo1.w, hi1.w, x.b1[b].w);
             const float x0 = scale_value((x.s0 >> (8 * b)) & 0xFFu), x1 = scale_value((x.s1 >> (8 * b)) & 0xFFu);
             acc[0] = fmaf(d[0] + f[0], w0 * x0, acc[0]);
             acc[1] = fmaf(d[1] + f[1], w0 * x1, acc[1]);
@@ -614,10 +630,16 @@ __device__ __forceinline__ void product(const Params &p, Smem &sm, const uint8_t
             __syncwarp();
             if (__shfl_sync(0xffffffffu, last, 0)) {
                 const int b = i >> 4;
-                for (int n = 0; n < T; ++n) {
-                    const int64_t slot = sm.slot[sm.first[lot] + n];
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(act + slot * a.I + b * 128) + lane);
-                    const float f[4] = {v.x, v.y, v.z, v.w};
+                const int16_t *slots = sm.slot + sm.first[lot];
+                float4 v[kLot];
+#pragma unroll
+                for (int n = 0; n < kLot; ++n)
+                    v[n] = __ldcg(reinterpret_cast<const float4 *>(act + static_cast<int64_t>(slots[n < T ? n : 0]) * a.I + b * 128) + lane);
+#pragma unroll
+                for (int n = 0; n < kLot; ++n) {
+                    if (n >= T) break;
+                    const int64_t slot = slots[n];
+                    const float f[4] = {v[n].x, v[n].y, v[n].z, v[n].w};
                     uint32_t byte;
                     const uint32_t q = quant_warp_block(f, byte);
                     __stcg(reinterpret_cast<uint32_t *>(ws + p.l.a8 + slot * a.I + b * 128) + lane, q);
