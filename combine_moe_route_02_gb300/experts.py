@@ -21,12 +21,13 @@ Kept from the forward to the backward pass: E4M3 rows only.  For serving a few t
 """
 from __future__ import annotations
 
+import functools
 from dataclasses import dataclass
 from typing import Optional
 
 import torch
 
-from . import (_check, _need, _ptr, _scale_dtype, _scale_format, _status_ptr, _stream, _workspace_arg, lib)
+from . import _check, _need, _scale_dtype, _scale_format, _status_ptr, _workspace_arg, lib
 
 __all__ = ["quantize_weight", "expert_gemm", "expert_wgrad", "swiglu", "swiglu_backward", "moe_layer",
            "layer_workspace_size", "layer_workspace", "SwiGLU", "SwiGLUGrad", "LayerOut"]
@@ -38,14 +39,40 @@ def _blocks(n: int) -> int:
     return -(-n // BLOCK)
 
 
-def _scales(t: torch.Tensor, name: str, shape) -> int:
-    """Checks block scales of either format and returns the format."""
+def _home(t: torch.Tensor, name: str) -> int:
+    """The current device, which a call's first tensor has to be on."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        _need(t, name, t.dtype)
+    return dev
+
+
+def _arg(t: torch.Tensor, name: str, dtype, shape, dev: int) -> int:
+    """The address of a tensor that _need accepts.  (These calls take up to a dozen tensors, and a small
+    one's kernel runs for a few microseconds: what is right is found out in one expression.)"""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == dev):
+        _need(t, name, dtype, shape)
+    return t.data_ptr()
+
+
+def _opt(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int):
+    return None if t is None else _arg(t, name, dtype, shape, dev)
+
+
+def _scales(t: torch.Tensor, name: str, shape, dev: int):
+    """The address of block scales of either format, and the format."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in (torch.float32, torch.uint8):
+    if t.dtype is torch.uint8:
+        return _arg(t, name, torch.uint8, shape, dev), 1
+    if t.dtype is not torch.float32:
         raise TypeError(f"{name} must be torch.float32 or torch.uint8 (UE8M0), got {t.dtype}")
-    _need(t, name, t.dtype, shape)
-    return 1 if t.dtype == torch.uint8 else 0
+    return _arg(t, name, torch.float32, shape, dev), 0
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _dims(t: torch.Tensor, name: str, n: int):
@@ -56,23 +83,25 @@ def _dims(t: torch.Tensor, name: str, n: int):
     return tuple(t.shape)
 
 
-def _groups(expert_offsets: Optional[torch.Tensor], E: Optional[int]) -> int:
+def _groups(expert_offsets: Optional[torch.Tensor], E: Optional[int], dev: int):
+    """The address of the offsets (or None), and the number of experts."""
     if expert_offsets is None:
         if E not in (None, 1):
             raise ValueError("expert_offsets is required for more than one expert")
-        return 1
-    n = _dims(expert_offsets, "expert_offsets", 1)[0] - 1
-    _need(expert_offsets, "expert_offsets", torch.int32, (n + 1 if E is None else E + 1,))
-    return n
+        return None, 1
+    if E is None:
+        E = _dims(expert_offsets, "expert_offsets", 1)[0] - 1
+    return _arg(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev), E
 
 
 def quantize_weight(W: torch.Tensor, scale_format: str = "fp32", out=None, stream=None):
     """bf16 [E, rows, cols] (or [rows, cols]) -> (E4M3 codes uint8, scales of 128x128 blocks).
     `out`: the two tensors to write."""
     fmt = _scale_format(scale_format)
-    _need(W, "W", torch.bfloat16)
-    if W.dim() not in (2, 3):
-        raise ValueError("W must be [E, rows, cols] or [rows, cols]")
+    if not isinstance(W, torch.Tensor) or W.dim() not in (2, 3):
+        raise ValueError("W must be a tensor [E, rows, cols] or [rows, cols]")
+    dev = _home(W, "W")
+    src = _arg(W, "W", torch.bfloat16, W.shape, dev)
     lead, (rows, cols) = W.shape[:-2], W.shape[-2:]
     E = lead[0] if lead else 1
     shape = (*lead, _blocks(rows), _blocks(cols))
@@ -80,9 +109,8 @@ def quantize_weight(W: torch.Tensor, scale_format: str = "fp32", out=None, strea
         out = (torch.empty(W.shape, dtype=torch.uint8, device=W.device),
                torch.empty(shape, dtype=_scale_dtype(scale_format), device=W.device))
     q, s = out
-    _need(q, "W_fp8", torch.uint8, W.shape)
-    _need(s, "W_scale", _scale_dtype(scale_format), shape)
-    _check(lib().moe_quantize_weight(_ptr(W), E, rows, cols, _ptr(q), _ptr(s), fmt, _stream(stream)),
+    _check(lib().moe_quantize_weight(src, E, rows, cols, _arg(q, "W_fp8", torch.uint8, W.shape, dev),
+                                     _arg(s, "W_scale", _scale_dtype(scale_format), shape, dev), fmt, _raw_stream(stream, dev)),
            "moe_quantize_weight")
     return q, s
 
@@ -99,18 +127,17 @@ def expert_gemm(X_fp8: torch.Tensor, X_scale: torch.Tensor, W_fp8: torch.Tensor,
     R, red = _dims(X_fp8, "X_fp8", 2)
     if red != (rows if transpose else cols):
         raise ValueError(f"X_fp8 has {red} columns, W_fp8 {tuple(W_fp8.shape)} takes {rows if transpose else cols}")
-    _need(X_fp8, "X_fp8", torch.uint8)
-    _need(W_fp8, "W_fp8", torch.uint8)
-    xf = _scales(X_scale, "X_scale", (R, red // BLOCK))
-    wf = _scales(W_scale, "W_scale", (E, _blocks(rows), _blocks(cols)))
-    _groups(expert_offsets, E)
+    dev = _home(X_fp8, "X_fp8")
+    x, w = _arg(X_fp8, "X_fp8", torch.uint8, (R, red), dev), _arg(W_fp8, "W_fp8", torch.uint8, (E, rows, cols), dev)
+    xs, xf = _scales(X_scale, "X_scale", (R, red // BLOCK), dev)
+    ws, wf = _scales(W_scale, "W_scale", (E, _blocks(rows), _blocks(cols)), dev)
+    off, _ = _groups(expert_offsets, E, dev)
     n = cols if transpose else rows
     if out is None:
         out = torch.empty((R, n), dtype=torch.bfloat16, device=X_fp8.device)
-    _need(out, "out", torch.bfloat16, (R, n))
-    _check(lib().moe_expert_gemm(_ptr(X_fp8), _ptr(X_scale), xf, _ptr(W_fp8), _ptr(W_scale), wf, _ptr(expert_offsets),
-                                 R, E, rows, cols, int(bool(transpose)), _ptr(out), _status_ptr(status),
-                                 _stream(stream)), "moe_expert_gemm")
+    _check(lib().moe_expert_gemm(x, xs, xf, w, ws, wf, off, R, E, rows, cols, int(bool(transpose)),
+                                 _arg(out, "out", torch.bfloat16, (R, n), dev), _status_ptr(status), _raw_stream(stream, dev)),
+           "moe_expert_gemm")
     return out
 
 
@@ -124,18 +151,17 @@ def expert_wgrad(dY: torch.Tensor, X_fp8: torch.Tensor, X_scale: torch.Tensor,
         raise TypeError("dtype must be torch.float32 or torch.bfloat16")
     R, rows = _dims(dY, "dY", 2)
     cols = _dims(X_fp8, "X_fp8", 2)[1]
-    _need(dY, "dY", torch.bfloat16)
-    _need(X_fp8, "X_fp8", torch.uint8, (R, cols))
-    xf = _scales(X_scale, "X_scale", (R, cols // BLOCK))
-    E = _groups(expert_offsets, None)
-    if add is not None:
-        _need(add, "add", torch.float32, (E, rows, cols))
+    dev = _home(dY, "dY")
+    dy, x = _arg(dY, "dY", torch.bfloat16, (R, rows), dev), _arg(X_fp8, "X_fp8", torch.uint8, (R, cols), dev)
+    xs, xf = _scales(X_scale, "X_scale", (R, cols // BLOCK), dev)
+    off, E = _groups(expert_offsets, None, dev)
+    shape = (E, rows, cols)
+    added = _opt(add, "add", torch.float32, shape, dev)
     if out is None:
-        out = torch.empty((E, rows, cols), dtype=dtype, device=dY.device)
-    _need(out, "out", dtype, (E, rows, cols))
-    _check(lib().moe_expert_wgrad(_ptr(dY), _ptr(X_fp8), _ptr(X_scale), xf, _ptr(expert_offsets), R, E, rows, cols,
-                                  _ptr(add), _ptr(out), int(dtype == torch.bfloat16), _status_ptr(status),
-                                  _stream(stream)), "moe_expert_wgrad")
+        out = torch.empty(shape, dtype=dtype, device=dY.device)
+    _check(lib().moe_expert_wgrad(dy, x, xs, xf, off, R, E, rows, cols, added, _arg(out, "out", dtype, shape, dev),
+                                  int(dtype is torch.bfloat16), _status_ptr(status), _raw_stream(stream, dev)),
+           "moe_expert_wgrad")
     return out
 
 
@@ -165,19 +191,17 @@ def swiglu(GU: torch.Tensor, keep: bool = True, scale_format: str = "fp32", out:
     which is all that swiglu_backward needs."""
     fmt = _scale_format(scale_format)
     R, C = _dims(GU, "GU", 2)
-    _need(GU, "GU", torch.bfloat16)
+    dev = _home(GU, "GU")
+    src = _arg(GU, "GU", torch.bfloat16, (R, C), dev)
     if C % (2 * BLOCK) != 0:
         raise ValueError("GU must be [R, 2I] with I a multiple of 128")
-    I = C // 2
+    I, sd = C // 2, _scale_dtype(scale_format)
     if out is None:
         out = SwiGLU(*_coded(R, I, scale_format, GU.device), *(_coded(R, C, scale_format, GU.device) if keep else (None, None)))
-    _need(out.A_fp8, "A_fp8", torch.uint8, (R, I))
-    _need(out.A_scale, "A_scale", _scale_dtype(scale_format), (R, I // BLOCK))
-    if out.GU_fp8 is not None:
-        _need(out.GU_fp8, "GU_fp8", torch.uint8, (R, C))
-        _need(out.GU_scale, "GU_scale", _scale_dtype(scale_format), (R, C // BLOCK))
-    _check(lib().moe_swiglu(_ptr(GU), R, I, _ptr(out.A_fp8), _ptr(out.A_scale), _ptr(out.GU_fp8), _ptr(out.GU_scale),
-                            fmt, _stream(stream)), "moe_swiglu")
+    _check(lib().moe_swiglu(src, R, I, _arg(out.A_fp8, "A_fp8", torch.uint8, (R, I), dev),
+                            _arg(out.A_scale, "A_scale", sd, (R, I // BLOCK), dev),
+                            _opt(out.GU_fp8, "GU_fp8", torch.uint8, (R, C), dev),
+                            _opt(out.GU_scale, "GU_scale", sd, (R, C // BLOCK), dev), fmt, _raw_stream(stream, dev)), "moe_swiglu")
     return out
 
 
@@ -188,20 +212,16 @@ def swiglu_backward(dA: torch.Tensor, GU_fp8: torch.Tensor, GU_scale: torch.Tens
     the transposed expert_gemm)."""
     fmt = _scale_format(scale_format)
     R, I = _dims(dA, "dA", 2)
-    _need(dA, "dA", torch.bfloat16)
-    _need(GU_fp8, "GU_fp8", torch.uint8, (R, 2 * I))
-    gf = _scales(GU_scale, "GU_scale", (R, 2 * I // BLOCK))
+    dev = _home(dA, "dA")
+    da, kept = _arg(dA, "dA", torch.bfloat16, (R, I), dev), _arg(GU_fp8, "GU_fp8", torch.uint8, (R, 2 * I), dev)
+    gs, gf = _scales(GU_scale, "GU_scale", (R, 2 * I // BLOCK), dev)
     if out is None:
         out = SwiGLUGrad(torch.empty((R, 2 * I), dtype=torch.bfloat16, device=dA.device) if bf16 else None,
                          *(_coded(R, 2 * I, scale_format, dA.device) if fp8 else (None, None)))
-    if out.dGU is not None:
-        _need(out.dGU, "dGU", torch.bfloat16, (R, 2 * I))
-    if out.dGU_fp8 is not None:
-        _need(out.dGU_fp8, "dGU_fp8", torch.uint8, (R, 2 * I))
-        _need(out.dGU_scale, "dGU_scale", _scale_dtype(scale_format), (R, 2 * I // BLOCK))
-    _check(lib().moe_swiglu_backward(_ptr(dA), _ptr(GU_fp8), _ptr(GU_scale), gf, R, I, _ptr(out.dGU),
-                                     _ptr(out.dGU_fp8), _ptr(out.dGU_scale), fmt, _status_ptr(status),
-                                     _stream(stream)), "moe_swiglu_backward")
+    _check(lib().moe_swiglu_backward(da, kept, gs, gf, R, I, _opt(out.dGU, "dGU", torch.bfloat16, (R, 2 * I), dev),
+                                     _opt(out.dGU_fp8, "dGU_fp8", torch.uint8, (R, 2 * I), dev),
+                                     _opt(out.dGU_scale, "dGU_scale", _scale_dtype(scale_format), (R, 2 * I // BLOCK), dev),
+                                     fmt, _status_ptr(status), _raw_stream(stream, dev)), "moe_swiglu_backward")
     return out
 
 
@@ -215,6 +235,7 @@ class LayerOut:
 _layer_workspaces = {}
 
 
+@functools.lru_cache(maxsize=None)
 def layer_workspace_size(N: int, H: int, I: int, E: int, K: int) -> int:
     """Bytes of workspace moe_layer needs (0 for sizes it does not take)."""
     return int(lib().moe_layer_workspace_size(N, H, I, E, K))
@@ -245,31 +266,33 @@ def moe_layer(X: torch.Tensor, W_gate: torch.Tensor, K: int, W1_fp8: torch.Tenso
     tokens in one launch.  W1 [E, 2I, H] (gate rows first) and W2 [E, H, I] in E4M3 with 128x128 scales
     of one format (quantize_weight); X bf16 [N, H].  `out.out` may be the residual."""
     N, H = _dims(X, "X", 2)
-    _need(X, "X", torch.bfloat16)
     E, two_i, _ = _dims(W1_fp8, "W1_fp8", 3)
     I = two_i // 2
-    _need(W_gate, "W_gate", torch.bfloat16, (H, E))
-    _need(W1_fp8, "W1_fp8", torch.uint8, (E, 2 * I, H))
-    _need(W2_fp8, "W2_fp8", torch.uint8, (E, H, I))
-    fmt = _scales(W1_scale, "W1_scale", (E, _blocks(2 * I), _blocks(H)))
-    if _scales(W2_scale, "W2_scale", (E, _blocks(H), _blocks(I))) != fmt:
+    dev = _home(X, "X")
+    x, wg = _arg(X, "X", torch.bfloat16, (N, H), dev), _arg(W_gate, "W_gate", torch.bfloat16, (H, E), dev)
+    w1, w2 = _arg(W1_fp8, "W1_fp8", torch.uint8, (E, 2 * I, H), dev), _arg(W2_fp8, "W2_fp8", torch.uint8, (E, H, I), dev)
+    s1, fmt = _scales(W1_scale, "W1_scale", (E, _blocks(2 * I), _blocks(H)), dev)
+    s2, fmt2 = _scales(W2_scale, "W2_scale", (E, _blocks(H), _blocks(I)), dev)
+    if fmt2 != fmt:
         raise TypeError("W1_scale and W2_scale must be of one format")
-    if bias is not None:
-        _need(bias, "bias", torch.float32, (E,))
-    if residual is not None:
-        _need(residual, "residual", torch.bfloat16, (N, H))
-    dev = X.device
+    b, res = _opt(bias, "bias", torch.float32, (E,), dev), _opt(residual, "residual", torch.bfloat16, (N, H), dev)
     if out is None:
-        out = LayerOut(torch.empty((N, H), dtype=torch.bfloat16, device=dev),
-                       torch.empty((N, K), dtype=torch.int32, device=dev),
-                       torch.empty((N, K), dtype=torch.float32, device=dev))
-    _need(out.out, "out", torch.bfloat16, (N, H))
-    _need(out.topk_idx, "topk_idx", torch.int32, (N, K))
-    _need(out.topk_w, "topk_w", torch.float32, (N, K))
-    if workspace is None and layer_workspace_size(N, H, I, E, K):
-        workspace = layer_workspace(N, H, I, E, K, dev, stream)
-    _check(lib().moe_layer(_ptr(X), _ptr(W_gate), _ptr(bias), _ptr(W1_fp8), _ptr(W1_scale), _ptr(W2_fp8),
-                           _ptr(W2_scale), fmt, _ptr(residual), N, H, I, E, K, int(bool(renorm)), _ptr(out.topk_idx),
-                           _ptr(out.topk_w), _ptr(out.out), _status_ptr(status), *_workspace_arg(workspace),
-                           _stream(stream)), "moe_layer")
+        out = LayerOut(torch.empty((N, H), dtype=torch.bfloat16, device=X.device),
+                       torch.empty((N, K), dtype=torch.int32, device=X.device),
+                       torch.empty((N, K), dtype=torch.float32, device=X.device))
+    raw = _raw_stream(stream, dev)
+    if workspace is not None:
+        ws, ws_bytes = _workspace_arg(workspace)
+    elif layer_workspace_size(N, H, I, E, K):
+        cached = _layer_workspaces.get((dev, raw, E, I))
+        if cached is None or cached.numel() < layer_workspace_size(N, H, I, E, K):
+            cached = layer_workspace(N, H, I, E, K, X.device, stream)
+        ws, ws_bytes = cached.data_ptr(), cached.numel()
+    else:
+        ws, ws_bytes = None, 0
+    _check(lib().moe_layer(x, wg, b, w1, s1, w2, s2, fmt, res, N, H, I, E, K, int(bool(renorm)),
+                           _arg(out.topk_idx, "topk_idx", torch.int32, (N, K), dev),
+                           _arg(out.topk_w, "topk_w", torch.float32, (N, K), dev),
+                           _arg(out.out, "out", torch.bfloat16, (N, H), dev), _status_ptr(status), ws, ws_bytes, raw),
+           "moe_layer")
     return out
