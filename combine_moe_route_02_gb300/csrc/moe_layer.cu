@@ -10,12 +10,13 @@
 // work is 16 weight rows of one expert (8 gate and 8 up rows of W1, or 16 rows of
 // W2); the units of all touched experts are split evenly and in order over the CTAs,
 // and a CTA's over its sixteen warps.  Each of those is on its own: it copies its
-// units in pieces of 16 rows x 256 bytes to a ring of three in shared memory (asynchronous
-// copies, W1's and then W2's without a pause between: they need only the routing, so
-// that W2 is in flight while the CTAs wait for each other between the products),
-// multiplies a piece by the tokens of its expert (mma.sync, 16 rows x 8 tokens, the
-// codes as f16: the tensor work is far below the stream's time), applies each 128-block's scales in fp32, and holds a unit's whole
-// reduction in its registers: no sum crosses warps, and none depends on an order.
+// units in pieces of 16 rows x 256 bytes to a ring of three in shared memory (TMA,
+// W1's and then W2's without a pause between: they need only the routing, so that W2
+// is in flight while the CTAs wait for each other between the products), multiplies a
+// piece by the tokens of its expert (mma.sync, 16 rows x 8 tokens, the codes as f16:
+// the tensor work is far below the stream's time), applies each 128-block's scales in
+// fp32, and holds a unit's whole reduction in its registers: no sum crosses warps but
+// those of shared units (two halves, added in order), none depends on timing.
 //
 // Phases, with grid barriers where marked:
 //   logits of row slices of W_gate, x to E4M3 | top-K, one CTA per token | lists of
@@ -32,11 +33,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kWide = 256;                    // reduction bytes of a row in one ring stage: two 128-blocks
 constexpr int kPieceBlocks = kWide / 128;
 constexpr int kStages = 3;                    // of each streaming warp
-// Rows in pairs, the second 64 bytes further on than it would be: eight lanes read two rows' 64 bytes at a
-// time, and meet different banks.
-constexpr int kPairBytes = 2 * kWide + 64;
-constexpr int kStageBytes = 8 * kPairBytes;
-__device__ __forceinline__ int row_at(int r) { return (r >> 1) * kPairBytes + (r & 1) * (kWide + 64); }
+constexpr int kStageBytes = 16 * kWide;
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kMostBlocks = 256;              // 128-blocks of the activation that a CTA counts for itself
 // An expert's tokens are taken 8 at a time, each lot as an entry of its own: a second one reads the expert's
@@ -51,15 +48,22 @@ struct Header {                               // zero before the first call, lef
 };
 
 struct Smem {
+    uint64_t full[kWarps][kStages];
     int abort;
     int active;                               // lots of all touched experts
-    uint32_t mask[kMaxE][2];                  // tokens of each expert
+    int unit_from[2], unit_to[2];             // the units of each product that this CTA takes
+    int shared[2];                            // whether two warps share each of them, a half of its reduction each
+    union {
+        struct {
+            uint32_t mask[kMaxE][2];          // tokens of each expert
+            float logit[kMaxE];
+        };
+        float4 half[kWarps / 2][32];          // (once the lists stand) the second halves of shared units' sums
+    };
     int16_t expert[kMostLots];                // of each lot, ascending
     int16_t first[kMostLots + 1];             // where its slots start
     int16_t idx[kRedundant * kMaxK];          // the top-K ids where every CTA has found them
     int16_t slot[kMaxN * kMaxK];              // slots n * K + k by expert, then token
-    int16_t token[kMaxN * kMaxK];             // their n
-    float logit[kMaxE];
     int done[kMostBlocks];                    // units that this CTA has done of its 128-blocks
 };
 constexpr size_t kSmemBytes = 1024 + kRingBytes + sizeof(Smem);
@@ -97,13 +101,9 @@ struct Params {
     LayerArgs a;
     Layout l;
 };
-
-// Which units of `total` this CTA takes.
-__device__ __forceinline__ void my_units(int total, int &from, int &to)
-{
-    from = static_cast<int>(static_cast<int64_t>(total) * blockIdx.x / gridDim.x);
-    to = static_cast<int>(static_cast<int64_t>(total) * (blockIdx.x + 1) / gridDim.x);
-}
+struct Maps {
+    CUtensorMap w1, w2;                       // boxes of 8 rows x 256 bytes
+};
 
 // All CTAs' threads; what they wrote before is visible to all after.  A CTA that gives up
 // goes on through the remaining phases (each wait then ends at once), so that every thread meets
@@ -234,8 +234,6 @@ __device__ void quantise_x(const Params &p)
     }
 }
 
-__device__ __forceinline__ bool above(float v, int e, float b, int be) { return v > b || (v == b && e < be); }
-
 // Top-K of token n from the slices' partial logits.
 __device__ void select(const Params &p, int n, Smem &sm, float *scratch)
 {
@@ -272,38 +270,40 @@ __device__ void select(const Params &p, int n, Smem &sm, float *scratch)
         float v[kMaxE / 32];
 #pragma unroll
         for (int i = 0; i < kMaxE / 32; ++i) v[i] = lane + 32 * i < E ? sm.logit[lane + 32 * i] : -INFINITY;
-        uint32_t taken = 0;
         float first = 0.f, sum = 0.f, my_p = 0.f;
         int my_i = 0;
+        // (the order of the values as unsigned numbers: + 0 makes one zero of two, a NaN is -inf already)
+        uint32_t key[kMaxE / 32];
+#pragma unroll
+        for (int i = 0; i < kMaxE / 32; ++i) {
+            const uint32_t w = __float_as_uint(v[i] + 0.f);
+            key[i] = lane + 32 * i < E ? (w & 0x80000000u ? ~w : w | 0x80000000u) : 0u;
+        }
         for (int k = 0; k < K; ++k) {
-            float bv = -INFINITY;
+            uint32_t best = 0;
             int bi = 0x7fffffff;
 #pragma unroll
-            for (int i = 0; i < kMaxE / 32; ++i) {
-                const int c = lane + 32 * i;
-                if (c < E && !((taken >> i) & 1u) && above(v[i], c, bv, bi)) {
-                    bv = v[i];
-                    bi = c;
+            for (int i = 0; i < kMaxE / 32; ++i)
+                if (key[i] > best) {          // (a taken one's key is 0, below that of -inf)
+                    best = key[i];
+                    bi = lane + 32 * i;
                 }
-            }
+            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+            bi = __reduce_min_sync(0xffffffffu, best == top ? bi : 0x7fffffff);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-                const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-                if (above(ov, oi, bv, bi)) {
-                    bv = ov;
-                    bi = oi;
-                }
-            }
-            if ((bi & 31) == lane) taken |= 1u << (bi >> 5);
-            if (k == 0) first = bv;
-            const float pr = expf(bv - first);
-            sum += pr;
+            for (int i = 0; i < kMaxE / 32; ++i)
+                if (bi == lane + 32 * i) key[i] = 0;
+            const float value = __uint_as_float(top & 0x80000000u ? top & 0x7FFFFFFFu : ~top);
+            if (k == 0) first = value;
             if (lane == k) {
-                my_p = pr;
+                my_p = value;
                 my_i = bi;
             }
         }
+        my_p = lane < K ? expf(my_p - first) : 0.f;
+        sum = my_p;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (!p.a.renorm) {
             sum = 0.f;
 #pragma unroll
@@ -367,6 +367,15 @@ __device__ void make_lists(const Params &p, Smem &sm)
             sm.active = active;
             sm.first[active] = static_cast<int16_t>(before);
         }
+        if (lane < 2) {
+            // (below 2^31: at most 384 lots of 8192 units, and some hundreds of CTAs)
+            const unsigned total = active * (lane == 0 ? p.a.I / 8 : p.a.H / 16), ctas = gridDim.x;
+            sm.unit_from[lane] = total / ctas * blockIdx.x + total % ctas * blockIdx.x / ctas;
+            sm.unit_to[lane] = total / ctas * (blockIdx.x + 1) + total % ctas * (blockIdx.x + 1) / ctas;
+            // where no CTA has more than half as many units as warps (one token, top 8 of 128 experts of
+            // 2048 x 1024: 33 us, 41 without)
+            sm.shared[lane] = (total + ctas - 1) / ctas * 2 <= kWarps;
+        }
     }
     __syncthreads();
 #pragma unroll
@@ -378,25 +387,27 @@ __device__ void make_lists(const Params &p, Smem &sm)
         const int rank = n < 32 ? __popc(m0 & below) : __popc(m0) + __popc(m1 & below);
         const int at = __float_as_int(sm.logit[e[i]]) + rank;
         sm.slot[at] = static_cast<int16_t>(s);
-        sm.token[at] = static_cast<int16_t>(n);
     }
     __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
-// The products.  FIRST: units of 8 gate + 8 up rows of W1, tokens from x8; else 16
-// rows of W2, slots from a8.
+// The products.  The first: units of 8 gate + 8 up rows of W1, tokens from x8; the
+// second: of 16 rows of W2, slots from a8.
 // ---------------------------------------------------------------------------
+// Where the second half of a shared unit starts: whole pieces.
+__device__ __forceinline__ int middle(int red) { return ((red + kWide - 1) / kWide + 1) / 2 * kWide; }
+
 // A streaming warp's walk over its units, u0, u0 + kWarps, ... of the CTA's: the lot of each and its place
 // in the lot.
 struct Units {
     int u, to, lot, i;
 
-    __device__ __forceinline__ void start(int active, int per, int warp)
+    __device__ __forceinline__ void start(const Smem &sm, int product, int per, int warp)
     {
-        my_units(active * per, u, to);
-        u += warp;
-        lot = u / per;
+        u = sm.unit_from[product] + (sm.shared[product] ? warp >> 1 : warp);
+        to = sm.unit_to[product];
+        lot = static_cast<unsigned>(u) / static_cast<unsigned>(per);
         i = u - lot * per;
     }
     __device__ __forceinline__ void next(int per)
@@ -410,67 +421,61 @@ struct Units {
     }
 };
 
-// What the warp asks for next: first W1's pieces, then W2's.  A piece is eight asynchronous copies of 16
-// bytes per lane, two rows each: lanes 0..15 the even one, 16..31 the odd one.  (As one bulk copy per row,
-// issued by sixteen lanes, asking took 1300 cycles a piece, more than the rest of the work on it.)
+// What the warp asks for next: first W1's pieces, then W2's.  A piece is two TMA boxes of 8 rows x 256 bytes.
+// (As one bulk copy per row, issued by sixteen lanes, asking took 1300 cycles a piece, as eight asynchronous
+// 16-byte copies per lane 400 to 750: more than the work on the piece.)
 struct Stream {
-    uint32_t ring;                // shared-memory address of this lane's place in stage 0, row 0 or 1
-    uint32_t asked, done;         // (asked counts every turn, also those with nothing left to ask for)
+    uint8_t *ring;
+    uint64_t *full;
+    uint32_t asked, done;
     int product, k, red, per;
+    int from, to;                 // the part of a row that this warp takes
     Units unit;
-    const uint8_t *row;           // this lane's bytes of row 0 or 1 of the unit
-    int64_t second;               // how far the ninth row lies behind the first
+    int row, second;              // the first row of each box
 
-    __device__ __forceinline__ void enter(const Params &p, const Smem &sm, int warp, int lane)
+    __device__ __forceinline__ void enter(const Params &p, const Smem &sm, int warp)
     {
         for (; product < 2; ++product) {
             red = product == 0 ? p.a.H : p.a.I;
             per = product == 0 ? p.a.I / 8 : p.a.H / 16;
-            unit.start(sm.active, per, warp);
-            if (unit.u < unit.to) break;
+            unit.start(sm, product, per, warp);
+            const bool shared = sm.shared[product] != 0;
+            from = shared && (warp & 1) ? middle(red) : 0;
+            to = shared && !(warp & 1) && middle(red) < red ? middle(red) : red;
+            if (unit.u < unit.to && from < to) break;
         }
-        k = 0;
-        if (product < 2) find_row(p, sm, lane);
+        k = from;
+        if (product < 2) find_row(p, sm);
     }
-    __device__ __forceinline__ void find_row(const Params &p, const Smem &sm, int lane)
+    __device__ __forceinline__ void find_row(const Params &p, const Smem &sm)
     {
-        const int64_t e = sm.expert[unit.lot];
-        const uint8_t *W = static_cast<const uint8_t *>(product == 0 ? p.a.W1 : p.a.W2);
-        const int64_t first = product == 0 ? e * 2 * p.a.I + unit.i * 8 : e * p.a.H + unit.i * 16;
-        row = W + (first + (lane >> 4)) * red + (lane & 15) * 16;
-        second = static_cast<int64_t>(product == 0 ? p.a.I : 8) * red;
+        const int e = sm.expert[unit.lot];
+        row = product == 0 ? e * 2 * p.a.I + unit.i * 8 : e * p.a.H + unit.i * 16;
+        second = row + (product == 0 ? p.a.I : 8);
     }
-    __device__ __forceinline__ void ask(const Params &p, const Smem &sm, int warp, int lane)
+    __device__ __forceinline__ void ask(const Params &p, const Maps &maps, const Smem &sm, int warp)
     {
-        if (product < 2) {
-            const uint32_t dst = ring + asked % kStages * kStageBytes;
-            if ((lane & 15) * 16 < red - k) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * kPairBytes),
-                                 "l"(row + k + (i < 4 ? 0 : second) + static_cast<int64_t>(2 * (i & 3)) * red)
-                                 : "memory");
-            }
-            k += kWide;
-            if (k >= red) {
-                k = 0;
-                unit.next(per);
-                if (unit.u < unit.to) {
-                    find_row(p, sm, lane);
-                } else {
-                    ++product;
-                    enter(p, sm, warp, lane);
-                }
-            }
+        if (product == 2) return;
+        const uint32_t s = asked % kStages;
+        if (elect_one()) {
+            const CUtensorMap *map = product == 0 ? &maps.w1 : &maps.w2;
+            const uint64_t keep = l2_policy_evict_normal();
+            mbar_arrive_expect_tx(full + s, kStageBytes);
+            tma_load_2d(ring + s * kStageBytes, map, full + s, k, row, keep);
+            tma_load_2d(ring + s * kStageBytes + kStageBytes / 2, map, full + s, k, second, keep);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        ++asked;
-    }
-    // Until the oldest piece that is not done has landed, for the whole warp.
-    __device__ __forceinline__ void wait() const
-    {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         __syncwarp();
+        ++asked;
+        k += kWide;
+        if (k < to) return;
+        k = from;
+        unit.next(per);
+        if (unit.u < unit.to) {
+            find_row(p, sm);
+        } else {
+            ++product;
+            enter(p, sm, warp);
+        }
     }
 };
 
@@ -493,35 +498,36 @@ struct Tokens {
     }
 };
 
-template <bool FIRST>
-__device__ __forceinline__ void unit_sums(const LayerArgs &a, const Smem &sm, const uint8_t *ring, Stream &st,
-                                          const Params &p, int warp, int lane, const uint8_t *src,
-                                          const uint8_t *src_scale, int lot, int T, int64_t sc0, int64_t sc1, bool &bad,
-                                          float (&acc)[4])
+__device__ __forceinline__ void unit_sums(bool first, const LayerArgs &a, const Smem &sm, volatile int *abort,
+                                          const Maps &maps, Stream &st, const Params &p, int warp, int lane, const uint8_t *src,
+                                          const uint8_t *src_scale, int lot, int T, int64_t sc0, int64_t sc1, int from,
+                                          int rblocks, bool &bad, float (&acc)[4])
 {
-    const int red = FIRST ? a.H : a.I, rblocks = red / 128, stride = scale_stride(red);
+    const int red = first ? a.H : a.I, stride = scale_stride(red);
     const int g = lane >> 2, t4 = lane & 3;
-    const void *W_scale = FIRST ? a.W1_scale : a.W2_scale;
-    const int16_t *who = (FIRST ? sm.token : sm.slot) + sm.first[lot];
+    const void *W_scale = first ? a.W1_scale : a.W2_scale;
+    const int16_t *slots = sm.slot + sm.first[lot];
+    auto who = [&](int col) { return first ? slots[col] / a.K : slots[col]; };
     // (places without a token take the lot's first one's: no sum crosses columns, and theirs goes nowhere)
-    const uint8_t *tok = src + static_cast<int64_t>(who[g < T ? g : 0]) * red + t4 * 16;
-    const uint8_t *ts0 = src_scale + who[t4 * 2 < T ? t4 * 2 : 0] * stride;
-    const uint8_t *ts1 = src_scale + who[t4 * 2 + 1 < T ? t4 * 2 + 1 : 0] * stride;
+    const uint8_t *tok = src + static_cast<int64_t>(who(g < T ? g : 0)) * red + t4 * 16;
+    const uint8_t *ts0 = src_scale + who(t4 * 2 < T ? t4 * 2 : 0) * stride;
+    const uint8_t *ts1 = src_scale + who(t4 * 2 + 1 < T ? t4 * 2 + 1 : 0) * stride;
 #pragma unroll
     for (int x = 0; x < 4; ++x) acc[x] = 0.f;
     uint32_t sw0 = 0, sw1 = 0;                       // bytes of block (32 at a time) + lane
-    const int lo_at = row_at(g) + t4 * 16, hi_at = row_at(g + 8) + t4 * 16;
+    const int lo_at = g * kWide + t4 * 16, hi_at = lo_at + 8 * kWide;
     // one piece, blocks k0 on, by the tokens `x`; those of the next piece are on their way meanwhile
     auto step = [&](const Tokens &x, Tokens &next, int k0) {
         const int nb = rblocks - k0;
         if (nb > kPieceBlocks) next.load(tok, ts0, ts1, k0 + kPieceBlocks, nb - kPieceBlocks);
-        if ((k0 & 31) == 0) {
-            const int b = k0 + lane < rblocks ? k0 + lane : rblocks - 1;
+        if ((k0 & 31) == 0 || k0 == from) {
+            const int at = (k0 & ~31) + lane, b = at < rblocks ? at : rblocks - 1;
             sw0 = load_scale_byte(W_scale, a.ue8m0, sc0 + b, bad);
-            sw1 = FIRST ? load_scale_byte(W_scale, a.ue8m0, sc1 + b, bad) : sw0;
+            sw1 = first ? load_scale_byte(W_scale, a.ue8m0, sc1 + b, bad) : sw0;
         }
-        st.wait();
-        const uint8_t *stage = ring + st.done % kStages * kStageBytes;
+        const uint32_t s = st.done % kStages;
+        warp_wait(st.full + s, (st.done / kStages) & 1u, abort);
+        const uint8_t *stage = st.ring + s * kStageBytes;
 #pragma unroll
         for (int b = 0; b < kPieceBlocks; ++b) {
             if (b >= nb) break;
@@ -530,7 +536,7 @@ __device__ __forceinline__ void unit_sums(const LayerArgs &a, const Smem &sm, co
             const uint4 hi0 = *reinterpret_cast<const uint4 *>(stage + hi_at + b * 128);
             const uint4 hi1 = *reinterpret_cast<const uint4 *>(stage + hi_at + b * 128 + 64);
             const float w0 = scale_value(__shfl_sync(0xffffffffu, sw0, (k0 + b) & 31));
-            const float w1 = FIRST ? scale_value(__shfl_sync(0xffffffffu, sw1, (k0 + b) & 31)) : w0;
+            const float w1 = first ? scale_value(__shfl_sync(0xffffffffu, sw1, (k0 + b) & 31)) : w0;
             // eight K = 16 steps in two chains
             float d[4] = {0.f, 0.f, 0.f, 0.f}, f[4] = {0.f, 0.f, 0.f, 0.f};
             mma_codes(d, lo0.x, hi0.x, x.b0[b].x);
@@ -549,19 +555,18 @@ __device__ __forceinline__ void unit_sums(const LayerArgs &a, const Smem &sm, co
         }
         __syncwarp();                                // all lanes have read the stage
         ++st.done;
-        st.ask(p, sm, warp, lane);
+        st.ask(p, maps, sm, warp);
     };
     Tokens x, y;
-    x.load(tok, ts0, ts1, 0, rblocks);
-    for (int k0 = 0; k0 < rblocks; k0 += 2 * kPieceBlocks) {
+    if (from < rblocks) x.load(tok, ts0, ts1, from, rblocks - from);
+    for (int k0 = from; k0 < rblocks; k0 += 2 * kPieceBlocks) {
         step(x, y, k0);
         if (k0 + kPieceBlocks < rblocks) step(y, x, k0 + kPieceBlocks);
     }
 }
 
 // A unit's sums to where they go: the activation of its 8 features, or 16 elements of y.
-template <bool FIRST>
-__device__ __forceinline__ void unit_out(const LayerArgs &a, const Smem &sm, float *dst, int lot, int i, int T, int lane,
+__device__ __forceinline__ void unit_out(bool first, const LayerArgs &a, const Smem &sm, float *dst, int lot, int i, int T, int lane,
                                          const float (&acc)[4])
 {
     const int g = lane >> 2, t4 = lane & 3;
@@ -570,7 +575,7 @@ __device__ __forceinline__ void unit_out(const LayerArgs &a, const Smem &sm, flo
         const int col = t4 * 2 + x;
         if (col >= T) continue;
         const int64_t slot = sm.slot[sm.first[lot] + col];
-        if (FIRST) {
+        if (first) {
             const float gate = acc[x], up = acc[2 + x];
             __stcg(dst + slot * a.I + i * 8 + g, gate / (1.f + __expf(-gate)) * up);
         } else {
@@ -580,32 +585,47 @@ __device__ __forceinline__ void unit_out(const LayerArgs &a, const Smem &sm, flo
     }
 }
 
-template <bool FIRST>
-__device__ __forceinline__ void product(const Params &p, Smem &sm, const uint8_t *ring, Stream &st)
+// (One body for both products, so that the second finds its code in the instruction cache: with a few units
+// for each warp, code that runs for the first time is what takes the time.)
+__device__ __forceinline__ void product(bool first, const Params &p, const Maps &maps, Smem &sm, Stream &st)
 {
     const LayerArgs &a = p.a;
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
-    const int rblocks = (FIRST ? a.H : a.I) / 128;
-    const int per = FIRST ? a.I / 8 : a.H / 16;      // units of a lot
+    const int rblocks = (first ? a.H : a.I) / 128;
+    const int per = first ? a.I / 8 : a.H / 16;      // units of a lot
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint8_t *src = ws + (FIRST ? p.l.x8 : p.l.a8), *src_scale = ws + (FIRST ? p.l.xs : p.l.as);
+    const uint8_t *src = ws + (first ? p.l.x8 : p.l.a8), *src_scale = ws + (first ? p.l.xs : p.l.as);
     float *act = reinterpret_cast<float *>(ws + p.l.a);
-    float *dst = FIRST ? act : reinterpret_cast<float *>(ws + p.l.y);
-    int from, to;
-    my_units(sm.active * per, from, to);
+    float *dst = first ? act : reinterpret_cast<float *>(ws + p.l.y);
+    const int from = sm.unit_from[first ? 0 : 1], to = sm.unit_to[first ? 0 : 1];
     bool bad = false;
+    const bool shared = sm.shared[first ? 0 : 1] != 0;
+    const int mid = middle(rblocks * 128) / 128;
+    const int k_from = shared && (warp & 1) ? mid : 0, k_to = shared && !(warp & 1) && mid < rblocks ? mid : rblocks;
     Units un;
-    un.start(sm.active, per, warp);
+    un.start(sm, first ? 0 : 1, per, warp);
     for (; un.u < to; un.next(per)) {
         const int lot = un.lot, i = un.i, e = sm.expert[lot], T = sm.first[lot + 1] - sm.first[lot];
         // where the scales of the unit's rows start; gate and up rows lie in different blocks
-        const int64_t sc0 = FIRST ? (static_cast<int64_t>(e) * (2 * a.I / 128) + i / 16) * rblocks
+        const int64_t sc0 = first ? (static_cast<int64_t>(e) * (2 * a.I / 128) + i / 16) * rblocks
                                   : (static_cast<int64_t>(e) * (a.H / 128) + i / 8) * rblocks;
-        const int64_t sc1 = FIRST ? sc0 + static_cast<int64_t>(a.I / 128) * rblocks : sc0;
+        const int64_t sc1 = first ? sc0 + static_cast<int64_t>(a.I / 128) * rblocks : sc0;
         float acc[4];
-        unit_sums<FIRST>(a, sm, ring, st, p, warp, lane, src, src_scale, lot, T, sc0, sc1, bad, acc);
-        unit_out<FIRST>(a, sm, dst, lot, i, T, lane, acc);
-        if (FIRST) {
+        unit_sums(first, a, sm, &sm.abort, maps, st, p, warp, lane, src, src_scale, lot, T, sc0, sc1, k_from, k_to,
+                         bad, acc);
+        if (shared) {
+            // (a warp has at most one shared unit of a product)
+            if (warp & 1) sm.half[warp >> 1][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            named_barrier_sync(1 + (warp >> 1), 64);
+            if (warp & 1) break;
+            const float4 h = sm.half[warp >> 1][lane];
+            acc[0] += h.x;
+            acc[1] += h.y;
+            acc[2] += h.z;
+            acc[3] += h.w;
+        }
+        unit_out(first, a, sm, dst, lot, i, T, lane, acc);
+        if (first) {
             // Whoever completes the sixteen units of a 128-block of the activation turns it into E4M3.  The
             // units that this CTA has of it are counted here, CTAs that share one meet in the workspace.
             const int b0 = un.u & ~15, b1 = b0 + 16;   // (a lot's units are whole blocks)
@@ -681,16 +701,21 @@ __device__ void combine(const Params &p)
     }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const Params p)
+__global__ void __launch_bounds__(kThreads, 1)
+    moe_layer_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Smem &sm = *reinterpret_cast<Smem *>(ring + kRingBytes);
     Header *hdr = static_cast<Header *>(p.a.workspace);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
 
     if (threadIdx.x == 0) {
+        for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&sm.full[0][0] + i, 1);
         sm.abort = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&maps.w1);
+        tma_prefetch_desc(&maps.w2);
     }
     for (int i = threadIdx.x; i < kMostBlocks; i += kThreads) sm.done[i] = 0;
     __syncthreads();
@@ -709,20 +734,28 @@ __global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const Params p)
         __syncthreads();
     else
         grid_barrier(hdr, 1, sm);
+    fence_proxy_async_smem();   // the ring's memory passes from these threads to the copies
     make_lists(p, sm);
     Stream st;
     st.asked = st.done = 0;
-    uint8_t *mine = ring + warp * kStages * kStageBytes;
-    st.ring = smem_u32(mine) + (lane >> 4) * (kWide + 64) + (lane & 15) * 16;
+    st.ring = ring + warp * kStages * kStageBytes;
+    st.full = sm.full[warp];
     st.product = 0;
-    st.enter(p, sm, warp, lane);
-    for (int i = 0; i < kStages; ++i) st.ask(p, sm, warp, lane);
-    product<true>(p, sm, mine, st);
-    grid_barrier(hdr, 2, sm);
-    product<false>(p, sm, mine, st);
-    asm volatile("cp.async.wait_all;" ::: "memory");   // (given up or not, none is in flight at the end)
-    grid_barrier(hdr, 3, sm);
+    st.enter(p, sm, warp);
+    for (int i = 0; i < kStages; ++i) st.ask(p, maps, sm, warp);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        product(i == 0, p, maps, sm, st);
+        grid_barrier(hdr, 2 + i, sm);
+    }
     combine(p);
+    if (*const_cast<volatile int *>(&sm.abort) != 0) {
+        // let the copies in flight land before the CTA ends
+        for (uint32_t x = st.asked > kStages ? st.asked - kStages : 0u; x < st.asked; ++x) {
+            volatile int no_abort = 0;
+            mbar_wait_bounded(st.full + x % kStages, (x / kStages) & 1u, &no_abort);
+        }
+    }
     __syncthreads();
     if (threadIdx.x == 0) {
         if (sm.abort) report_status(p.a.status, MOE_ERR_TIMEOUT);
@@ -757,7 +790,14 @@ cudaError_t launch_layer(const LayerArgs &a, cudaStream_t stream)
         if (err != cudaSuccess) return err;
         done.fetch_or(bit, std::memory_order_relaxed);
     }
-    Params p{a, make_layout(a.N, a.H, a.I, a.E, a.K)};
+    Maps maps;
+    const uint64_t d1[2] = {static_cast<uint64_t>(a.H), static_cast<uint64_t>(a.E) * 2 * a.I};
+    const uint64_t d2[2] = {static_cast<uint64_t>(a.I), static_cast<uint64_t>(a.E) * a.H};
+    const uint32_t box[2] = {kWide, 8};
+    if (!encode_map(&maps.w1, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.W1, 2, d1, box, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_map(&maps.w2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.W2, 2, d2, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cudaErrorInvalidValue;
+    const Params p{a, make_layout(a.N, a.H, a.I, a.E, a.K)};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(device_sm_count(dev));
     cfg.blockDim = dim3(kThreads);
@@ -768,7 +808,7 @@ cudaError_t launch_layer(const LayerArgs &a, cudaStream_t stream)
     at[0].val.cooperative = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, moe_layer_kernel, p);
+    return cudaLaunchKernelEx(&cfg, moe_layer_kernel, maps, p);
 }
 
 }  // namespace moe
