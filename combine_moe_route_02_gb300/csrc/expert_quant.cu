@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kActThreads)
         bf16x8_to_f32(g[i], fg);
         bf16x8_to_f32(u[i], fu);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) a[x] = fg[x] / (1.f + __expf(-fg[x])) * fu[x];
+        for (int x = 0; x < 8; ++x) a[x] = __fdividef(fg[x], 1.f + __expf(-fg[x])) * fu[x];
         uint32_t sa, sg, su;
         const uint2 qa = quant_block(a, sa);
         uint2 qg = make_uint2(0, 0), qu = make_uint2(0, 0);
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kActThreads)
         codes8_to_f32(u[i], scale_value(su[i]), fu);
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-            const float s = 1.f / (1.f + __expf(-fg[x]));
+            const float s = __fdividef(1.f, 1.f + __expf(-fg[x]));
             const float as = fa[x] * s;
             du[x] = as * fg[x];
             dg[x] = as * fu[x] * (1.f + fg[x] * (1.f - s));
