@@ -35,27 +35,50 @@ __device__ __forceinline__ float amax8(const float (&f)[8])
     return m;
 }
 
-// Eight values of a 1x128 block held by 16 lanes: their codes, and the block's scale byte.
-__device__ __forceinline__ uint2 quant_block(const float (&f)[8], uint32_t &byte)
+// 16 values of a 1x128 block held by 8 lanes: their codes, and the block's scale byte.
+__device__ __forceinline__ uint4 quant_block(const float (&f)[16], uint32_t &byte)
 {
-    float m = amax8(f);
+    float m = 0.f;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(f[i]));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
     byte = block_scale_byte(m);
     const float inv = scale_reciprocal(byte);
-    return make_uint2(f32x4_to_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                      f32x4_to_e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        q[i] = f32x4_to_e4m3x4(f[4 * i] * inv, f[4 * i + 1] * inv, f[4 * i + 2] * inv, f[4 * i + 3] * inv);
+    return make_uint4(q[0], q[1], q[2], q[3]);
 }
 
-__device__ __forceinline__ void codes8_to_f32(const uint2 &q, float s, float (&f)[8])
+__device__ __forceinline__ void codes_to_f32(const uint4 &q, float s, float (&f)[16])
 {
-    const uint32_t w[4] = {q.x & 0xFFFFu, q.x >> 16, q.y & 0xFFFFu, q.y >> 16};
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 v = e4m3x2_to_f32x2(w[i]);
-        f[2 * i] = v.x * s;
-        f[2 * i + 1] = v.y * s;
+        const float2 lo = e4m3x2_to_f32x2(w[i] & 0xFFFFu), hi = e4m3x2_to_f32x2(w[i] >> 16);
+        f[4 * i] = lo.x * s;
+        f[4 * i + 1] = lo.y * s;
+        f[4 * i + 2] = hi.x * s;
+        f[4 * i + 3] = hi.y * s;
     }
+}
+
+__device__ __forceinline__ void bf16x16_to_f32(const uint4 &a, const uint4 &b, float (&f)[16])
+{
+    bf16x8_to_f32(a, *reinterpret_cast<float (*)[8]>(&f[0]));
+    bf16x8_to_f32(b, *reinterpret_cast<float (*)[8]>(&f[8]));
+}
+
+// 1 / (1 + exp(-g)) by the approximate exponential and reciprocal (2 units in the last place each); 0 where
+// the exponential overflows.
+__device__ __forceinline__ float sigmoid(float g)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504088896340736f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
 }
 
 // ---------------------------------------------------------------------------
@@ -108,12 +131,14 @@ __global__ void __launch_bounds__(kQwThreads)
 }
 
 // ---------------------------------------------------------------------------
-// Gated activation.  A unit is one row's block of 128 columns of A, held by 16
-// lanes of 8 columns; unit u lies in row u / nb (nb = I / 128), its columns of A
-// start at 128 u, those of the gate at 128 u + row * I, of the up half I further.
+// Gated activation.  A unit is one row's block of 128 columns of A, held by 8 lanes
+// of 16 columns; unit u lies in row u / nb (nb = I / 128), its columns of A start at
+// 128 u, those of the gate at 128 u + row * I, of the up half I further.  The bound is
+// the memory's, but not by much: a lane of 16 columns instead of 8 halves the share of
+// the scales and shuffles (131072 x 1024: 184 us with 8).
 // ---------------------------------------------------------------------------
 constexpr int kActThreads = 256;
-constexpr int kUnits = 2;   // units per half warp, all loaded before the first is used
+constexpr int kLanes = 8;
 
 struct Rows {
     int64_t units;
@@ -124,52 +149,39 @@ struct Rows {
     }
 };
 
+template <bool kKeep>
 __global__ void __launch_bounds__(kActThreads)
     swiglu_kernel(const __nv_bfloat16 *__restrict__ GU, const Rows d, uint8_t *__restrict__ A, void *A_scale,
                   uint8_t *__restrict__ K, void *K_scale, int ue8m0)
 {
-    const int l = threadIdx.x & 15;
-    const int64_t u0 = (static_cast<int64_t>(blockIdx.x) * (kActThreads / 16)) * kUnits + (threadIdx.x >> 4);
-    uint4 g[kUnits], u[kUnits];
-    int64_t row[kUnits];
+    const int l = threadIdx.x & (kLanes - 1);
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kActThreads / kLanes) + threadIdx.x / kLanes;
+    const bool there = unit < d.units;
+    const int64_t u = there ? unit : d.units - 1, row = d.row(u);
+    const uint4 *src = reinterpret_cast<const uint4 *>(GU + u * 128 + row * d.I + l * 16);
+    const uint4 g0 = __ldcs(src), g1 = __ldcs(src + 1), u0 = __ldcs(src + d.I / 8), u1 = __ldcs(src + d.I / 8 + 1);
+    float fg[16], fu[16], a[16];
+    bf16x16_to_f32(g0, g1, fg);
+    bf16x16_to_f32(u0, u1, fu);
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const int64_t unit = u0 + i * (kActThreads / 16);
-        g[i] = u[i] = make_uint4(0, 0, 0, 0);
-        row[i] = 0;
-        if (unit < d.units) {
-            row[i] = d.row(unit);
-            const __nv_bfloat16 *src = GU + unit * 128 + row[i] * d.I + l * 8;
-            g[i] = __ldcs(reinterpret_cast<const uint4 *>(src));
-            u[i] = __ldcs(reinterpret_cast<const uint4 *>(src + d.I));
-        }
+    for (int x = 0; x < 16; ++x) a[x] = fg[x] * sigmoid(fg[x]) * fu[x];
+    uint32_t sa, sg, su;
+    const uint4 qa = quant_block(a, sa);
+    uint4 qg, qu;
+    if (kKeep) {
+        qg = quant_block(fg, sg);
+        qu = quant_block(fu, su);
     }
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const int64_t unit = u0 + i * (kActThreads / 16);
-        float fg[8], fu[8], a[8];
-        bf16x8_to_f32(g[i], fg);
-        bf16x8_to_f32(u[i], fu);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) a[x] = __fdividef(fg[x], 1.f + __expf(-fg[x])) * fu[x];
-        uint32_t sa, sg, su;
-        const uint2 qa = quant_block(a, sa);
-        uint2 qg = make_uint2(0, 0), qu = make_uint2(0, 0);
-        if (K) {
-            qg = quant_block(fg, sg);
-            qu = quant_block(fu, su);
-        }
-        if (unit >= d.units) continue;
-        *reinterpret_cast<uint2 *>(A + unit * 128 + l * 8) = qa;
-        if (l == 0) store_scale(A_scale, ue8m0, unit, sa);
-        if (K) {
-            uint8_t *dst = K + unit * 128 + row[i] * d.I + l * 8;
-            *reinterpret_cast<uint2 *>(dst) = qg;
-            *reinterpret_cast<uint2 *>(dst + d.I) = qu;
-            if (l == 0) {
-                store_scale(K_scale, ue8m0, unit + row[i] * d.nb, sg);
-                store_scale(K_scale, ue8m0, unit + row[i] * d.nb + d.nb, su);
-            }
+    if (!there) return;
+    *reinterpret_cast<uint4 *>(A + u * 128 + l * 16) = qa;
+    if (l == 0) store_scale(A_scale, ue8m0, u, sa);
+    if (kKeep) {
+        uint8_t *dst = K + u * 128 + row * d.I + l * 16;
+        *reinterpret_cast<uint4 *>(dst) = qg;
+        *reinterpret_cast<uint4 *>(dst + d.I) = qu;
+        if (l == 0) {
+            store_scale(K_scale, ue8m0, u + row * d.nb, sg);
+            store_scale(K_scale, ue8m0, u + row * d.nb + d.nb, su);
         }
     }
 }
@@ -179,63 +191,45 @@ __global__ void __launch_bounds__(kActThreads)
                            int k_ue8m0, const Rows d, __nv_bfloat16 *__restrict__ dGU, uint8_t *__restrict__ Q,
                            void *Q_scale, int ue8m0, int32_t *status)
 {
-    const int l = threadIdx.x & 15;
-    const int64_t u0 = (static_cast<int64_t>(blockIdx.x) * (kActThreads / 16)) * kUnits + (threadIdx.x >> 4);
-    uint4 da[kUnits];
-    uint2 g[kUnits], u[kUnits];
-    uint32_t sg[kUnits], su[kUnits];
-    int64_t row[kUnits];
+    const int l = threadIdx.x & (kLanes - 1);
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kActThreads / kLanes) + threadIdx.x / kLanes;
+    const bool there = unit < d.units;
+    const int64_t u = there ? unit : d.units - 1, row = d.row(u), at = u * 128 + row * d.I + l * 16;
+    const uint4 *da = reinterpret_cast<const uint4 *>(dA + u * 128 + l * 16);
+    const uint4 a0 = __ldcs(da), a1 = __ldcs(da + 1);
+    const uint4 qg = __ldcs(reinterpret_cast<const uint4 *>(K + at));
+    const uint4 qu = __ldcs(reinterpret_cast<const uint4 *>(K + at + d.I));
     bool bad = false;
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const int64_t unit = u0 + i * (kActThreads / 16);
-        da[i] = make_uint4(0, 0, 0, 0);
-        g[i] = u[i] = make_uint2(0, 0);
-        sg[i] = su[i] = 127;
-        row[i] = 0;
-        if (unit < d.units) {
-            row[i] = d.row(unit);
-            const uint8_t *src = K + unit * 128 + row[i] * d.I + l * 8;
-            da[i] = __ldcs(reinterpret_cast<const uint4 *>(dA + unit * 128 + l * 8));
-            g[i] = __ldcs(reinterpret_cast<const uint2 *>(src));
-            u[i] = __ldcs(reinterpret_cast<const uint2 *>(src + d.I));
-            sg[i] = load_scale_byte(K_scale, k_ue8m0, unit + row[i] * d.nb, bad);
-            su[i] = load_scale_byte(K_scale, k_ue8m0, unit + row[i] * d.nb + d.nb, bad);
-        }
-    }
+    const uint32_t sg = load_scale_byte(K_scale, k_ue8m0, u + row * d.nb, bad);
+    const uint32_t su = load_scale_byte(K_scale, k_ue8m0, u + row * d.nb + d.nb, bad);
     if (bad) report_status(status, MOE_ERR_BAD_SCALE);
+    float fa[16], dg[16], du[16];
+    bf16x16_to_f32(a0, a1, fa);
+    codes_to_f32(qg, scale_value(sg), dg);
+    codes_to_f32(qu, scale_value(su), du);
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const int64_t unit = u0 + i * (kActThreads / 16);
-        float fa[8], fg[8], fu[8], dg[8], du[8];
-        bf16x8_to_f32(da[i], fa);
-        codes8_to_f32(g[i], scale_value(sg[i]), fg);
-        codes8_to_f32(u[i], scale_value(su[i]), fu);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            const float s = __fdividef(1.f, 1.f + __expf(-fg[x]));
-            const float as = fa[x] * s;
-            du[x] = as * fg[x];
-            dg[x] = as * fu[x] * (1.f + fg[x] * (1.f - s));
-        }
-        uint32_t bg = 0, bu = 0;
-        uint2 qg = make_uint2(0, 0), qu = make_uint2(0, 0);
-        if (Q) {
-            qg = quant_block(dg, bg);
-            qu = quant_block(du, bu);
-        }
-        if (unit >= d.units) continue;
-        const int64_t at = unit * 128 + row[i] * d.I + l * 8;
-        if (dGU) {
-            *reinterpret_cast<uint4 *>(dGU + at) = f32_to_bf16x8(dg);
-            *reinterpret_cast<uint4 *>(dGU + at + d.I) = f32_to_bf16x8(du);
-        }
-        if (Q) {
-            *reinterpret_cast<uint2 *>(Q + at) = qg;
-            *reinterpret_cast<uint2 *>(Q + at + d.I) = qu;
+    for (int x = 0; x < 16; ++x) {
+        const float g = dg[x], up = du[x], s = sigmoid(g), as = fa[x] * s;
+        du[x] = as * g;
+        dg[x] = as * up * (1.f + g * (1.f - s));
+    }
+    if (dGU && there) {
+        uint4 *dst = reinterpret_cast<uint4 *>(dGU + at);
+        dst[0] = f32_to_bf16x8(*reinterpret_cast<float (*)[8]>(&dg[0]));
+        dst[1] = f32_to_bf16x8(*reinterpret_cast<float (*)[8]>(&dg[8]));
+        dst += d.I / 8;
+        dst[0] = f32_to_bf16x8(*reinterpret_cast<float (*)[8]>(&du[0]));
+        dst[1] = f32_to_bf16x8(*reinterpret_cast<float (*)[8]>(&du[8]));
+    }
+    if (Q) {
+        uint32_t bg, bu;
+        const uint4 cg = quant_block(dg, bg), cu = quant_block(du, bu);
+        if (there) {
+            *reinterpret_cast<uint4 *>(Q + at) = cg;
+            *reinterpret_cast<uint4 *>(Q + at + d.I) = cu;
             if (l == 0) {
-                store_scale(Q_scale, ue8m0, unit + row[i] * d.nb, bg);
-                store_scale(Q_scale, ue8m0, unit + row[i] * d.nb + d.nb, bu);
+                store_scale(Q_scale, ue8m0, u + row * d.nb, bg);
+                store_scale(Q_scale, ue8m0, u + row * d.nb + d.nb, bu);
             }
         }
     }
@@ -245,7 +239,7 @@ Rows make_rows(int64_t R, int I) { return Rows{R * (I / 128), I / 128, I}; }
 
 unsigned act_grid(const Rows &d)
 {
-    const int64_t per = static_cast<int64_t>(kActThreads / 16) * kUnits;
+    const int64_t per = kActThreads / kLanes;
     return static_cast<unsigned>((d.units + per - 1) / per);
 }
 
@@ -264,9 +258,9 @@ cudaError_t launch_swiglu(const void *GU, int64_t R, int I, void *A_fp8, void *A
                           int ue8m0, cudaStream_t stream)
 {
     const Rows d = make_rows(R, I);
-    swiglu_kernel<<<act_grid(d), kActThreads, 0, stream>>>(static_cast<const __nv_bfloat16 *>(GU), d,
-                                                           static_cast<uint8_t *>(A_fp8), A_scale,
-                                                           static_cast<uint8_t *>(GU_fp8), GU_scale, ue8m0);
+    const auto kernel = GU_fp8 ? swiglu_kernel<true> : swiglu_kernel<false>;
+    kernel<<<act_grid(d), kActThreads, 0, stream>>>(static_cast<const __nv_bfloat16 *>(GU), d, static_cast<uint8_t *>(A_fp8),
+                                                    A_scale, static_cast<uint8_t *>(GU_fp8), GU_scale, ue8m0);
     return cudaGetLastError();
 }
 
