@@ -117,6 +117,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
     return warp_wait_slow(bar, parity, abort);
 }
+// TMA load of a box with the default cache policy.
+__device__ __forceinline__ void tma_load_2d_plain(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int32_t c0, int32_t c1)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                     smem_u32(smem_dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 // TMA store of a box (what lies outside the tensor is left out), in this thread's bulk async-group.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *smem_src, int32_t c0, int32_t c1, int32_t c2)
 {

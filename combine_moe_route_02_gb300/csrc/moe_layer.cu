@@ -34,6 +34,7 @@ constexpr int kWide = 256;                    // reduction bytes of a row in one
 constexpr int kPieceBlocks = kWide / 128;
 constexpr int kStages = 3;                    // of each streaming warp
 constexpr int kStageBytes = 16 * kWide;
+constexpr int kTaken = 8;                     // units (and ends of products) that a warp may be ahead of its work
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kMostBlocks = 256;              // 128-blocks of the activation that a CTA counts for itself
 // An expert's tokens are taken 8 at a time, each lot as an entry of its own: a second one reads the expert's
@@ -53,6 +54,8 @@ struct Smem {
     int active;                               // lots of all touched experts
     int unit_from[2], unit_to[2];             // the units of each product that this CTA takes
     int shared[2];                            // whether two warps share each of them, a half of its reduction each
+    int next[2];                              // the first of them that no warp has taken
+    int taken[kWarps][kTaken];                // each warp's own, in order, unit_to behind a product's last
     union {
         struct {
             uint32_t mask[kMaxE][2];          // tokens of each expert
@@ -370,7 +373,7 @@ __device__ void make_lists(const Params &p, Smem &sm)
         if (lane < 2) {
             // (below 2^31: at most 384 lots of 8192 units, and some hundreds of CTAs)
             const unsigned total = active * (lane == 0 ? p.a.I / 8 : p.a.H / 16), ctas = gridDim.x;
-            sm.unit_from[lane] = total / ctas * blockIdx.x + total % ctas * blockIdx.x / ctas;
+            sm.next[lane] = sm.unit_from[lane] = total / ctas * blockIdx.x + total % ctas * blockIdx.x / ctas;
             sm.unit_to[lane] = total / ctas * (blockIdx.x + 1) + total % ctas * (blockIdx.x + 1) / ctas;
             // where no CTA has more than half as many units as warps (one token, top 8 of 128 experts of
             // 2048 x 1024: 33 us, 41 without)
@@ -398,29 +401,6 @@ __device__ void make_lists(const Params &p, Smem &sm)
 // Where the second half of a shared unit starts: whole pieces.
 __device__ __forceinline__ int middle(int red) { return ((red + kWide - 1) / kWide + 1) / 2 * kWide; }
 
-// A streaming warp's walk over its units, u0, u0 + kWarps, ... of the CTA's: the lot of each and its place
-// in the lot.
-struct Units {
-    int u, to, lot, i;
-
-    __device__ __forceinline__ void start(const Smem &sm, int product, int per, int warp)
-    {
-        u = sm.unit_from[product] + (sm.shared[product] ? warp >> 1 : warp);
-        to = sm.unit_to[product];
-        lot = static_cast<unsigned>(u) / static_cast<unsigned>(per);
-        i = u - lot * per;
-    }
-    __device__ __forceinline__ void next(int per)
-    {
-        u += kWarps;
-        i += kWarps;
-        while (i >= per) {
-            i -= per;
-            ++lot;
-        }
-    }
-};
-
 // What the warp asks for next: first W1's pieces, then W2's.  A piece is two TMA boxes of 8 rows x 256 bytes.
 // (As one bulk copy per row, issued by sixteen lanes, asking took 1300 cycles a piece, as eight asynchronous
 // 16-byte copies per lane 400 to 750: more than the work on the piece.)
@@ -430,52 +410,63 @@ struct Stream {
     uint32_t asked, done;
     int product, k, red, per;
     int from, to;                 // the part of a row that this warp takes
-    Units unit;
     int row, second;              // the first row of each box
+    uint32_t taken, worked;       // units (and ends) taken, and worked on
 
-    __device__ __forceinline__ void enter(const Params &p, const Smem &sm, int warp)
+    // The next unit: whichever of the CTA's no warp has taken yet (a fixed share for each warp left some
+    // with a seventh unit where others had six).  Behind a product's last, its end is noted and the next
+    // product entered; a half without pieces is only noted.
+    __device__ __forceinline__ void take(const Params &p, Smem &sm, int warp, int lane, bool enter)
     {
-        for (; product < 2; ++product) {
-            red = product == 0 ? p.a.H : p.a.I;
-            per = product == 0 ? p.a.I / 8 : p.a.H / 16;
-            unit.start(sm, product, per, warp);
-            const bool shared = sm.shared[product] != 0;
-            from = shared && (warp & 1) ? middle(red) : 0;
-            to = shared && !(warp & 1) && middle(red) < red ? middle(red) : red;
-            if (unit.u < unit.to && from < to) break;
+        while (product < 2) {
+            if (enter) {
+                red = product == 0 ? p.a.H : p.a.I;
+                per = product == 0 ? p.a.I / 8 : p.a.H / 16;
+                const bool shared = sm.shared[product] != 0;
+                from = shared && (warp & 1) ? middle(red) : 0;
+                to = shared && !(warp & 1) && middle(red) < red ? middle(red) : red;
+            }
+            const int end = sm.unit_to[product];
+            int u = end;
+            if (!sm.shared[product]) {
+                if (lane == 0) {
+                    u = atomicAdd(&sm.next[product], 1);
+                    u = u < end ? u : end;
+                }
+                u = __shfl_sync(0xffffffffu, u, 0);
+            } else if (enter && sm.unit_from[product] + (warp >> 1) < end) {
+                u = sm.unit_from[product] + (warp >> 1);    // (at most one)
+            }
+            if (lane == 0) sm.taken[warp][taken % kTaken] = u;
+            ++taken;
+            enter = u == end;
+            if (enter) {
+                ++product;
+                continue;
+            }
+            if (from >= to) continue;
+            const int lot = static_cast<unsigned>(u) / static_cast<unsigned>(per), i = u - lot * per, e = sm.expert[lot];
+            row = product == 0 ? e * 2 * p.a.I + i * 8 : e * p.a.H + i * 16;
+            second = row + (product == 0 ? p.a.I : 8);
+            break;
         }
         k = from;
-        if (product < 2) find_row(p, sm);
+        __syncwarp();
     }
-    __device__ __forceinline__ void find_row(const Params &p, const Smem &sm)
-    {
-        const int e = sm.expert[unit.lot];
-        row = product == 0 ? e * 2 * p.a.I + unit.i * 8 : e * p.a.H + unit.i * 16;
-        second = row + (product == 0 ? p.a.I : 8);
-    }
-    __device__ __forceinline__ void ask(const Params &p, const Maps &maps, const Smem &sm, int warp)
+    __device__ __forceinline__ void ask(const Params &p, const Maps &maps, Smem &sm, int warp, int lane)
     {
         if (product == 2) return;
         const uint32_t s = asked % kStages;
         if (elect_one()) {
             const CUtensorMap *map = product == 0 ? &maps.w1 : &maps.w2;
-            const uint64_t keep = l2_policy_evict_normal();
             mbar_arrive_expect_tx(full + s, kStageBytes);
-            tma_load_2d(ring + s * kStageBytes, map, full + s, k, row, keep);
-            tma_load_2d(ring + s * kStageBytes + kStageBytes / 2, map, full + s, k, second, keep);
+            tma_load_2d_plain(ring + s * kStageBytes, map, full + s, k, row);
+            tma_load_2d_plain(ring + s * kStageBytes + kStageBytes / 2, map, full + s, k, second);
         }
         __syncwarp();
         ++asked;
         k += kWide;
-        if (k < to) return;
-        k = from;
-        unit.next(per);
-        if (unit.u < unit.to) {
-            find_row(p, sm);
-        } else {
-            ++product;
-            enter(p, sm, warp);
-        }
+        if (k >= to) take(p, sm, warp, lane, false);
     }
 };
 
@@ -498,7 +489,7 @@ struct Tokens {
     }
 };
 
-__device__ __forceinline__ void unit_sums(bool first, const LayerArgs &a, const Smem &sm, volatile int *abort,
+__device__ __forceinline__ void unit_sums(bool first, const LayerArgs &a, Smem &sm, volatile int *abort,
                                           const Maps &maps, Stream &st, const Params &p, int warp, int lane, const uint8_t *src,
                                           const uint8_t *src_scale, int lot, int T, int64_t sc0, int64_t sc1, int from,
                                           int rblocks, bool &bad, float (&acc)[4])
@@ -555,7 +546,7 @@ __device__ __forceinline__ void unit_sums(bool first, const LayerArgs &a, const 
         }
         __syncwarp();                                // all lanes have read the stage
         ++st.done;
-        st.ask(p, maps, sm, warp);
+        st.ask(p, maps, sm, warp, lane);
     };
     Tokens x, y;
     if (from < rblocks) x.load(tok, ts0, ts1, from, rblocks - from);
@@ -602,10 +593,12 @@ __device__ __forceinline__ void product(bool first, const Params &p, const Maps 
     const bool shared = sm.shared[first ? 0 : 1] != 0;
     const int mid = middle(rblocks * 128) / 128;
     const int k_from = shared && (warp & 1) ? mid : 0, k_to = shared && !(warp & 1) && mid < rblocks ? mid : rblocks;
-    Units un;
-    un.start(sm, first ? 0 : 1, per, warp);
-    for (; un.u < to; un.next(per)) {
-        const int lot = un.lot, i = un.i, e = sm.expert[lot], T = sm.first[lot + 1] - sm.first[lot];
+    for (;;) {
+        const int u = sm.taken[warp][st.worked % kTaken];
+        ++st.worked;
+        if (u == to) break;
+        const int lot = static_cast<unsigned>(u) / static_cast<unsigned>(per), i = u - lot * per;
+        const int e = sm.expert[lot], T = sm.first[lot + 1] - sm.first[lot];
         // where the scales of the unit's rows start; gate and up rows lie in different blocks
         const int64_t sc0 = first ? (static_cast<int64_t>(e) * (2 * a.I / 128) + i / 16) * rblocks
                                   : (static_cast<int64_t>(e) * (a.H / 128) + i / 8) * rblocks;
@@ -617,7 +610,7 @@ __device__ __forceinline__ void product(bool first, const Params &p, const Maps 
             // (a warp has at most one shared unit of a product)
             if (warp & 1) sm.half[warp >> 1][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
             named_barrier_sync(1 + (warp >> 1), 64);
-            if (warp & 1) break;
+            if (warp & 1) continue;
             const float4 h = sm.half[warp >> 1][lane];
             acc[0] += h.x;
             acc[1] += h.y;
@@ -628,9 +621,9 @@ __device__ __forceinline__ void product(bool first, const Params &p, const Maps 
         if (first) {
             // Whoever completes the sixteen units of a 128-block of the activation turns it into E4M3.  The
             // units that this CTA has of it are counted here, CTAs that share one meet in the workspace.
-            const int b0 = un.u & ~15, b1 = b0 + 16;   // (a lot's units are whole blocks)
+            const int b0 = u & ~15, b1 = b0 + 16;   // (a lot's units are whole blocks)
             const int ours = (b1 < to ? b1 : to) - (b0 > from ? b0 : from);
-            const int at = (un.u >> 4) - (from >> 4);
+            const int at = (u >> 4) - (from >> 4);
             const bool count_here = ((to - 1) >> 4) - (from >> 4) < kMostBlocks;
             int last = 0;
             __threadfence_block();
@@ -639,7 +632,7 @@ __device__ __forceinline__ void product(bool first, const Params &p, const Maps 
                 const int n = count_here ? ours : 1;
                 last = !count_here || atomicAdd(&sm.done[at], 1) == ours - 1;
                 if (last && n != 16) {
-                    unsigned *counter = reinterpret_cast<unsigned *>(ws + p.l.counters) + (un.u >> 4);
+                    unsigned *counter = reinterpret_cast<unsigned *>(ws + p.l.counters) + (u >> 4);
                     __threadfence();
                     last = atomicAdd(counter, n) + n == 16;
                     if (last) *counter = 0;
@@ -708,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Smem &sm = *reinterpret_cast<Smem *>(ring + kRingBytes);
     Header *hdr = static_cast<Header *>(p.a.workspace);
-    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&sm.full[0][0] + i, 1);
@@ -741,8 +734,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     st.ring = ring + warp * kStages * kStageBytes;
     st.full = sm.full[warp];
     st.product = 0;
-    st.enter(p, sm, warp);
-    for (int i = 0; i < kStages; ++i) st.ask(p, maps, sm, warp);
+    st.taken = st.worked = 0;
+    st.take(p, sm, warp, lane, true);
+    for (int i = 0; i < kStages; ++i) st.ask(p, maps, sm, warp, lane);
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
         product(i == 0, p, maps, sm, st);
