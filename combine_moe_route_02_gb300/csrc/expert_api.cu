@@ -13,6 +13,10 @@ inline bool format_ok(int f) { return f == MOE_SCALE_FP32 || f == MOE_SCALE_UE8M
 // scales: floats are 4-byte aligned, bytes need nothing
 inline bool scale_aligned(const void *p, int f) { return f == MOE_SCALE_UE8M0 || aligned(p, 4); }
 inline bool rows_ok(int64_t R) { return R >= 0 && R < INT_MAX; }
+// sides of a weight: what the kernels' 32-bit tile numbers hold with 256 experts
+inline bool sides_ok(int rows, int cols) { return rows >= 1 && cols >= 1 && rows <= (1 << 18) && cols <= (1 << 18); }
+// blocks of 128 columns in all rows, and a grid of one CTA for 32 of them
+inline bool blocks_ok(int64_t R, int I) { return R * (I / 128) < (int64_t(1) << 36); }
 
 // The status of a launch; a device that cannot run these kernels is not a CUDA failure.
 moe_status launched(cudaError_t e) { return e == cudaErrorNotSupported ? MOE_ERR_UNSUPPORTED : from_cuda(e); }
@@ -39,7 +43,8 @@ moe_status moe_expert_gemm(const void *X_fp8, const void *X_scale, int x_scale_f
                            int rows, int cols, int transpose, void *Y, int32_t *status_word, moe_stream_t stream)
 {
     NvtxRange nvtx_range("moe_expert_gemm");
-    if (E < 1 || E > 256 || !rows_ok(R) || rows < 1 || cols < 1) return MOE_ERR_INVALID_ARG;
+    if (E < 1 || E > 256 || !rows_ok(R) || !sides_ok(rows, cols)) return MOE_ERR_INVALID_ARG;
+    if ((R / 224 + 256) * ((rows > cols ? rows : cols) / 256 + 1) > INT_MAX) return MOE_ERR_INVALID_ARG;  // tiles
     if (!format_ok(x_scale_format) || !format_ok(w_scale_format)) return MOE_ERR_INVALID_ARG;
     const int red = transpose ? rows : cols, out = transpose ? cols : rows;
     if (red % 128 != 0 || out % 16 != 0) return MOE_ERR_INVALID_ARG;
@@ -59,7 +64,7 @@ moe_status moe_expert_wgrad(const void *dY, const void *X_fp8, const void *X_sca
                             void *dW, int dw_bf16, int32_t *status_word, moe_stream_t stream)
 {
     NvtxRange nvtx_range("moe_expert_wgrad");
-    if (E < 1 || E > 256 || !rows_ok(R) || rows < 1 || cols < 1 || !format_ok(x_scale_format))
+    if (E < 1 || E > 256 || !rows_ok(R) || !sides_ok(rows, cols) || !format_ok(x_scale_format))
         return MOE_ERR_INVALID_ARG;
     if (rows % 8 != 0 || cols % 128 != 0) return MOE_ERR_INVALID_ARG;
     if (!expert_offsets && E != 1) return MOE_ERR_INVALID_ARG;
@@ -77,7 +82,8 @@ moe_status moe_swiglu(const void *GU, int64_t R, int I, void *A_fp8, void *A_sca
                       int scale_format, moe_stream_t stream)
 {
     NvtxRange nvtx_range("moe_swiglu");
-    if (!rows_ok(R) || I < 1 || I > (1 << 20) || I % 128 != 0 || !format_ok(scale_format)) return MOE_ERR_INVALID_ARG;
+    if (!rows_ok(R) || I < 1 || I > (1 << 20) || I % 128 != 0 || !blocks_ok(R, I) || !format_ok(scale_format))
+        return MOE_ERR_INVALID_ARG;
     if ((GU_fp8 == nullptr) != (GU_scale == nullptr)) return MOE_ERR_INVALID_ARG;
     if (R == 0) return MOE_OK;
     if (!GU || !A_fp8 || !A_scale) return MOE_ERR_INVALID_ARG;
@@ -93,7 +99,7 @@ moe_status moe_swiglu_backward(const void *dA, const void *GU_fp8, const void *G
                                int32_t *status_word, moe_stream_t stream)
 {
     NvtxRange nvtx_range("moe_swiglu_backward");
-    if (!rows_ok(R) || I < 1 || I > (1 << 20) || I % 128 != 0) return MOE_ERR_INVALID_ARG;
+    if (!rows_ok(R) || I < 1 || I > (1 << 20) || I % 128 != 0 || !blocks_ok(R, I)) return MOE_ERR_INVALID_ARG;
     if (!format_ok(gu_scale_format) || !format_ok(scale_format)) return MOE_ERR_INVALID_ARG;
     if ((dGU_fp8 == nullptr) != (dGU_scale == nullptr)) return MOE_ERR_INVALID_ARG;
     if (R == 0) return MOE_OK;

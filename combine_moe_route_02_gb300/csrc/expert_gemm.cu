@@ -44,7 +44,11 @@ constexpr int kScaleSlotBytes = 4 * kScaleQuadBytes;
 constexpr int kEpiBytes = 4 * 32 * 64;        // per epilogue warp 32 tokens x 32 features
 constexpr int kThreads = 320;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSfCol = 2 * kTileN;       // scales behind the two accumulators: 2 x (4 + 8) columns
+// Scales lie behind the two accumulators: 4 + 8 columns for four blocks.  Five places in turn: when one is
+// written again its MMAs have completed, those of the tile before the last by the wait for its accumulator,
+// nearer ones because at least six blocks of the ring lie between.
+constexpr uint32_t kSfCol = 2 * kTileN, kSfCols = 12, kSfPlaces = 5;
+static_assert(kSfCol + kSfPlaces * kSfCols <= kTmemCols, "TMEM");
 constexpr int kMaxE = 256;
 
 struct Tail {
@@ -327,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t a0 = make_smem_desc_sw128(smem_u32(ring), 16, 1024);
         const uint64_t b0 = make_smem_desc_sw128(smem_u32(ring + kABytes), 16, 1024);
         const uint32_t a_step = p.transpose ? 32 * 128 / 16 : 2;
-        uint32_t s = 0, ph = 0, q = 0, qph = 0;
+        uint32_t s = 0, ph = 0, q = 0, qph = 0, sf_place = 0;
         int j = 0;
         bool ok = true;
         for (Walk walk(pair, p.m_tiles); walk.tile < tiles; walk.next(pairs, p.m_tiles)) {
@@ -345,7 +349,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tc_fence_after_sync();
                 }
                 const uint32_t src = smem_u32(sf_ring + q * kScaleSlotBytes) + ((k0 >> 2) & 3) * kScaleQuadBytes;
-                const uint32_t sfa = tmem + kSfCol + ((k0 >> 2) & 1) * 12, sfb = sfa + 4;
+                const uint32_t sfa = tmem + kSfCol + sf_place * kSfCols, sfb = sfa + 4;
+                sf_place = sf_place + 1 == kSfPlaces ? 0 : sf_place + 1;
                 const bool last = (k0 & 15) == 12 || k0 + 4 >= blocks;    // of the slot
                 if (elect_one()) {
                     copy_scales(sfa, src);

@@ -27,7 +27,8 @@ __device__ __forceinline__ uint32_t block_scale_byte(float amax)
 __device__ __forceinline__ float scale_reciprocal(uint32_t b) { return __uint_as_float((254u - b) << 23); }
 __device__ __forceinline__ float scale_value(uint32_t b)
 {
-    return __uint_as_float(b ? b << 23 : 0x00400000u);  // byte 0 is 2^-127, a subnormal
+    // byte 0 is 2^-127, a subnormal; byte 255 a NaN
+    return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7FFFFFFFu : b << 23);
 }
 
 // Four fp32 values to four E4M3 codes (round to nearest even, saturating), the first in the low byte.
@@ -60,7 +61,7 @@ __device__ __forceinline__ uint32_t load_scale_bits(const void *p, int ue8m0, in
 __device__ __forceinline__ uint32_t scale_bits_byte(uint32_t w, int ue8m0, bool &bad)
 {
     if (ue8m0) return w;
-    bad |= (w & 0x807FFFFFu) != 0 || w == 0;
+    bad |= (w & 0x807FFFFFu) != 0 || w - 1u >= 0x7F7FFFFFu;   // (not 0, below infinity)
     return (w >> 23) & 0xFFu;
 }
 __device__ __forceinline__ uint32_t load_scale_byte(const void *p, int ue8m0, int64_t at, bool &bad)

@@ -172,7 +172,7 @@ __device__ __forceinline__ uint4 convert_codes(const uint2 &w, uint32_t f)
     return make_uint4(a.x, a.y, b.x, b.y);
 }
 
-// The same with NaN codes, and where 2^120 * s (s = 2^(byte - 127)) is beyond bf16's range.
+// The same with NaN codes, the NaN scale 255, and where 2^120 * s (s = 2^(byte - 127)) is beyond bf16's range.
 __device__ __forceinline__ uint4 convert_codes_rare(const uint2 &w, uint32_t byte)
 {
     const uint32_t ex = 120u + byte, ex1 = ex < 254u ? ex : 254u;
@@ -182,6 +182,7 @@ __device__ __forceinline__ uint4 convert_codes_rare(const uint2 &w, uint32_t byt
     b = make_uint2(mul_bf16x2(b.x, f2), mul_bf16x2(b.y, f2));
     a = make_uint2(set_nan(a.x, w.x, 0), set_nan(a.y, w.x, 2));
     b = make_uint2(set_nan(b.x, w.y, 0), set_nan(b.y, w.y, 2));
+    if (byte == 255) a = b = make_uint2(0x7FFF7FFFu, 0x7FFF7FFFu);
     return make_uint4(a.x, a.y, b.x, b.y);
 }
 
@@ -382,9 +383,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         convert_codes(v[x], __shfl_sync(0xffffffffu, factor, 2 * x + (r0 & 1)));
             } else {
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
+                for (int x = 0; x < 8; ++x) {
+                    const uint32_t y = __shfl_sync(0xffffffffu, byte, 2 * x + (r0 & 1));
                     *reinterpret_cast<uint4 *>(b + dst_at + x * 1024) =
-                        convert_codes_rare(v[x], __shfl_sync(0xffffffffu, byte, 2 * x + (r0 & 1)));
+                        r0 + 8 * x < valid ? convert_codes_rare(v[x], y) : make_uint4(0, 0, 0, 0);
+                }
             }
             // (each CTA's tensor core reads these bytes from its own shared memory: once they are ordered
             // before the async proxy, the arrival at the leader has no other memory to order)

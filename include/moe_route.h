@@ -391,7 +391,9 @@ MOE_API moe_status moe_combine_residual(const void *Y, const int32_t *row_map, c
  * ([E, ceil(rows/128), ceil(cols/128)], the last blocks cut at the edges), in
  * either moe_scale_format.  A value is code * scale.  An fp32 scale that is not a
  * positive normal power of two is reported as MOE_ERR_BAD_SCALE in status_word
- * (its exponent is used).  A NaN code gives NaN results.
+ * (its exponent is used).  A NaN code, and UE8M0's NaN 255, give NaN results.  The
+ * quantisers leave NaNs out of a block's maximum and write them as NaN codes; a block
+ * with an infinity gets the largest scale, NaN codes for the infinities and zeros.
  * expert_offsets is moe_dispatch's: int32 [E+1], the rows of expert e are
  * [offsets[e], offsets[e+1]); a group may be empty.  NULL with E = 1 means one group
  * of all R rows (a plain product).  A group that is not inside [0, R] or runs
@@ -420,7 +422,7 @@ MOE_API moe_status moe_quantize_weight(const void *W, int E, int rows, int cols,
  *   X_fp8 uint8 [R, red], X_scale [R, red/128], W_fp8 uint8 [E, rows, cols], W_scale
  *   Y bf16; rows of no group are left as they are
  * The reduction (cols, or rows when transposed) is a multiple of 128, the other
- * side of 16.  R == 0 is a no-op.  One launch.
+ * side of 16, both at most 2^18.  R == 0 is a no-op.  One launch.
  * Errors: MOE_ERR_INVALID_ARG (sizes, NULLs, expert_offsets NULL with E > 1),
  * MOE_ERR_MISALIGNED, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.
  */
@@ -437,7 +439,7 @@ MOE_API moe_status moe_expert_gemm(const void *X_fp8, const void *X_scale, int x
  *   add fp32 [E, rows, cols] or NULL (nothing is added); may be dW itself when that is fp32
  *   dW  fp32 (dw_bf16 == 0) or bf16 [E, rows, cols]; an empty group gives add, or zeros
  * x is a bf16 number exactly (an E4M3 value times a power of two), the products are
- * accumulated in fp32.  rows % 8 == 0, cols % 128 == 0.  One launch.
+ * accumulated in fp32.  rows % 8 == 0, cols % 128 == 0, both at most 2^18.  One launch.
  */
 MOE_API moe_status moe_expert_wgrad(const void *dY, const void *X_fp8, const void *X_scale, int x_scale_format,
                             const int32_t *expert_offsets, int64_t R, int E, int rows, int cols,
@@ -449,7 +451,7 @@ MOE_API moe_status moe_expert_wgrad(const void *dY, const void *X_fp8, const voi
  *   A_fp8 uint8 [R, I], A_scale [R, I/128]: a in E4M3 (the rule of moe_permute)
  *   GU_fp8 uint8 [R, 2I], GU_scale [R, 2I/128], or both NULL: GU in E4M3, the
  *   checkpoint that moe_swiglu_backward reads instead of GU
- * I % 128 == 0.  One launch.
+ * I % 128 == 0, I <= 2^20, R * I / 128 < 2^36.  One launch.
  */
 MOE_API moe_status moe_swiglu(const void *GU, int64_t R, int I, void *A_fp8, void *A_scale,
                       void *GU_fp8, void *GU_scale, int scale_format, moe_stream_t stream);

@@ -36,6 +36,7 @@ def gemm(L, X=A, xs=B, xf=0, W=C, ws=D, wf=0, off=A, R=16, E=4, rows=256, cols=1
 def test_expert_gemm_refusals(L):
     assert gemm(L, R=0) == OK
     for bad in (dict(E=0), dict(E=257), dict(R=-1), dict(R=2 ** 31), dict(rows=0), dict(cols=0), dict(xf=2), dict(wf=-1),
+                dict(rows=2 ** 18 + 16), dict(cols=2 ** 18 + 128), dict(R=2 ** 31 - 2, rows=2 ** 18),
                 dict(cols=192), dict(rows=200), dict(off=None), dict(X=None), dict(xs=None), dict(W=None),
                 dict(ws=None), dict(Y=None), dict(t=1, rows=192), dict(t=1, cols=136)):
         assert gemm(L, **bad) == INVALID, bad
@@ -48,7 +49,8 @@ def wgrad(L, dY=A, X=B, xs=C, xf=0, off=A, R=16, E=4, rows=64, cols=128, add=Non
 
 
 def test_expert_wgrad_refusals(L):
-    for bad in (dict(E=0), dict(E=257), dict(R=-1), dict(R=2 ** 31), dict(rows=0), dict(rows=60), dict(cols=64), dict(xf=3),
+    for bad in (dict(E=0), dict(E=257), dict(R=-1), dict(R=2 ** 31), dict(rows=0), dict(rows=60), dict(cols=64), dict(rows=2 ** 18 + 8),
+                dict(cols=2 ** 18 + 128), dict(xf=3),
                 dict(off=None), dict(dY=None), dict(X=None), dict(xs=None), dict(dW=None), dict(dW=None, R=0),
                 dict(add=F, dW=F, bf16=1)):
         assert wgrad(L, **bad) == INVALID, bad
@@ -61,7 +63,7 @@ def test_swiglu_refusals(L):
         return L.moe_swiglu(GU, R, I, Aq, As, K, Ks, fmt, None)
 
     assert f(R=0) == OK
-    for bad in (dict(GU=None), dict(I=0), dict(I=192), dict(R=-1), dict(Aq=None), dict(As=None), dict(fmt=2), dict(K=D), dict(Ks=D)):
+    for bad in (dict(GU=None), dict(I=0), dict(I=192), dict(R=2 ** 30, I=2 ** 14), dict(R=-1), dict(Aq=None), dict(As=None), dict(fmt=2), dict(K=D), dict(Ks=D)):
         assert f(**bad) == INVALID, bad
     for bad in (dict(GU=A + 2), dict(Aq=A + 8), dict(As=A + 2), dict(K=A + 8, Ks=D), dict(K=D, Ks=A + 1)):
         assert f(**bad) == MISALIGNED, bad
@@ -206,6 +208,8 @@ COUNTS = [
     (128, 16, True, "fp32", "fp32"),
     (640, 272, True, "ue8m0", "ue8m0"),
     (1024, 144, True, "fp32", "ue8m0"),
+    (272, 2176, False, "fp32", "ue8m0"),    # more blocks than the scales are gathered at a time
+    (2304, 528, True, "ue8m0", "fp32"),
 ])
 def test_expert_gemm(dev, counts, rows, cols, transpose, xf, wf):
     E, R = len(counts), sum(counts) + 5      # five rows of no group
@@ -236,6 +240,47 @@ def test_expert_gemm_one_group_without_offsets(dev):
     within(y, xd @ Wd.T, acc_slack(256, 32, xd.abs() @ Wd.abs().T))
     assert torch.equal(y.view(torch.int16), y2.view(torch.int16))
     assert moe.expert_gemm(x8[:0], xs[:0], W8, ws).shape == (0, 192)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["fp32", "ue8m0"])
+def test_scales_need_no_alignment_beyond_their_type(dev, fmt):
+    """The same bits from scales that start one element into an allocation."""
+    counts = [40, 0, 33]
+    x8, xs = ref.encode_rows(normal((73, 2048), 14, dev), fmt)
+    W8, ws = ref.encode_weight(normal((3, 256, 2048), 15, dev), fmt)
+    off, dY = ref.offsets_of(counts, dev), normal((73, 256), 16, dev)
+
+    def moved(t):
+        big = torch.empty(t.numel() + 1, dtype=t.dtype, device=dev)
+        big[1:] = t.flatten()
+        return big[1:].view(t.shape)
+
+    y, dW = moe.expert_gemm(x8, xs, W8, ws, off), moe.expert_wgrad(dY, x8, xs, off)
+    assert torch.equal(moe.expert_gemm(x8, moved(xs), W8, moved(ws), off).view(torch.int16), y.view(torch.int16))
+    assert torch.equal(moe.expert_wgrad(dY, x8, moved(xs), off), dW)
+
+
+@gpu
+def test_expert_products_repeat_bit_for_bit(dev):
+    """Uneven groups, many tiles: a wait that was missing somewhere would show as a difference."""
+    g = torch.Generator().manual_seed(17)
+    counts = [int(c) for c in torch.randint(0, 700, (24,), generator=g)]
+    R = sum(counts)
+    x8, xs = ref.encode_rows(normal((R, 1152), 18, dev), "ue8m0")
+    W8, ws = ref.encode_weight(normal((24, 640, 1152), 19, dev, 0.05), "ue8m0")
+    off, dY = ref.offsets_of(counts, dev), normal((R, 640), 20, dev)
+    y, dW = moe.expert_gemm(x8, xs, W8, ws, off), moe.expert_wgrad(dY, x8, xs, off)
+    for _ in range(30):
+        assert torch.equal(moe.expert_gemm(x8, xs, W8, ws, off).view(torch.int16), y.view(torch.int16))
+        assert torch.equal(moe.expert_wgrad(dY, x8, xs, off), dW)
+    xd, a = ref.decode(x8, xs, 1), 0
+    for e, c in enumerate(counts):
+        Wd = ref.decode(W8[e], ws[e], ref.BLK)
+        within(y[a:a + c], xd[a:a + c] @ Wd.T, acc_slack(1152, 32, xd[a:a + c].abs() @ Wd.abs().T))
+        d = dY[a:a + c].double()
+        within(dW[e], d.T @ xd[a:a + c], acc_slack(c, 16, d.abs().T @ xd[a:a + c].abs()))
+        a += c
 
 
 @gpu
@@ -280,15 +325,13 @@ def test_expert_bad_scales_and_offsets_are_reported(dev):
         st = status_word(dev)
         moe.expert_gemm(x8, bad, W8, ws, good, status=st)
         expect = moe.ERR_BAD_SCALE
-        if poison != float("inf"):           # (infinity has the bits of a power of two: it gives NaN)
-            assert st.item() == expect, poison
+        assert st.item() == expect, poison
         st.zero_()
         moe.expert_gemm(x8, xs, W8, torch.full_like(ws, 3.0), good, status=st)
         assert st.item() == expect
         st.zero_()
         moe.expert_wgrad(dY, x8, bad, good, status=st)
-        if poison != float("inf"):
-            assert st.item() == expect
+        assert st.item() == expect, poison
     for off in ([0, 20, 41], [-1, 20, 40], [0, 30, 20], [50, 60, 70]):
         st = status_word(dev)
         o = torch.tensor(off, dtype=torch.int32, device=dev)
