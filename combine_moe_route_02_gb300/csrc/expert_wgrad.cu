@@ -18,8 +18,8 @@
 //   warp 1        MMA issuer (one thread of the leader)
 //   warp 3        allocates TMEM
 //   warps 4..11   epilogue, two warps to a quarter of the TMEM lanes
-//   warps 12..23  three teams of converters E4M3 -> bf16, which take the stages in turn;
-//                 in a group's last stage they also clear the rows behind its end
+//   warps 12..23  three teams of converters E4M3 -> bf16, each with its own places of
+//                 the ring; in a group's last stage they also clear the rows behind its end
 //                 (the next group's, or none)
 #include "expert_internal.cuh"
 
@@ -91,21 +91,32 @@ __device__ __forceinline__ Tile get_tile(const Tail &t, const Params &p, int til
     return r;
 }
 
-// Every kTeams-th ring stage of a CTA pair's walk (groups without rows have none), as a converter needs
-// it: how many rows of the group from its first on there are, and where their scales of this CTA's
-// columns are.
+// The stages of a CTA pair's walk (groups without rows have none) that a team converts: those in its own
+// places of the ring, place % kTeams == team.  (A place has to be one team's: a wait by parity is right only
+// for who waits for every phase.)  Of each, how many rows of the group from its first on there are, and where
+// their scales of this CTA's columns are.
+template <int kStages>
 struct Stages {
     int tile, i, count;           // the tile, the first row in its group, the group's rows
+    int place, team;
     int64_t scales;               // of the group's first row
 
     __device__ __forceinline__ Stages(const Tail &t, const Params &p, int pair, int pairs, int tiles, int team, int rank)
-        : tile(pair - pairs), i(team * kRows), count(0)
+        : tile(pair - pairs), i(team * kRows), count(0), place(team), team(team)
     {
         settle(t, p, pairs, tiles, rank);
     }
+    // How many stages on the team's next place is.
+    static __device__ __forceinline__ int step(int place, int team)
+    {
+        return place + kTeams < kStages ? kTeams : kStages - place + team;
+    }
     __device__ __forceinline__ void next(const Tail &t, const Params &p, int pairs, int tiles, int rank)
     {
-        i += kTeams * kRows;
+        const int n = step(place, team);
+        i += n * kRows;
+        place += n;
+        if (place >= kStages) place -= kStages;
         if (i >= count) settle(t, p, pairs, tiles, rank);
     }
     __device__ __forceinline__ void settle(const Tail &t, const Params &p, int pairs, int tiles, int rank)
@@ -331,14 +342,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // A warp converts 16 rows of a stage, two at a time: lane l (and l + 16) loads the scale of the row
         // r0 of lanes 16 (l & 1) on, 8 (l / 2) further, and hands it out by shuffles
         const int srow = 2 * (t >> 5) + (lane & 1) + 8 * ((lane & 15) >> 1);
-        auto fetch = [&](const Stages &g) {
+        using Walk = Stages<kStages>;
+        auto fetch = [&](const Walk &g) {
             // (rows behind the group's end: any scale will do for their zeros)
             const int row = g.i + srow < g.count ? g.i + srow : g.count - 1;
             return load_scale_bits(p.X_scale, p.x_ue8m0, g.scales + static_cast<int64_t>(row) * kblocks);
         };
         // The scales of this team's next two stages are on their way while it converts one (with one, the
         // wait for them was a third of the team's time).  rows: of the stage; 0: there is none.
-        Stages ahead(tail, p, pair, pairs, tiles, team, rank);
+        Walk ahead(tail, p, pair, pairs, tiles, team, rank);
         auto take = [&](uint32_t &scale, int &rows) {
             rows = 0;
             if (ahead.tile < tiles) {
@@ -394,7 +406,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_at(&tail.conv[s], 0);
-            s += kTeams;
+            s += Walk::step(s, team);
             if (s >= kStages) {
                 s -= kStages;
                 ph ^= 1u;

@@ -271,9 +271,16 @@ def test_expert_products_repeat_bit_for_bit(dev):
     W8, ws = ref.encode_weight(normal((24, 640, 1152), 19, dev, 0.05), "ue8m0")
     off, dY = ref.offsets_of(counts, dev), normal((R, 640), 20, dev)
     y, dW = moe.expert_gemm(x8, xs, W8, ws, off), moe.expert_wgrad(dY, x8, xs, off)
+    base = torch.randn(dW.shape, generator=g).to(dev)
+    half = moe.expert_wgrad(dY, x8, xs, off, dtype=torch.bfloat16)
+    assert torch.equal(half, dW.to(torch.bfloat16))
     for _ in range(30):
         assert torch.equal(moe.expert_gemm(x8, xs, W8, ws, off).view(torch.int16), y.view(torch.int16))
         assert torch.equal(moe.expert_wgrad(dY, x8, xs, off), dW)
+        assert torch.equal(moe.expert_wgrad(dY, x8, xs, off, add=base), base + dW)
+        buf = base.clone()
+        assert torch.equal(moe.expert_wgrad(dY, x8, xs, off, add=buf, out=buf), base + dW)
+        assert torch.equal(moe.expert_wgrad(dY, x8, xs, off, dtype=torch.bfloat16), half)
     xd, a = ref.decode(x8, xs, 1), 0
     for e, c in enumerate(counts):
         Wd = ref.decode(W8[e], ws[e], ref.BLK)
