@@ -8,6 +8,12 @@
 // bf16 one with fp32 accumulation.  The E4M3 rows are read as they are (half the
 // bytes of bf16) and become bf16 on their way through shared memory.
 //
+// The tensor cores cut where they add to an accumulator (measured: a sum of 16384 rows
+// comes out 7e-6 of its size too small).  A 32-bit result is therefore summed in
+// segments of 2048 rows, each in an accumulator of its own, and the segments are
+// added to what is in dW already, rounding to nearest (2048 rows: 6e-7).  A result of bf16 type is off
+// by 2^-9 anyway and takes a group in one segment.
+//
 // Both operands have the reduction on their slow axis (MN-major).  Persistent CTA
 // pairs (cta_group::2); a tile is 256 weight rows x 256 weight columns of one expert,
 // a ring stage 64 rows of the group.  Each CTA holds the accumulators of 128 of the
@@ -21,6 +27,8 @@
 //   warps 12..23  three teams of converters E4M3 -> bf16, each with its own places of
 //                 the ring; in a group's last stage they also clear the rows behind its end
 //                 (the next group's, or none)
+#include <climits>
+
 #include "expert_internal.cuh"
 
 namespace moe {
@@ -39,10 +47,11 @@ constexpr int kBufBytes = 32 * 64;                // a buffer of an epilogue war
 // bound by its way in: four buffers keep three boxes of it in flight for each of the eight warps (64 experts
 // of 512 x 1024 with 32 rows each: 65 us, 82 us with two thirds of that in flight).  Without, a sixth stage
 // covers more of the ring's latency (128 experts of 2048 x 2048, 1024 rows each: 683 us, 724 us with five).
-template <bool kAdd>
+template <bool kLoads>
 struct Split {
-    static constexpr int kStages = kAdd ? 5 : 6, kBufs = kAdd ? 4 : 2;
+    static constexpr int kStages = kLoads ? 5 : 6, kBufs = kLoads ? 4 : 2;
 };
+constexpr int kSegment = 2048;                    // rows, whole stages
 constexpr int kMostStages = 6, kMostBufs = 4;
 constexpr int kThreads = 32 * (4 + kEpiWarps + kTeams * kTeamWarps);
 constexpr uint32_t kTmemCols = 512;
@@ -57,10 +66,10 @@ struct Tail {
     uint32_t valid[kMaxE / 32];   // a bit for each group that lies inside [0, R]
     int off[kMaxE + 1];
 };
-template <bool kAdd>
+template <bool kLoads>
 constexpr size_t smem_bytes()
 {
-    return 1024 + Split<kAdd>::kStages * kStageBytes + Split<kAdd>::kBufs * kEpiWarps * kBufBytes + sizeof(Tail);
+    return 1024 + Split<kLoads>::kStages * kStageBytes + Split<kLoads>::kBufs * kEpiWarps * kBufBytes + sizeof(Tail);
 }
 static_assert(smem_bytes<false>() <= 227 * 1024 && smem_bytes<true>() <= 227 * 1024, "shared memory");
 
@@ -68,7 +77,8 @@ struct Params {
     const void *X_scale;
     const int32_t *offsets;
     int64_t R;
-    int E, rows, cols, x_ue8m0, bf16_out;
+    int E, rows, cols, x_ue8m0, bf16_out, has_add;
+    int segment;                  // rows that go into one accumulator
     int m_tiles, n_tiles;
     int32_t *status;
 };
@@ -197,12 +207,12 @@ __device__ __forceinline__ uint4 convert_codes_rare(const uint2 &w, uint32_t byt
     return make_uint4(a.x, a.y, b.x, b.y);
 }
 
-template <bool kAdd>
+template <bool kLoads>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expert_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX,
                         const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmAdd, const Params p)
 {
-    constexpr int kStages = Split<kAdd>::kStages, kBufs = Split<kAdd>::kBufs;
+    constexpr int kStages = Split<kLoads>::kStages, kBufs = Split<kLoads>::kBufs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *epi = ring + kStages * kStageBytes;
@@ -229,7 +239,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmY);
         tma_prefetch_desc(&tmX);
         tma_prefetch_desc(&tmW);
-        if (kAdd) tma_prefetch_desc(&tmAdd);
+        if (kLoads) tma_prefetch_desc(&tmAdd);
     }
     if (warp == 3) tmem_alloc_pair(&tail.tmem_base, kTmemCols);
     __syncthreads();
@@ -296,33 +306,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int tile = pair; tile < tiles; tile += pairs) {
             const int count = get_tile(tail, p, tile).count;
-            if (count == 0) continue;
-            const int b = j & 1;
-            ok = warp_wait(&tail.acc_empty[b], ((j >> 1) & 1) ^ 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint32_t d = tmem + b * kTileN;
-            for (int r = 0; r < count; r += kRows) {
-                ok = warp_wait(&tail.conv[s], ph, abort_flag);
+            for (int r0 = 0; r0 < count && ok; r0 += p.segment) {
+                const int end = count - r0 < p.segment ? count : r0 + p.segment, b = j & 1;
+                ok = warp_wait(&tail.acc_empty[b], ((j >> 1) & 1) ^ 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after_sync();
-                const uint64_t at = (s * kStageBytes) >> 4;
-                if (elect_one()) {
+                const uint32_t d = tmem + b * kTileN;
+                for (int r = r0; r < end; r += kRows) {
+                    ok = warp_wait(&tail.conv[s], ph, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint64_t at = (s * kStageBytes) >> 4;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kRows / 16; ++k)
-                        mma_f16_pair(d, a0 + at + k * 128, b0 + at + k * 128, idesc, (r | k) != 0);
-                    tc_commit_pair(&tail.empty[s]);
+                        for (int k = 0; k < kRows / 16; ++k)
+                            mma_f16_pair(d, a0 + at + k * 128, b0 + at + k * 128, idesc, ((r - r0) | k) != 0);
+                        tc_commit_pair(&tail.empty[s]);
+                    }
+                    __syncwarp();
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
+                if (!ok) break;
+                if (elect_one()) tc_commit_pair(&tail.acc_full[b]);
                 __syncwarp();
-                if (++s == kStages) {
-                    s = 0;
-                    ph ^= 1u;
-                }
+                ++j;
             }
             if (!ok) break;
-            if (elect_one()) tc_commit_pair(&tail.acc_full[b]);
-            __syncwarp();
-            ++j;
         }
         if (elect_one()) tc_commit_pair(&tail.drain);
         __syncwarp();
@@ -429,9 +441,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int dm = rank * kHalf + quarter * 32, dn = side * 128;
         // place of a lane's 16-byte piece x: its row's bytes, swizzled as the boxes are (64- or 32-byte rows)
         const int row64 = lane * 64, swz64 = (lane >> 1) & 3, row32 = lane * 32, swz32 = (lane >> 2) & 1;
-        // the boxes that are to be added: of which tile, which columns, how many have been asked for
-        int a_tile = pair, a_c = 0;
-        uint32_t asked = 0, q = 0;                                // q: boxes done
+        // The boxes to come: of which tile, segment and columns the next one is.  A first segment's is added
+        // to `add`'s, if there is one, a later one's to what this warp has stored of the one before.
+        int a_tile = pair, a_row = 0, a_c = 0;
+        uint32_t asked = 0, q = 0, landed = 0;                    // q: boxes done; landed: a phase bit per buffer
+        uint32_t wanted = 0;                                      // a bit per buffer: its box has been asked for
         auto ask = [&]() {
             Tile t;
             while (a_tile < tiles) {
@@ -440,96 +454,114 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 a_tile += pairs;
             }
             if (a_tile >= tiles) return;
-            if (lane == 0) {
-                uint64_t *bar = &tail.added[w][asked % kBufs];
-                mbar_arrive_expect_tx(bar, kBufBytes);
-                tma_load_3d(bufs + (asked % kBufs) * kBufBytes, &tmAdd, bar, t.n0 + dn + a_c, t.m0 + dm, t.e,
-                            l2_policy_evict_first());
+            const uint32_t b = asked % kBufs;
+            if (a_row > 0 || p.has_add) {
+                if (lane == 0) {
+                    uint64_t *bar = &tail.added[w][b];
+                    // eight boxes lie between a segment's and the next one's, three of which are asked for ahead
+                    if (a_row > 0) {
+                        bulk_wait<4>();
+                        fence_proxy_async_all();
+                    }
+                    mbar_arrive_expect_tx(bar, kBufBytes);
+                    tma_load_3d(bufs + b * kBufBytes, a_row > 0 ? &tmW : &tmAdd, bar, t.n0 + dn + a_c, t.m0 + dm, t.e,
+                                l2_policy_evict_first());
+                }
+                wanted |= 1u << b;
             }
             __syncwarp();
             ++asked;
             a_c += 16;
             if (a_c == kHalf) {
                 a_c = 0;
-                a_tile += pairs;
+                a_row += p.segment;
+                if (t.count - a_row <= 0) {
+                    a_row = 0;
+                    a_tile += pairs;
+                }
             }
         };
-        if (kAdd)
+        if (kLoads)
             for (int i = 0; i < kBufs - 1; ++i) ask();
         int j = 0;
         bool ok = true;
-        for (int tile = pair; tile < tiles; tile += pairs) {
+        for (int tile = pair; tile < tiles && ok; tile += pairs) {
             const Tile t = get_tile(tail, p, tile);
             const bool some = t.count != 0;
             const int m = t.m0 + dm, n = t.n0 + dn;
             const bool inside = n < p.cols && m < p.rows;         // (columns come in whole 128)
-            const int b = j & 1;
-            if (some) {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, abort_flag, 64));
-                if (!ok) break;
-                tc_fence_after_sync();
-                ++j;
-            }
-            for (int c = 0; c < kHalf && inside; c += 16, ++q) {
-                uint8_t *buf = bufs + (q % kBufs) * kBufBytes;
-                if (kAdd) {
-                    // the buffer of the box before this one is free again once it has been read
-                    bulk_wait_read<0>();
-                    __syncwarp();
-                    ask();
-                } else {
-                    bulk_wait_read<kBufs - 1>();
-                    __syncwarp();
-                }
-                float v[16];
+            for (int r0 = 0; (r0 < t.count || r0 == 0) && ok; r0 += p.segment) {
+                const int b = j & 1;
                 if (some) {
-                    tmem_ld_32x32b_x16(lane_addr + b * kTileN + c, v);
-                    tmem_ld_wait();
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) v[x] = 0.f;
-                }
-                if (kAdd) {
-                    ok = warp_wait(&tail.added[w][q % kBufs], (q / kBufs) & 1u, abort_flag);
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, abort_flag, 64));
                     if (!ok) break;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float4 z = *reinterpret_cast<const float4 *>(buf + row64 + ((x ^ swz64) << 4));
-                        v[4 * x] += z.x;
-                        v[4 * x + 1] += z.y;
-                        v[4 * x + 2] += z.z;
-                        v[4 * x + 3] += z.w;
-                    }
-                    if (p.bf16_out) __syncwarp();                 // (other lanes' rows lie where this one writes)
+                    tc_fence_after_sync();
+                    ++j;
                 }
-                if (p.bf16_out) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        uint4 h;
-                        __nv_bfloat162 *hp = reinterpret_cast<__nv_bfloat162 *>(&h);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) hp[i] = __floats2bfloat162_rn(v[8 * x + 2 * i], v[8 * x + 2 * i + 1]);
-                        *reinterpret_cast<uint4 *>(buf + row32 + ((x ^ swz32) << 4)) = h;
+                for (int c = 0; c < kHalf && inside; c += 16, ++q) {
+                    const uint32_t at = q % kBufs;
+                    uint8_t *buf = bufs + at * kBufBytes;
+                    if (kLoads) {
+                        // the buffer of the box before this one is free again once it has been read
+                        bulk_wait_read<0>();
+                        __syncwarp();
+                        ask();
+                    } else {
+                        bulk_wait_read<kBufs - 1>();
+                        __syncwarp();
                     }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        *reinterpret_cast<float4 *>(buf + row64 + ((x ^ swz64) << 4)) =
-                            make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                    float v[16];
+                    if (some) {
+                        tmem_ld_32x32b_x16(lane_addr + b * kTileN + c, v);
+                        tmem_ld_wait();
+                    } else {
+    #pragma unroll
+                        for (int x = 0; x < 16; ++x) v[x] = 0.f;
+                    }
+                    if (kLoads && (wanted >> at & 1u)) {
+                        ok = warp_wait(&tail.added[w][at], landed >> at & 1u, abort_flag);
+                        if (!ok) break;
+                        landed ^= 1u << at;
+                        wanted ^= 1u << at;
+    #pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const float4 z = *reinterpret_cast<const float4 *>(buf + row64 + ((x ^ swz64) << 4));
+                            v[4 * x] += z.x;
+                            v[4 * x + 1] += z.y;
+                            v[4 * x + 2] += z.z;
+                            v[4 * x + 3] += z.w;
+                        }
+                        if (p.bf16_out) __syncwarp();                 // (other lanes' rows lie where this one writes)
+                    }
+                    if (p.bf16_out) {
+    #pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            uint4 h;
+                            __nv_bfloat162 *hp = reinterpret_cast<__nv_bfloat162 *>(&h);
+    #pragma unroll
+                            for (int i = 0; i < 4; ++i) hp[i] = __floats2bfloat162_rn(v[8 * x + 2 * i], v[8 * x + 2 * i + 1]);
+                            *reinterpret_cast<uint4 *>(buf + row32 + ((x ^ swz32) << 4)) = h;
+                        }
+                    } else {
+    #pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            *reinterpret_cast<float4 *>(buf + row64 + ((x ^ swz64) << 4)) =
+                                make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tma_store_3d(&tmW, buf, n + c, m, t.e);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) tma_store_3d(&tmW, buf, n + c, m, t.e);
-            }
-            if (!ok) break;
-            if (some) {
-                tc_fence_before_sync();
-                if (lane == 0) mbar_arrive_at(&tail.acc_empty[b], 0);
+                if (!ok) break;
+                if (some) {
+                    tc_fence_before_sync();
+                    if (lane == 0) mbar_arrive_at(&tail.acc_empty[b], 0);
+                }
             }
         }
-        for (; q < asked; ++q) {                                  // (given up: what was asked for still lands here)
+        for (uint32_t x = 0; x < kBufs; ++x) {                    // (given up: what was asked for still lands here)
             volatile int no_abort = 0;
-            mbar_wait_bounded(&tail.added[w][q % kBufs], (q / kBufs) & 1u, &no_abort);
+            if (wanted >> x & 1u) mbar_wait_bounded(&tail.added[w][x], landed >> x & 1u, &no_abort);
         }
         bulk_wait_all();
     }
@@ -545,20 +577,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-template <bool kAdd>
+template <bool kLoads>
 cudaError_t launch(int dev, dim3 grid, cudaStream_t stream, const CUtensorMap &tmY, const CUtensorMap &tmX,
                    const CUtensorMap &tmW, const CUtensorMap &tmAdd, const Params &p)
 {
-    constexpr size_t bytes = smem_bytes<kAdd>();
+    constexpr size_t bytes = smem_bytes<kLoads>();
     static std::atomic<uint64_t> done{0};
     const uint64_t bit = 1ull << (dev & 63);
     if (!(done.load(std::memory_order_relaxed) & bit)) {
-        const cudaError_t err = cudaFuncSetAttribute(expert_wgrad_kernel<kAdd>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t err = cudaFuncSetAttribute(expert_wgrad_kernel<kLoads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                      static_cast<int>(bytes));
         if (err != cudaSuccess) return err;
         done.fetch_or(bit, std::memory_order_relaxed);
     }
-    expert_wgrad_kernel<kAdd><<<grid, kThreads, bytes, stream>>>(tmY, tmX, tmW, tmAdd, p);
+    expert_wgrad_kernel<kLoads><<<grid, kThreads, bytes, stream>>>(tmY, tmX, tmW, tmAdd, p);
     return cudaGetLastError();
 }
 
@@ -595,6 +627,8 @@ cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream)
     p.offsets = a.offsets;
     p.R = a.R;
     p.E = a.E;
+    p.has_add = a.add != nullptr;
+    p.segment = a.bf16_out ? INT_MAX : kSegment;
     p.rows = a.rows;
     p.cols = a.cols;
     p.x_ue8m0 = a.x_ue8m0;
@@ -605,7 +639,7 @@ cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream)
     const int64_t tiles = static_cast<int64_t>(a.E) * p.m_tiles * p.n_tiles;
     const int pairs = device_sm_count(dev) / 2;
     const dim3 grid(2 * static_cast<unsigned>(tiles < pairs ? tiles : pairs));
-    return a.add ? launch<true>(dev, grid, stream, tmY, tmX, tmW, tmAdd, p)
+    return a.add || a.R > p.segment ? launch<true>(dev, grid, stream, tmY, tmX, tmW, tmAdd, p)
                  : launch<false>(dev, grid, stream, tmY, tmX, tmW, tmAdd, p);
 }
 

@@ -388,6 +388,33 @@ def test_expert_wgrad(dev, counts, rows, cols, xf, dtype, add):
 
 
 @gpu
+@pytest.mark.parametrize("add", [False, True])
+def test_expert_wgrad_long_groups_keep_32_bits(dev, add):
+    """Groups longer than the 2048 rows that go into one accumulator.  A tensor core's sum of 2048 rows is cut
+    128 times by at most 2^-23 of what it has reached, on average two thirds of the end: 1e-5 at the worst, a
+    tenth of that as it comes out; segments added with rounding to nearest keep to it however long the group."""
+    counts = [5000, 0, 2048, 2049, 1, 9000]
+    R, rows, cols = sum(counts), 264, 256
+    x8, xs = ref.encode_rows(normal((R, cols), 24, dev), "fp32")
+    dY, off = normal((R, rows), 25, dev), ref.offsets_of(counts, dev)
+    base = torch.randn((len(counts), rows, cols), generator=torch.Generator().manual_seed(26)).to(dev) if add else None
+    dW = moe.expert_wgrad(dY, x8, xs, off, add=base)
+    for _ in range(10):
+        assert torch.equal(moe.expert_wgrad(dY, x8, xs, off, add=base), dW)
+    if add:
+        buf = base.clone()
+        assert torch.equal(moe.expert_wgrad(dY, x8, xs, off, add=buf, out=buf), dW)
+    xd, a = ref.decode(x8, xs, 1), 0
+    for e, c in enumerate(counts):
+        d = dY[a:a + c].double()
+        want = d.T @ xd[a:a + c] + (base[e].double() if add else 0)
+        if c:
+            assert (dW[e].double() - want).norm() <= 2.0 ** -20 * want.norm()
+        within(dW[e], want, acc_slack(c, 16, d.abs().T @ xd[a:a + c].abs()))
+        a += c
+
+
+@gpu
 def test_expert_wgrad_values_at_the_edges_of_e4m3(dev):
     """Every code under scales from the smallest bf16 holds to the largest, NaN codes included: a
     product with one-hot rows gives each value back."""
