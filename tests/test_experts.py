@@ -704,6 +704,25 @@ def test_moe_layer_repeats_on_one_workspace_and_as_a_graph(dev):
 
 
 @gpu
+@pytest.mark.parametrize("n", [1, 7])
+def test_moe_layer_gives_up_a_wait_and_recovers(dev, n):
+    """An arrival counter that can never be reached (it wraps one short): every CTA gives up after its limit,
+    the status word says so, the counters end at zero and the next call is right."""
+    E, I, H, K = 16, 256, 512, 4
+    t = layer_inputs(n, H, I, E, K, "fp32", dev, seed=85)
+    ws = torch.zeros(moe.layer_workspace_size(n, H, I, E, K), dtype=torch.uint8, device=dev)
+    ws[:4] = 255
+    st = status_word(dev)
+    moe.moe_layer(t[0], t[1], K, *t[2:], workspace=ws, status=st)
+    assert st.item() == moe.ERR_TIMEOUT
+    assert bool((ws[:256 + 4 * (E + 128) * (I // 128)] == 0).all())
+    st.zero_()
+    r = moe.moe_layer(t[0], t[1], K, *t[2:], workspace=ws, status=st)
+    assert st.item() == 0
+    check_layer(r, *t, K)
+
+
+@gpu
 def test_moe_layer_agrees_with_the_batch_path(dev):
     """dispatch, the two products with the activation between them, and combine: the same layer up to
     the bf16 roundings between its steps."""
