@@ -100,18 +100,21 @@ def quantize_weight(W: torch.Tensor, scale_format: str = "fp32", out=None, strea
     fmt = _scale_format(scale_format)
     if not isinstance(W, torch.Tensor) or W.dim() not in (2, 3):
         raise ValueError("W must be a tensor [E, rows, cols] or [rows, cols]")
-    dev = _home(W, "W")
-    src = _arg(W, "W", torch.bfloat16, W.shape, dev)
-    lead, (rows, cols) = W.shape[:-2], W.shape[-2:]
-    E = lead[0] if lead else 1
-    shape = (*lead, _blocks(rows), _blocks(cols))
+    dev, whole = _home(W, "W"), W.shape
+    src = _arg(W, "W", torch.bfloat16, whole, dev)
+    E, rows, cols = whole if len(whole) == 3 else (1, *whole)
+    shape = (E, _blocks(rows), _blocks(cols)) if len(whole) == 3 else (_blocks(rows), _blocks(cols))
     if out is None:
-        out = (torch.empty(W.shape, dtype=torch.uint8, device=W.device),
-               torch.empty(shape, dtype=_scale_dtype(scale_format), device=W.device))
-    q, s = out
-    _check(lib().moe_quantize_weight(src, E, rows, cols, _arg(q, "W_fp8", torch.uint8, W.shape, dev),
-                                     _arg(s, "W_scale", _scale_dtype(scale_format), shape, dev), fmt, _raw_stream(stream, dev)),
-           "moe_quantize_weight")
+        q = torch.empty(whole, dtype=torch.uint8, device=W.device)
+        s = torch.empty(shape, dtype=_scale_dtype(scale_format), device=W.device)
+        qp, sp = q.data_ptr(), s.data_ptr()
+    else:
+        q, s = out
+        qp = _arg(q, "W_fp8", torch.uint8, whole, dev)
+        sp = _arg(s, "W_scale", _scale_dtype(scale_format), shape, dev)
+    code = lib().moe_quantize_weight(src, E, rows, cols, qp, sp, fmt, _raw_stream(stream, dev))
+    if code:
+        _check(code, "moe_quantize_weight")
     return q, s
 
 
@@ -135,9 +138,13 @@ def expert_gemm(X_fp8: torch.Tensor, X_scale: torch.Tensor, W_fp8: torch.Tensor,
     n = cols if transpose else rows
     if out is None:
         out = torch.empty((R, n), dtype=torch.bfloat16, device=X_fp8.device)
-    _check(lib().moe_expert_gemm(x, xs, xf, w, ws, wf, off, R, E, rows, cols, int(bool(transpose)),
-                                 _arg(out, "out", torch.bfloat16, (R, n), dev), _status_ptr(status), _raw_stream(stream, dev)),
-           "moe_expert_gemm")
+        y = out.data_ptr()
+    else:
+        y = _arg(out, "out", torch.bfloat16, (R, n), dev)
+    code = lib().moe_expert_gemm(x, xs, xf, w, ws, wf, off, R, E, rows, cols, int(bool(transpose)), y,
+                                 _status_ptr(status), _raw_stream(stream, dev))
+    if code:
+        _check(code, "moe_expert_gemm")
     return out
 
 
