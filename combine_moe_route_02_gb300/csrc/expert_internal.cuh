@@ -119,12 +119,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return warp_wait_slow(bar, parity, abort);
 }
 // TMA load of a box with the default cache policy.
-__device__ __forceinline__ void tma_load_2d_plain(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int32_t c0, int32_t c1)
+__device__ __forceinline__ void tma_load_3d_plain(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int32_t c0, int32_t c1,
+                                                  int32_t c2)
 {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                     smem_u32(smem_dst)),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-                 : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
 }
 
 // TMA store of a box (what lies outside the tensor is left out), in this thread's bulk async-group.

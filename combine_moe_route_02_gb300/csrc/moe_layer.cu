@@ -109,7 +109,7 @@ struct Params {
     Layout l;
 };
 struct Maps {
-    CUtensorMap w1, w2;                       // boxes of 8 rows x 256 bytes
+    CUtensorMap w1, w2;                       // boxes of 2 x 8 rows (gate, up) and of 16 rows, x 256 bytes
 };
 
 // All CTAs' threads; what they wrote before is visible to all after.  A CTA that gives up
@@ -405,17 +405,19 @@ __device__ void make_lists(const Params &p, Smem &sm)
 // Where the second half of a shared unit starts: whole pieces.
 __device__ __forceinline__ int middle(int red) { return ((red + kWide - 1) / kWide + 1) / 2 * kWide; }
 
-// What the warp asks for next: first W1's pieces, then W2's.  A piece is two TMA boxes of 8 rows x 256 bytes.
+// What the warp asks for next: first W1's pieces, then W2's.  A piece is one TMA box: 8 gate and 8 up rows, or
+// 16 rows, of 256 bytes.
 // (As one bulk copy per row, issued by sixteen lanes, asking took 1300 cycles a piece, as eight asynchronous
 // 16-byte copies per lane 400 to 750: more than the work on the piece.)
 struct Stream {
     uint8_t *ring;
     uint64_t *full;
-    uint32_t asked, done;
+    uint32_t asked, place;        // pieces asked for, and the ring's place for the next
+    uint32_t done, phase;         // the place of the next piece to work on, and its phase
     bool ok;                      // no wait has run out; then nothing more is asked for
     int product, k, red, per;
     int from, to;                 // the part of a row that this warp takes
-    int row, second;              // the first row of each box
+    int row, outer;               // the box's first row, and its expert (for W1: gate half)
     uint32_t taken, worked;       // units (and ends) taken, and worked on
 
     // The next unit: whichever of the CTA's no warp has taken yet (a fixed share for each warp left some
@@ -451,8 +453,8 @@ struct Stream {
             }
             if (from >= to) continue;
             const int lot = static_cast<unsigned>(u) / static_cast<unsigned>(per), i = u - lot * per, e = sm.expert[lot];
-            row = product == 0 ? e * 2 * p.a.I + i * 8 : e * p.a.H + i * 16;
-            second = row + (product == 0 ? p.a.I : 8);
+            row = product == 0 ? i * 8 : i * 16;
+            outer = product == 0 ? 2 * e : e;
             break;
         }
         k = from;
@@ -461,15 +463,13 @@ struct Stream {
     __device__ __forceinline__ void ask(const Params &p, const Maps &maps, Smem &sm, int warp, int lane)
     {
         if (product == 2) return;
-        const uint32_t s = asked % kStages;
         if (ok && elect_one()) {
-            const CUtensorMap *map = product == 0 ? &maps.w1 : &maps.w2;
-            mbar_arrive_expect_tx(full + s, kStageBytes);
-            tma_load_2d_plain(ring + s * kStageBytes, map, full + s, k, row);
-            tma_load_2d_plain(ring + s * kStageBytes + kStageBytes / 2, map, full + s, k, second);
+            mbar_arrive_expect_tx(full + place, kStageBytes);
+            tma_load_3d_plain(ring + place * kStageBytes, product == 0 ? &maps.w1 : &maps.w2, full + place, k, row, outer);
         }
         __syncwarp();
         asked += ok;
+        place = place + 1 == kStages ? 0 : place + 1;
         k += kWide;
         if (k >= to) take(p, sm, warp, lane, false);
     }
@@ -510,7 +510,7 @@ __device__ __forceinline__ void unit_sums(bool first, const LayerArgs &a, Smem &
     const uint8_t *ts1 = src_scale + who(t4 * 2 + 1 < T ? t4 * 2 + 1 : 0) * stride;
 #pragma unroll
     for (int x = 0; x < 4; ++x) acc[x] = 0.f;
-    uint32_t sw0 = 0, sw1 = 0;                       // bytes of block (32 at a time) + lane
+    float sw0 = 0.f, sw1 = 0.f;                      // scales of block (32 at a time) + lane
     const int lo_at = g * kWide + t4 * 16, hi_at = lo_at + 8 * kWide;
     // one piece, blocks k0 on, by the tokens `x`; those of the next piece are on their way meanwhile
     auto step = [&](const Tokens &x, Tokens &next, int k0) {
@@ -518,12 +518,11 @@ __device__ __forceinline__ void unit_sums(bool first, const LayerArgs &a, Smem &
         if (nb > kPieceBlocks) next.load(tok, ts0, ts1, k0 + kPieceBlocks, nb - kPieceBlocks);
         if ((k0 & 31) == 0 || k0 == from) {
             const int at = (k0 & ~31) + lane, b = at < rblocks ? at : rblocks - 1;
-            sw0 = load_scale_byte(W_scale, a.ue8m0, sc0 + b, bad);
-            sw1 = first ? load_scale_byte(W_scale, a.ue8m0, sc1 + b, bad) : sw0;
+            sw0 = scale_value(load_scale_byte(W_scale, a.ue8m0, sc0 + b, bad));
+            sw1 = first ? scale_value(load_scale_byte(W_scale, a.ue8m0, sc1 + b, bad)) : sw0;
         }
-        const uint32_t s = st.done % kStages;
-        st.ok = st.ok && warp_wait(st.full + s, (st.done / kStages) & 1u, abort);
-        const uint8_t *stage = st.ring + s * kStageBytes;
+        st.ok = st.ok && warp_wait(st.full + st.done, st.phase, abort);
+        const uint8_t *stage = st.ring + st.done * kStageBytes;
 #pragma unroll
         for (int b = 0; b < kPieceBlocks; ++b) {
             if (b >= nb) break;
@@ -531,8 +530,7 @@ __device__ __forceinline__ void unit_sums(bool first, const LayerArgs &a, Smem &
             const uint4 lo1 = *reinterpret_cast<const uint4 *>(stage + lo_at + b * 128 + 64);
             const uint4 hi0 = *reinterpret_cast<const uint4 *>(stage + hi_at + b * 128);
             const uint4 hi1 = *reinterpret_cast<const uint4 *>(stage + hi_at + b * 128 + 64);
-            const float w0 = scale_value(__shfl_sync(0xffffffffu, sw0, (k0 + b) & 31));
-            const float w1 = first ? scale_value(__shfl_sync(0xffffffffu, sw1, (k0 + b) & 31)) : w0;
+            const float w0 = __shfl_sync(0xffffffffu, sw0, (k0 + b) & 31), w1 = __shfl_sync(0xffffffffu, sw1, (k0 + b) & 31);
             // eight K = 16 steps in two chains
             float d[4] = {0.f, 0.f, 0.f, 0.f}, f[4] = {0.f, 0.f, 0.f, 0.f};
             mma_codes(d, lo0.x, hi0.x, x.b0[b].x);
@@ -543,14 +541,16 @@ __device__ __forceinline__ void unit_sums(bool first, const LayerArgs &a, Smem &
             mma_codes(f, lo1.z, hi1.z, x.b1[b].z);
             mma_codes(d, lo0.w, hi0.w, x.b0[b].w);
             mma_codes(f, lo1.w, hi1.w, x.b1[b].w);
-            const float x0 = scale_value((x.s0 >> (8 * b)) & 0xFFu), x1 = scale_value((x.s1 >> (8 * b)) & 0xFFu);
+            // (the tokens' scales are this kernel's own: bytes 105 to 254)
+            const float x0 = __uint_as_float((x.s0 >> (8 * b) & 0xFFu) << 23), x1 = __uint_as_float((x.s1 >> (8 * b) & 0xFFu) << 23);
             acc[0] = fmaf(d[0] + f[0], w0 * x0, acc[0]);
             acc[1] = fmaf(d[1] + f[1], w0 * x1, acc[1]);
             acc[2] = fmaf(d[2] + f[2], w1 * x0, acc[2]);
             acc[3] = fmaf(d[3] + f[3], w1 * x1, acc[3]);
         }
         __syncwarp();                                // all lanes have read the stage
-        ++st.done;
+        st.done = st.done + 1 == kStages ? 0 : st.done + 1;
+        st.phase ^= st.done == 0;
         st.ask(p, maps, sm, warp, lane);
     };
     Tokens x, y;
@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_proxy_async_smem();   // the ring's memory passes from these threads to the copies
     make_lists(p, sm);
     Stream st;
-    st.asked = st.done = 0;
+    st.asked = st.place = st.done = st.phase = 0;
     st.ring = ring + warp * kStages * kStageBytes;
     st.full = sm.full[warp];
     st.product = 0;
@@ -791,11 +791,11 @@ cudaError_t launch_layer(const LayerArgs &a, cudaStream_t stream)
         done.fetch_or(bit, std::memory_order_relaxed);
     }
     Maps maps;
-    const uint64_t d1[2] = {static_cast<uint64_t>(a.H), static_cast<uint64_t>(a.E) * 2 * a.I};
-    const uint64_t d2[2] = {static_cast<uint64_t>(a.I), static_cast<uint64_t>(a.E) * a.H};
-    const uint32_t box[2] = {kWide, 8};
-    if (!encode_map(&maps.w1, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.W1, 2, d1, box, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-        !encode_map(&maps.w2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.W2, 2, d2, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+    const uint64_t d1[3] = {static_cast<uint64_t>(a.H), static_cast<uint64_t>(a.I), static_cast<uint64_t>(a.E) * 2};
+    const uint64_t d2[3] = {static_cast<uint64_t>(a.I), static_cast<uint64_t>(a.H), static_cast<uint64_t>(a.E)};
+    const uint32_t b1[3] = {kWide, 8, 2}, b2[3] = {kWide, 16, 1};
+    if (!encode_map(&maps.w1, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.W1, 3, d1, b1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_map(&maps.w2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.W2, 3, d2, b2, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     const Params p{a, make_layout(a.N, a.H, a.I, a.E, a.K)};
     cudaLaunchConfig_t cfg = {};
