@@ -8,8 +8,8 @@
 // With N <= 64 tokens the time is the weights of the experts that are touched, read
 // once; everything else is arranged around that stream.  One CTA per SM.  A unit of
 // work is 16 weight rows of one expert (8 gate and 8 up rows of W1, or 16 rows of
-// W2); the units of all touched experts are split evenly and in order over the CTAs,
-// and a CTA's over its sixteen warps.  Each of those is on its own: it copies its
+// W2); the units of all touched experts (but the last fifth, where there are many) are
+// split evenly and in order over the CTAs, and a CTA's over its sixteen warps.  Each of those is on its own: it copies its
 // units in pieces of 16 rows x 256 bytes to a ring of three in shared memory (TMA,
 // W1's and then W2's without a pause between: they need only the routing, so that W2
 // is in flight while the CTAs wait for each other between the products), multiplies a
@@ -23,9 +23,12 @@
 //   each expert's tokens; W1 units, the activation in fp32, and by whoever completes
 //   a 128-block its E4M3 form | W2 units | weighted sum.
 //
-// Measured, H = 2048, I = 1024, 128 experts, top 8: 64 tokens 182 us (795 MB, 4.4 TB/s): the stream waits for
-// instructions, 9 cycles each at four warps a scheduler.  One token 34 us for 51 MB: the phases one after the
-// other, each some microseconds of first-touch latency, 9.5 of them before the first weight is asked for.
+// Measured, H = 2048, I = 1024, 128 experts, top 8: 64 tokens 169 us (795 MB, 4.7 TB/s).  Without the tensor work
+// it takes 6 us less: what bounds it is the stream (5.5 TB/s while it runs), 17 us before the
+// first weight is asked for, and some 6 us at each product's end.  One token 35 us for 51 MB: the phases one after
+// the other, each some microseconds of first-touch latency, 9.5 of them before the first weight.  (W1's first
+// 32 to 96 MB asked into L2 at the start, before the routing is known: 2 to 6 us slower; the routing's own loads
+// and barriers then wait behind them.)
 #include "expert_internal.cuh"
 
 namespace moe {
@@ -46,20 +49,27 @@ constexpr int kMostBlocks = 256;              // 128-blocks of the activation th
 // for 64 tokens on 128 experts, top 8.)
 constexpr int kLot = 8;
 constexpr int kMostLots = kMaxE + kMaxN * kMaxK / kLot;
+// The last units of a product are common: a CTA that is done with its own takes one after the other, as some get
+// a fifth less of the memory's rate than others (64 tokens as above: 169 us, 180 without, 173 with an eighth or
+// a half common).  With fewer than four units for each warp it does not pay (10 tokens: 115 us, 111 without).
+constexpr int kPoolRounds = 4, kPoolShare = 5;
 constexpr int kRedundant = 2;                 // up to this many tokens every CTA finds their top-K itself
 
 struct Header {                               // zero before the first call, left zero by every call
     unsigned barrier[4], done, aborted;
+    unsigned pool[2];                         // how many of each product's common units are taken
 };
 
 struct Smem {
     uint64_t full[kWarps][kStages];
     int abort;
     int active;                               // lots of all touched experts
-    int unit_from[2], unit_to[2];             // the units of each product that this CTA takes
+    int units[2];                             // of each product
+    int pool_from[2];                         // those from here on are common to the CTAs
+    int unit_from[2], unit_to[2];             // those that this CTA has of its own
     int shared[2];                            // whether two warps share each of them, a half of its reduction each
-    int next[2];                              // the first of them that no warp has taken
-    int taken[kWarps][kTaken];                // each warp's own, in order, unit_to behind a product's last
+    int next[2];                              // the first of its own that no warp has taken
+    int taken[kWarps][kTaken];                // each warp's, in order, `units` behind a product's last
     union {
         struct {
             uint32_t mask[kMaxE][2];          // tokens of each expert
@@ -376,7 +386,10 @@ __device__ void make_lists(const Params &p, Smem &sm)
         }
         if (lane < 2) {
             // (below 2^31: at most 384 lots of 8192 units, and some hundreds of CTAs)
-            const unsigned total = active * (lane == 0 ? p.a.I / 8 : p.a.H / 16), ctas = gridDim.x;
+            const unsigned units = active * (lane == 0 ? p.a.I / 8 : p.a.H / 16), ctas = gridDim.x;
+            const unsigned total = units < ctas * kWarps * kPoolRounds ? units : units - units / kPoolShare;
+            sm.units[lane] = units;
+            sm.pool_from[lane] = total;
             sm.next[lane] = sm.unit_from[lane] = total / ctas * blockIdx.x + total % ctas * blockIdx.x / ctas;
             sm.unit_to[lane] = total / ctas * (blockIdx.x + 1) + total % ctas * (blockIdx.x + 1) / ctas;
             // where no CTA has more than half as many units as warps (one token, top 8 of 128 experts of
@@ -433,15 +446,19 @@ struct Stream {
                 from = shared && (warp & 1) ? middle(red) : 0;
                 to = shared && !(warp & 1) && middle(red) < red ? middle(red) : red;
             }
-            const int end = sm.unit_to[product];
+            const int end = sm.units[product];
             int u = end;
             if (!sm.shared[product]) {
                 if (lane == 0) {
                     u = atomicAdd(&sm.next[product], 1);
-                    u = u < end ? u : end;
+                    if (u >= sm.unit_to[product]) {
+                        u = sm.pool_from[product];
+                        if (u < end) u += atomicAdd(&static_cast<Header *>(p.a.workspace)->pool[product], 1u);
+                        u = u < end ? u : end;
+                    }
                 }
                 u = __shfl_sync(0xffffffffu, u, 0);
-            } else if (enter && sm.unit_from[product] + (warp >> 1) < end) {
+            } else if (enter && sm.unit_from[product] + (warp >> 1) < sm.unit_to[product]) {
                 u = sm.unit_from[product] + (warp >> 1);    // (at most one)
             }
             if (lane == 0) sm.taken[warp][taken % kTaken] = u;
@@ -593,7 +610,7 @@ __device__ __forceinline__ void product(bool first, const Params &p, const Maps 
     const uint8_t *src = ws + (first ? p.l.x8 : p.l.a8), *src_scale = ws + (first ? p.l.xs : p.l.as);
     float *act = reinterpret_cast<float *>(ws + p.l.a);
     float *dst = first ? act : reinterpret_cast<float *>(ws + p.l.y);
-    const int from = sm.unit_from[first ? 0 : 1], to = sm.unit_to[first ? 0 : 1];
+    const int from = sm.unit_from[first ? 0 : 1], to = sm.unit_to[first ? 0 : 1], end = sm.units[first ? 0 : 1];
     bool bad = false;
     const bool shared = sm.shared[first ? 0 : 1] != 0;
     const int mid = middle(rblocks * 128) / 128;
@@ -601,7 +618,7 @@ __device__ __forceinline__ void product(bool first, const Params &p, const Maps 
     for (;;) {
         const int u = sm.taken[warp][st.worked % kTaken];
         ++st.worked;
-        if (u == to) break;
+        if (u == end) break;
         const int lot = static_cast<unsigned>(u) / static_cast<unsigned>(per), i = u - lot * per;
         const int e = sm.expert[lot], T = sm.first[lot + 1] - sm.first[lot];
         // where the scales of the unit's rows start; gate and up rows lie in different blocks
@@ -625,11 +642,11 @@ __device__ __forceinline__ void product(bool first, const Params &p, const Maps 
         unit_out(first, a, sm, dst, lot, i, T, lane, acc);
         if (first) {
             // Whoever completes the sixteen units of a 128-block of the activation turns it into E4M3.  The
-            // units that this CTA has of it are counted here, CTAs that share one meet in the workspace.
+            // units that this CTA has of its own are counted here, CTAs that share a block meet in the workspace.
             const int b0 = u & ~15, b1 = b0 + 16;   // (a lot's units are whole blocks)
             const int ours = (b1 < to ? b1 : to) - (b0 > from ? b0 : from);
             const int at = (u >> 4) - (from >> 4);
-            const bool count_here = ((to - 1) >> 4) - (from >> 4) < kMostBlocks;
+            const bool count_here = u < to && ((to - 1) >> 4) - (from >> 4) < kMostBlocks;
             int last = 0;
             __threadfence_block();
             __syncwarp();
@@ -768,6 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < (p.a.E + kMaxN * kMaxK / kLot) * (p.a.I / 128); ++i) counters[i] = 0;
             }
             for (int i = 0; i < 4; ++i) hdr->barrier[i] = 0;
+            hdr->pool[0] = hdr->pool[1] = 0;
             hdr->done = 0;
         }
     }

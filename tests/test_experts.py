@@ -642,6 +642,25 @@ def test_moe_layer(dev, N, H, I, E, K, fmt):
 
 
 @gpu
+@pytest.mark.parametrize("H,I,E", [
+    (768, 384, 256),      # some 10600 units of weights in each product: the last are common to the CTAs
+    (512, 640, 160),      # 12000 and 4800: in the first product only
+])
+def test_moe_layer_with_common_units(dev, H, I, E):
+    """Which CTA takes a common unit changes nothing, and the count of them starts anew with every call."""
+    N, K = 64, 8
+    t = layer_inputs(N, H, I, E, K, "ue8m0", dev, seed=90)
+    ws = moe.layer_workspace(N, H, I, E, K)
+    st = status_word(dev)
+    first = moe.moe_layer(t[0], t[1], K, *t[2:], workspace=ws, status=st)
+    check_layer(first, *t, K)
+    for rep in range(30):
+        r = moe.moe_layer(t[0], t[1], K, *t[2:], workspace=ws, status=st)
+        assert torch.equal(r.out.view(torch.int16), first.out.view(torch.int16)), rep
+    assert st.item() == 0, moe.status_string(st.item())
+
+
+@gpu
 @pytest.mark.parametrize("renorm", [True, False])
 def test_moe_layer_bias_residual_and_in_place(dev, renorm):
     t = layer_inputs(7, 256, 128, 16, 3, "fp32", dev, seed=50)
