@@ -248,14 +248,32 @@ def layer_workspace_size(N: int, H: int, I: int, E: int, K: int) -> int:
     return int(lib().moe_layer_workspace_size(N, H, I, E, K))
 
 
+def _capturing(stream) -> bool:
+    """Whether a CUDA graph is being captured on `stream` (None: the current one)."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def layer_workspace(N: int, H: int, I: int, E: int, K: int, device=None, stream=None) -> torch.Tensor:
     """A workspace for moe_layer, cached per (device, stream, E, I) and grown where a call needs more.
     Its counters start at zero and every call leaves them there, so one buffer serves all calls of one
-    stream; calls that may overlap on the GPU must not share it."""
+    stream; calls that may overlap on the GPU must not share it.
+
+    While a graph is being captured on the stream the buffer is a new one of the capture's own memory, its
+    counters cleared by the graph, and the cache is left alone: graphs may be replayed in any order and next
+    to plain calls, and what a graph holds is neither shared with a later call nor freed when one needs more.
+    (A buffer taken outside and passed to a captured call is the graph's for as long as the graph is used.)"""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     if stream is None:
         stream = torch.cuda.current_stream(device)
     need = layer_workspace_size(N, H, I, E, K)
+    if _capturing(stream):
+        with torch.cuda.stream(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device=device)
+            ws[:256 + 4 * (E + 128) * (I // BLOCK)].zero_()     # what moe_route.h asks to be zero
+        return ws
     key = (device.index, stream.cuda_stream, E, I)
     ws = _layer_workspaces.get(key)
     if ws is None or ws.numel() < need:
@@ -291,7 +309,7 @@ def moe_layer(X: torch.Tensor, W_gate: torch.Tensor, K: int, W1_fp8: torch.Tenso
     if workspace is not None:
         ws, ws_bytes = _workspace_arg(workspace)
     elif layer_workspace_size(N, H, I, E, K):
-        cached = _layer_workspaces.get((dev, raw, E, I))
+        cached = None if _capturing(stream) else _layer_workspaces.get((dev, raw, E, I))
         if cached is None or cached.numel() < layer_workspace_size(N, H, I, E, K):
             cached = layer_workspace(N, H, I, E, K, X.device, stream)
         ws, ws_bytes = cached.data_ptr(), cached.numel()

@@ -488,6 +488,8 @@ MOE_API size_t moe_layer_workspace_size(int N, int H, int I, int E, int K);
  *   workspace  moe_layer_workspace_size() bytes, 256-byte aligned; its first
  *              256 + 4 * (E + 128) * (I/128) bytes zero before the first call with these E and I
  *              (every call leaves them zero).  Calls that may overlap need their own.
+ *              A call captured into a graph keeps the address: the buffer has to live as long as
+ *              the graph, and a clearing that was captured has happened only once that graph ran.
  * H % 128 == 0, I % 128 == 0, both <= 65536, 1 <= K <= min(E, 16), E <= 256.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_MISALIGNED, MOE_ERR_WORKSPACE,
  * MOE_ERR_UNSUPPORTED (N > 64), MOE_ERR_CUDA; status_word: MOE_ERR_TIMEOUT, MOE_ERR_BAD_SCALE.
