@@ -18,6 +18,9 @@ for weights.  A training step of one layer's MLP::
 
 Kept from the forward to the backward pass: E4M3 rows only.  For serving a few tokens,
 ``moe_layer`` is the whole layer in one launch.
+
+With ``stream`` a call launches there, and what it allocates is that stream's memory, as under
+``torch.cuda.stream(stream)``; ordering it against other streams is the caller's.
 """
 from __future__ import annotations
 
@@ -75,6 +78,15 @@ def _raw_stream(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for a result, of the stream that will write it: a block of the current stream may still be read by
+    what is queued there, or be handed out again there, while another stream writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dims(t: torch.Tensor, name: str, n: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -105,8 +117,8 @@ def quantize_weight(W: torch.Tensor, scale_format: str = "fp32", out=None, strea
     E, rows, cols = whole if len(whole) == 3 else (1, *whole)
     shape = (E, _blocks(rows), _blocks(cols)) if len(whole) == 3 else (_blocks(rows), _blocks(cols))
     if out is None:
-        q = torch.empty(whole, dtype=torch.uint8, device=W.device)
-        s = torch.empty(shape, dtype=_scale_dtype(scale_format), device=W.device)
+        q = _new(whole, torch.uint8, W.device, stream)
+        s = _new(shape, _scale_dtype(scale_format), W.device, stream)
         qp, sp = q.data_ptr(), s.data_ptr()
     else:
         q, s = out
@@ -137,7 +149,7 @@ def expert_gemm(X_fp8: torch.Tensor, X_scale: torch.Tensor, W_fp8: torch.Tensor,
     off, _ = _groups(expert_offsets, E, dev)
     n = cols if transpose else rows
     if out is None:
-        out = torch.empty((R, n), dtype=torch.bfloat16, device=X_fp8.device)
+        out = _new((R, n), torch.bfloat16, X_fp8.device, stream)
         y = out.data_ptr()
     else:
         y = _arg(out, "out", torch.bfloat16, (R, n), dev)
@@ -165,7 +177,7 @@ def expert_wgrad(dY: torch.Tensor, X_fp8: torch.Tensor, X_scale: torch.Tensor,
     shape = (E, rows, cols)
     added = _opt(add, "add", torch.float32, shape, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dY.device)
+        out = _new(shape, dtype, dY.device, stream)
     _check(lib().moe_expert_wgrad(dy, x, xs, xf, off, R, E, rows, cols, added, _arg(out, "out", dtype, shape, dev),
                                   int(dtype is torch.bfloat16), _status_ptr(status), _raw_stream(stream, dev)),
            "moe_expert_wgrad")
@@ -187,9 +199,9 @@ class SwiGLUGrad:
     dGU_scale: Optional[torch.Tensor]
 
 
-def _coded(R: int, C: int, scale_format: str, device):
-    return (torch.empty((R, C), dtype=torch.uint8, device=device),
-            torch.empty((R, C // BLOCK), dtype=_scale_dtype(scale_format), device=device))
+def _coded(R: int, C: int, scale_format: str, device, stream):
+    return (_new((R, C), torch.uint8, device, stream),
+            _new((R, C // BLOCK), _scale_dtype(scale_format), device, stream))
 
 
 def swiglu(GU: torch.Tensor, keep: bool = True, scale_format: str = "fp32", out: Optional[SwiGLU] = None,
@@ -204,7 +216,8 @@ def swiglu(GU: torch.Tensor, keep: bool = True, scale_format: str = "fp32", out:
         raise ValueError("GU must be [R, 2I] with I a multiple of 128")
     I, sd = C // 2, _scale_dtype(scale_format)
     if out is None:
-        out = SwiGLU(*_coded(R, I, scale_format, GU.device), *(_coded(R, C, scale_format, GU.device) if keep else (None, None)))
+        out = SwiGLU(*_coded(R, I, scale_format, GU.device, stream),
+                     *(_coded(R, C, scale_format, GU.device, stream) if keep else (None, None)))
     _check(lib().moe_swiglu(src, R, I, _arg(out.A_fp8, "A_fp8", torch.uint8, (R, I), dev),
                             _arg(out.A_scale, "A_scale", sd, (R, I // BLOCK), dev),
                             _opt(out.GU_fp8, "GU_fp8", torch.uint8, (R, C), dev),
@@ -223,8 +236,8 @@ def swiglu_backward(dA: torch.Tensor, GU_fp8: torch.Tensor, GU_scale: torch.Tens
     da, kept = _arg(dA, "dA", torch.bfloat16, (R, I), dev), _arg(GU_fp8, "GU_fp8", torch.uint8, (R, 2 * I), dev)
     gs, gf = _scales(GU_scale, "GU_scale", (R, 2 * I // BLOCK), dev)
     if out is None:
-        out = SwiGLUGrad(torch.empty((R, 2 * I), dtype=torch.bfloat16, device=dA.device) if bf16 else None,
-                         *(_coded(R, 2 * I, scale_format, dA.device) if fp8 else (None, None)))
+        out = SwiGLUGrad(_new((R, 2 * I), torch.bfloat16, dA.device, stream) if bf16 else None,
+                         *(_coded(R, 2 * I, scale_format, dA.device, stream) if fp8 else (None, None)))
     _check(lib().moe_swiglu_backward(da, kept, gs, gf, R, I, _opt(out.dGU, "dGU", torch.bfloat16, (R, 2 * I), dev),
                                      _opt(out.dGU_fp8, "dGU_fp8", torch.uint8, (R, 2 * I), dev),
                                      _opt(out.dGU_scale, "dGU_scale", _scale_dtype(scale_format), (R, 2 * I // BLOCK), dev),
@@ -302,9 +315,8 @@ def moe_layer(X: torch.Tensor, W_gate: torch.Tensor, K: int, W1_fp8: torch.Tenso
         raise TypeError("W1_scale and W2_scale must be of one format")
     b, res = _opt(bias, "bias", torch.float32, (E,), dev), _opt(residual, "residual", torch.bfloat16, (N, H), dev)
     if out is None:
-        out = LayerOut(torch.empty((N, H), dtype=torch.bfloat16, device=X.device),
-                       torch.empty((N, K), dtype=torch.int32, device=X.device),
-                       torch.empty((N, K), dtype=torch.float32, device=X.device))
+        out = LayerOut(_new((N, H), torch.bfloat16, X.device, stream), _new((N, K), torch.int32, X.device, stream),
+                       _new((N, K), torch.float32, X.device, stream))
     raw = _raw_stream(stream, dev)
     if workspace is not None:
         ws, ws_bytes = _workspace_arg(workspace)
