@@ -597,9 +597,8 @@ bool encode_map(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes, cons
 cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t stream)
 {
     int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    cudaError_t err = expert_device(&dev);
     if (err != cudaSuccess) return err;
-    if (device_cc_major(dev) != 10) return cudaErrorNotSupported;
     const int red = a.transpose ? a.rows : a.cols, out = a.transpose ? a.cols : a.rows;
 
     TokenMaps tmX;

@@ -190,6 +190,14 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t *bar)
 // ---------------------------------------------------------------------------
 // Launchers (validated arguments, the launch's cudaError_t)
 // ---------------------------------------------------------------------------
+// The current device, if it is one that these kernels are for; cudaErrorNotSupported otherwise.
+inline cudaError_t expert_device(int *dev)
+{
+    const cudaError_t err = cudaGetDevice(dev);
+    if (err != cudaSuccess) return err;
+    return device_cc_major(*dev) == 10 ? cudaSuccess : cudaErrorNotSupported;
+}
+
 struct ExpertGemmArgs {
     const void *X, *X_scale;
     const void *W, *W_scale;

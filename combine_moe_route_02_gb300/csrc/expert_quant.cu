@@ -250,6 +250,9 @@ unsigned act_grid(const Rows &d)
 cudaError_t launch_quantize_weight(const void *W, int E, int rows, int cols, void *q, void *scale, int ue8m0,
                                    cudaStream_t stream)
 {
+    int dev = 0;
+    const cudaError_t err = expert_device(&dev);
+    if (err != cudaSuccess) return err;
     const dim3 grid((cols + 127) / 128, (rows + 127) / 128, E);
     quantize_weight_kernel<<<grid, kQwThreads, 0, stream>>>(static_cast<const uint4 *>(W), rows, cols,
                                                             static_cast<uint8_t *>(q), scale, ue8m0);
@@ -259,6 +262,9 @@ cudaError_t launch_quantize_weight(const void *W, int E, int rows, int cols, voi
 cudaError_t launch_swiglu(const void *GU, int64_t R, int I, void *A_fp8, void *A_scale, void *GU_fp8, void *GU_scale,
                           int ue8m0, cudaStream_t stream)
 {
+    int dev = 0;
+    const cudaError_t err = expert_device(&dev);
+    if (err != cudaSuccess) return err;
     const Rows d = make_rows(R, I);
     const auto kernel = GU_fp8 ? swiglu_kernel<true> : swiglu_kernel<false>;
     kernel<<<act_grid(d), kActThreads, 0, stream>>>(static_cast<const __nv_bfloat16 *>(GU), d, static_cast<uint8_t *>(A_fp8),
@@ -270,6 +276,9 @@ cudaError_t launch_swiglu_backward(const void *dA, const void *GU_fp8, const voi
                                    int I, void *dGU, void *dGU_fp8, void *dGU_scale, int ue8m0, int32_t *status,
                                    cudaStream_t stream)
 {
+    int dev = 0;
+    const cudaError_t err = expert_device(&dev);
+    if (err != cudaSuccess) return err;
     const Rows d = make_rows(R, I);
     swiglu_backward_kernel<<<act_grid(d), kActThreads, 0, stream>>>(
         static_cast<const __nv_bfloat16 *>(dA), static_cast<const uint8_t *>(GU_fp8), GU_scale, gu_ue8m0, d,

@@ -604,9 +604,8 @@ cudaError_t launch(int dev, dim3 grid, cudaStream_t stream, const CUtensorMap &t
 cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream)
 {
     int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    cudaError_t err = expert_device(&dev);
     if (err != cudaSuccess) return err;
-    if (device_cc_major(dev) != 10) return cudaErrorNotSupported;
     CUtensorMap tmY, tmX, tmW, tmAdd;
     const uint64_t R = a.R > 0 ? a.R : 1;   // (no rows: the maps are not used)
     const uint64_t yd[2] = {static_cast<uint64_t>(a.rows), R};

@@ -798,7 +798,7 @@ size_t layer_workspace_bytes(int N, int H, int I, int E, int K) { return make_la
 cudaError_t launch_layer(const LayerArgs &a, cudaStream_t stream)
 {
     int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    cudaError_t err = expert_device(&dev);
     if (err != cudaSuccess) return err;
     static std::atomic<uint64_t> done{0};
     const uint64_t bit = 1ull << (dev & 63);
