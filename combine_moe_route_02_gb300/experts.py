@@ -136,8 +136,8 @@ def expert_gemm(X_fp8: torch.Tensor, X_scale: torch.Tensor, W_fp8: torch.Tensor,
     """Each expert's rows times its weight [rows, cols], bf16: x W^T, or x W with `transpose`
     (the gradient of the first one's input).  Without expert_offsets all rows are one group
     (W [1, rows, cols] or [rows, cols]).  Rows of no group are left as `out` has them."""
-    if W_fp8.dim() == 2:
-        W_fp8, W_scale = W_fp8[None], W_scale[None]
+    if isinstance(W_fp8, torch.Tensor) and W_fp8.dim() == 2:
+        W_fp8, W_scale = W_fp8[None], W_scale[None] if isinstance(W_scale, torch.Tensor) else W_scale
     E, rows, cols = _dims(W_fp8, "W_fp8", 3)
     R, red = _dims(X_fp8, "X_fp8", 2)
     if red != (rows if transpose else cols):
