@@ -253,7 +253,7 @@ cudaError_t launch_quantize_weight(const void *W, int E, int rows, int cols, voi
     int dev = 0;
     const cudaError_t err = expert_device(&dev);
     if (err != cudaSuccess) return err;
-    const dim3 grid((cols + 127) / 128, (rows + 127) / 128, E);
+    const dim3 grid((cols - 1) / 128 + 1, (rows - 1) / 128 + 1, E);   // (cols may be within 127 of 2^31)
     quantize_weight_kernel<<<grid, kQwThreads, 0, stream>>>(static_cast<const uint4 *>(W), rows, cols,
                                                             static_cast<uint8_t *>(q), scale, ue8m0);
     return cudaGetLastError();

@@ -121,5 +121,7 @@ int main(int argc, char **argv)
     report("moe_swiglu_backward", moe_swiglu_backward(a, b, c, 0, 64, 128, d, NULL, NULL, 0, NULL, NULL));
     report("moe_layer", moe_layer(a, b, NULL, c, d, e, a, 0, NULL, 4, 256, 128, 8, 2, 1, (int32_t *)b, (float *)c, d, NULL,
                                   a, moe_layer_workspace_size(4, 256, 128, 8, 2), NULL));
+    /* the widest row that an int counts in whole eights */
+    report("moe_quantize_weight:widest", moe_quantize_weight(a, 1, 1, 2147483640, b, c, 0, NULL));
     return 0;
 }
