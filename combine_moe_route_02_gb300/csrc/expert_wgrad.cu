@@ -12,7 +12,9 @@
 // comes out 7e-6 of its size too small).  A 32-bit result is therefore summed in
 // segments of 2048 rows, each in an accumulator of its own, and the segments are
 // added to what is in dW already, rounding to nearest (2048 rows: 6e-7).  A result of bf16 type is off
-// by 2^-9 anyway and takes a group in one segment.
+// by 2^-9 anyway and takes segments of 16384 rows (2e-5); those of a longer group are added up, in 32 bits,
+// in the other of the two accumulators (with one segment for any length, 2^20 rows of positive products
+// came out 4e-3 of their sum too small, 2^22 rows 2e-2).
 //
 // Both operands have the reduction on their slow axis (MN-major).  Persistent CTA
 // pairs (cta_group::2); a tile is 256 weight rows x 256 weight columns of one expert,
@@ -56,7 +58,7 @@ template <bool kLoads>
 struct Split {
     static constexpr int kStages = kLoads ? 5 : 6, kBufs = kLoads ? 4 : 2;
 };
-constexpr int kSegment = 2048;                    // rows, whole stages
+constexpr int kSegment = 2048, kSegmentBf16 = 16384;   // rows, whole stages
 constexpr int kMostStages = 6, kMostBufs = 4;
 constexpr int kThreads = 32 * (4 + kEpiWarps + kTeams * kTeamWarps);
 constexpr uint32_t kTmemCols = 512;
@@ -83,7 +85,7 @@ struct Params {
     const int32_t *offsets;
     int64_t R;
     int E, rows, cols, x_ue8m0, bf16_out, has_add;
-    int segment;                  // rows that go into one accumulator
+    int segment;                  // rows that are summed in one go
     int m_tiles, n_tiles;
     int32_t *status;
 };
@@ -212,7 +214,10 @@ __device__ __forceinline__ uint4 convert_codes_rare(const uint2 &w, uint32_t byt
     return make_uint4(a.x, a.y, b.x, b.y);
 }
 
-template <bool kLoads>
+// kLoads: boxes come in to the epilogue (something to add, or fp32 groups of several segments).  kHeld: a bf16 result
+// whose groups may have several segments (a kernel of its own: together with the reading of fp32 segments it took
+// more than the 80 registers that a thread has).
+template <bool kLoads, bool kHeld>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expert_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX,
                         const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmAdd, const Params p)
@@ -307,14 +312,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t b0 = make_smem_desc_sw128(smem_u32(ring + kABytes), kBox, 1024);
         const uint32_t idesc = make_idesc_bf16_f32(kTileM, kTileN, 1, 1);
         uint32_t s = 0, ph = 0;
-        int j = 0;
+        uint32_t b = 0, used = 0;     // the accumulator, and a phase bit for each
         bool ok = true;
         for (int tile = pair; tile < tiles; tile += pairs) {
             const int count = get_tile(tail, p, tile).count;
+            // (such a tile's segments take turns in one accumulator, their sum is in the other; the next tile starts
+            // in the same one, so that its wait covers both)
+            const bool held = kHeld && count > p.segment;
             for (int r0 = 0; r0 < count && ok; r0 += p.segment) {
-                const int end = count - r0 < p.segment ? count : r0 + p.segment, b = j & 1;
-                ok = warp_wait(&tail.acc_empty[b], ((j >> 1) & 1) ^ 1, abort_flag);
+                const int end = count - r0 < p.segment ? count : r0 + p.segment;
+                ok = warp_wait(&tail.acc_empty[b], (used >> b & 1u) ^ 1u, abort_flag);
                 if (!ok) break;
+                used ^= 1u << b;
                 tc_fence_after_sync();
                 const uint32_t d = tmem + b * kTileN;
                 for (int r = r0; r < end; r += kRows) {
@@ -337,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 if (elect_one()) tc_commit_pair(&tail.acc_full[b]);
                 __syncwarp();
-                ++j;
+                if (!held) b ^= 1u;
             }
             if (!ok) break;
         }
@@ -451,6 +460,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int a_tile = pair, a_row = 0, a_c = 0;
         uint32_t asked = 0, q = 0, landed = 0;                    // q: boxes done; landed: a phase bit per buffer
         uint32_t wanted = 0;                                      // a bit per buffer: its box has been asked for
+        const bool bf16_out = kHeld || p.bf16_out;
         auto ask = [&]() {
             Tile t;
             while (a_tile < tiles) {
@@ -460,16 +470,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (a_tile >= tiles) return;
             const uint32_t b = asked % kBufs;
-            if (a_row > 0 || p.has_add) {
+            if ((!kHeld && a_row > 0) || p.has_add) {
                 if (lane == 0) {
                     uint64_t *bar = &tail.added[w][b];
                     // eight boxes lie between a segment's and the next one's, three of which are asked for ahead
-                    if (a_row > 0) {
+                    if (!kHeld && a_row > 0) {
                         bulk_wait<4>();
                         fence_proxy_async_all();
                     }
                     mbar_arrive_expect_tx(bar, kBufBytes);
-                    tma_load_3d(bufs + b * kBufBytes, a_row > 0 ? &tmW : &tmAdd, bar, t.n0 + dn + a_c, t.m0 + dm, t.e,
+                    tma_load_3d(bufs + b * kBufBytes, !kHeld && a_row > 0 ? &tmW : &tmAdd, bar, t.n0 + dn + a_c, t.m0 + dm, t.e,
                                 l2_policy_evict_first());
                 }
                 wanted |= 1u << b;
@@ -480,7 +490,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (a_c == kHalf) {
                 a_c = 0;
                 a_row += p.segment;
-                if (t.count - a_row <= 0) {
+                if (bf16_out || t.count - a_row <= 0) {           // (a bf16 result is written once)
                     a_row = 0;
                     a_tile += pairs;
                 }
@@ -488,20 +498,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         if (kLoads)
             for (int i = 0; i < kBufs - 1; ++i) ask();
-        int j = 0;
+        uint32_t acc = lane_addr, used = 0;                       // the accumulator, and a phase bit for each
         bool ok = true;
         for (int tile = pair; tile < tiles && ok; tile += pairs) {
             const Tile t = get_tile(tail, p, tile);
-            const bool some = t.count != 0;
+            const bool some = t.count != 0, held = kHeld && t.count > p.segment;
             const int m = t.m0 + dm, n = t.n0 + dn;
             const bool inside = n < p.cols && m < p.rows;         // (columns come in whole 128)
             for (int r0 = 0; (r0 < t.count || r0 == 0) && ok; r0 += p.segment) {
-                const int b = j & 1;
                 if (some) {
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, abort_flag, 64));
+                    const uint32_t b = acc / kTileN & 1u;
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.acc_full[b], used >> b & 1u, abort_flag, 64));
                     if (!ok) break;
                     tc_fence_after_sync();
-                    ++j;
+                    used ^= 1u << b;
+                }
+                if (held && t.count - r0 > p.segment) {
+                    // not the last segment: to the sum so far, which this warp alone reads and writes
+                    for (int c = 0; c < kHalf && inside; c += 8) {
+                        float v[8], z[8];
+                        tmem_ld_32x32b_x8(acc + c, v);
+                        if (r0 > 0) tmem_ld_32x32b_x8((acc ^ kTileN) + c, z);
+                        tmem_ld_wait();
+                        if (r0 > 0) {
+    #pragma unroll
+                            for (int x = 0; x < 8; ++x) v[x] += z[x];
+                        }
+                        tmem_st_32x32b_x8((acc ^ kTileN) + c, v);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    if (lane == 0) mbar_arrive_at(&tail.acc_empty[acc / kTileN & 1u], 0);
+                    continue;
                 }
                 for (int c = 0; c < kHalf && inside; c += 16, ++q) {
                     const uint32_t at = q % kBufs;
@@ -517,8 +545,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     float v[16];
                     if (some) {
-                        tmem_ld_32x32b_x16(lane_addr + b * kTileN + c, v);
+                        tmem_ld_32x32b_x16(acc + c, v);
                         tmem_ld_wait();
+                        if (held) {
+    #pragma unroll
+                            for (int h = 0; h < 16; h += 8) {
+                                float z[8];
+                                tmem_ld_32x32b_x8((acc ^ kTileN) + c + h, z);
+                                tmem_ld_wait();
+    #pragma unroll
+                                for (int x = 0; x < 8; ++x) v[h + x] += z[x];
+                            }
+                        }
                     } else {
     #pragma unroll
                         for (int x = 0; x < 16; ++x) v[x] = 0.f;
@@ -536,9 +574,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             v[4 * x + 2] += z.z;
                             v[4 * x + 3] += z.w;
                         }
-                        if (p.bf16_out) __syncwarp();                 // (other lanes' rows lie where this one writes)
+                        if (bf16_out) __syncwarp();                 // (other lanes' rows lie where this one writes)
                     }
-                    if (p.bf16_out) {
+                    if (bf16_out) {
     #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             uint4 h;
@@ -560,7 +598,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 if (some) {
                     tc_fence_before_sync();
-                    if (lane == 0) mbar_arrive_at(&tail.acc_empty[b], 0);
+                    if (lane == 0) mbar_arrive_at(&tail.acc_empty[acc / kTileN & 1u], 0);
+                    if (!held) acc ^= kTileN;
                 }
             }
         }
@@ -582,7 +621,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-template <bool kLoads>
+template <bool kLoads, bool kHeld>
 cudaError_t launch(int dev, dim3 grid, cudaStream_t stream, const CUtensorMap &tmY, const CUtensorMap &tmX,
                    const CUtensorMap &tmW, const CUtensorMap &tmAdd, const Params &p)
 {
@@ -590,12 +629,12 @@ cudaError_t launch(int dev, dim3 grid, cudaStream_t stream, const CUtensorMap &t
     static std::atomic<uint64_t> done{0};
     const uint64_t bit = 1ull << (dev & 63);
     if (!(done.load(std::memory_order_relaxed) & bit)) {
-        const cudaError_t err = cudaFuncSetAttribute(expert_wgrad_kernel<kLoads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t err = cudaFuncSetAttribute(expert_wgrad_kernel<kLoads, kHeld>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                      static_cast<int>(bytes));
         if (err != cudaSuccess) return err;
         done.fetch_or(bit, std::memory_order_relaxed);
     }
-    expert_wgrad_kernel<kLoads><<<grid, kThreads, bytes, stream>>>(tmY, tmX, tmW, tmAdd, p);
+    expert_wgrad_kernel<kLoads, kHeld><<<grid, kThreads, bytes, stream>>>(tmY, tmX, tmW, tmAdd, p);
     return cudaGetLastError();
 }
 
@@ -632,7 +671,7 @@ cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream)
     p.R = a.R;
     p.E = a.E;
     p.has_add = a.add != nullptr;
-    p.segment = a.bf16_out ? INT_MAX : kSegment;
+    p.segment = a.bf16_out ? kSegmentBf16 : kSegment;
     p.rows = a.rows;
     p.cols = a.cols;
     p.x_ue8m0 = a.x_ue8m0;
@@ -643,8 +682,11 @@ cudaError_t launch_expert_wgrad(const ExpertWgradArgs &a, cudaStream_t stream)
     const int64_t tiles = static_cast<int64_t>(a.E) * p.m_tiles * p.n_tiles;
     const int pairs = device_sm_count(dev) / 2;
     const dim3 grid(2 * static_cast<unsigned>(tiles < pairs ? tiles : pairs));
-    return a.add || a.R > p.segment ? launch<true>(dev, grid, stream, tmY, tmX, tmW, tmAdd, p)
-                 : launch<false>(dev, grid, stream, tmY, tmX, tmW, tmAdd, p);
+    const bool several = a.R > p.segment;
+    const auto run = a.bf16_out ? several ? a.add ? launch<true, true> : launch<false, true>
+                                          : a.add ? launch<true, false> : launch<false, false>
+                                : a.add || several ? launch<true, false> : launch<false, false>;
+    return run(dev, grid, stream, tmY, tmX, tmW, tmAdd, p);
 }
 
 }  // namespace moe

@@ -439,7 +439,8 @@ MOE_API moe_status moe_expert_gemm(const void *X_fp8, const void *X_scale, int x
  *   add fp32 [E, rows, cols] or NULL (nothing is added); may be dW itself when that is fp32
  *   dW  fp32 (dw_bf16 == 0) or bf16 [E, rows, cols]; an empty group gives add, or zeros
  * x is a bf16 number exactly (an E4M3 value times a power of two), the products are
- * accumulated in fp32.  rows % 8 == 0, cols % 128 == 0, both at most 2^18.  One launch.
+ * accumulated in fp32: segments of 2048 rows (bf16 result: 16384) in the tensor cores,
+ * which cut where they add, the segments of a longer group rounding to nearest.  rows % 8 == 0, cols % 128 == 0, both at most 2^18.  One launch.
  */
 MOE_API moe_status moe_expert_wgrad(const void *dY, const void *X_fp8, const void *X_scale, int x_scale_format,
                             const int32_t *expert_offsets, int64_t R, int E, int rows, int cols,
