@@ -71,8 +71,9 @@ __device__ __forceinline__ void bf16x16_to_f32(const uint4 &a, const uint4 &b, f
     bf16x8_to_f32(b, *reinterpret_cast<float (*)[8]>(&f[8]));
 }
 
-// 1 / (1 + exp(-g)) by the approximate exponential and reciprocal (2 units in the last place each); 0 where
-// the exponential overflows.
+// 1 / (1 + exp(-g)) by the approximate exponential and reciprocal (2 units in the last place each); the product
+// that is the exponent is rounded to 32 bits, which makes the exponential some |g| 2^-24 off besides.  0 where it
+// overflows.  What comes of it is rounded to E4M3 (2^-4) or bf16 (2^-8).
 __device__ __forceinline__ float sigmoid(float g)
 {
     float e, r;
@@ -83,7 +84,7 @@ __device__ __forceinline__ float sigmoid(float g)
 
 // ---------------------------------------------------------------------------
 // Weights: one CTA per 128x128 block, the block in registers between the maximum and the codes.  One read and
-// one write, HBM-bound: 64 x 2048 x 2048 in 123 us, 6.5 TB/s.
+// one write, HBM-bound: 64 x 2048 x 2048 in 124 us, 6.5 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kQwThreads = 256;
 
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kQwThreads)
 // 128 u, those of the gate at 128 u + row * I, of the up half I further.  The bound is
 // the memory's, but not by much (60% of the issue slots): a lane of 16 columns instead
 // of 8 halves the share of the scales and shuffles.  131072 x 1024 with the checkpoint:
-// 146 us, 6.5 TB/s (184 us with 8); the gradient of 32761 x 1024: 54 us, 6.3 TB/s.
+// 147 us, 6.4 TB/s (184 us with 8); the gradient of 32761 x 1024: 55 us, 6.2 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kActThreads = 256;
 constexpr int kLanes = 8;

@@ -30,8 +30,8 @@
 //                 the ring; in a group's last stage they also clear the rows behind its end
 //                 (the next group's, or none)
 //
-// Measured (burst): 16384 tokens on 128 experts, top 8, 2048 x 2048, bf16: 673 us, 1.63 PFLOP/s, the tensor
-// pipe 69% busy beside converters that take 58% of the issue slots (back to back, at the power limit, 790 us).
+// Measured (burst): 16384 tokens on 128 experts, top 8, 2048 x 2048, bf16: 672 us, 1.64 PFLOP/s, the tensor
+// pipe 69% busy beside converters that take 56% of the issue slots (back to back, at the power limit, 781 us).
 // 1023 tokens on 64 experts of 512 x 1024, added to 32-bit gradients: 65 us for 273 MB (4.2 TB/s), bound by the
 // latency of the boxes in and out of tiles that have 32 rows to reduce.
 #include <climits>

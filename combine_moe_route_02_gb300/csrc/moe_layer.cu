@@ -23,7 +23,7 @@
 //   each expert's tokens; W1 units, the activation in fp32, and by whoever completes
 //   a 128-block its E4M3 form | W2 units | weighted sum.
 //
-// Measured, H = 2048, I = 1024, 128 experts, top 8: 64 tokens 169 us (795 MB, 4.7 TB/s).  Without the tensor work
+// Measured, H = 2048, I = 1024, 128 experts, top 8: 64 tokens 166 us (795 MB, 4.8 TB/s).  Without the tensor work
 // it takes 6 us less: what bounds it is the stream (5.5 TB/s while it runs), 17 us before the
 // first weight is asked for, and some 6 us at each product's end.  One token 35 us for 51 MB: the phases one after
 // the other, each some microseconds of first-touch latency, 9.5 of them before the first weight.  (W1's first
@@ -578,7 +578,8 @@ __device__ __forceinline__ void unit_sums(bool first, const LayerArgs &a, Smem &
     }
 }
 
-// A unit's sums to where they go: the activation of its 8 features, or 16 elements of y.
+// A unit's sums to where they go: the activation of its 8 features, or 16 elements of y.  (The approximate exponential
+// is some |gate| 2^-24 off, as its argument is scaled in 32 bits; the activation is then rounded to E4M3.)
 __device__ __forceinline__ void unit_out(bool first, const LayerArgs &a, const Smem &sm, float *dst, int lot, int i, int T, int lane,
                                          const float (&acc)[4])
 {

@@ -418,7 +418,8 @@ MOE_API moe_status moe_quantize_weight(const void *W, int E, int rows, int cols,
  *   transpose == 0:  Y[r, m] = sum_k x[r,k] W[e(r), m, k]    x [R, cols], Y [R, rows]
  *   transpose != 0:  Y[r, k] = sum_m x[r,m] W[e(r), m, k]    x [R, rows], Y [R, cols]
  * (the second is the gradient with respect to the first one's x).  fp32
- * accumulation over the whole reduction, one rounding to bf16.
+ * accumulation over the whole reduction in the tensor cores, which cut where they add
+ * (2^18 positive products: 3e-4 of their sum), one rounding to bf16.
  *   X_fp8 uint8 [R, red], X_scale [R, red/128], W_fp8 uint8 [E, rows, cols], W_scale
  *   Y bf16; rows of no group are left as they are
  * The reduction (cols, or rows when transposed) is a multiple of 128, the other
@@ -440,7 +441,8 @@ MOE_API moe_status moe_expert_gemm(const void *X_fp8, const void *X_scale, int x
  *   dW  fp32 (dw_bf16 == 0) or bf16 [E, rows, cols]; an empty group gives add, or zeros
  * x is a bf16 number exactly (an E4M3 value times a power of two), the products are
  * accumulated in fp32: segments of 2048 rows (bf16 result: 16384) in the tensor cores,
- * which cut where they add, the segments of a longer group rounding to nearest.  rows % 8 == 0, cols % 128 == 0, both at most 2^18.  One launch.
+ * which cut where they add, the segments of a longer group rounding to nearest.
+ * rows % 8 == 0, cols % 128 == 0, both at most 2^18.  One launch.
  */
 MOE_API moe_status moe_expert_wgrad(const void *dY, const void *X_fp8, const void *X_scale, int x_scale_format,
                             const int32_t *expert_offsets, int64_t R, int E, int rows, int cols,
