@@ -23,8 +23,8 @@ __all__ = [
     "build", "lib", "MoeError", "route", "route_stats", "load_stats", "dispatch", "dispatch_ep", "permute",
     "combine", "dispatch_workspace_size", "dispatch_workspace", "status_string", "ROUTE_AUTO", "ROUTE_TCGEN05",
     "ROUTE_SIMT", "SCALE_FP32", "SCALE_UE8M0", "Dispatch", "DispatchEP", "route_dispatch",
-    "quantize_weight", "expert_gemm", "expert_wgrad", "swiglu", "swiglu_backward", "moe_layer",
-    "layer_workspace_size", "layer_workspace", "SwiGLU", "SwiGLUGrad", "LayerOut",
+    "quantize_weight", "expert_gemm", "expert_wgrad", "swiglu", "swiglu_backward", "expert_swiglu",
+    "expert_swiglu_backward", "moe_layer", "layer_workspace_size", "layer_workspace", "SwiGLU", "SwiGLUGrad", "LayerOut",
 ]
 
 MOE_OK = 0
@@ -49,6 +49,7 @@ EXPORTED_SYMBOLS = (
     "moe_combine_residual", "moe_dispatch_ex", "moe_permute_ex", "moe_route_stats", "moe_load_stats",
     "moe_dispatch_ep", "moe_route_dispatch", "moe_quantize_weight", "moe_expert_gemm", "moe_expert_wgrad",
     "moe_swiglu", "moe_swiglu_backward", "moe_layer_workspace_size", "moe_layer",
+    "moe_expert_swiglu", "moe_expert_swiglu_backward",
 )
 
 SCALE_FP32, SCALE_UE8M0 = 0, 1
@@ -126,6 +127,10 @@ def lib():
     L.moe_swiglu.restype = I32
     L.moe_swiglu_backward.argtypes = [P, P, P, I32, I64, I32, P, P, P, I32, P, P]
     L.moe_swiglu_backward.restype = I32
+    L.moe_expert_swiglu.argtypes = [P, P, I32, P, P, I32, P, I64, I32, I32, I32, P, P, P, P, I32, P, P]
+    L.moe_expert_swiglu.restype = I32
+    L.moe_expert_swiglu_backward.argtypes = [P, P, I32, P, P, I32, P, P, P, I32, I64, I32, I32, I32, P, P, P, I32, P, P]
+    L.moe_expert_swiglu_backward.restype = I32
     L.moe_layer_workspace_size.argtypes = [I32, I32, I32, I32, I32]
     L.moe_layer_workspace_size.restype = SZ
     L.moe_layer.argtypes = [P, P, P, P, P, P, P, I32, P, I32, I32, I32, I32, I32, I32, P, P, P, P, P, SZ, P]
@@ -497,5 +502,6 @@ def combine(Y: torch.Tensor, row_map: torch.Tensor, topk_w: torch.Tensor, out=No
     return out
 
 
-from .experts import (LayerOut, SwiGLU, SwiGLUGrad, expert_gemm, expert_wgrad, layer_workspace,  # noqa: E402
-                      layer_workspace_size, moe_layer, quantize_weight, swiglu, swiglu_backward)
+from .experts import (LayerOut, SwiGLU, SwiGLUGrad, expert_gemm, expert_swiglu, expert_swiglu_backward,  # noqa: E402
+                      expert_wgrad, layer_workspace, layer_workspace_size, moe_layer, quantize_weight, swiglu,
+                      swiglu_backward)

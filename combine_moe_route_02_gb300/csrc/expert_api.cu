@@ -112,6 +112,95 @@ moe_status moe_swiglu_backward(const void *dA, const void *GU_fp8, const void *G
 }
 
 namespace {
+// sizes and formats of the products joined with the activation: W1 [E, 2I, H], W2 [E, H, I]
+bool expert_swiglu_ok(int64_t R, int E, int H, int I, int x_format, int w_format, int scale_format, const int32_t *offsets)
+{
+    if (E < 1 || E > 256 || !rows_ok(R) || I < 1 || I > (1 << 17) || !sides_ok(H, 2 * I) || H % 128 != 0 || I % 128 != 0)
+        return false;
+    if ((R / 224 + 256) * (I / 128 + 1) > INT_MAX) return false;  // tiles
+    return format_ok(x_format) && format_ok(w_format) && format_ok(scale_format) && (offsets || E == 1);
+}
+}  // namespace
+
+moe_status moe_expert_swiglu(const void *X_fp8, const void *X_scale, int x_scale_format, const void *W1_fp8,
+                             const void *W1_scale, int w_scale_format, const int32_t *expert_offsets, int64_t R, int E,
+                             int H, int I, void *A_fp8, void *A_scale, void *GU_fp8, void *GU_scale, int scale_format,
+                             int32_t *status_word, moe_stream_t stream)
+{
+    NvtxRange nvtx_range("moe_expert_swiglu");
+    if (!expert_swiglu_ok(R, E, H, I, x_scale_format, w_scale_format, scale_format, expert_offsets)) return MOE_ERR_INVALID_ARG;
+    if ((GU_fp8 == nullptr) != (GU_scale == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (R == 0) return MOE_OK;
+    if (!X_fp8 || !X_scale || !W1_fp8 || !W1_scale || !A_fp8 || !A_scale) return MOE_ERR_INVALID_ARG;
+    if (!aligned(X_fp8, 16) || !aligned(W1_fp8, 16) || !aligned(A_fp8, 16) || !aligned(GU_fp8, 16) ||
+        !scale_aligned(X_scale, x_scale_format) || !scale_aligned(W1_scale, w_scale_format) ||
+        !scale_aligned(A_scale, scale_format) || !scale_aligned(GU_scale, scale_format) || !aligned(expert_offsets, 4) ||
+        !aligned(status_word, 4))
+        return MOE_ERR_MISALIGNED;
+    ExpertSwigluArgs a{};
+    a.X = X_fp8;
+    a.X_scale = X_scale;
+    a.x_ue8m0 = x_scale_format;
+    a.W = W1_fp8;
+    a.W_scale = W1_scale;
+    a.w_ue8m0 = w_scale_format;
+    a.offsets = expert_offsets;
+    a.R = R;
+    a.E = E;
+    a.H = H;
+    a.I = I;
+    a.A = A_fp8;
+    a.A_scale = A_scale;
+    a.GU = GU_fp8;
+    a.GU_scale = GU_scale;
+    a.gu_ue8m0 = a.out_ue8m0 = scale_format;
+    a.status = status_word;
+    return launched(launch_expert_swiglu(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_expert_swiglu_backward(const void *dY_fp8, const void *dY_scale, int dy_scale_format, const void *W2_fp8,
+                                      const void *W2_scale, int w_scale_format, const int32_t *expert_offsets,
+                                      const void *GU_fp8, const void *GU_scale, int gu_scale_format, int64_t R, int E,
+                                      int H, int I, void *dGU, void *dGU_fp8, void *dGU_scale, int scale_format,
+                                      int32_t *status_word, moe_stream_t stream)
+{
+    NvtxRange nvtx_range("moe_expert_swiglu_backward");
+    if (!expert_swiglu_ok(R, E, H, I, dy_scale_format, w_scale_format, scale_format, expert_offsets) ||
+        !format_ok(gu_scale_format))
+        return MOE_ERR_INVALID_ARG;
+    if ((dGU_fp8 == nullptr) != (dGU_scale == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (R == 0) return MOE_OK;
+    if (!dY_fp8 || !dY_scale || !W2_fp8 || !W2_scale || !GU_fp8 || !GU_scale || (!dGU && !dGU_fp8)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(dY_fp8, 16) || !aligned(W2_fp8, 16) || !aligned(GU_fp8, 16) || !aligned(dGU, 16) || !aligned(dGU_fp8, 16) ||
+        !scale_aligned(dY_scale, dy_scale_format) || !scale_aligned(W2_scale, w_scale_format) ||
+        !scale_aligned(GU_scale, gu_scale_format) || !scale_aligned(dGU_scale, scale_format) ||
+        !aligned(expert_offsets, 4) || !aligned(status_word, 4))
+        return MOE_ERR_MISALIGNED;
+    ExpertSwigluArgs a{};
+    a.X = dY_fp8;
+    a.X_scale = dY_scale;
+    a.x_ue8m0 = dy_scale_format;
+    a.W = W2_fp8;
+    a.W_scale = W2_scale;
+    a.w_ue8m0 = w_scale_format;
+    a.offsets = expert_offsets;
+    a.R = R;
+    a.E = E;
+    a.H = H;
+    a.I = I;
+    a.backward = 1;
+    a.GU = const_cast<void *>(GU_fp8);
+    a.GU_scale = const_cast<void *>(GU_scale);
+    a.gu_ue8m0 = gu_scale_format;
+    a.dGU = dGU;
+    a.dGU_fp8 = dGU_fp8;
+    a.dGU_scale = dGU_scale;
+    a.out_ue8m0 = scale_format;
+    a.status = status_word;
+    return launched(launch_expert_swiglu(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+namespace {
 bool layer_sizes_ok(int H, int I, int E, int K)
 {
     return H >= 128 && H % 128 == 0 && H <= 65536 && I >= 128 && I % 128 == 0 && I <= 65536 && E >= 1 && E <= 256 &&

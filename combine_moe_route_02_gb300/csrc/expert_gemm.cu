@@ -22,9 +22,10 @@
 //   warp 0      TMA producer (weights 128 x 128, the tokens in one box)
 //   warp 1      leader: MMA issuer (one thread), copies the scales to TMEM
 //               (tcgen05.cp); other CTA: tells the leader which stages have landed
-//   warps 2, 3, 8, 9  scale producers: gather the bytes of 16 128-blocks per row; warp 3
+//   warps 2, 3 and the last two  scale producers: gather the bytes of 16 128-blocks per row; warp 3
 //               allocates TMEM
-//   warps 4..7  epilogue: TMEM -> registers -> bf16, transposed through shared memory
+//   warps 4..7  epilogue: TMEM -> registers -> bf16, transposed through shared memory; with the gated
+//               activation or its gradient (expert_gemm_epilogue.cuh) warps 8..11 too
 //
 // Measured (burst, 1.94 GHz): 16384 tokens on 128 experts, top 8, 2048 x 2048: 354 us, 3.1 PFLOP/s, the
 // tensor pipe 67% busy; the rest is the latency of a ring that 180 KiB in flight per SM do not quite cover
@@ -32,181 +33,20 @@
 // tokens, 64 experts of 1024 x 4096: 122 us against 85 for its bytes.
 #include <mutex>
 
-#include "expert_internal.cuh"
+#include "expert_gemm_epilogue.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTileM = 256;        // output features per tile, half of them in each CTA
-constexpr int kHalfM = 128;
-constexpr int kTileN = 224;        // most tokens per tile: two accumulators and the scales fit TMEM
-constexpr int kBlk = 128;          // reduction block of a scale, and of a ring stage
-constexpr int kStages = 6;
-constexpr int kScaleSlots = 2;
-constexpr int kABytes = kHalfM * kBlk;
-constexpr int kBBytes = kTileN / 2 * kBlk;      // half of the tokens
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kScaleQuadBytes = 512 + 1024;   // four blocks: 128 feature words, 256 token words
-constexpr int kScaleSlotBytes = 4 * kScaleQuadBytes;
-constexpr int kEpiBytes = 4 * 32 * 64;        // per epilogue warp 32 tokens x 32 features
-constexpr int kThreads = 320;
-constexpr uint32_t kTmemCols = 512;
-// Scales lie behind the two accumulators: 4 + 8 columns for four blocks.  Five places in turn: when one is
-// written again its MMAs have completed, those of the tile before the last by the wait for its accumulator,
-// nearer ones because at least six blocks of the ring lie between.
-constexpr uint32_t kSfCol = 2 * kTileN, kSfCols = 12, kSfPlaces = 5;
-static_assert(kSfCol + kSfPlaces * kSfCols <= kTmemCols, "TMEM");
-constexpr int kMaxE = 256;
-
-struct Tail {
-    uint64_t full[kStages], empty[kStages];
-    uint64_t sf_full[kScaleSlots], sf_empty[kScaleSlots];
-    uint64_t acc_full[2], acc_empty[2], drain;
-    uint32_t tmem_base;
-    int abort, bad_index, bad_scale;
-    int tiles;                    // token tiles of all groups
-    int first[kMaxE + 1];         // first token tile of each group
-    int begin[kMaxE], count[kMaxE], size[kMaxE];   // its rows, and the rows of its tiles but the last
-};
-
-constexpr size_t kSmemBytes =
-    1024 + kStages * kStageBytes + kScaleSlots * kScaleSlotBytes + kEpiBytes + sizeof(Tail);
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-
-// Boxes of token rows: a tile takes the smallest that holds its half, so that a stage is two copies
-// (issuing a copy took ~90 cycles: with one for every 32 rows the producer set the pace).
-constexpr int kBoxes = 5;
-__host__ __device__ constexpr int box_rows(int i) { return i == 0 ? 112 : i == 1 ? 96 : i == 2 ? 80 : i == 3 ? 64 : 32; }
-struct TokenMaps {
-    CUtensorMap map[kBoxes];
-};
-
-struct Params {
-    const void *X_scale, *W_scale;
-    const int32_t *offsets;
-    int64_t R;
-    int E, out, red;              // output features, reduction length
-    int transpose, x_ue8m0, w_ue8m0;
-    int x_vec;                    // 1: a row's four scales are one aligned vector; 2: sixteen are (bytes)
-    int m_tiles;
-    void *Y;
-    int32_t *status;
-};
-
-// One tile of a group: its features, where its rows start, how many it holds.
-struct Tile {
-    int e, m0, rows;
-    int64_t row0;
-};
-
-// A role's walk over its CTA pair's tiles (pair, pair + pairs, ...; the features of a token tile
-// follow each other): the group only ever moves forward.
-struct Walk {
-    int tile, j, i, e;            // tile, its token tile and feature tile, the group reached
-
-    __device__ __forceinline__ Walk(int pair, int m_tiles) : tile(pair), j(pair / m_tiles), i(pair - j * m_tiles), e(0) {}
-
-    __device__ __forceinline__ void next(int pairs, int m_tiles)
-    {
-        tile += pairs;
-        i += pairs;
-        if (i >= m_tiles) {
-            const int n = i / m_tiles;
-            j += n;
-            i -= n * m_tiles;
-        }
-    }
-
-    __device__ __forceinline__ Tile get(const Tail &t)
-    {
-        while (t.first[e + 1] <= j) ++e;
-        Tile r;
-        r.e = e;
-        r.m0 = i * kTileM;
-        const int size = t.size[e], at = (j - t.first[e]) * size;
-        r.row0 = static_cast<int64_t>(t.begin[e]) + at;
-        const int left = t.count[e] - at;
-        r.rows = left < size ? left : size;
-        return r;
-    }
-};
-
-// kind::mxf8f6f4, E4M3 x E4M3 -> fp32, UE8M0 scales; the scale byte of the word is `sf`.
-__device__ __forceinline__ uint32_t make_idesc(uint32_t N, uint32_t a_mn_major, uint32_t sf)
-{
-    return (sf << 4) | (a_mn_major << 15) | ((N >> 3) << 17) | (1u << 23) | ((kTileM >> 4) << 24) | (sf << 29);
-}
-
-__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                           uint32_t sfb, uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
-}
-
-// 32 rows of 16 bytes from shared memory to 4 TMEM columns, repeated in the four lane quarters; each
-// CTA of the pair from its own memory to its own TMEM.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr)
-{
-    const uint64_t desc = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
-                          (1ull << 46);   // no swizzle, 8-row groups 128 B apart
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
-
-// 32 lanes x 32 columns of TMEM as fragments of 8x8: v[16 h + 4 c + 2 r + i] is row 16 h + 8 r + lane / 4,
-// column 8 c + 2 (lane % 4) + i.
-__device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, float (&v)[32])
-{
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t r[16];
-        asm volatile(
-            "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-            : "r"(taddr + (static_cast<uint32_t>(16 * h) << 16))
-            : "memory");
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[16 * h + i] = __uint_as_float(r[i]);
-    }
-}
-
-// Those fragments (rows features, columns tokens) as bf16 to shared memory with the tokens as rows of 64
-// bytes: stmatrix transposes each 8x8.  The 16-byte piece f of token t lies at place f ^ (t / 2 % 4).
-__device__ __forceinline__ void store_transposed(uint32_t buf, int lane, const float (&v)[32])
-{
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        // the four matrices: features 0..7, 8..15, 16..23, 24..31 of tokens 8 c .. 8 c + 7
-        uint32_t m[4];
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            const int at = 16 * (f >> 1) + 4 * c + 2 * (f & 1);
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[at], v[at + 1]);
-            m[f] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-        // lane l gives the address of row l % 8 of matrix l / 8
-        const int tok = 8 * c + (lane & 7), f = lane >> 3;
-        const uint32_t addr = buf + tok * 64 + ((f ^ ((tok >> 1) & 3)) << 4);
-        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(m[0]),
-                     "r"(m[1]), "r"(m[2]), "r"(m[3])
-                     : "memory");
-    }
-}
-
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <Mode kMode>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
     expert_gemm_kernel(const __grid_constant__ TokenMaps tmX, const __grid_constant__ CUtensorMap tmW, const Params p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sf_ring = ring + kStages * kStageBytes;
     uint8_t *epi = sf_ring + kScaleSlots * kScaleSlotBytes;
-    Tail &tail = *reinterpret_cast<Tail *>(epi + kEpiBytes);
+    Tail &tail = *reinterpret_cast<Tail *>(epi + epi_bytes(kMode));
     volatile int *abort_flag = &tail.abort;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -223,7 +63,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tail.acc_full[b], 1);
-            mbar_init(&tail.acc_empty[b], 8);
+            mbar_init(&tail.acc_empty[b], 8 * teams(kMode));
+            mbar_init(&tail.words[b][0], 1);
+            mbar_init(&tail.words[b][1], 1);
         }
         mbar_init(&tail.drain, 1);
         tail.abort = tail.bad_index = tail.bad_scale = 0;
@@ -298,7 +140,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 uint8_t *a = ring + s * kStageBytes, *b = a + kABytes;
                 if (elect_one()) {
                     mbar_arrive_expect_tx(&tail.full[s], bytes);
-                    tma_load_3d(a, &tmW, &tail.full[s], p.transpose ? m0 : kb * kBlk, p.transpose ? kb * kBlk : m0, t.e, keep);
+                    if constexpr (kMode == kGated) {
+                        // 16 rows of the gate half, then the same 16 of the up half, four times
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            tma_load_5d(a + g * 32 * kBlk, &tmW, &tail.full[s], kb * kBlk, 0, (m0 >> 5) + g, 0, t.e, keep);
+                    } else {
+                        tma_load_3d(a, &tmW, &tail.full[s], p.transpose ? m0 : kb * kBlk, p.transpose ? kb * kBlk : m0, t.e, keep);
+                    }
                     tma_load_2d(b, map, &tail.full[s], kb * kBlk, row0, keep);
                 }
                 __syncwarp();
@@ -400,7 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         volatile int no_abort = 0;
         mbar_wait_bounded(&tail.drain, 0, &no_abort);
-    } else if (warp == 2 || warp == 3 || warp >= 8) {
+    } else if (warp < 4 || warp >= 4 + 4 * teams(kMode)) {
         // Scale words: byte i of a row's word is the scale of 128-block 4 q + i.  Tokens: row r at
         // lane r % 32, word r / 32 of a 128-row atom; features: one word for the whole 128.  Two warps,
         // one for each atom, fill a slot with 16 blocks; two such teams take turns, so that a team has
@@ -420,7 +269,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int n = blocks - k0;
                 uint32_t feat[4], tok[4][4];
                 if (half == 0) {
-                    const int mb = t.m0 / kBlk + rank < m_blocks ? t.m0 / kBlk + rank : m_blocks - 1;
+                    // (kGated: lane and row, modulo 32, are a row of the gate half below 16, of the up half from 16)
+                    const int mb = kMode == kGated ? t.m0 / kTileM + (lane < 16 ? 0 : m_blocks >> 1)
+                                   : t.m0 / kBlk + rank < m_blocks ? t.m0 / kBlk + rank : m_blocks - 1;
                     const int step = p.transpose ? m_blocks : 1;
                     const int64_t at = p.transpose ? static_cast<int64_t>(t.e) * blocks * m_blocks + mb
                                                    : (static_cast<int64_t>(t.e) * m_blocks + mb) * blocks;
@@ -507,44 +358,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (bad) tail.bad_scale = 1;
     } else {
-        const int w = warp - 4;
-        uint8_t *buf = epi + w * 32 * 64;
-        const uint32_t buf_addr = smem_u32(buf);
-        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(w * 32) << 16);
-        int j = 0;
-        for (Walk walk(pair, p.m_tiles); walk.tile < tiles; walk.next(pairs, p.m_tiles)) {
-            const Tile t = walk.get(tail);
-            const int b = j & 1;
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, abort_flag, 64))) break;
-            tc_fence_after_sync();
-            const int m = t.m0 + rank * kHalfM + w * 32;  // this warp's features
-            const int feats = p.out - m;                 // a multiple of 16, may be <= 0
-            // a lane's four 16-byte pieces of a chunk: tokens lane / 4 + 8 i, features 8 (lane % 4) on
-            const bool part_ok = (lane & 3) * 8 < feats;
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.Y) + (t.row0 + (lane >> 2)) * p.out + m + (lane & 3) * 8;
-            float v[2][32];
-            tmem_ld_fragments(lane_addr + b * kTileN, v[0]);
-#pragma unroll 2
-            for (int c = 0, x = 0; c < t.rows; c += 32, x ^= 1) {
-                tmem_ld_wait();
-                store_transposed(buf_addr, lane, v[x]);
-                if (c + 32 < t.rows) tmem_ld_fragments(lane_addr + b * kTileN + c + 32, v[x ^ 1]);
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = i * 8 + (lane >> 2);
-                    const uint4 y = *reinterpret_cast<const uint4 *>(buf + tok * 64 + (((lane & 3) ^ ((tok >> 1) & 3)) << 4));
-                    if (c + tok < t.rows && part_ok)
-                        *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(c + 8 * i) * p.out) = y;
-                }
-                __syncwarp();
-            }
-            tc_fence_before_sync();
-            if (lane == 0) mbar_arrive_at(&tail.acc_empty[b], 0);
-            ++j;
-        }
+        const EpilogueWarp wp{epi, tmem, static_cast<int>(rank), warp < 8 ? 0 : 1, warp & 3, lane, pair, pairs, tiles};
+        if constexpr (kMode == kPlain)
+            plain_epilogue(p, tail, wp);
+        else if constexpr (kMode == kGated)
+            gated_epilogue(p, tail, wp);
+        else
+            gated_grad_epilogue(p, tail, wp);
     }
 
+    if constexpr (kMode == kGated) {
+        // a CTA that gave up a wait may have words on their way to the other's memory: they have landed long
+        // before this time is over
+        if (*abort_flag) __nanosleep(1000000);
+    }
     tc_fence_before_sync();
     cluster_sync();               // the leader's MMAs have read the other CTA's memory
     tc_fence_after_sync();
@@ -596,55 +423,100 @@ bool encode_map(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes, cons
               swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t stream)
+namespace {
+
+// What the three launches share: the tensor maps of the rows and (but for kGated) of the weights, the scales' vector
+// width, the grid.
+template <Mode kMode>
+cudaError_t launch(Params &p, const void *X, const void *W, int rows, int cols, cudaStream_t stream)
 {
     int dev = 0;
     cudaError_t err = expert_device(&dev);
     if (err != cudaSuccess) return err;
-    const int red = a.transpose ? a.rows : a.cols, out = a.transpose ? a.cols : a.rows;
 
     TokenMaps tmX;
     CUtensorMap tmW;
-    const uint64_t xd[2] = {static_cast<uint64_t>(red), static_cast<uint64_t>(a.R)};
-    const uint64_t wd[3] = {static_cast<uint64_t>(a.cols), static_cast<uint64_t>(a.rows), static_cast<uint64_t>(a.E)};
-    const uint32_t wb[3] = {128, 128, 1};
+    const uint64_t xd[2] = {static_cast<uint64_t>(p.red), static_cast<uint64_t>(p.R)};
     for (int i = 0; i < kBoxes; ++i) {
         const uint32_t xb[2] = {kBlk, static_cast<uint32_t>(box_rows(i))};
-        if (!encode_map(&tmX.map[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.X, 2, xd, xb)) return cudaErrorInvalidValue;
+        if (!encode_map(&tmX.map[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, X, 2, xd, xb)) return cudaErrorInvalidValue;
     }
-    if (!encode_map(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.W, 3, wd, wb)) return cudaErrorInvalidValue;
+    if (kMode == kGated) {
+        // 16 rows of either half in one box
+        const uint64_t wd[5] = {static_cast<uint64_t>(cols), 16, static_cast<uint64_t>(rows / 32), 2, static_cast<uint64_t>(p.E)};
+        const uint32_t wb[5] = {kBlk, 16, 1, 2, 1};
+        if (!encode_map(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, W, 5, wd, wb)) return cudaErrorInvalidValue;
+    } else {
+        const uint64_t wd[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), static_cast<uint64_t>(p.E)};
+        const uint32_t wb[3] = {128, 128, 1};
+        if (!encode_map(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, W, 3, wd, wb)) return cudaErrorInvalidValue;
+    }
 
     static std::atomic<uint64_t> done{0};
     const uint64_t bit = 1ull << (dev & 63);
     if (!(done.load(std::memory_order_relaxed) & bit)) {
-        err = cudaFuncSetAttribute(expert_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(kSmemBytes));
+        err = cudaFuncSetAttribute(expert_gemm_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(smem_bytes(kMode)));
         if (err != cudaSuccess) return err;
         done.fetch_or(bit, std::memory_order_relaxed);
     }
-    Params p;
+    const uintptr_t xs = reinterpret_cast<uintptr_t>(p.X_scale);
+    p.x_vec = (p.red / kBlk) % 4 == 0 && xs % (p.x_ue8m0 ? 4 : 16) == 0;
+    if (p.x_ue8m0 && (p.red / kBlk) % 16 == 0 && xs % 16 == 0) p.x_vec = 2;
+    p.m_tiles = (p.out + kTileM - 1) / kTileM;
+    // the most tiles that R rows in E groups can make; no more pairs than that
+    const int64_t most = (p.R / kTileN + (p.R < p.E ? p.R : p.E) + 1) * p.m_tiles;
+    const int pairs = device_sm_count(dev) / 2;
+    const int grid = 2 * static_cast<int>(most < pairs ? most : pairs);
+    expert_gemm_kernel<kMode><<<grid, threads(kMode), smem_bytes(kMode), stream>>>(tmX, tmW, p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t stream)
+{
+    Params p{};
     p.X_scale = a.X_scale;
     p.W_scale = a.W_scale;
     p.offsets = a.offsets;
     p.R = a.R;
     p.E = a.E;
-    p.out = out;
-    p.red = red;
+    p.out = a.transpose ? a.cols : a.rows;
+    p.red = a.transpose ? a.rows : a.cols;
     p.transpose = a.transpose;
     p.x_ue8m0 = a.x_ue8m0;
     p.w_ue8m0 = a.w_ue8m0;
-    const uintptr_t xs = reinterpret_cast<uintptr_t>(a.X_scale);
-    p.x_vec = (red / kBlk) % 4 == 0 && xs % (a.x_ue8m0 ? 4 : 16) == 0;
-    if (a.x_ue8m0 && (red / kBlk) % 16 == 0 && xs % 16 == 0) p.x_vec = 2;
-    p.m_tiles = (out + kTileM - 1) / kTileM;
     p.Y = a.Y;
     p.status = a.status;
-    // the most tiles that R rows in E groups can make; no more pairs than that
-    const int64_t most = (a.R / kTileN + (a.R < a.E ? a.R : a.E) + 1) * p.m_tiles;
-    const int pairs = device_sm_count(dev) / 2;
-    const int grid = 2 * static_cast<int>(most < pairs ? most : pairs);
-    expert_gemm_kernel<<<grid, kThreads, kSmemBytes, stream>>>(tmX, tmW, p);
-    return cudaGetLastError();
+    return launch<kPlain>(p, a.X, a.W, a.rows, a.cols, stream);
+}
+
+cudaError_t launch_expert_swiglu(const ExpertSwigluArgs &a, cudaStream_t stream)
+{
+    Params p{};
+    p.X_scale = a.X_scale;
+    p.W_scale = a.W_scale;
+    p.offsets = a.offsets;
+    p.R = a.R;
+    p.E = a.E;
+    p.I = a.I;
+    p.out = a.backward ? a.I : 2 * a.I;
+    p.red = a.H;
+    p.transpose = a.backward;
+    p.x_ue8m0 = a.x_ue8m0;
+    p.w_ue8m0 = a.w_ue8m0;
+    p.k_ue8m0 = a.gu_ue8m0;
+    p.out_ue8m0 = a.out_ue8m0;
+    p.K = static_cast<uint8_t *>(a.GU);
+    p.K_scale = a.GU_scale;
+    p.A = static_cast<uint8_t *>(a.A);
+    p.A_scale = a.A_scale;
+    p.Y = a.dGU;
+    p.Q = static_cast<uint8_t *>(a.dGU_fp8);
+    p.Q_scale = a.dGU_scale;
+    p.status = a.status;
+    return a.backward ? launch<kGatedGrad>(p, a.X, a.W, a.H, a.I, stream) : launch<kGated>(p, a.X, a.W, 2 * a.I, a.H, stream);
 }
 
 }  // namespace moe

@@ -1,0 +1,407 @@
+// expert_gemm_epilogue.cuh -- what follows the product in its own launch: bf16 rows; the gated activation; the
+// gated activation's gradient.
+//
+// A warp reads its quarter of the accumulator (32 lanes: features) in chunks of 32 tokens (columns), as fragments of
+// 8x8: element 16 h + 4 c + 2 r + i of a lane is feature 16 h + 8 r + lane / 4 of token 8 c + 2 (lane % 4) + i.
+// With s = 2 c + i a lane has eight tokens, the same ones as the lanes that agree with it modulo 4.
+//
+// E4M3 codes leave through shared memory.  stmatrix and ldmatrix move 8x8 matrices of two bytes; the two bytes here
+// are the codes of features j and j + 8 (r = 0 and 1) of one token, so that 16 features are 16 bytes of a token's
+// row in the order 0, 8, 1, 9, ...; four byte permutations put them right on the way to global memory.
+#pragma once
+
+#include "expert_gemm.cuh"
+
+namespace moe {
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+
+struct EpilogueWarp {
+    uint8_t *epi;                 // the epilogue's shared memory
+    uint32_t tmem;
+    int rank, team, w, lane;      // CTA of the pair, team of four warps, warp of the team
+    int pair, pairs, tiles;
+};
+
+// The accumulator has been read: one arrival of each warp at the leader.
+__device__ __forceinline__ void release_accumulator(Tail &tail, int b, int lane)
+{
+    tc_fence_before_sync();
+    if (lane == 0) mbar_arrive_at(&tail.acc_empty[b], 0);
+}
+
+__device__ __forceinline__ void plain_epilogue(const Params &p, Tail &tail, const EpilogueWarp &e)
+{
+    const int w = e.w, lane = e.lane;
+    uint8_t *buf = e.epi + w * 32 * 64;
+    const uint32_t buf_addr = smem_u32(buf);
+    const uint32_t lane_addr = e.tmem + (static_cast<uint32_t>(w * 32) << 16);
+    int j = 0;
+    for (Walk walk(e.pair, p.m_tiles); walk.tile < e.tiles; walk.next(e.pairs, p.m_tiles)) {
+        const Tile t = walk.get(tail);
+        const int b = j & 1;
+        if (!__all_sync(kAll, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, &tail.abort, 64))) break;
+        tc_fence_after_sync();
+        const int m = t.m0 + e.rank * kHalfM + w * 32;  // this warp's features
+        const int feats = p.out - m;                 // a multiple of 16, may be <= 0
+        // a lane's four 16-byte pieces of a chunk: tokens lane / 4 + 8 i, features 8 (lane % 4) on
+        const bool part_ok = (lane & 3) * 8 < feats;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.Y) + (t.row0 + (lane >> 2)) * p.out + m + (lane & 3) * 8;
+        float v[2][32];
+        tmem_ld_fragments(lane_addr + b * kTileN, v[0]);
+#pragma unroll 2
+        for (int c = 0, x = 0; c < t.rows; c += 32, x ^= 1) {
+            tmem_ld_wait();
+            store_transposed(buf_addr, lane, v[x]);
+            if (c + 32 < t.rows) tmem_ld_fragments(lane_addr + b * kTileN + c + 32, v[x ^ 1]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tok = i * 8 + (lane >> 2);
+                const uint4 y = *reinterpret_cast<const uint4 *>(buf + tok * 64 + (((lane & 3) ^ ((tok >> 1) & 3)) << 4));
+                if (c + tok < t.rows && part_ok)
+                    *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(c + 8 * i) * p.out) = y;
+            }
+            __syncwarp();
+        }
+        release_accumulator(tail, b, lane);
+        ++j;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Pieces of the activation's two epilogues
+// ---------------------------------------------------------------------------
+// Whether all of a team's 128 threads say so (they go on or stop together: a warp that left alone would leave the
+// others at their next barrier).
+__device__ __forceinline__ bool team_all(int team, bool ok)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.aligned.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(__all_sync(kAll, ok))), "r"(2 + team)
+        : "memory");
+    return r != 0;
+}
+
+// The largest of m[s] over the eight lanes that share tokens: lane l is left with that of s = l / 4, which is token
+// lane_token(l).
+__device__ __forceinline__ float max_of_lanes(const float (&m)[8], int lane)
+{
+    float a[4], b[2];
+    const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a[k] = fmaxf(h16 ? m[k + 4] : m[k], __shfl_xor_sync(kAll, h16 ? m[k] : m[k + 4], 16));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) b[k] = fmaxf(h8 ? a[k + 2] : a[k], __shfl_xor_sync(kAll, h8 ? a[k] : a[k + 2], 8));
+    return fmaxf(h4 ? b[1] : b[0], __shfl_xor_sync(kAll, h4 ? b[0] : b[1], 4));
+}
+__device__ __forceinline__ int lane_token(int lane) { return (lane >> 3) * 8 + (lane & 3) * 2 + ((lane >> 2) & 1); }
+// What the lane of token s of this lane's eight holds.
+__device__ __forceinline__ uint32_t of_token(uint32_t word, int s, int lane) { return __shfl_sync(kAll, word, 4 * s + (lane & 3)); }
+
+// The larger of each of three bytes.
+__device__ __forceinline__ uint32_t max_bytes(uint32_t a, uint32_t b)
+{
+    return __vmaxu2(a & 0x00FF00FFu, b & 0x00FF00FFu) | max(a & 0xFF00u, b & 0xFF00u);
+}
+
+// Codes of two values, the first in the low byte.
+__device__ __forceinline__ uint32_t codes_of(float lo, float hi)
+{
+    uint16_t q;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(hi), "f"(lo));
+    return q;
+}
+
+// 16 bytes of a row in the order 0, 8, 1, 9, ... put right, and back.
+__device__ __forceinline__ uint4 in_order(const uint4 &x)
+{
+    return make_uint4(__byte_perm(x.x, x.y, 0x6420), __byte_perm(x.z, x.w, 0x6420), __byte_perm(x.x, x.y, 0x7531),
+                      __byte_perm(x.z, x.w, 0x7531));
+}
+__device__ __forceinline__ uint4 in_pairs(const uint4 &x)
+{
+    return make_uint4(__byte_perm(x.x, x.z, 0x5140), __byte_perm(x.x, x.z, 0x7362), __byte_perm(x.y, x.w, 0x5140),
+                      __byte_perm(x.y, x.w, 0x7362));
+}
+
+// Four 8x8 matrices of two bytes, transposed, to / from rows of 16 bytes: lane l gives the address of row l.
+__device__ __forceinline__ void store_rows(uint32_t row_addr, const uint32_t (&m)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(row_addr), "r"(m[0]),
+                 "r"(m[1]), "r"(m[2]), "r"(m[3])
+                 : "memory");
+}
+__device__ __forceinline__ void load_rows(uint32_t row_addr, uint32_t (&m)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(m[0]), "=r"(m[1]), "=r"(m[2]), "=r"(m[3])
+                 : "r"(row_addr)
+                 : "memory");
+}
+
+// A word to CTA `rank`'s shared memory at this offset, counted there on the barrier at that one.
+__device__ __forceinline__ void send_word(uint32_t addr, uint32_t word, uint32_t bar, uint32_t rank)
+{
+    asm volatile(
+        "{\n\t.reg .b32 a, b;\n\t"
+        "mapa.shared::cluster.u32 a, %0, %3;\n\t"
+        "mapa.shared::cluster.u32 b, %2, %3;\n\t"
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [a], %1, [b];\n\t}" ::"r"(addr),
+        "r"(word), "r"(bar), "r"(rank)
+        : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// Gated activation: a = g / (1 + exp(-g)) u of the product, in E4M3, and (checkpoint) g and u in E4M3.
+//
+// The rows of the weights lie in the tile so that a warp's 32 lanes of TMEM are 16 features of the gate half, then
+// the same 16 of the up half (h = 0 and 1 of the fragments): a lane has both.  A block of 128 features is the pair's
+// eight warps; each finds the scale bytes of its 16 features (the byte of the largest is the largest byte), sends a
+// word of three for each token to both CTAs, and takes the largest of eight.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, const EpilogueWarp &e)
+{
+    const int team = e.team, w = e.w, lane = e.lane, tok = lane_token(lane);
+    uint8_t *stage = e.epi + team * 3 * 2048;         // codes of a, g, u: 32 tokens x 64 features each
+    uint32_t *words = reinterpret_cast<uint32_t *>(e.epi + stage_bytes(kGated)) + team * 2 * 256;
+    // 16-byte piece f of token t lies at place f ^ (t / 2 % 4)
+    const uint32_t put = smem_u32(stage) + lane * 64 + ((w ^ ((lane >> 1) & 3)) << 4);
+    const int out_tok = w * 8 + (lane >> 2), piece = lane & 3;
+    const uint8_t *take = stage + out_tok * 64 + ((piece ^ ((out_tok >> 1) & 3)) << 4);
+    const uint32_t lane_addr = e.tmem + (static_cast<uint32_t>(w * 32) << 16);
+    const int nb = p.I / kBlk;
+    int j = 0;
+    uint32_t n = 0;                                    // this team's chunks
+    bool ok = true;
+    for (Walk walk(e.pair, p.m_tiles); walk.tile < e.tiles; walk.next(e.pairs, p.m_tiles), ++j) {
+        const Tile t = walk.get(tail);
+        const int b = j & 1, fb = t.m0 / kTileM;       // its block of 128 features
+        ok = team_all(team, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, &tail.abort, 64));
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (team * 32 >= t.rows) release_accumulator(tail, b, lane);
+        for (int c0 = team * 32; c0 < t.rows; c0 += 64, ++n) {
+            float v[32], a[16];
+            tmem_ld_fragments(lane_addr + b * kTileN + c0, v);
+            tmem_ld_wait();
+            if (c0 + 64 >= t.rows) release_accumulator(tail, b, lane);
+            float ma[8], mg[8], mu[8];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) a[x] = v[x] * sigmoid(v[x]) * v[16 + x];
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int x = 4 * (s >> 1) + (s & 1);
+                ma[s] = fmaxf(fabsf(a[x]), fabsf(a[x + 2]));
+                mg[s] = fmaxf(fabsf(v[x]), fabsf(v[x + 2]));
+                mu[s] = fmaxf(fabsf(v[16 + x]), fabsf(v[18 + x]));
+            }
+            uint32_t word = block_scale_byte(max_of_lanes(ma, lane));
+            if (p.K) word |= block_scale_byte(max_of_lanes(mg, lane)) << 8 | block_scale_byte(max_of_lanes(mu, lane)) << 16;
+            // eight warps' words for each token; a buffer is written again two chunks later, when the words of the
+            // chunk between have come from every warp, which each sent after it had read this one
+            uint32_t *slot = words + (n & 1) * 256;
+            uint64_t *bar = &tail.words[team][n & 1];
+            if (w == 0 && lane == 0) mbar_arrive_expect_tx(bar, 8 * 32 * 4);
+            const uint32_t to = smem_u32(slot + (e.rank * 4 + w) * 32 + tok);
+            send_word(to, word, smem_u32(bar), 0);
+            send_word(to, word, smem_u32(bar), 1);
+            ok = mbar_wait_bounded(bar, (n >> 1) & 1, &tail.abort);
+            word = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) word = max_bytes(word, slot[k * 32 + tok]);
+            if (e.rank == 0 && c0 + tok < t.rows) {
+                const int64_t row = t.row0 + c0 + tok;
+                if (w == 0) store_scale(p.A_scale, p.out_ue8m0, row * nb + fb, word & 0xFFu);
+                if (p.K && w == 1) store_scale(p.K_scale, p.out_ue8m0, row * 2 * nb + fb, (word >> 8) & 0xFFu);
+                if (p.K && w == 2) store_scale(p.K_scale, p.out_ue8m0, (row * 2 + 1) * nb + fb, word >> 16);
+            }
+            uint32_t q[3][4];
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int x = 4 * (s >> 1) + (s & 1), c = s >> 1;
+                const uint32_t of = of_token(word, s, lane);
+                const float ia = scale_reciprocal(of & 0xFFu), ig = scale_reciprocal((of >> 8) & 0xFFu),
+                            iu = scale_reciprocal(of >> 16);
+                const uint32_t qa = codes_of(a[x] * ia, a[x + 2] * ia), qg = codes_of(v[x] * ig, v[x + 2] * ig),
+                               qu = codes_of(v[16 + x] * iu, v[18 + x] * iu);
+                q[0][c] = s & 1 ? q[0][c] | qa << 16 : qa;
+                q[1][c] = s & 1 ? q[1][c] | qg << 16 : qg;
+                q[2][c] = s & 1 ? q[2][c] | qu << 16 : qu;
+            }
+            // (the codes of the chunk before have been read: its words came after that)
+            store_rows(put, q[0]);
+            if (p.K) {
+                store_rows(put + 2048, q[1]);
+                store_rows(put + 4096, q[2]);
+            }
+            ok = team_all(team, ok);
+            if (!ok) break;
+            if (c0 + out_tok < t.rows) {
+                const int64_t row = t.row0 + c0 + out_tok;
+                const int f = fb * kBlk + e.rank * 64 + piece * 16;
+                *reinterpret_cast<uint4 *>(p.A + row * p.I + f) = in_order(*reinterpret_cast<const uint4 *>(take));
+                if (p.K) {
+                    uint8_t *k = p.K + row * 2 * p.I + f;
+                    *reinterpret_cast<uint4 *>(k) = in_order(*reinterpret_cast<const uint4 *>(take + 2048));
+                    *reinterpret_cast<uint4 *>(k + p.I) = in_order(*reinterpret_cast<const uint4 *>(take + 4096));
+                }
+            }
+        }
+        if (!ok) break;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The activation's gradient: the product is da; g and u come from the checkpoint (codes and scales).
+//   s = 1 / (1 + exp(-g));  dg = da u s (1 + g (1 - s));  du = da g s
+// in bf16 and in E4M3.  A CTA's 128 features are a block, its scale bytes are joined over a team's four warps.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void gated_grad_epilogue(const Params &p, Tail &tail, const EpilogueWarp &e)
+{
+    const int team = e.team, w = e.w, lane = e.lane, tok = lane_token(lane);
+    uint8_t *buf = e.epi + (team * 4 + w) * 2048;
+    const uint32_t buf_addr = smem_u32(buf);
+    uint32_t *words = reinterpret_cast<uint32_t *>(e.epi + stage_bytes(kGatedGrad)) + team * 2 * 128;
+    const uint32_t lane_addr = e.tmem + (static_cast<uint32_t>(w * 32) << 16);
+    const int nb = p.I / kBlk;
+    // E4M3 rows are read and written by two lanes for a token's 32 features
+    const int k_tok = lane >> 1, k_half = lane & 1;
+    int j = 0;
+    uint32_t n = 0;
+    bool bad = false;
+    for (Walk walk(e.pair, p.m_tiles); walk.tile < e.tiles; walk.next(e.pairs, p.m_tiles), ++j) {
+        const Tile t = walk.get(tail);
+        const int b = j & 1, fb = t.m0 / kBlk + e.rank;
+        const bool there = fb < nb;                    // (the last tile of an odd number of blocks is half empty)
+        uint4 kg[2], ku[2];
+        uint32_t sg = 0, su = 0;
+        const auto fetch = [&](int c0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = c0 + k_tok + 16 * i;
+                const uint8_t *k = p.K + (t.row0 + (r < t.rows ? r : t.rows - 1)) * 2 * p.I + fb * kBlk + w * 32 + k_half * 16;
+                kg[i] = __ldcs(reinterpret_cast<const uint4 *>(k));
+                ku[i] = __ldcs(reinterpret_cast<const uint4 *>(k + p.I));
+            }
+            const int r = c0 + lane;
+            const int64_t at = (t.row0 + (r < t.rows ? r : t.rows - 1)) * 2 * nb + fb;
+            sg = load_scale_bits(p.K_scale, p.k_ue8m0, at);
+            su = load_scale_bits(p.K_scale, p.k_ue8m0, at + nb);
+        };
+        if (there && team * 32 < t.rows) fetch(team * 32);
+        if (!team_all(team, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, &tail.abort, 64))) break;
+        tc_fence_after_sync();
+        if (!there || team * 32 >= t.rows) {
+            release_accumulator(tail, b, lane);
+            continue;
+        }
+        for (int c0 = team * 32; c0 < t.rows; c0 += 64, ++n) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                *reinterpret_cast<uint4 *>(buf + k_half * 512 + (k_tok + 16 * i) * 16) = in_pairs(kg[i]);
+                *reinterpret_cast<uint4 *>(buf + 1024 + k_half * 512 + (k_tok + 16 * i) * 16) = in_pairs(ku[i]);
+            }
+            const uint32_t scales = scale_bits_byte(sg, p.k_ue8m0, bad) | scale_bits_byte(su, p.k_ue8m0, bad) << 8;
+            __syncwarp();
+            uint32_t k[2][2][4];                       // [gate, up][h][c]
+#pragma unroll
+            for (int x = 0; x < 4; ++x) load_rows(buf_addr + x * 512 + lane * 16, k[x >> 1][x & 1]);
+            if (c0 + 64 < t.rows) fetch(c0 + 64);
+            float du[32], dg[32];
+            tmem_ld_fragments(lane_addr + b * kTileN + c0, du);
+            tmem_ld_wait();
+            if (c0 + 64 >= t.rows) release_accumulator(tail, b, lane);
+            float mg[8], mu[8];
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int c = s >> 1, i = s & 1;
+                const uint32_t of = __shfl_sync(kAll, scales, 8 * c + 2 * (lane & 3) + i);
+                const float gs = scale_value(of & 0xFFu), us = scale_value(of >> 8);
+                mg[s] = mu[s] = 0.f;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 g2 = e4m3x2_to_f32x2(i ? k[0][h][c] >> 16 : k[0][h][c] & 0xFFFFu);
+                    const float2 u2 = e4m3x2_to_f32x2(i ? k[1][h][c] >> 16 : k[1][h][c] & 0xFFFFu);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int x = 16 * h + 4 * c + 2 * r + i;
+                        const float g = (r ? g2.y : g2.x) * gs, u = (r ? u2.y : u2.x) * us;
+                        const float sig = sigmoid(g), as = du[x] * sig;
+                        du[x] = as * g;
+                        dg[x] = as * u * (1.f + g * (1.f - sig));
+                        mg[s] = fmaxf(mg[s], fabsf(dg[x]));
+                        mu[s] = fmaxf(mu[s], fabsf(du[x]));
+                    }
+                }
+            }
+            uint32_t *slot = words + (n & 1) * 128;
+            if (p.Q) slot[w * 32 + tok] = block_scale_byte(max_of_lanes(mg, lane)) | block_scale_byte(max_of_lanes(mu, lane)) << 16;
+            if (p.Y) {
+                const int64_t pitch = 2 * static_cast<int64_t>(p.I);
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.Y) + (t.row0 + c0 + (lane >> 2)) * pitch + fb * kBlk + w * 32 + (lane & 3) * 8;
+#pragma unroll
+                for (int gu = 0; gu < 2; ++gu, dst += p.I) {
+                    __syncwarp();
+                    store_transposed(buf_addr, lane, gu ? du : dg);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = i * 8 + (lane >> 2);
+                        const uint4 y = *reinterpret_cast<const uint4 *>(buf + at * 64 + (((lane & 3) ^ ((at >> 1) & 3)) << 4));
+                        if (c0 + at < t.rows) *reinterpret_cast<uint4 *>(dst + 8 * i * pitch) = y;
+                    }
+                }
+            }
+            if (p.Q) {
+                // (a slot is written again two chunks later, behind the barrier of the one between)
+                named_barrier_sync(2 + team, 128);
+                uint32_t word = 0;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) word = __vmaxu2(word, slot[x * 32 + tok]);
+                if (c0 + tok < t.rows && w < 2)
+                    store_scale(p.Q_scale, p.out_ue8m0, (t.row0 + c0 + tok) * 2 * nb + w * nb + fb, w ? word >> 16 : word & 0xFFu);
+                uint32_t q[2][2][4];
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const int c = s >> 1;
+                    const uint32_t of = of_token(word, s, lane);
+                    const float ig = scale_reciprocal(of & 0xFFu), iu = scale_reciprocal(of >> 16);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int x = 16 * h + 4 * c + (s & 1);
+                        const uint32_t qg = codes_of(dg[x] * ig, dg[x + 2] * ig), qu = codes_of(du[x] * iu, du[x + 2] * iu);
+                        q[0][h][c] = s & 1 ? q[0][h][c] | qg << 16 : qg;
+                        q[1][h][c] = s & 1 ? q[1][h][c] | qu << 16 : qu;
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int x = 0; x < 4; ++x) store_rows(buf_addr + x * 512 + lane * 16, q[x >> 1][x & 1]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int at = k_tok + 16 * i;
+                    const uint4 yg = in_order(*reinterpret_cast<const uint4 *>(buf + k_half * 512 + at * 16));
+                    const uint4 yu = in_order(*reinterpret_cast<const uint4 *>(buf + 1024 + k_half * 512 + at * 16));
+                    if (c0 + at < t.rows) {
+                        uint8_t *dst = p.Q + (t.row0 + c0 + at) * 2 * p.I + fb * kBlk + w * 32 + k_half * 16;
+                        *reinterpret_cast<uint4 *>(dst) = yg;
+                        *reinterpret_cast<uint4 *>(dst + p.I) = yu;
+                    }
+                }
+            }
+        }
+    }
+    if (bad) tail.bad_scale = 1;
+}
+
+}  // namespace
+}  // namespace moe

@@ -69,6 +69,17 @@ __device__ __forceinline__ uint32_t load_scale_byte(const void *p, int ue8m0, in
     return scale_bits_byte(load_scale_bits(p, ue8m0, at), ue8m0, bad);
 }
 
+// 1 / (1 + exp(-g)) by the approximate exponential and reciprocal (2 units in the last place each); the product
+// that is the exponent is rounded to 32 bits, which makes the exponential some |g| 2^-24 off besides.  0 where it
+// overflows.  What comes of it is rounded to E4M3 (2^-4) or bf16 (2^-8).
+__device__ __forceinline__ float sigmoid(float g)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504088896340736f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
+
 __device__ __forceinline__ void store_scale(void *p, int ue8m0, int64_t at, uint32_t byte)
 {
     if (ue8m0)
@@ -126,6 +137,18 @@ __device__ __forceinline__ void tma_load_3d_plain(void *smem_dst, const CUtensor
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
             smem_u32(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// TMA load of a box of five dimensions.
+__device__ __forceinline__ void tma_load_5d(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3, int32_t c4, uint64_t cache_policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar)),
+        "l"(cache_policy)
         : "memory");
 }
 
@@ -221,6 +244,20 @@ struct ExpertGemmArgs {
     int32_t *status;
 };
 cudaError_t launch_expert_gemm(const ExpertGemmArgs &a, cudaStream_t stream);
+
+// The product joined with the gated activation (backward: its input gradient with the activation's gradient).
+struct ExpertSwigluArgs {
+    const void *X, *X_scale;     // rows [R, H]
+    const void *W, *W_scale;     // [E, 2I, H]; backward: [E, H, I]
+    const int32_t *offsets;
+    int64_t R;
+    int E, H, I, backward, x_ue8m0, w_ue8m0, out_ue8m0, gu_ue8m0;
+    void *GU, *GU_scale;         // the checkpoint, written (or nullptr) or, backward, read
+    void *A, *A_scale;
+    void *dGU, *dGU_fp8, *dGU_scale;
+    int32_t *status;
+};
+cudaError_t launch_expert_swiglu(const ExpertSwigluArgs &a, cudaStream_t stream);
 
 struct ExpertWgradArgs {
     const void *dY;

@@ -71,17 +71,6 @@ __device__ __forceinline__ void bf16x16_to_f32(const uint4 &a, const uint4 &b, f
     bf16x8_to_f32(b, *reinterpret_cast<float (*)[8]>(&f[8]));
 }
 
-// 1 / (1 + exp(-g)) by the approximate exponential and reciprocal (2 units in the last place each); the product
-// that is the exponent is rounded to 32 bits, which makes the exponential some |g| 2^-24 off besides.  0 where it
-// overflows.  What comes of it is rounded to E4M3 (2^-4) or bf16 (2^-8).
-__device__ __forceinline__ float sigmoid(float g)
-{
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504088896340736f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return r;
-}
-
 // ---------------------------------------------------------------------------
 // Weights: one CTA per 128x128 block, the block in registers between the maximum and the codes.  One read and
 // one write, HBM-bound: 64 x 2048 x 2048 in 124 us, 6.5 TB/s.

@@ -32,8 +32,8 @@ import torch
 
 from . import _check, _need, _scale_dtype, _scale_format, _status_ptr, _workspace_arg, lib
 
-__all__ = ["quantize_weight", "expert_gemm", "expert_wgrad", "swiglu", "swiglu_backward", "moe_layer",
-           "layer_workspace_size", "layer_workspace", "SwiGLU", "SwiGLUGrad", "LayerOut"]
+__all__ = ["quantize_weight", "expert_gemm", "expert_wgrad", "swiglu", "swiglu_backward", "expert_swiglu",
+           "expert_swiglu_backward", "moe_layer", "layer_workspace_size", "layer_workspace", "SwiGLU", "SwiGLUGrad", "LayerOut"]
 
 BLOCK = 128
 
@@ -242,6 +242,71 @@ def swiglu_backward(dA: torch.Tensor, GU_fp8: torch.Tensor, GU_scale: torch.Tens
                                      _opt(out.dGU_fp8, "dGU_fp8", torch.uint8, (R, 2 * I), dev),
                                      _opt(out.dGU_scale, "dGU_scale", _scale_dtype(scale_format), (R, 2 * I // BLOCK), dev),
                                      fmt, _status_ptr(status), _raw_stream(stream, dev)), "moe_swiglu_backward")
+    return out
+
+
+def _joined(X_fp8, X_scale, W_fp8, W_scale, expert_offsets, names, backward):
+    """The arguments that expert_swiglu and its gradient share: (device, addresses and formats, R, E, H, I)."""
+    x_name, w_name = names
+    if isinstance(W_fp8, torch.Tensor) and W_fp8.dim() == 2:
+        W_fp8, W_scale = W_fp8[None], W_scale[None] if isinstance(W_scale, torch.Tensor) else W_scale
+    E, rows, cols = _dims(W_fp8, w_name + "_fp8", 3)
+    R, H = _dims(X_fp8, x_name + "_fp8", 2)
+    if H != (rows if backward else cols):
+        raise ValueError(f"{x_name}_fp8 has {H} columns, {w_name}_fp8 {tuple(W_fp8.shape)} takes {rows if backward else cols}")
+    I = cols if backward else rows // 2
+    if H % BLOCK != 0 or I % BLOCK != 0 or (not backward and rows % 2 != 0):
+        raise ValueError(f"{w_name}_fp8 must be [E, {'H, I' if backward else '2I, H'}] with H and I multiples of 128")
+    dev = _home(X_fp8, x_name + "_fp8")
+    x = _arg(X_fp8, x_name + "_fp8", torch.uint8, (R, H), dev)
+    xs, xf = _scales(X_scale, x_name + "_scale", (R, H // BLOCK), dev)
+    w = _arg(W_fp8, w_name + "_fp8", torch.uint8, (E, rows, cols), dev)
+    ws, wf = _scales(W_scale, w_name + "_scale", (E, rows // BLOCK, cols // BLOCK), dev)
+    off, _ = _groups(expert_offsets, E, dev)
+    return dev, (x, xs, xf, w, ws, wf, off), R, E, H, I
+
+
+def expert_swiglu(X_fp8: torch.Tensor, X_scale: torch.Tensor, W1_fp8: torch.Tensor, W1_scale: torch.Tensor,
+                  expert_offsets: Optional[torch.Tensor] = None, keep: bool = True, scale_format: str = "fp32",
+                  out: Optional[SwiGLU] = None, status=None, stream=None) -> SwiGLU:
+    """swiglu(expert_gemm(X, W1)) in one launch, without the bf16 rows between: W1 [E, 2I, H] (gate rows first)
+    or [2I, H].  With `keep` also the products in E4M3, for expert_swiglu_backward or swiglu_backward.  Rows of
+    no group are left as `out` has them."""
+    fmt, sd = _scale_format(scale_format), _scale_dtype(scale_format)
+    dev, args, R, E, H, I = _joined(X_fp8, X_scale, W1_fp8, W1_scale, expert_offsets, ("X", "W1"), False)
+    if out is None:
+        out = SwiGLU(*_coded(R, I, scale_format, X_fp8.device, stream),
+                     *(_coded(R, 2 * I, scale_format, X_fp8.device, stream) if keep else (None, None)))
+    code = lib().moe_expert_swiglu(*args, R, E, H, I, _arg(out.A_fp8, "A_fp8", torch.uint8, (R, I), dev),
+                                   _arg(out.A_scale, "A_scale", sd, (R, I // BLOCK), dev),
+                                   _opt(out.GU_fp8, "GU_fp8", torch.uint8, (R, 2 * I), dev),
+                                   _opt(out.GU_scale, "GU_scale", sd, (R, 2 * I // BLOCK), dev), fmt,
+                                   _status_ptr(status), _raw_stream(stream, dev))
+    if code:
+        _check(code, "moe_expert_swiglu")
+    return out
+
+
+def expert_swiglu_backward(dY_fp8: torch.Tensor, dY_scale: torch.Tensor, W2_fp8: torch.Tensor, W2_scale: torch.Tensor,
+                           GU_fp8: torch.Tensor, GU_scale: torch.Tensor, expert_offsets: Optional[torch.Tensor] = None,
+                           bf16: bool = True, fp8: bool = True, scale_format: str = "fp32",
+                           out: Optional[SwiGLUGrad] = None, status=None, stream=None) -> SwiGLUGrad:
+    """swiglu_backward(expert_gemm(dY, W2, transpose=True), GU) in one launch, without the bf16 rows between:
+    W2 [E, H, I] or [H, I]; dGU in bf16 (for expert_wgrad) and/or in E4M3 (for the transposed expert_gemm)."""
+    fmt = _scale_format(scale_format)
+    dev, args, R, E, H, I = _joined(dY_fp8, dY_scale, W2_fp8, W2_scale, expert_offsets, ("dY", "W2"), True)
+    kept = _arg(GU_fp8, "GU_fp8", torch.uint8, (R, 2 * I), dev)
+    gs, gf = _scales(GU_scale, "GU_scale", (R, 2 * I // BLOCK), dev)
+    if out is None:
+        out = SwiGLUGrad(_new((R, 2 * I), torch.bfloat16, dY_fp8.device, stream) if bf16 else None,
+                         *(_coded(R, 2 * I, scale_format, dY_fp8.device, stream) if fp8 else (None, None)))
+    code = lib().moe_expert_swiglu_backward(*args, kept, gs, gf, R, E, H, I,
+                                            _opt(out.dGU, "dGU", torch.bfloat16, (R, 2 * I), dev),
+                                            _opt(out.dGU_fp8, "dGU_fp8", torch.uint8, (R, 2 * I), dev),
+                                            _opt(out.dGU_scale, "dGU_scale", _scale_dtype(scale_format), (R, 2 * I // BLOCK), dev),
+                                            fmt, _status_ptr(status), _raw_stream(stream, dev))
+    if code:
+        _check(code, "moe_expert_swiglu_backward")
     return out
 
 

@@ -472,6 +472,38 @@ MOE_API moe_status moe_swiglu_backward(const void *dA, const void *GU_fp8, const
                                int64_t R, int I, void *dGU, void *dGU_fp8, void *dGU_scale, int scale_format,
                                int32_t *status_word, moe_stream_t stream);
 
+/*
+ * moe_expert_swiglu -- both projections, the activation and their product in one launch:
+ *   gu[r] = x[r] W1[e(r)]^T (fp32: g, then u);  a = g / (1 + exp(-g)) * u
+ *   X_fp8 uint8 [R, H], X_scale [R, H/128]; W1_fp8 uint8 [E, 2I, H] (gate rows, then up rows), W1_scale
+ *   A_fp8, A_scale; GU_fp8, GU_scale or both NULL: as moe_swiglu writes them (scale_format)
+ * What moe_expert_gemm and moe_swiglu compute, without the bf16 rounding between them: both outputs are
+ * quantised from the products' fp32 sums, and no bf16 row is written.  Rows of no group are left as they are.
+ * H % 128 == 0, I % 128 == 0, H <= 2^18, I <= 2^17.  R == 0 is a no-op.
+ * Errors: as moe_expert_gemm.
+ */
+MOE_API moe_status moe_expert_swiglu(const void *X_fp8, const void *X_scale, int x_scale_format,
+                             const void *W1_fp8, const void *W1_scale, int w_scale_format,
+                             const int32_t *expert_offsets, int64_t R, int E, int H, int I,
+                             void *A_fp8, void *A_scale, void *GU_fp8, void *GU_scale, int scale_format,
+                             int32_t *status_word, moe_stream_t stream);
+
+/*
+ * moe_expert_swiglu_backward -- the down projection's input gradient joined with the activation's:
+ *   da[r] = dy[r] W2[e(r)] (fp32);  dg, du of da as in moe_swiglu_backward
+ *   dY_fp8 uint8 [R, H], dY_scale [R, H/128] (dy_scale_format); W2_fp8 uint8 [E, H, I], W2_scale
+ *   GU_fp8, GU_scale (gu_scale_format): the checkpoint of moe_expert_swiglu or moe_swiglu
+ *   dGU, or dGU_fp8 and dGU_scale (scale_format), or all three: as moe_swiglu_backward writes them
+ * What moe_expert_gemm (transposed) and moe_swiglu_backward compute, without the bf16 rounding of da between
+ * them.  Sizes, rows of no group, errors: as moe_expert_swiglu.  One launch.
+ */
+MOE_API moe_status moe_expert_swiglu_backward(const void *dY_fp8, const void *dY_scale, int dy_scale_format,
+                             const void *W2_fp8, const void *W2_scale, int w_scale_format,
+                             const int32_t *expert_offsets, const void *GU_fp8, const void *GU_scale,
+                             int gu_scale_format, int64_t R, int E, int H, int I,
+                             void *dGU, void *dGU_fp8, void *dGU_scale, int scale_format,
+                             int32_t *status_word, moe_stream_t stream);
+
 /* Bytes of device workspace moe_layer needs. */
 MOE_API size_t moe_layer_workspace_size(int N, int H, int I, int E, int K);
 
