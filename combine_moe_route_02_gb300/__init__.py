@@ -25,6 +25,7 @@ __all__ = [
     "ROUTE_SIMT", "SCALE_FP32", "SCALE_UE8M0", "Dispatch", "DispatchEP", "route_dispatch",
     "quantize_weight", "expert_gemm", "expert_wgrad", "swiglu", "swiglu_backward", "expert_swiglu",
     "expert_swiglu_backward", "moe_layer", "layer_workspace_size", "layer_workspace", "SwiGLU", "SwiGLUGrad", "LayerOut",
+    "rms_norm", "rms_norm_backward", "grad_norm", "clip_grad_norm", "RMSNorm", "RMSNormGrad",
 ]
 
 MOE_OK = 0
@@ -49,7 +50,8 @@ EXPORTED_SYMBOLS = (
     "moe_combine_residual", "moe_dispatch_ex", "moe_permute_ex", "moe_route_stats", "moe_load_stats",
     "moe_dispatch_ep", "moe_route_dispatch", "moe_quantize_weight", "moe_expert_gemm", "moe_expert_wgrad",
     "moe_swiglu", "moe_swiglu_backward", "moe_layer_workspace_size", "moe_layer",
-    "moe_expert_swiglu", "moe_expert_swiglu_backward",
+    "moe_expert_swiglu", "moe_expert_swiglu_backward", "moe_rms_norm", "moe_rms_norm_backward_workspace_size",
+    "moe_rms_norm_backward", "moe_grad_norm_workspace_size", "moe_grad_norm", "moe_clip_grad_norm",
 )
 
 SCALE_FP32, SCALE_UE8M0 = 0, 1
@@ -135,6 +137,18 @@ def lib():
     L.moe_layer_workspace_size.restype = SZ
     L.moe_layer.argtypes = [P, P, P, P, P, P, P, I32, P, I32, I32, I32, I32, I32, I32, P, P, P, P, P, SZ, P]
     L.moe_layer.restype = I32
+    L.moe_rms_norm.argtypes = [P, P, P, I32, ctypes.c_float, I64, I32, P, P, P, P, I32, P, P]
+    L.moe_rms_norm.restype = I32
+    L.moe_rms_norm_backward_workspace_size.argtypes = [I64, I32]
+    L.moe_rms_norm_backward_workspace_size.restype = SZ
+    L.moe_rms_norm_backward.argtypes = [P, P, P, I32, P, P, P, I64, I32, P, P, P, SZ, P]
+    L.moe_rms_norm_backward.restype = I32
+    L.moe_grad_norm_workspace_size.argtypes = [I32]
+    L.moe_grad_norm_workspace_size.restype = SZ
+    L.moe_grad_norm.argtypes = [P, P, P, I32, P, P, SZ, P]
+    L.moe_grad_norm.restype = I32
+    L.moe_clip_grad_norm.argtypes = [P, P, P, P, I32, ctypes.c_double, P, P, SZ, P]
+    L.moe_clip_grad_norm.restype = I32
     L.moe_status_string.argtypes = [I32]
     L.moe_status_string.restype = ctypes.c_char_p
     L.moe_abi_version.argtypes = []
@@ -505,3 +519,4 @@ def combine(Y: torch.Tensor, row_map: torch.Tensor, topk_w: torch.Tensor, out=No
 from .experts import (LayerOut, SwiGLU, SwiGLUGrad, expert_gemm, expert_swiglu, expert_swiglu_backward,  # noqa: E402
                       expert_wgrad, layer_workspace, layer_workspace_size, moe_layer, quantize_weight, swiglu,
                       swiglu_backward)
+from .norms import RMSNorm, RMSNormGrad, clip_grad_norm, grad_norm, rms_norm, rms_norm_backward  # noqa: E402

@@ -294,6 +294,42 @@ struct LayerArgs {
 size_t layer_workspace_bytes(int N, int H, int I, int E, int K);
 cudaError_t launch_layer(const LayerArgs &a, cudaStream_t stream);
 
+struct RmsNormArgs {
+    const void *X, *residual, *weight;
+    int64_t N;
+    int H, w_bf16, ue8m0;
+    float eps;
+    void *S, *Y, *Y_fp8, *Y_scale;
+    float *rstd;
+};
+cudaError_t launch_rms_norm(const RmsNormArgs &a, cudaStream_t stream);
+
+struct RmsNormBackwardArgs {
+    const void *dY, *S, *dS, *weight;
+    const float *rstd, *add;
+    int64_t N;
+    int H, w_bf16;
+    void *dX;
+    float *dweight;
+    void *workspace;             // rms_norm_table_rows(N, H) rows of H floats
+};
+int rms_norm_table_rows(int64_t N, int H);
+cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs &a, cudaStream_t stream);
+
+struct GradArgs {
+    const void *const *grads;    // (arrays of the host)
+    void *const *out;            // nullptr: in place
+    const int64_t *sizes;
+    const int *types;
+    int n, clip;
+    double max_norm;
+    float *norm;
+    void *workspace;
+};
+constexpr int kGradNormCtas = 608;
+size_t grad_norm_workspace_bytes(int n);
+cudaError_t launch_grad_norm(const GradArgs &a, cudaStream_t stream);
+
 // A tiled tensor map, 128-byte swizzle unless told otherwise; false if the driver refuses it.
 bool encode_map(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes, const void *base, int rank,
                 const uint64_t *dims, const uint32_t *box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);

@@ -1,0 +1,168 @@
+"""The norms around the experts (``include/moe_route.h``, "The norms around the experts"): the RMS norm in front
+of the router with the residual stream's addition, and the norm of all gradients with its clipping.
+
+A block and its training step::
+
+    n   = rms_norm(attn, w, residual=x)              # n.S is the stream, n.Y what the router reads
+    idx, rw, d, _ = route_dispatch(n.Y, W_gate, K)
+    ...                                              # the experts: see experts.py
+    out = combine(y, d.row_map, rw, residual=n.S)
+    ...
+    g = rms_norm_backward(dY, n.S, w, n.rstd, dS=dout)   # dout: out's gradient, through the stream
+    clip_grad_norm([dW1, dW2, g.dweight], 1.0)
+
+With ``stream`` a call launches there, and what it allocates is that stream's memory, as in experts.py.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+from typing import Optional, Sequence
+
+import torch
+
+from . import _check, _need, _scale_dtype, _scale_format, lib
+from .experts import BLOCK, _arg, _coded, _dims, _home, _new, _opt, _raw_stream
+
+__all__ = ["rms_norm", "rms_norm_backward", "grad_norm", "clip_grad_norm", "RMSNorm", "RMSNormGrad"]
+
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _weight(w: torch.Tensor, H: int, dev: int):
+    """The address of a weight of either type, and the type."""
+    if not isinstance(w, torch.Tensor):
+        raise TypeError("weight must be a torch.Tensor")
+    if w.dtype not in _TYPES:
+        raise TypeError(f"weight must be torch.float32 or torch.bfloat16, got {w.dtype}")
+    return _arg(w, "weight", w.dtype, (H,), dev), _TYPES[w.dtype]
+
+
+@dataclass
+class RMSNorm:
+    Y: Optional[torch.Tensor]
+    Y_fp8: Optional[torch.Tensor]
+    Y_scale: Optional[torch.Tensor]
+    S: torch.Tensor
+    rstd: Optional[torch.Tensor]
+
+
+@dataclass
+class RMSNormGrad:
+    dX: torch.Tensor
+    dweight: torch.Tensor
+
+
+def rms_norm(X: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+             bf16: bool = True, fp8: bool = False, scale_format: str = "fp32", out: Optional[RMSNorm] = None,
+             stream=None) -> RMSNorm:
+    """y = s * rstd * weight with s = bf16(X + residual) (S; X itself without a residual) and rstd = 1 / sqrt(mean
+    s^2 + eps): in bf16 (Y) and/or in E4M3 with 1x128 scales (Y_fp8, Y_scale).  X, residual bf16 [N, H], weight [H]
+    float32 or bfloat16.  `out` names the tensors to write (None: not wanted; its S may be the residual)."""
+    fmt = _scale_format(scale_format)
+    N, H = _dims(X, "X", 2)
+    dev = _home(X, "X")
+    x, res = _arg(X, "X", torch.bfloat16, (N, H), dev), _opt(residual, "residual", torch.bfloat16, (N, H), dev)
+    w, wt = _weight(weight, H, dev)
+    if out is None:
+        if fp8 and H % BLOCK != 0:
+            raise ValueError("E4M3 rows need H to be a multiple of 128")
+        out = RMSNorm(_new((N, H), torch.bfloat16, X.device, stream) if bf16 else None,
+                      *(_coded(N, H, scale_format, X.device, stream) if fp8 else (None, None)),
+                      X if residual is None else _new((N, H), torch.bfloat16, X.device, stream),
+                      _new((N,), torch.float32, X.device, stream))
+    s = None if residual is None else _arg(out.S, "S", torch.bfloat16, (N, H), dev)
+    code = lib().moe_rms_norm(x, res, w, wt, eps, N, H, s, _opt(out.Y, "Y", torch.bfloat16, (N, H), dev),
+                              _opt(out.Y_fp8, "Y_fp8", torch.uint8, (N, H), dev),
+                              _opt(out.Y_scale, "Y_scale", _scale_dtype(scale_format), (N, H // BLOCK), dev), fmt,
+                              _opt(out.rstd, "rstd", torch.float32, (N,), dev), _raw_stream(stream, dev))
+    if code:
+        _check(code, "moe_rms_norm")
+    return out
+
+
+def rms_norm_backward(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                      dS: Optional[torch.Tensor] = None, add: Optional[torch.Tensor] = None,
+                      out: Optional[RMSNormGrad] = None, stream=None) -> RMSNormGrad:
+    """Gradient of rms_norm from its S and rstd: dX (of X and of the residual alike; dS, the gradient that reaches S
+    through the stream, is added) and dweight float32 [H] = add + the sum over the rows."""
+    N, H = _dims(dY, "dY", 2)
+    dev = _home(dY, "dY")
+    dy, s = _arg(dY, "dY", torch.bfloat16, (N, H), dev), _arg(S, "S", torch.bfloat16, (N, H), dev)
+    w, wt = _weight(weight, H, dev)
+    r, ds = _arg(rstd, "rstd", torch.float32, (N,), dev), _opt(dS, "dS", torch.bfloat16, (N, H), dev)
+    added = _opt(add, "add", torch.float32, (H,), dev)
+    if out is None:
+        out = RMSNormGrad(_new((N, H), torch.bfloat16, dY.device, stream), _new((H,), torch.float32, dY.device, stream))
+    need = lib().moe_rms_norm_backward_workspace_size(N, H)
+    ws = _new((need,), torch.uint8, dY.device, stream)
+    code = lib().moe_rms_norm_backward(dy, s, w, wt, r, ds, added, N, H, _arg(out.dX, "dX", torch.bfloat16, (N, H), dev),
+                                       _arg(out.dweight, "dweight", torch.float32, (H,), dev), ws.data_ptr(), need,
+                                       _raw_stream(stream, dev))
+    if code:
+        _check(code, "moe_rms_norm_backward")
+    return out
+
+
+def _list(tensors: Sequence[torch.Tensor], name: str, dev: int):
+    """(addresses, sizes, dtypes) of a list of tensors on the current device."""
+    try:
+        where = set(map(torch.Tensor.get_device, tensors))
+        flat = all(map(torch.Tensor.is_contiguous, tensors))
+        ptrs, sizes, dtypes = list(map(torch.Tensor.data_ptr, tensors)), list(map(torch.Tensor.numel, tensors)), [t.dtype for t in tensors]
+    except TypeError:
+        raise TypeError(f"{name} must be a list of torch.Tensors") from None
+    if not (flat and where <= {dev} and set(dtypes) <= _TYPES.keys()):
+        for i, t in enumerate(tensors):
+            if t.dtype not in _TYPES:
+                raise TypeError(f"{name}[{i}] must be torch.float32 or torch.bfloat16, got {t.dtype}")
+            _need(t, f"{name}[{i}]", t.dtype)
+    return ptrs, sizes, dtypes
+
+
+def _norm_call(grads, out, max_norm, norm, stream):
+    grads = list(grads)
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
+    ptrs, sizes, dtypes = _list(grads, "grads", dev)
+    n, device = len(grads), torch.device("cuda", dev) if dev >= 0 else None
+    if device is None:
+        raise ValueError("gradients must be CUDA tensors (the library has no CPU path)")
+    if norm is None:
+        norm = _new((1,), torch.float32, device, stream)
+    P, I64, I32 = ctypes.c_void_p * n, ctypes.c_int64 * n, ctypes.c_int * n
+    src, count, types = P(*ptrs), I64(*sizes), I32(*[_TYPES[t] for t in dtypes])
+    need = lib().moe_grad_norm_workspace_size(n)
+    ws, raw = _new((need,), torch.uint8, device, stream), _raw_stream(stream, dev)
+    res = _arg(norm, "norm", torch.float32, (1,), dev)
+    if max_norm is None:
+        code = lib().moe_grad_norm(src, count, types, n, res, ws.data_ptr(), need, raw)
+    else:
+        dst, written = None, ptrs
+        if out is not None:
+            out = list(out)
+            written, out_sizes, out_dtypes = _list(out, "out", dev)
+            if out_sizes != sizes or out_dtypes != dtypes:
+                raise ValueError("out must have the sizes and types of grads")
+            dst = P(*written)
+        if len(set(written)) != n and len({p for p, k in zip(written, sizes) if k}) != sum(1 for k in sizes if k):
+            raise ValueError("a tensor is listed twice: it would be scaled twice")
+        code = lib().moe_clip_grad_norm(src, dst, count, types, n, max_norm, res, ws.data_ptr(), need, raw)
+    if code:
+        _check(code, "moe_grad_norm" if max_norm is None else "moe_clip_grad_norm")
+    return norm
+
+
+def grad_norm(grads: Sequence[torch.Tensor], out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The 2-norm of a list of float32 and bfloat16 tensors together, float32 [1] on the device."""
+    return _norm_call(grads, None, None, out, stream)
+
+
+def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None,
+                   norm: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Scale the tensors by min(1, max_norm / (norm + 1e-6)), in place or into the tensors of `out`, without the
+    host seeing the norm; returns it (before the scaling), float32 [1].  If it is not finite, the tensors are left
+    as they are (copied to `out`)."""
+    max_norm = float(max_norm)
+    if not max_norm >= 0:
+        raise ValueError("max_norm must not be negative or NaN")
+    return _norm_call(grads, out, max_norm, norm, stream)

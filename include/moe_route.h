@@ -535,6 +535,85 @@ MOE_API moe_status moe_layer(const void *X, const void *W_gate, const float *bia
                      int32_t *topk_idx, float *topk_w, void *out, int32_t *status_word,
                      void *workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The norms around the experts.  Both need a GPU of compute capability 10.x
+ * (MOE_ERR_UNSUPPORTED elsewhere).
+ * ---------------------------------------------------------------------------
+ */
+typedef enum moe_grad_type { MOE_GRAD_FP32 = 0, MOE_GRAD_BF16 = 1 } moe_grad_type;
+
+/*
+ * moe_rms_norm -- the norm in front of the router, with the residual stream's addition:
+ *   s = bf16(x + residual) (x itself without a residual);  rstd = 1 / sqrt(mean of s^2 + eps)
+ *   y = s * rstd * weight
+ *   X, residual bf16 [N, H] (residual may be NULL), weight [H] (weight_type: a moe_grad_type), 0 < eps <= 1
+ *   S bf16 [N, H]: with a residual, and only then; may be the residual or X
+ *   Y bf16 [N, H] or NULL (may be X): what moe_route and moe_dispatch read
+ *   Y_fp8 uint8 [N, H], Y_scale [N, H/128] (scale_format) or both NULL (H % 128 == 0): y in E4M3 by the
+ *   rule of moe_permute, quantised from the unrounded y, for products of all rows (a shared expert)
+ *   rstd fp32 [N] or NULL: what moe_rms_norm_backward reads
+ * Y or Y_fp8 is required.  The mean is summed in fp32: a row whose sum of squares leaves its range gives zeros
+ * (rows of values beyond 1e17 or so).  H % 8 == 0, 8 <= H <= 16384, N < 2^31.  One launch.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_MISALIGNED, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.
+ */
+MOE_API moe_status moe_rms_norm(const void *X, const void *residual, const void *weight, int weight_type, float eps,
+                             int64_t N, int H, void *S, void *Y, void *Y_fp8, void *Y_scale, int scale_format,
+                             float *rstd, moe_stream_t stream);
+
+/* Bytes of device workspace moe_rms_norm_backward needs (0 for sizes it does not take). */
+MOE_API size_t moe_rms_norm_backward_workspace_size(int64_t N, int H);
+
+/*
+ * moe_rms_norm_backward -- its gradient:
+ *   xh = s * rstd;  d = dy * weight;  dx = rstd * (d - xh * mean of d xh) + dS
+ *   dweight[h] = add[h] + sum_n dy[n,h] * xh[n,h]
+ *   dY bf16 [N, H]; S bf16 [N, H] and rstd fp32 [N] as moe_rms_norm left them (S is X without a residual)
+ *   dS bf16 [N, H] or NULL: the gradient that reaches s through the residual stream
+ *   add fp32 [H] or NULL, may be dweight
+ *   dX bf16 [N, H] (the gradient of x and of the residual alike); may be dY, S or dS
+ *   dweight fp32 [H], summed in fp32 in an order that depends on N and H alone
+ *   workspace  moe_rms_norm_backward_workspace_size() bytes, 16-byte aligned, in any state; calls that
+ *              may overlap need their own
+ * N == 0 writes dweight (add, or zeros).  Sizes as moe_rms_norm.  Two launches.
+ * Errors: as moe_rms_norm, and MOE_ERR_WORKSPACE.
+ */
+MOE_API moe_status moe_rms_norm_backward(const void *dY, const void *S, const void *weight, int weight_type,
+                             const float *rstd, const void *dS, const float *add, int64_t N, int H,
+                             void *dX, float *dweight, void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Bytes of device workspace moe_grad_norm and moe_clip_grad_norm need for n tensors. */
+MOE_API size_t moe_grad_norm_workspace_size(int n);
+
+/*
+ * moe_grad_norm -- the 2-norm of n tensors together: norm = sqrt(sum of g^2), fp32 [1].
+ *   grads   HOST array of n device pointers, aligned to their elements only
+ *   sizes   HOST array: elements of each (0 allowed, the pointer is then not looked at), 2^44 bytes at most
+ *           together, counted as four an element
+ *   types   HOST array: the moe_grad_type of each
+ *   workspace  moe_grad_norm_workspace_size(n) bytes, 16-byte aligned, in any state; calls that may
+ *              overlap need their own
+ * The host arrays are read during the call only.  Squares are added in fp32 for up to 65 values and in 64 bits
+ * beyond (also where a square would leave the range of fp32), in an order that depends on the list alone; NaNs and
+ * infinities propagate.  n == 0 gives 0.  A launch for each 1024 tensors (one up to 128) and one more.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_MISALIGNED, MOE_ERR_WORKSPACE, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.
+ */
+MOE_API moe_status moe_grad_norm(const void *const *grads, const int64_t *sizes, const int *types, int n,
+                             float *norm, void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * moe_clip_grad_norm -- the tensors scaled down to a largest norm, which the host never sees:
+ *   out[i] = grads[i] * c,  c = min(1, max_norm / (norm + 1e-6)) rounded to fp32,  norm as moe_grad_norm
+ *   out   HOST array of n device pointers of the same types, or NULL: in place (nothing is written if c is 1).
+ *         out[i] may be grads[i]; any other overlap, and a tensor that is listed twice, is undefined
+ *   max_norm >= 0
+ * If any value is infinite or NaN, c is 1: the caller sees it in norm.
+ * Errors: as moe_grad_norm.
+ */
+MOE_API moe_status moe_clip_grad_norm(const void *const *grads, void *const *out, const int64_t *sizes,
+                             const int *types, int n, double max_norm, float *norm,
+                             void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
 /* A static, human-readable name for a status code. */
 MOE_API const char *moe_status_string(moe_status status);
 
