@@ -25,7 +25,7 @@
 //   warps 2, 3 and the last two  scale producers: gather the bytes of 16 128-blocks per row; warp 3
 //               allocates TMEM
 //   warps 4..7  epilogue: TMEM -> registers -> bf16, transposed through shared memory; with the gated
-//               activation or its gradient (expert_gemm_epilogue.cuh) warps 8..11 too
+//               activation or its gradient (expert_gemm_epilogue.cuh) warps 4..15
 //
 // Measured (burst, 1.94 GHz): 16384 tokens on 128 experts, top 8, 2048 x 2048: 354 us, 3.1 PFLOP/s, the
 // tensor pipe 67% busy; the rest is the latency of a ring that 180 KiB in flight per SM do not quite cover
@@ -42,9 +42,10 @@ template <Mode kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
     expert_gemm_kernel(const __grid_constant__ TokenMaps tmX, const __grid_constant__ CUtensorMap tmW, const Params p)
 {
+    constexpr int kRing = stages(kMode);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sf_ring = ring + kStages * kStageBytes;
+    uint8_t *sf_ring = ring + kRing * kStageBytes;
     uint8_t *epi = sf_ring + kScaleSlots * kScaleSlotBytes;
     Tail &tail = *reinterpret_cast<Tail *>(epi + epi_bytes(kMode));
     volatile int *abort_flag = &tail.abort;
@@ -53,7 +54,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kRing; ++s) {
             mbar_init(&tail.full[s], rank == 0 ? 2 : 1);   // the leader's: its own stage and the other CTA's
             mbar_init(&tail.empty[s], 1);
         }
@@ -64,8 +65,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tail.acc_full[b], 1);
             mbar_init(&tail.acc_empty[b], 8 * teams(kMode));
-            mbar_init(&tail.words[b][0], 1);
-            mbar_init(&tail.words[b][1], 1);
+        }
+        for (int i = 0; i < kTeams; ++i) {
+            mbar_init(&tail.words[i][0], 1);
+            mbar_init(&tail.words[i][1], 1);
         }
         mbar_init(&tail.drain, 1);
         tail.abort = tail.bad_index = tail.bad_scale = 0;
@@ -152,7 +155,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
                 }
                 __syncwarp();
                 ++issued;
-                if (++s == kStages) {
+                if (++s == kRing) {
                     s = 0;
                     ph ^= 1u;
                 }
@@ -160,10 +163,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
         }
         if (!ok) {
             // let the copies already issued land before the CTA ends
-            const uint32_t from = issued > kStages ? issued - kStages : 0u;
+            const uint32_t from = issued > kRing ? issued - kRing : 0u;
             for (uint32_t x = from; x < issued; ++x) {
                 volatile int no_abort = 0;
-                mbar_wait_bounded(&tail.full[x % kStages], (x / kStages) & 1u, &no_abort);
+                mbar_wait_bounded(&tail.full[x % kRing], (x / kRing) & 1u, &no_abort);
             }
         }
     } else if (warp == 1 && rank != 0) {
@@ -175,7 +178,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
                 if (!ok) break;
                 if (elect_one()) mbar_arrive_at(&tail.full[s], 0);
                 __syncwarp();
-                if (++s == kStages) {
+                if (++s == kRing) {
                     s = 0;
                     ph ^= 1u;
                 }
@@ -234,7 +237,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
                         tc_commit_pair(&tail.empty[s]);
                     }
                     __syncwarp();
-                    if (++s == kStages) {
+                    if (++s == kRing) {
                         s = 0;
                         ph ^= 1u;
                     }
@@ -253,8 +256,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
         // Scale words: byte i of a row's word is the scale of 128-block 4 q + i.  Tokens: row r at
         // lane r % 32, word r / 32 of a 128-row atom; features: one word for the whole 128.  Two warps,
         // one for each atom, fill a slot with 16 blocks; two such teams take turns, so that a team has
-        // two tiles' time (16 blocks each) for the loads' latency and the hand-over.
-        const int team = warp >= 8, half = warp & 1;
+        // two tiles' time (16 blocks each) for the loads' latency and the hand-over.  (With the activation's
+        // epilogue the one team fills both slots.)
+        constexpr bool kTurns = scale_teams(kMode) == 2;
+        const int team = warp >= 4, half = warp & 1;
         const int m_blocks = (p.out + kBlk - 1) / kBlk;
         uint32_t turn = 0, ph = 0;
         bool bad = false, ok = true;
@@ -262,7 +267,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
             Tile t;
             t.e = -1;
             for (int k0 = 0; k0 < blocks && ok; k0 += 16, turn ^= 1u) {
-                if (turn != static_cast<uint32_t>(team)) continue;
+                if (kTurns && turn != static_cast<uint32_t>(team)) continue;
                 if (t.e < 0) t = walk.get(tail);
                 // (blocks and rows that are not there read their neighbour's scale and are never used: the
                 // loads carry no condition and are all in flight together)
@@ -340,9 +345,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
                         }
                     }
                 }
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.sf_empty[team], ph ^ 1u, abort_flag, 32));
-                ph ^= 1u;
-                uint4 *slot = reinterpret_cast<uint4 *>(sf_ring + team * kScaleSlotBytes);
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tail.sf_empty[turn], ph ^ 1u, abort_flag, 32));
+                if (kTurns || turn) ph ^= 1u;
+                uint4 *slot = reinterpret_cast<uint4 *>(sf_ring + turn * kScaleSlotBytes);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint4 *quad = slot + i * (kScaleQuadBytes / 16);
@@ -353,12 +358,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
                 // before the async proxy, the arrival at the leader has no other memory to order)
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_at(&tail.sf_full[team], 0);
+                if (lane == 0) mbar_arrive_at(&tail.sf_full[turn], 0);
             }
         }
         if (bad) tail.bad_scale = 1;
     } else {
-        const EpilogueWarp wp{epi, tmem, static_cast<int>(rank), warp < 8 ? 0 : 1, warp & 3, lane, pair, pairs, tiles};
+        const EpilogueWarp wp{epi, tmem, static_cast<int>(rank), (warp >> 2) - 1, warp & 3, lane, pair, pairs, tiles};
         if constexpr (kMode == kPlain)
             plain_epilogue(p, tail, wp);
         else if constexpr (kMode == kGated)

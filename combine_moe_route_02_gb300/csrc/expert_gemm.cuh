@@ -11,7 +11,6 @@ constexpr int kTileM = 256;        // output features per tile, half of them in 
 constexpr int kHalfM = 128;
 constexpr int kTileN = 224;        // most tokens per tile: two accumulators and the scales fit TMEM
 constexpr int kBlk = 128;          // reduction block of a scale, and of a ring stage
-constexpr int kStages = 6;
 constexpr int kScaleSlots = 2;
 constexpr int kABytes = kHalfM * kBlk;
 constexpr int kBBytes = kTileN / 2 * kBlk;      // half of the tokens
@@ -22,28 +21,32 @@ constexpr int kScaleSlotBytes = 4 * kScaleQuadBytes;
 // What follows the product: nothing (bf16 rows out), the gated activation (the product is both halves of its
 // input), or the activation's gradient (the product is the gradient of its output).
 enum Mode { kPlain, kGated, kGatedGrad };
-// The activation's modes have a second team of four epilogue warps (warps 8..11), the teams take the chunks of 32
-// tokens in turn.
-constexpr int teams(Mode m) { return m == kPlain ? 1 : 2; }
-constexpr int threads(Mode m) { return 32 * (6 + 4 * teams(m)); }
-// Staging of the epilogue: per warp 32 tokens x 64 bytes; kGated has three arrays (codes of the activation and of
-// both halves) for each team's four warps instead.  Then the words in which warps tell each other scales.
-constexpr int stage_bytes(Mode m) { return m == kPlain ? 4 * 2048 : m == kGated ? 2 * 3 * 2048 : 8 * 2048; }
-constexpr int kWordBytes = 2 * 2 * 8 * 32 * 4;   // teams x buffers in turn x warps (of both CTAs) x tokens
-constexpr int epi_bytes(Mode m) { return stage_bytes(m) + (m == kPlain ? 0 : kWordBytes); }
+// The activation's modes have three teams of four epilogue warps, which take the chunks of 32 tokens in turn, and one
+// team of scale producers instead of two: 16 warps, the most that have 128 registers a thread.
+constexpr int kTeams = 3;
+constexpr int teams(Mode m) { return m == kPlain ? 1 : kTeams; }
+constexpr int scale_teams(Mode m) { return m == kPlain ? 2 : 1; }
+constexpr int threads(Mode m) { return 32 * (2 + 2 * scale_teams(m) + 4 * teams(m)); }
+constexpr int stages(Mode m) { return m == kGatedGrad ? 5 : 6; }
+// Staging of the epilogue.  kPlain: 32 tokens x 64 bytes a warp; kGated: three arrays of that (codes of the activation
+// and of both halves) a team; kGatedGrad: two (both halves) a warp.  Then the words in which warps tell each other
+// scales: two buffers in turn for each team, of a word for each token and warp (kGated: of both CTAs).
+constexpr int stage_bytes(Mode m) { return m == kPlain ? 4 * 2048 : m == kGated ? kTeams * 3 * 2048 : kTeams * 4 * 4096; }
+constexpr int word_warps(Mode m) { return m == kPlain ? 0 : m == kGated ? 8 : 4; }
+constexpr int epi_bytes(Mode m) { return stage_bytes(m) + kTeams * 2 * word_warps(m) * 32 * 4; }
 constexpr uint32_t kTmemCols = 512;
 // Scales lie behind the two accumulators: 4 + 8 columns for four blocks.  Five places in turn: when one is
 // written again its MMAs have completed, those of the tile before the last by the wait for its accumulator,
-// nearer ones because at least six blocks of the ring lie between.
+// nearer ones because at least as many blocks as the ring holds lie between.
 constexpr uint32_t kSfCol = 2 * kTileN, kSfCols = 12, kSfPlaces = 5;
 static_assert(kSfCol + kSfPlaces * kSfCols <= kTmemCols, "TMEM");
 constexpr int kMaxE = 256;
 
 struct Tail {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[6], empty[6];
     uint64_t sf_full[kScaleSlots], sf_empty[kScaleSlots];
     uint64_t acc_full[2], acc_empty[2], drain;
-    uint64_t words[2][2];         // kGated: the scale words of a team's chunk, two in turn
+    uint64_t words[kTeams][2];    // kGated: the scale words of a team's chunk, two in turn
     uint32_t tmem_base;
     int abort, bad_index, bad_scale;
     int tiles;                    // token tiles of all groups
@@ -53,7 +56,7 @@ struct Tail {
 
 constexpr size_t smem_bytes(Mode m)
 {
-    return 1024 + kStages * kStageBytes + kScaleSlots * kScaleSlotBytes + epi_bytes(m) + sizeof(Tail);
+    return 1024 + stages(m) * kStageBytes + kScaleSlots * kScaleSlotBytes + epi_bytes(m) + sizeof(Tail);
 }
 static_assert(smem_bytes(kPlain) <= 227 * 1024 && smem_bytes(kGated) <= 227 * 1024 && smem_bytes(kGatedGrad) <= 227 * 1024,
               "shared memory");

@@ -89,6 +89,15 @@ __device__ __forceinline__ bool team_all(int team, bool ok)
     return r != 0;
 }
 
+// The teams take a tile's chunks in turn, and with every tile another team begins (a tile of 7 chunks is 3, 2 and 2).
+struct Chunks {
+    int first;
+    __device__ __forceinline__ explicit Chunks(int team) : first(team) {}
+    __device__ __forceinline__ void next() { first = first == 0 ? kTeams - 1 : first - 1; }
+    __device__ __forceinline__ int begin() const { return first * 32; }
+};
+constexpr int kChunkStep = kTeams * 32;
+
 // The largest of m[s] over the eight lanes that share tokens: lane l is left with that of s = l / 4, which is token
 // lane_token(l).
 __device__ __forceinline__ float max_of_lanes(const float (&m)[8], int lane)
@@ -111,12 +120,32 @@ __device__ __forceinline__ uint32_t max_bytes(uint32_t a, uint32_t b)
     return __vmaxu2(a & 0x00FF00FFu, b & 0x00FF00FFu) | max(a & 0xFF00u, b & 0xFF00u);
 }
 
-// Codes of two values, the first in the low byte.
-__device__ __forceinline__ uint32_t codes_of(float lo, float hi)
+// Two tokens at a time (i = 0, 1): the values of feature r of chunk column c, and codes of features r = 0 and 1 of
+// both tokens, the first token's in the low half.
+__device__ __forceinline__ float2 both(const float (&v)[32], int at) { return make_float2(v[at], v[at + 1]); }
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+__device__ __forceinline__ uint32_t codes_of(float2 r0, float2 r1)
 {
-    uint16_t q;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(hi), "f"(lo));
+    uint32_t q;
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 a, %3, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 b, %4, %2;\n\t"
+        "mov.b32 %0, {a, b};\n\t}"
+        : "=r"(q)
+        : "f"(r0.x), "f"(r0.y), "f"(r1.x), "f"(r1.y));
     return q;
+}
+__device__ __forceinline__ float2 sigmoid2(float2 g)
+{
+    // (as sigmoid(), both at a time)
+    const float2 t = __fmul2_rn(g, twice(-1.44269504088896340736f));
+    float2 e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    e = __fadd2_rn(e, twice(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+    return r;
 }
 
 // 16 bytes of a row in the order 0, 8, 1, 9, ... put right, and back.
@@ -177,33 +206,42 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
     const uint8_t *take = stage + out_tok * 64 + ((piece ^ ((out_tok >> 1) & 3)) << 4);
     const uint32_t lane_addr = e.tmem + (static_cast<uint32_t>(w * 32) << 16);
     const int nb = p.I / kBlk;
+    const bool keep = p.K != nullptr;
     int j = 0;
     uint32_t n = 0;                                    // this team's chunks
     bool ok = true;
-    for (Walk walk(e.pair, p.m_tiles); walk.tile < e.tiles; walk.next(e.pairs, p.m_tiles), ++j) {
+    Chunks chunks(team);
+    for (Walk walk(e.pair, p.m_tiles); walk.tile < e.tiles; walk.next(e.pairs, p.m_tiles), chunks.next(), ++j) {
         const Tile t = walk.get(tail);
         const int b = j & 1, fb = t.m0 / kTileM;       // its block of 128 features
         ok = team_all(team, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, &tail.abort, 64));
         if (!ok) break;
         tc_fence_after_sync();
-        if (team * 32 >= t.rows) release_accumulator(tail, b, lane);
-        for (int c0 = team * 32; c0 < t.rows; c0 += 64, ++n) {
-            float v[32], a[16];
+        if (chunks.begin() >= t.rows) release_accumulator(tail, b, lane);
+        for (int c0 = chunks.begin(); c0 < t.rows; c0 += kChunkStep, ++n) {
+            float v[32];
             tmem_ld_fragments(lane_addr + b * kTileN + c0, v);
             tmem_ld_wait();
-            if (c0 + 64 >= t.rows) release_accumulator(tail, b, lane);
+            if (c0 + kChunkStep >= t.rows) release_accumulator(tail, b, lane);
+            float2 a[4][2];
             float ma[8], mg[8], mu[8];
 #pragma unroll
-            for (int x = 0; x < 16; ++x) a[x] = v[x] * sigmoid(v[x]) * v[16 + x];
+            for (int c = 0; c < 4; ++c) {
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const int x = 4 * (s >> 1) + (s & 1);
-                ma[s] = fmaxf(fabsf(a[x]), fabsf(a[x + 2]));
-                mg[s] = fmaxf(fabsf(v[x]), fabsf(v[x + 2]));
-                mu[s] = fmaxf(fabsf(v[16 + x]), fabsf(v[18 + x]));
+                for (int r = 0; r < 2; ++r) {
+                    const float2 g = both(v, 4 * c + 2 * r);
+                    a[c][r] = __fmul2_rn(__fmul2_rn(g, sigmoid2(g)), both(v, 16 + 4 * c + 2 * r));
+                }
+                ma[2 * c] = fmaxf(fabsf(a[c][0].x), fabsf(a[c][1].x));
+                ma[2 * c + 1] = fmaxf(fabsf(a[c][0].y), fabsf(a[c][1].y));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    mg[2 * c + i] = fmaxf(fabsf(v[4 * c + i]), fabsf(v[4 * c + 2 + i]));
+                    mu[2 * c + i] = fmaxf(fabsf(v[16 + 4 * c + i]), fabsf(v[18 + 4 * c + i]));
+                }
             }
             uint32_t word = block_scale_byte(max_of_lanes(ma, lane));
-            if (p.K) word |= block_scale_byte(max_of_lanes(mg, lane)) << 8 | block_scale_byte(max_of_lanes(mu, lane)) << 16;
+            if (keep) word |= block_scale_byte(max_of_lanes(mg, lane)) << 8 | block_scale_byte(max_of_lanes(mu, lane)) << 16;
             // eight warps' words for each token; a buffer is written again two chunks later, when the words of the
             // chunk between have come from every warp, which each sent after it had read this one
             uint32_t *slot = words + (n & 1) * 256;
@@ -219,25 +257,28 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
             if (e.rank == 0 && c0 + tok < t.rows) {
                 const int64_t row = t.row0 + c0 + tok;
                 if (w == 0) store_scale(p.A_scale, p.out_ue8m0, row * nb + fb, word & 0xFFu);
-                if (p.K && w == 1) store_scale(p.K_scale, p.out_ue8m0, row * 2 * nb + fb, (word >> 8) & 0xFFu);
-                if (p.K && w == 2) store_scale(p.K_scale, p.out_ue8m0, (row * 2 + 1) * nb + fb, word >> 16);
+                if (keep && w == 1) store_scale(p.K_scale, p.out_ue8m0, row * 2 * nb + fb, (word >> 8) & 0xFFu);
+                if (keep && w == 2) store_scale(p.K_scale, p.out_ue8m0, (row * 2 + 1) * nb + fb, word >> 16);
             }
+            word = 0x00FEFEFEu - word;                 // the exponents of the scales' reciprocals (no byte is above 254)
             uint32_t q[3][4];
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const int x = 4 * (s >> 1) + (s & 1), c = s >> 1;
-                const uint32_t of = of_token(word, s, lane);
-                const float ia = scale_reciprocal(of & 0xFFu), ig = scale_reciprocal((of >> 8) & 0xFFu),
-                            iu = scale_reciprocal(of >> 16);
-                const uint32_t qa = codes_of(a[x] * ia, a[x + 2] * ia), qg = codes_of(v[x] * ig, v[x + 2] * ig),
-                               qu = codes_of(v[16 + x] * iu, v[18 + x] * iu);
-                q[0][c] = s & 1 ? q[0][c] | qa << 16 : qa;
-                q[1][c] = s & 1 ? q[1][c] | qg << 16 : qg;
-                q[2][c] = s & 1 ? q[2][c] | qu << 16 : qu;
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t t0 = of_token(word, 2 * c, lane), t1 = of_token(word, 2 * c + 1, lane);
+                const auto inv = [&](int left) {
+                    return make_float2(__uint_as_float(t0 << left & 0x7F800000u), __uint_as_float(t1 << left & 0x7F800000u));
+                };
+                const float2 ia = inv(23);
+                q[0][c] = codes_of(__fmul2_rn(a[c][0], ia), __fmul2_rn(a[c][1], ia));
+                if (keep) {
+                    const float2 ig = inv(15), iu = inv(7);
+                    q[1][c] = codes_of(__fmul2_rn(both(v, 4 * c), ig), __fmul2_rn(both(v, 4 * c + 2), ig));
+                    q[2][c] = codes_of(__fmul2_rn(both(v, 16 + 4 * c), iu), __fmul2_rn(both(v, 18 + 4 * c), iu));
+                }
             }
             // (the codes of the chunk before have been read: its words came after that)
             store_rows(put, q[0]);
-            if (p.K) {
+            if (keep) {
                 store_rows(put + 2048, q[1]);
                 store_rows(put + 4096, q[2]);
             }
@@ -247,7 +288,7 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
                 const int64_t row = t.row0 + c0 + out_tok;
                 const int f = fb * kBlk + e.rank * 64 + piece * 16;
                 *reinterpret_cast<uint4 *>(p.A + row * p.I + f) = in_order(*reinterpret_cast<const uint4 *>(take));
-                if (p.K) {
+                if (keep) {
                     uint8_t *k = p.K + row * 2 * p.I + f;
                     *reinterpret_cast<uint4 *>(k) = in_order(*reinterpret_cast<const uint4 *>(take + 2048));
                     *reinterpret_cast<uint4 *>(k + p.I) = in_order(*reinterpret_cast<const uint4 *>(take + 4096));
@@ -266,17 +307,19 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
 __device__ __forceinline__ void gated_grad_epilogue(const Params &p, Tail &tail, const EpilogueWarp &e)
 {
     const int team = e.team, w = e.w, lane = e.lane, tok = lane_token(lane);
-    uint8_t *buf = e.epi + (team * 4 + w) * 2048;
+    uint8_t *buf = e.epi + (team * 4 + w) * 4096;
     const uint32_t buf_addr = smem_u32(buf);
     uint32_t *words = reinterpret_cast<uint32_t *>(e.epi + stage_bytes(kGatedGrad)) + team * 2 * 128;
     const uint32_t lane_addr = e.tmem + (static_cast<uint32_t>(w * 32) << 16);
     const int nb = p.I / kBlk;
+    const int64_t pitch = 2 * static_cast<int64_t>(p.I);
     // E4M3 rows are read and written by two lanes for a token's 32 features
     const int k_tok = lane >> 1, k_half = lane & 1;
     int j = 0;
     uint32_t n = 0;
     bool bad = false;
-    for (Walk walk(e.pair, p.m_tiles); walk.tile < e.tiles; walk.next(e.pairs, p.m_tiles), ++j) {
+    Chunks chunks(team);
+    for (Walk walk(e.pair, p.m_tiles); walk.tile < e.tiles; walk.next(e.pairs, p.m_tiles), chunks.next(), ++j) {
         const Tile t = walk.get(tail);
         const int b = j & 1, fb = t.m0 / kBlk + e.rank;
         const bool there = fb < nb;                    // (the last tile of an odd number of blocks is half empty)
@@ -286,7 +329,7 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, Tail &tail,
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = c0 + k_tok + 16 * i;
-                const uint8_t *k = p.K + (t.row0 + (r < t.rows ? r : t.rows - 1)) * 2 * p.I + fb * kBlk + w * 32 + k_half * 16;
+                const uint8_t *k = p.K + (t.row0 + (r < t.rows ? r : t.rows - 1)) * pitch + fb * kBlk + w * 32 + k_half * 16;
                 kg[i] = __ldcs(reinterpret_cast<const uint4 *>(k));
                 ku[i] = __ldcs(reinterpret_cast<const uint4 *>(k + p.I));
             }
@@ -295,68 +338,74 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, Tail &tail,
             sg = load_scale_bits(p.K_scale, p.k_ue8m0, at);
             su = load_scale_bits(p.K_scale, p.k_ue8m0, at + nb);
         };
-        if (there && team * 32 < t.rows) fetch(team * 32);
+        if (there && chunks.begin() < t.rows) fetch(chunks.begin());
         if (!team_all(team, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, &tail.abort, 64))) break;
         tc_fence_after_sync();
-        if (!there || team * 32 >= t.rows) {
+        if (!there || chunks.begin() >= t.rows) {
             release_accumulator(tail, b, lane);
             continue;
         }
-        for (int c0 = team * 32; c0 < t.rows; c0 += 64, ++n) {
+        for (int c0 = chunks.begin(); c0 < t.rows; c0 += kChunkStep, ++n) {
+            float du[32], dg[32];
+            tmem_ld_fragments(lane_addr + b * kTileN + c0, du);
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 *reinterpret_cast<uint4 *>(buf + k_half * 512 + (k_tok + 16 * i) * 16) = in_pairs(kg[i]);
                 *reinterpret_cast<uint4 *>(buf + 1024 + k_half * 512 + (k_tok + 16 * i) * 16) = in_pairs(ku[i]);
             }
-            const uint32_t scales = scale_bits_byte(sg, p.k_ue8m0, bad) | scale_bits_byte(su, p.k_ue8m0, bad) << 8;
+            // both scales as bf16 numbers
+            const uint32_t scales = __float_as_uint(scale_value(scale_bits_byte(sg, p.k_ue8m0, bad))) >> 16 |
+                                    (__float_as_uint(scale_value(scale_bits_byte(su, p.k_ue8m0, bad))) & 0xFFFF0000u);
             __syncwarp();
             uint32_t k[2][2][4];                       // [gate, up][h][c]
 #pragma unroll
             for (int x = 0; x < 4; ++x) load_rows(buf_addr + x * 512 + lane * 16, k[x >> 1][x & 1]);
-            if (c0 + 64 < t.rows) fetch(c0 + 64);
-            float du[32], dg[32];
-            tmem_ld_fragments(lane_addr + b * kTileN + c0, du);
+            if (c0 + kChunkStep < t.rows) fetch(c0 + kChunkStep);
             tmem_ld_wait();
-            if (c0 + 64 >= t.rows) release_accumulator(tail, b, lane);
+            if (c0 + kChunkStep >= t.rows) release_accumulator(tail, b, lane);
             float mg[8], mu[8];
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const int c = s >> 1, i = s & 1;
-                const uint32_t of = __shfl_sync(kAll, scales, 8 * c + 2 * (lane & 3) + i);
-                const float gs = scale_value(of & 0xFFu), us = scale_value(of >> 8);
-                mg[s] = mu[s] = 0.f;
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t t0 = __shfl_sync(kAll, scales, 8 * c + 2 * (lane & 3)), t1 = __shfl_sync(kAll, scales, 8 * c + 2 * (lane & 3) + 1);
+                const float2 gs = make_float2(__uint_as_float(t0 << 16), __uint_as_float(t1 << 16));
+                const float2 us = make_float2(__uint_as_float(t0 & 0xFFFF0000u), __uint_as_float(t1 & 0xFFFF0000u));
+                mg[2 * c] = mg[2 * c + 1] = mu[2 * c] = mu[2 * c + 1] = 0.f;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float2 g2 = e4m3x2_to_f32x2(i ? k[0][h][c] >> 16 : k[0][h][c] & 0xFFFFu);
-                    const float2 u2 = e4m3x2_to_f32x2(i ? k[1][h][c] >> 16 : k[1][h][c] & 0xFFFFu);
+                    // the two tokens' codes of r = 0, then of r = 1
+                    const uint32_t kg4 = __byte_perm(k[0][h][c], 0, 0x3120), ku4 = __byte_perm(k[1][h][c], 0, 0x3120);
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const int x = 16 * h + 4 * c + 2 * r + i;
-                        const float g = (r ? g2.y : g2.x) * gs, u = (r ? u2.y : u2.x) * us;
-                        const float sig = sigmoid(g), as = du[x] * sig;
-                        du[x] = as * g;
-                        dg[x] = as * u * (1.f + g * (1.f - sig));
-                        mg[s] = fmaxf(mg[s], fabsf(dg[x]));
-                        mu[s] = fmaxf(mu[s], fabsf(du[x]));
+                        const int x = 16 * h + 4 * c + 2 * r;
+                        const float2 g = __fmul2_rn(e4m3x2_to_f32x2(r ? kg4 >> 16 : kg4 & 0xFFFFu), gs);
+                        const float2 u = __fmul2_rn(e4m3x2_to_f32x2(r ? ku4 >> 16 : ku4 & 0xFFFFu), us);
+                        const float2 s = sigmoid2(g), as = __fmul2_rn(both(du, x), s);
+                        const float2 slope = __ffma2_rn(g, __ffma2_rn(s, twice(-1.f), twice(1.f)), twice(1.f));
+                        const float2 dg2 = __fmul2_rn(__fmul2_rn(as, u), slope), du2 = __fmul2_rn(as, g);
+                        dg[x] = dg2.x, dg[x + 1] = dg2.y;
+                        du[x] = du2.x, du[x + 1] = du2.y;
+                        mg[2 * c] = fmaxf(mg[2 * c], fabsf(dg2.x)), mg[2 * c + 1] = fmaxf(mg[2 * c + 1], fabsf(dg2.y));
+                        mu[2 * c] = fmaxf(mu[2 * c], fabsf(du2.x)), mu[2 * c + 1] = fmaxf(mu[2 * c + 1], fabsf(du2.y));
                     }
                 }
             }
             uint32_t *slot = words + (n & 1) * 128;
             if (p.Q) slot[w * 32 + tok] = block_scale_byte(max_of_lanes(mg, lane)) | block_scale_byte(max_of_lanes(mu, lane)) << 16;
             if (p.Y) {
-                const int64_t pitch = 2 * static_cast<int64_t>(p.I);
                 __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.Y) + (t.row0 + c0 + (lane >> 2)) * pitch + fb * kBlk + w * 32 + (lane & 3) * 8;
+                __syncwarp();
+                store_transposed(buf_addr, lane, dg);
+                store_transposed(buf_addr + 2048, lane, du);
+                __syncwarp();
 #pragma unroll
-                for (int gu = 0; gu < 2; ++gu, dst += p.I) {
-                    __syncwarp();
-                    store_transposed(buf_addr, lane, gu ? du : dg);
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int at = i * 8 + (lane >> 2);
-                        const uint4 y = *reinterpret_cast<const uint4 *>(buf + at * 64 + (((lane & 3) ^ ((at >> 1) & 3)) << 4));
-                        if (c0 + at < t.rows) *reinterpret_cast<uint4 *>(dst + 8 * i * pitch) = y;
+                for (int i = 0; i < 4; ++i) {
+                    const int at = i * 8 + (lane >> 2);
+                    const uint8_t *y = buf + at * 64 + (((lane & 3) ^ ((at >> 1) & 3)) << 4);
+                    const uint4 yg = *reinterpret_cast<const uint4 *>(y), yu = *reinterpret_cast<const uint4 *>(y + 2048);
+                    if (c0 + at < t.rows) {
+                        *reinterpret_cast<uint4 *>(dst + 8 * i * pitch) = yg;
+                        *reinterpret_cast<uint4 *>(dst + 8 * i * pitch + p.I) = yu;
                     }
                 }
             }
@@ -368,18 +417,18 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, Tail &tail,
                 for (int x = 0; x < 4; ++x) word = __vmaxu2(word, slot[x * 32 + tok]);
                 if (c0 + tok < t.rows && w < 2)
                     store_scale(p.Q_scale, p.out_ue8m0, (t.row0 + c0 + tok) * 2 * nb + w * nb + fb, w ? word >> 16 : word & 0xFFu);
+                word = (0x00FE00FEu - word) << 7;      // the scales' reciprocals as bf16 numbers
                 uint32_t q[2][2][4];
 #pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    const int c = s >> 1;
-                    const uint32_t of = of_token(word, s, lane);
-                    const float ig = scale_reciprocal(of & 0xFFu), iu = scale_reciprocal(of >> 16);
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t t0 = of_token(word, 2 * c, lane), t1 = of_token(word, 2 * c + 1, lane);
+                    const float2 ig = make_float2(__uint_as_float(t0 << 16), __uint_as_float(t1 << 16));
+                    const float2 iu = make_float2(__uint_as_float(t0 & 0xFFFF0000u), __uint_as_float(t1 & 0xFFFF0000u));
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int x = 16 * h + 4 * c + (s & 1);
-                        const uint32_t qg = codes_of(dg[x] * ig, dg[x + 2] * ig), qu = codes_of(du[x] * iu, du[x + 2] * iu);
-                        q[0][h][c] = s & 1 ? q[0][h][c] | qg << 16 : qg;
-                        q[1][h][c] = s & 1 ? q[1][h][c] | qu << 16 : qu;
+                        const int x = 16 * h + 4 * c;
+                        q[0][h][c] = codes_of(__fmul2_rn(both(dg, x), ig), __fmul2_rn(both(dg, x + 2), ig));
+                        q[1][h][c] = codes_of(__fmul2_rn(both(du, x), iu), __fmul2_rn(both(du, x + 2), iu));
                     }
                 }
                 __syncwarp();
@@ -392,7 +441,7 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, Tail &tail,
                     const uint4 yg = in_order(*reinterpret_cast<const uint4 *>(buf + k_half * 512 + at * 16));
                     const uint4 yu = in_order(*reinterpret_cast<const uint4 *>(buf + 1024 + k_half * 512 + at * 16));
                     if (c0 + at < t.rows) {
-                        uint8_t *dst = p.Q + (t.row0 + c0 + at) * 2 * p.I + fb * kBlk + w * 32 + k_half * 16;
+                        uint8_t *dst = p.Q + (t.row0 + c0 + at) * pitch + fb * kBlk + w * 32 + k_half * 16;
                         *reinterpret_cast<uint4 *>(dst) = yg;
                         *reinterpret_cast<uint4 *>(dst + p.I) = yu;
                     }
