@@ -40,7 +40,8 @@ namespace {
 
 template <Mode kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
-    expert_gemm_kernel(const __grid_constant__ TokenMaps tmX, const __grid_constant__ CUtensorMap tmW, const Params p)
+    expert_gemm_kernel(const __grid_constant__ TokenMaps tmX, const __grid_constant__ CUtensorMap tmW,
+                       const __grid_constant__ CUtensorMap tmY, const Params p)
 {
     constexpr int kRing = stages(kMode);
     extern __shared__ uint8_t smem_raw[];
@@ -369,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
         else if constexpr (kMode == kGated)
             gated_epilogue(p, tail, wp);
         else
-            gated_grad_epilogue(p, tail, wp);
+            gated_grad_epilogue(p, tmY, tail, wp);
     }
 
     if constexpr (kMode == kGated) {
@@ -457,6 +458,15 @@ cudaError_t launch(Params &p, const void *X, const void *W, int rows, int cols, 
         if (!encode_map(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, W, 3, wd, wb)) return cudaErrorInvalidValue;
     }
 
+    CUtensorMap tmY = tmW;
+    if (kMode == kGatedGrad && p.Y) {
+        // a warp's 32 features of 32 tokens
+        const uint64_t yd[2] = {2 * static_cast<uint64_t>(p.I), static_cast<uint64_t>(p.R)};
+        const uint32_t yb[2] = {32, 32};
+        if (!encode_map(&tmY, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.Y, 2, yd, yb, CU_TENSOR_MAP_SWIZZLE_64B))
+            return cudaErrorInvalidValue;
+    }
+
     static std::atomic<uint64_t> done{0};
     const uint64_t bit = 1ull << (dev & 63);
     if (!(done.load(std::memory_order_relaxed) & bit)) {
@@ -473,7 +483,7 @@ cudaError_t launch(Params &p, const void *X, const void *W, int rows, int cols, 
     const int64_t most = (p.R / kTileN + (p.R < p.E ? p.R : p.E) + 1) * p.m_tiles;
     const int pairs = device_sm_count(dev) / 2;
     const int grid = 2 * static_cast<int>(most < pairs ? most : pairs);
-    expert_gemm_kernel<kMode><<<grid, threads(kMode), smem_bytes(kMode), stream>>>(tmX, tmW, p);
+    expert_gemm_kernel<kMode><<<grid, threads(kMode), smem_bytes(kMode), stream>>>(tmX, tmW, tmY, p);
     return cudaGetLastError();
 }
 

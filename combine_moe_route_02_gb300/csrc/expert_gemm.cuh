@@ -27,11 +27,12 @@ constexpr int kTeams = 3;
 constexpr int teams(Mode m) { return m == kPlain ? 1 : kTeams; }
 constexpr int scale_teams(Mode m) { return m == kPlain ? 2 : 1; }
 constexpr int threads(Mode m) { return 32 * (2 + 2 * scale_teams(m) + 4 * teams(m)); }
-constexpr int stages(Mode m) { return m == kGatedGrad ? 5 : 6; }
+constexpr int stages(Mode m) { return m == kGatedGrad ? 4 : 6; }
 // Staging of the epilogue.  kPlain: 32 tokens x 64 bytes a warp; kGated: three arrays of that (codes of the activation
-// and of both halves) a team; kGatedGrad: two (both halves) a warp.  Then the words in which warps tell each other
+// and of both halves) a team; kGatedGrad: one (codes) and two for the
+// TMA (both halves) a warp.  Then the words in which warps tell each other
 // scales: two buffers in turn for each team, of a word for each token and warp (kGated: of both CTAs).
-constexpr int stage_bytes(Mode m) { return m == kPlain ? 4 * 2048 : m == kGated ? kTeams * 3 * 2048 : kTeams * 4 * 4096; }
+constexpr int stage_bytes(Mode m) { return m == kPlain ? 4 * 2048 : m == kGated ? kTeams * 3 * 2048 : kTeams * 4 * 6144; }
 constexpr int word_warps(Mode m) { return m == kPlain ? 0 : m == kGated ? 8 : 4; }
 constexpr int epi_bytes(Mode m) { return stage_bytes(m) + kTeams * 2 * word_warps(m) * 32 * 4; }
 constexpr uint32_t kTmemCols = 512;

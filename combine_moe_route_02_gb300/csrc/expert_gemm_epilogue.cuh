@@ -304,48 +304,62 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
 //   s = 1 / (1 + exp(-g));  dg = da u s (1 + g (1 - s));  du = da g s
 // in bf16 and in E4M3.  A CTA's 128 features are a block, its scale bytes are joined over a team's four warps.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void gated_grad_epilogue(const Params &p, Tail &tail, const EpilogueWarp &e)
+__device__ __forceinline__ void gated_grad_epilogue(const Params &p, const CUtensorMap &tmY, Tail &tail, const EpilogueWarp &e)
 {
     const int team = e.team, w = e.w, lane = e.lane, tok = lane_token(lane);
-    uint8_t *buf = e.epi + (team * 4 + w) * 4096;
-    const uint32_t buf_addr = smem_u32(buf);
+    uint8_t *rows = e.epi + (team * 4 + w) * 4096;                       // bf16 rows of both halves, for the TMA
+    uint8_t *buf = e.epi + kTeams * 4 * 4096 + (team * 4 + w) * 2048;    // codes
+    const uint32_t buf_addr = smem_u32(buf), rows_addr = smem_u32(rows);
     uint32_t *words = reinterpret_cast<uint32_t *>(e.epi + stage_bytes(kGatedGrad)) + team * 2 * 128;
     const uint32_t lane_addr = e.tmem + (static_cast<uint32_t>(w * 32) << 16);
     const int nb = p.I / kBlk;
     const int64_t pitch = 2 * static_cast<int64_t>(p.I);
     // E4M3 rows are read and written by two lanes for a token's 32 features
     const int k_tok = lane >> 1, k_half = lane & 1;
-    int j = 0;
     uint32_t n = 0;
     bool bad = false;
-    Chunks chunks(team);
-    for (Walk walk(e.pair, p.m_tiles); walk.tile < e.tiles; walk.next(e.pairs, p.m_tiles), chunks.next(), ++j) {
-        const Tile t = walk.get(tail);
-        const int b = j & 1, fb = t.m0 / kBlk + e.rank;
-        const bool there = fb < nb;                    // (the last tile of an odd number of blocks is half empty)
-        uint4 kg[2], ku[2];
-        uint32_t sg = 0, su = 0;
-        const auto fetch = [&](int c0) {
+    uint4 kg[2], ku[2];
+    uint32_t sg = 0, su = 0;
+    // A chunk's part of the checkpoint is asked for while the chunk before is worked on, across tiles too.
+    const auto fetch = [&](const Tile &t, int c0) {
+        const int fb = t.m0 / kBlk + e.rank;
+        if (fb >= nb || c0 >= t.rows) return;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = c0 + k_tok + 16 * i;
-                const uint8_t *k = p.K + (t.row0 + (r < t.rows ? r : t.rows - 1)) * pitch + fb * kBlk + w * 32 + k_half * 16;
-                kg[i] = __ldcs(reinterpret_cast<const uint4 *>(k));
-                ku[i] = __ldcs(reinterpret_cast<const uint4 *>(k + p.I));
-            }
-            const int r = c0 + lane;
-            const int64_t at = (t.row0 + (r < t.rows ? r : t.rows - 1)) * 2 * nb + fb;
-            sg = load_scale_bits(p.K_scale, p.k_ue8m0, at);
-            su = load_scale_bits(p.K_scale, p.k_ue8m0, at + nb);
-        };
-        if (there && chunks.begin() < t.rows) fetch(chunks.begin());
+        for (int i = 0; i < 2; ++i) {
+            const int r = c0 + k_tok + 16 * i;
+            const uint8_t *k = p.K + (t.row0 + (r < t.rows ? r : t.rows - 1)) * pitch + fb * kBlk + w * 32 + k_half * 16;
+            kg[i] = __ldcs(reinterpret_cast<const uint4 *>(k));
+            ku[i] = __ldcs(reinterpret_cast<const uint4 *>(k + p.I));
+        }
+        const int r = c0 + lane;
+        const int64_t at = (t.row0 + (r < t.rows ? r : t.rows - 1)) * 2 * nb + fb;
+        sg = load_scale_bits(p.K_scale, p.k_ue8m0, at);
+        su = load_scale_bits(p.K_scale, p.k_ue8m0, at + nb);
+    };
+    Chunks chunks(team);
+    Walk walk(e.pair, p.m_tiles);
+    Tile next{};
+    if (walk.tile < e.tiles) {
+        next = walk.get(tail);
+        fetch(next, chunks.begin());
+    }
+    for (int j = 0; walk.tile < e.tiles; ++j) {
+        const Tile t = next;
+        const int b = j & 1, fb = t.m0 / kBlk + e.rank, begin = chunks.begin();
+        walk.next(e.pairs, p.m_tiles);
+        chunks.next();
+        next.rows = 0;
+        if (walk.tile < e.tiles) next = walk.get(tail);
         if (!team_all(team, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, &tail.abort, 64))) break;
         tc_fence_after_sync();
-        if (!there || chunks.begin() >= t.rows) {
+        // (the last tile of an odd number of blocks is half empty)
+        if (fb >= nb || begin >= t.rows) {
             release_accumulator(tail, b, lane);
+            fetch(next, chunks.begin());
             continue;
         }
-        for (int c0 = chunks.begin(); c0 < t.rows; c0 += kChunkStep, ++n) {
+        for (int c0 = begin; c0 < t.rows; c0 += kChunkStep, ++n) {
+            const bool last = c0 + kChunkStep >= t.rows;
             float du[32], dg[32];
             tmem_ld_fragments(lane_addr + b * kTileN + c0, du);
             __syncwarp();
@@ -361,9 +375,9 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, Tail &tail,
             uint32_t k[2][2][4];                       // [gate, up][h][c]
 #pragma unroll
             for (int x = 0; x < 4; ++x) load_rows(buf_addr + x * 512 + lane * 16, k[x >> 1][x & 1]);
-            if (c0 + kChunkStep < t.rows) fetch(c0 + kChunkStep);
+            fetch(last ? next : t, last ? chunks.begin() : c0 + kChunkStep);
             tmem_ld_wait();
-            if (c0 + kChunkStep >= t.rows) release_accumulator(tail, b, lane);
+            if (last) release_accumulator(tail, b, lane);
             float mg[8], mu[8];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -393,19 +407,32 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, Tail &tail,
             uint32_t *slot = words + (n & 1) * 128;
             if (p.Q) slot[w * 32 + tok] = block_scale_byte(max_of_lanes(mg, lane)) | block_scale_byte(max_of_lanes(mu, lane)) << 16;
             if (p.Y) {
-                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.Y) + (t.row0 + c0 + (lane >> 2)) * pitch + fb * kBlk + w * 32 + (lane & 3) * 8;
+                if (lane == 0) bulk_wait_read<0>();    // the chunk before
                 __syncwarp();
-                store_transposed(buf_addr, lane, dg);
-                store_transposed(buf_addr + 2048, lane, du);
-                __syncwarp();
+                store_transposed(rows_addr, lane, dg);
+                store_transposed(rows_addr + 2048, lane, du);
+                const int f = fb * kBlk + w * 32;
+                if (c0 + 32 <= t.rows) {
+                    // whole: two boxes (pieces of 16 bytes lie as the TMA's swizzle of 64 bytes has them)
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        const int32_t r = static_cast<int32_t>(t.row0) + c0;
+                        tma_store_2d(&tmY, rows_addr, f, r);
+                        tma_store_2d(&tmY, rows_addr + 2048, f + p.I, r);
+                        bulk_commit();
+                    }
+                } else {
+                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.Y) + (t.row0 + c0 + (lane >> 2)) * pitch + f + (lane & 3) * 8;
+                    __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = i * 8 + (lane >> 2);
-                    const uint8_t *y = buf + at * 64 + (((lane & 3) ^ ((at >> 1) & 3)) << 4);
-                    const uint4 yg = *reinterpret_cast<const uint4 *>(y), yu = *reinterpret_cast<const uint4 *>(y + 2048);
-                    if (c0 + at < t.rows) {
-                        *reinterpret_cast<uint4 *>(dst + 8 * i * pitch) = yg;
-                        *reinterpret_cast<uint4 *>(dst + 8 * i * pitch + p.I) = yu;
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = i * 8 + (lane >> 2);
+                        const uint8_t *y = rows + at * 64 + (((lane & 3) ^ ((at >> 1) & 3)) << 4);
+                        if (c0 + at < t.rows) {
+                            *reinterpret_cast<uint4 *>(dst + 8 * i * pitch) = *reinterpret_cast<const uint4 *>(y);
+                            *reinterpret_cast<uint4 *>(dst + 8 * i * pitch + p.I) = *reinterpret_cast<const uint4 *>(y + 2048);
+                        }
                     }
                 }
             }
@@ -450,6 +477,7 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, Tail &tail,
         }
     }
     if (bad) tail.bad_scale = 1;
+    if (lane == 0) bulk_wait_all();
 }
 
 }  // namespace
