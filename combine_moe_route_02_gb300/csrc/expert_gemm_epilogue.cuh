@@ -160,6 +160,25 @@ __device__ __forceinline__ uint4 in_pairs(const uint4 &x)
                       __byte_perm(x.y, x.w, 0x7362));
 }
 
+// Shared memory by its address (through a pointer that went through a struct the accesses are generic ones).
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint4 &v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
+
 // Four 8x8 matrices of two bytes, transposed, to / from rows of 16 bytes: lane l gives the address of row l.
 __device__ __forceinline__ void store_rows(uint32_t row_addr, const uint32_t (&m)[4])
 {
@@ -198,12 +217,12 @@ __device__ __forceinline__ void send_word(uint32_t addr, uint32_t word, uint32_t
 __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, const EpilogueWarp &e)
 {
     const int team = e.team, w = e.w, lane = e.lane, tok = lane_token(lane);
-    uint8_t *stage = e.epi + team * 3 * 2048;         // codes of a, g, u: 32 tokens x 64 features each
-    uint32_t *words = reinterpret_cast<uint32_t *>(e.epi + stage_bytes(kGated)) + team * 2 * 256;
+    const uint32_t stage = smem_u32(e.epi) + team * 3 * 2048;         // codes of a, g, u: 32 tokens x 64 features each
+    const uint32_t words = smem_u32(e.epi) + stage_bytes(kGated) + team * 2 * 1024;
     // 16-byte piece f of token t lies at place f ^ (t / 2 % 4)
-    const uint32_t put = smem_u32(stage) + lane * 64 + ((w ^ ((lane >> 1) & 3)) << 4);
+    const uint32_t put = stage + lane * 64 + ((w ^ ((lane >> 1) & 3)) << 4);
     const int out_tok = w * 8 + (lane >> 2), piece = lane & 3;
-    const uint8_t *take = stage + out_tok * 64 + ((piece ^ ((out_tok >> 1) & 3)) << 4);
+    const uint32_t take = stage + out_tok * 64 + ((piece ^ ((out_tok >> 1) & 3)) << 4);
     const uint32_t lane_addr = e.tmem + (static_cast<uint32_t>(w * 32) << 16);
     const int nb = p.I / kBlk;
     const bool keep = p.K != nullptr;
@@ -244,16 +263,16 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
             if (keep) word |= block_scale_byte(max_of_lanes(mg, lane)) << 8 | block_scale_byte(max_of_lanes(mu, lane)) << 16;
             // eight warps' words for each token; a buffer is written again two chunks later, when the words of the
             // chunk between have come from every warp, which each sent after it had read this one
-            uint32_t *slot = words + (n & 1) * 256;
+            const uint32_t slot = words + (n & 1) * 1024;
             uint64_t *bar = &tail.words[team][n & 1];
             if (w == 0 && lane == 0) mbar_arrive_expect_tx(bar, 8 * 32 * 4);
-            const uint32_t to = smem_u32(slot + (e.rank * 4 + w) * 32 + tok);
+            const uint32_t to = slot + ((e.rank * 4 + w) * 32 + tok) * 4;
             send_word(to, word, smem_u32(bar), 0);
             send_word(to, word, smem_u32(bar), 1);
             ok = mbar_wait_bounded(bar, (n >> 1) & 1, &tail.abort);
             word = 0;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) word = max_bytes(word, slot[k * 32 + tok]);
+            for (int k = 0; k < 8; ++k) word = max_bytes(word, lds32(slot + (k * 32 + tok) * 4));
             if (e.rank == 0 && c0 + tok < t.rows) {
                 const int64_t row = t.row0 + c0 + tok;
                 if (w == 0) store_scale(p.A_scale, p.out_ue8m0, row * nb + fb, word & 0xFFu);
@@ -287,11 +306,11 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
             if (c0 + out_tok < t.rows) {
                 const int64_t row = t.row0 + c0 + out_tok;
                 const int f = fb * kBlk + e.rank * 64 + piece * 16;
-                *reinterpret_cast<uint4 *>(p.A + row * p.I + f) = in_order(*reinterpret_cast<const uint4 *>(take));
+                *reinterpret_cast<uint4 *>(p.A + row * p.I + f) = in_order(lds128(take));
                 if (keep) {
                     uint8_t *k = p.K + row * 2 * p.I + f;
-                    *reinterpret_cast<uint4 *>(k) = in_order(*reinterpret_cast<const uint4 *>(take + 2048));
-                    *reinterpret_cast<uint4 *>(k + p.I) = in_order(*reinterpret_cast<const uint4 *>(take + 4096));
+                    *reinterpret_cast<uint4 *>(k) = in_order(lds128(take + 2048));
+                    *reinterpret_cast<uint4 *>(k + p.I) = in_order(lds128(take + 4096));
                 }
             }
         }
@@ -307,10 +326,9 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
 __device__ __forceinline__ void gated_grad_epilogue(const Params &p, const CUtensorMap &tmY, Tail &tail, const EpilogueWarp &e)
 {
     const int team = e.team, w = e.w, lane = e.lane, tok = lane_token(lane);
-    uint8_t *rows = e.epi + (team * 4 + w) * 4096;                       // bf16 rows of both halves, for the TMA
-    uint8_t *buf = e.epi + kTeams * 4 * 4096 + (team * 4 + w) * 2048;    // codes
-    const uint32_t buf_addr = smem_u32(buf), rows_addr = smem_u32(rows);
-    uint32_t *words = reinterpret_cast<uint32_t *>(e.epi + stage_bytes(kGatedGrad)) + team * 2 * 128;
+    const uint32_t rows = smem_u32(e.epi) + (team * 4 + w) * 4096;                       // bf16 rows of both halves, for the TMA
+    const uint32_t buf = smem_u32(e.epi) + kTeams * 4 * 4096 + (team * 4 + w) * 2048;    // codes
+    const uint32_t words = smem_u32(e.epi) + stage_bytes(kGatedGrad) + team * 2 * 512;
     const uint32_t lane_addr = e.tmem + (static_cast<uint32_t>(w * 32) << 16);
     const int nb = p.I / kBlk;
     const int64_t pitch = 2 * static_cast<int64_t>(p.I);
@@ -365,8 +383,8 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, const CUten
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                *reinterpret_cast<uint4 *>(buf + k_half * 512 + (k_tok + 16 * i) * 16) = in_pairs(kg[i]);
-                *reinterpret_cast<uint4 *>(buf + 1024 + k_half * 512 + (k_tok + 16 * i) * 16) = in_pairs(ku[i]);
+                sts128(buf + k_half * 512 + (k_tok + 16 * i) * 16, in_pairs(kg[i]));
+                sts128(buf + 1024 + k_half * 512 + (k_tok + 16 * i) * 16, in_pairs(ku[i]));
             }
             // both scales as bf16 numbers
             const uint32_t scales = __float_as_uint(scale_value(scale_bits_byte(sg, p.k_ue8m0, bad))) >> 16 |
@@ -374,7 +392,7 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, const CUten
             __syncwarp();
             uint32_t k[2][2][4];                       // [gate, up][h][c]
 #pragma unroll
-            for (int x = 0; x < 4; ++x) load_rows(buf_addr + x * 512 + lane * 16, k[x >> 1][x & 1]);
+            for (int x = 0; x < 4; ++x) load_rows(buf + x * 512 + lane * 16, k[x >> 1][x & 1]);
             fetch(last ? next : t, last ? chunks.begin() : c0 + kChunkStep);
             tmem_ld_wait();
             if (last) release_accumulator(tail, b, lane);
@@ -404,13 +422,13 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, const CUten
                     }
                 }
             }
-            uint32_t *slot = words + (n & 1) * 128;
-            if (p.Q) slot[w * 32 + tok] = block_scale_byte(max_of_lanes(mg, lane)) | block_scale_byte(max_of_lanes(mu, lane)) << 16;
+            const uint32_t slot = words + (n & 1) * 512;
+            if (p.Q) sts32(slot + (w * 32 + tok) * 4, block_scale_byte(max_of_lanes(mg, lane)) | block_scale_byte(max_of_lanes(mu, lane)) << 16);
             if (p.Y) {
                 if (lane == 0) bulk_wait_read<0>();    // the chunk before
                 __syncwarp();
-                store_transposed(rows_addr, lane, dg);
-                store_transposed(rows_addr + 2048, lane, du);
+                store_transposed(rows, lane, dg);
+                store_transposed(rows + 2048, lane, du);
                 const int f = fb * kBlk + w * 32;
                 if (c0 + 32 <= t.rows) {
                     // whole: two boxes (pieces of 16 bytes lie as the TMA's swizzle of 64 bytes has them)
@@ -418,8 +436,8 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, const CUten
                     __syncwarp();
                     if (lane == 0) {
                         const int32_t r = static_cast<int32_t>(t.row0) + c0;
-                        tma_store_2d(&tmY, rows_addr, f, r);
-                        tma_store_2d(&tmY, rows_addr + 2048, f + p.I, r);
+                        tma_store_2d(&tmY, rows, f, r);
+                        tma_store_2d(&tmY, rows + 2048, f + p.I, r);
                         bulk_commit();
                     }
                 } else {
@@ -428,10 +446,10 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, const CUten
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int at = i * 8 + (lane >> 2);
-                        const uint8_t *y = rows + at * 64 + (((lane & 3) ^ ((at >> 1) & 3)) << 4);
+                        const uint32_t y = rows + at * 64 + (((lane & 3) ^ ((at >> 1) & 3)) << 4);
                         if (c0 + at < t.rows) {
-                            *reinterpret_cast<uint4 *>(dst + 8 * i * pitch) = *reinterpret_cast<const uint4 *>(y);
-                            *reinterpret_cast<uint4 *>(dst + 8 * i * pitch + p.I) = *reinterpret_cast<const uint4 *>(y + 2048);
+                            *reinterpret_cast<uint4 *>(dst + 8 * i * pitch) = lds128(y);
+                            *reinterpret_cast<uint4 *>(dst + 8 * i * pitch + p.I) = lds128(y + 2048);
                         }
                     }
                 }
@@ -441,7 +459,7 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, const CUten
                 named_barrier_sync(2 + team, 128);
                 uint32_t word = 0;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) word = __vmaxu2(word, slot[x * 32 + tok]);
+                for (int x = 0; x < 4; ++x) word = __vmaxu2(word, lds32(slot + (x * 32 + tok) * 4));
                 if (c0 + tok < t.rows && w < 2)
                     store_scale(p.Q_scale, p.out_ue8m0, (t.row0 + c0 + tok) * 2 * nb + w * nb + fb, w ? word >> 16 : word & 0xFFu);
                 word = (0x00FE00FEu - word) << 7;      // the scales' reciprocals as bf16 numbers
@@ -460,13 +478,13 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, const CUten
                 }
                 __syncwarp();
 #pragma unroll
-                for (int x = 0; x < 4; ++x) store_rows(buf_addr + x * 512 + lane * 16, q[x >> 1][x & 1]);
+                for (int x = 0; x < 4; ++x) store_rows(buf + x * 512 + lane * 16, q[x >> 1][x & 1]);
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int at = k_tok + 16 * i;
-                    const uint4 yg = in_order(*reinterpret_cast<const uint4 *>(buf + k_half * 512 + at * 16));
-                    const uint4 yu = in_order(*reinterpret_cast<const uint4 *>(buf + 1024 + k_half * 512 + at * 16));
+                    const uint4 yg = in_order(lds128(buf + k_half * 512 + at * 16));
+                    const uint4 yu = in_order(lds128(buf + 1024 + k_half * 512 + at * 16));
                     if (c0 + at < t.rows) {
                         uint8_t *dst = p.Q + (t.row0 + c0 + at) * pitch + fb * kBlk + w * 32 + k_half * 16;
                         *reinterpret_cast<uint4 *>(dst) = yg;
