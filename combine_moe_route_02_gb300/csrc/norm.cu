@@ -3,8 +3,9 @@
 //   s = bf16(x + residual);  rstd = 1 / sqrt(mean s^2 + eps);  y = s rstd w
 //   dx = rstd (d - xh mean(d xh)) + dS,  d = dy w,  xh = s rstd;   dw = sum over the rows of dy xh (+ add)
 //
-// One pass over the rows: a row stays in the registers of kT threads (16 bytes a lane and chunk, neighbouring lanes
-// neighbouring chunks) between its sum and what is written.  The sums are held in 32 bits.
+// One pass over the rows: a row stays in the registers of its threads (a warp's for short rows, else a CTA's; kV
+// chunks of 16 bytes each, neighbouring threads neighbouring chunks) between its sum and what is written.  The sums
+// are held in 32 bits.
 #include "expert_internal.cuh"
 
 namespace moe {
@@ -42,28 +43,27 @@ __device__ __forceinline__ void load_weight(const void *w, int bf16, int c, floa
     }
 }
 
-// The sum over the kT threads of a row, the same in each of them.  `part`: kT / 32 floats of the row's own; a second
-// call of the same threads takes another.
-template <int kT>
+constexpr int kWarpRows = 4;      // rows of a CTA where a row is a warp's
+constexpr int kMostThreads = 512;
+constexpr int kTwoThreads = 384;  // the most with two chunks each
+
+// The sum over the threads of a row, the same in each of them.  `part`: a float for each warp; a second call takes
+// another array.
+template <bool kWarp>
 __device__ __forceinline__ float row_sum(float v, float *part)
 {
 #pragma unroll
-    for (int o = (kT < 32 ? kT : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    if constexpr (kT > 32) {
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    if constexpr (!kWarp) {
         if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
         __syncthreads();
-        v = 0.f;
+        // every warp adds them up in the same order
+        const int warps = blockDim.x >> 5, i = threadIdx.x & 15;
+        v = i < warps ? part[i] : 0.f;
 #pragma unroll
-        for (int i = 0; i < kT / 32; ++i) v += part[i];
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
     }
     return v;
-}
-
-// A CTA has kT threads for its one row, or, where a row is a warp's, four of them.
-template <int kT>
-constexpr int block_threads()
-{
-    return kT > 32 ? kT : 128;
 }
 
 struct Forward {
@@ -78,18 +78,18 @@ struct Forward {
     float *rstd;
 };
 
-template <int kT, int kV>
-__global__ void __launch_bounds__(block_threads<kT>()) rms_norm_kernel(const Forward p)
+template <bool kWarp, int kV>
+__global__ void __launch_bounds__(kMostThreads) rms_norm_kernel(const Forward p)
 {
-    __shared__ float part[kT > 32 ? kT / 32 : 1];
-    const int t = threadIdx.x & (kT - 1), chunks = p.H >> 3;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (block_threads<kT>() / kT) + threadIdx.x / kT;
-    if (kT <= 32 && row >= p.N) return;
+    __shared__ float part[kMostThreads / 32];
+    const int T = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x & 31 : threadIdx.x, chunks = p.H >> 3;
+    const int64_t row = kWarp ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    if (kWarp && row >= p.N) return;
     const int64_t base = row * chunks;
     uint4 x[kV], r[kV];
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
-        const int c = t + kT * j;
+        const int c = t + T * j;
         x[j] = r[j] = make_uint4(0, 0, 0, 0);
         if (c < chunks) x[j] = __ldcs(p.X + base + c);
         if (p.residual && c < chunks) r[j] = __ldcs(p.residual + base + c);
@@ -106,19 +106,19 @@ __global__ void __launch_bounds__(block_threads<kT>()) rms_norm_kernel(const For
 #pragma unroll
             for (int i = 0; i < 8; ++i) a[i] += b[i];
             x[j] = pack(a);
-            if (p.S && t + kT * j < chunks) p.S[base + t + kT * j] = x[j];
+            if (p.S && t + T * j < chunks) p.S[base + t + T * j] = x[j];
         }
         float a[8];
         unpack(x[j], a);
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum = fmaf(a[i], a[i], sum);
     }
-    const float rstd = 1.f / sqrtf(row_sum<kT>(sum, part) / static_cast<float>(p.H) + p.eps);
+    const float rstd = 1.f / sqrtf(row_sum<kWarp>(sum, part) / static_cast<float>(p.H) + p.eps);
     if (p.rstd && t == 0) p.rstd[row] = rstd;
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
-        const int c = t + kT * j;
-        if (kT * j >= chunks) break;
+        const int c = t + T * j;
+        if (T * j >= chunks) break;
         float y[8], w[8];
         const bool there = c < chunks;
         load_weight(p.w, p.w_bf16, there ? c : chunks - 1, w);
@@ -145,9 +145,10 @@ __global__ void __launch_bounds__(block_threads<kT>()) rms_norm_kernel(const For
 }
 
 // ---------------------------------------------------------------------------
-// Gradient.  A CTA takes rows blockIdx.x, + gridDim.x, ...: its threads keep to their columns and sum dy xh for them.
-// kFlush rows at a time are summed in registers, those sums in the CTA's own row of the workspace's table; a second
-// launch adds the table's rows up.  The order is the same in every call.
+// Gradient.  A CTA takes rows blockIdx.x, + gridDim.x, ... (a warp's rows: kWarpRows at a time): its threads keep to
+// their columns and sum dy xh for them.  kFlush rows at a time are summed in registers, those sums in shared memory,
+// and the CTA's own row of the workspace's table is their sum; a second launch adds the table's rows up.  The order
+// is the same in every call.
 // ---------------------------------------------------------------------------
 constexpr int kFlush = 64;
 
@@ -161,13 +162,14 @@ struct Backward {
     float *table;                 // [gridDim.x][H]
 };
 
-template <int kT, int kV>
-__global__ void __launch_bounds__(block_threads<kT>()) rms_norm_backward_kernel(const Backward p)
+template <bool kWarp, int kV>
+__global__ void __launch_bounds__(kV <= 2 ? kTwoThreads : kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backward_kernel(const Backward p)
 {
-    constexpr int kRows = block_threads<kT>() / kT;
-    __shared__ float part[2][kT > 32 ? kT / 32 : 1];
+    __shared__ float part[2][kMostThreads / 32];
     extern __shared__ float sums[];       // [kV][8][threads], so that neighbouring threads are neighbours
-    const int t = threadIdx.x & (kT - 1), chunks = p.H >> 3;
+    const int T = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x & 31 : threadIdx.x, chunks = p.H >> 3;
+    const int rows = kWarp ? kWarpRows : 1;
+    const float of_H = static_cast<float>(p.H);
     float acc[kV][8];
 #pragma unroll
     for (int j = 0; j < kV; ++j)
@@ -177,14 +179,14 @@ __global__ void __launch_bounds__(block_threads<kT>()) rms_norm_backward_kernel(
             sums[(j * 8 + i) * blockDim.x + threadIdx.x] = 0.f;
         }
     int n = 0;
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows; r < p.N; r += static_cast<int64_t>(gridDim.x) * kRows, ++n) {
-        const int64_t row = r + (kT > 32 ? 0 : threadIdx.x / kT);
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * rows; r < p.N; r += static_cast<int64_t>(gridDim.x) * rows, ++n) {
+        const int64_t row = kWarp ? r + (threadIdx.x >> 5) : r;
         const bool row_ok = row < p.N;
         const int64_t base = (row_ok ? row : p.N - 1) * chunks;
         uint4 dy[kV], s[kV], ds[kV];
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
-            const int c = t + kT * j;
+            const int c = t + T * j;
             dy[j] = s[j] = ds[j] = make_uint4(0, 0, 0, 0);
             if (c < chunks) {
                 dy[j] = __ldcs(p.dY + base + c);
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(block_threads<kT>()) rms_norm_backward_kernel(
         float dot = 0.f;
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
-            const int c = t + kT * j;
+            const int c = t + T * j;
             float a[8], b[8], w[8];
             unpack(dy[j], a);
             unpack(s[j], b);
@@ -218,10 +220,10 @@ __global__ void __launch_bounds__(block_threads<kT>()) rms_norm_backward_kernel(
                 if (row_ok) acc[j][i] += v;
             }
         }
-        const float mean = row_sum<kT>(dot, part[n & 1]) / static_cast<float>(p.H);
+        const float mean = row_sum<kWarp>(dot, part[n & 1]) / of_H;
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
-            const int c = t + kT * j;
+            const int c = t + T * j;
             if (c >= chunks) break;
             float a[8], b[8], e[8], w[8];
             unpack(dy[j], a);
@@ -233,12 +235,13 @@ __global__ void __launch_bounds__(block_threads<kT>()) rms_norm_backward_kernel(
             if (row_ok) p.dX[base + c] = pack(a);
         }
     }
+    pdl_launch_dependents();
 #pragma unroll
     for (int j = 0; j < kV; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[j][i] += sums[(j * 8 + i) * blockDim.x + threadIdx.x];
-    if constexpr (kT == 32) {
-        // the four warps' sums, added by the first
+    if constexpr (kWarp) {
+        // the warps' sums, added by the first
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kV; ++j)
@@ -252,12 +255,12 @@ __global__ void __launch_bounds__(block_threads<kT>()) rms_norm_backward_kernel(
             for (int i = 0; i < 8; ++i) {
                 acc[j][i] = 0.f;
 #pragma unroll
-                for (int k = 0; k < kRows; ++k) acc[j][i] += sums[(j * 8 + i) * blockDim.x + threadIdx.x + 32 * k];
+                for (int k = 0; k < kWarpRows; ++k) acc[j][i] += sums[(j * 8 + i) * blockDim.x + threadIdx.x + 32 * k];
             }
     }
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
-        const int c = t + kT * j;
+        const int c = t + T * j;
         if (c >= chunks) break;
         float4 *dst = reinterpret_cast<float4 *>(p.table + static_cast<int64_t>(blockIdx.x) * p.H) + 2 * c;
         dst[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
@@ -265,51 +268,46 @@ __global__ void __launch_bounds__(block_threads<kT>()) rms_norm_backward_kernel(
     }
 }
 
-// dw = the sum of the table's rows (+ add): 32 columns a CTA, 16 threads for the rows of each.
+// dw = the sum of the table's rows (+ add): 32 columns a CTA, 16 threads for the rows of each, four sums a thread.
 constexpr int kSumThreads = 512;
 
 __global__ void __launch_bounds__(kSumThreads) rms_norm_dweight_kernel(const float *__restrict__ table, int rows, int H, const float *add, float *dw)
 {
     __shared__ float part[kSumThreads / 32][32];
+    constexpr int kStep = kSumThreads / 32;
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
     pdl_wait_prior_grids();
-    float v = 0.f;
-    if (c < H)
-        for (int r = k; r < rows; r += kSumThreads / 32) v += table[static_cast<int64_t>(r) * H + c];
-    part[k][threadIdx.x & 31] = v;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (c < H) {
+        const float *at = table + c;
+        int r = k;
+        for (; r + 3 * kStep < rows; r += 4 * kStep)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += at[static_cast<int64_t>(r + i * kStep) * H];
+        for (int i = 0; r < rows; r += kStep, ++i) v[i & 3] += at[static_cast<int64_t>(r) * H];
+    }
+    part[k][threadIdx.x & 31] = (v[0] + v[1]) + (v[2] + v[3]);
     __syncthreads();
     if (k == 0 && c < H) {
-        v = 0.f;
+        float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kSumThreads / 32; ++i) v += part[i][threadIdx.x];
-        dw[c] = add ? add[c] + v : v;
+        for (int i = 0; i < kStep; ++i) sum += part[i][threadIdx.x];
+        dw[c] = add ? add[c] + sum : sum;
     }
 }
 
-// kT threads of kV chunks hold a row of at most 8 kT kV columns.
-template <int kT, int kV>
-cudaError_t launch_forward(const Forward &p, cudaStream_t stream)
+// How a row of H columns is held: a warp of one or two chunks a lane up to 512 columns, else as many threads, whole
+// warps, as two chunks each (beyond 6144 columns four) make of it.
+struct Shape {
+    bool warp;
+    int per, threads;
+};
+Shape shape_of(int H)
 {
-    constexpr int rows = block_threads<kT>() / kT;
-    rms_norm_kernel<kT, kV><<<static_cast<unsigned>((p.N + rows - 1) / rows), block_threads<kT>(), 0, stream>>>(p);
-    return cudaGetLastError();
-}
-
-template <int kT, int kV>
-cudaError_t launch_gradient(const Backward &p, int grid, int dev, cudaStream_t stream)
-{
-    constexpr size_t smem = kV * 8 * block_threads<kT>() * sizeof(float);
-    if (smem > 48 * 1024) {
-        static std::atomic<uint64_t> done{0};
-        const uint64_t bit = 1ull << (dev & 63);
-        if (!(done.load(std::memory_order_relaxed) & bit)) {
-            const cudaError_t err = cudaFuncSetAttribute(rms_norm_backward_kernel<kT, kV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (err != cudaSuccess) return err;
-            done.fetch_or(bit, std::memory_order_relaxed);
-        }
-    }
-    rms_norm_backward_kernel<kT, kV><<<grid, block_threads<kT>(), smem, stream>>>(p);
-    return cudaGetLastError();
+    const int chunks = H / 8;
+    if (chunks <= 64) return Shape{true, chunks <= 32 ? 1 : 2, 32 * kWarpRows};
+    const int per = chunks <= 2 * kTwoThreads ? 2 : 4;
+    return Shape{false, per, ((chunks + per - 1) / per + 31) / 32 * 32};
 }
 
 }  // namespace
@@ -333,26 +331,29 @@ cudaError_t launch_rms_norm(const RmsNormArgs &a, cudaStream_t stream)
     p.Q = static_cast<uint2 *>(a.Y_fp8);
     p.Q_scale = a.Y_scale;
     p.rstd = a.rstd;
-    if (a.H <= 256) return launch_forward<32, 1>(p, stream);
-    if (a.H <= 1024) return launch_forward<32, 4>(p, stream);
-    if (a.H <= 2048) return launch_forward<128, 2>(p, stream);
-    if (a.H <= 4096) return launch_forward<128, 4>(p, stream);
-    if (a.H <= 8192) return launch_forward<256, 4>(p, stream);
-    return launch_forward<512, 4>(p, stream);
+    const Shape f = shape_of(a.H);
+    const unsigned grid = static_cast<unsigned>(f.warp ? (a.N + kWarpRows - 1) / kWarpRows : a.N);
+    const auto kernel = f.warp ? (f.per == 1 ? rms_norm_kernel<true, 1> : rms_norm_kernel<true, 2>)
+                               : (f.per == 2 ? rms_norm_kernel<false, 2> : rms_norm_kernel<false, 4>);
+    kernel<<<grid, f.threads, 0, stream>>>(p);
+    return cudaGetLastError();
 }
 
 int rms_norm_table_rows(int64_t N, int H)
 {
-    // at most as many CTAs as the SMs of a GB300 hold at a time, and no more than there are rows for
-    const int rows = H <= 1024 ? 4 : 1, most = H <= 4096 ? 152 * 4 : 152;
-    const int64_t n = (N + rows - 1) / rows;
+    // as many CTAs as the 152 SMs of a GB300 hold at 80 registers a thread (128 where a thread has four chunks), eight
+    // an SM at most, and no more than there are rows for.  (Of 65536 x 4096 and 16381 x 1032, bursts: 351 and 39 us; with
+    // 64 registers, 4/3 of the threads and some spills 368 and 42; with 96 registers 415 and 42.)
+    const Shape f = shape_of(H);
+    const int fit = (f.per <= 2 ? 2 * kTwoThreads : 512) / f.threads, most = 152 * (fit < 8 ? fit : 8);
+    const int64_t n = f.warp ? (N + kWarpRows - 1) / kWarpRows : N;
     return static_cast<int>(n < most ? n : most);
 }
 
 cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs &a, cudaStream_t stream)
 {
     int dev = 0;
-    cudaError_t err = expert_device(&dev);
+    const cudaError_t err = expert_device(&dev);
     if (err != cudaSuccess) return err;
     Backward p;
     p.dY = static_cast<const uint4 *>(a.dY);
@@ -366,23 +367,30 @@ cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs &a, cudaStream_t 
     p.dX = static_cast<uint4 *>(a.dX);
     p.table = static_cast<float *>(a.workspace);
     const int grid = rms_norm_table_rows(a.N, a.H);
-    if (grid > 0) {
-        if (a.H <= 256)
-            err = launch_gradient<32, 1>(p, grid, dev, stream);
-        else if (a.H <= 1024)
-            err = launch_gradient<32, 4>(p, grid, dev, stream);
-        else if (a.H <= 4096)
-            err = launch_gradient<128, 4>(p, grid, dev, stream);
-        else if (a.H <= 8192)
-            err = launch_gradient<256, 4>(p, grid, dev, stream);
-        else
-            err = launch_gradient<512, 4>(p, grid, dev, stream);
-        if (err != cudaSuccess) return err;
-    }
     cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
+    if (grid > 0) {
+        const Shape f = shape_of(a.H);
+        const auto kernel = f.warp ? (f.per == 1 ? rms_norm_backward_kernel<true, 1> : rms_norm_backward_kernel<true, 2>)
+                                   : (f.per == 2 ? rms_norm_backward_kernel<false, 2> : rms_norm_backward_kernel<false, 4>);
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(f.threads);
+        cfg.dynamicSmemBytes = f.per * 8 * f.threads * sizeof(float);
+        if (cfg.dynamicSmemBytes > 48 * 1024) {
+            static std::atomic<uint64_t> done{0};
+            const uint64_t bit = 1ull << (dev & 63);
+            if (!(done.load(std::memory_order_relaxed) & bit)) {
+                const cudaError_t e = cudaFuncSetAttribute(rms_norm_backward_kernel<false, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+                if (e != cudaSuccess) return e;
+                done.fetch_or(bit, std::memory_order_relaxed);
+            }
+        }
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+        if (e != cudaSuccess) return e;
+    }
     cfg.gridDim = dim3((a.H + 31) / 32);
     cfg.blockDim = dim3(kSumThreads);
-    cfg.stream = stream;
+    cfg.dynamicSmemBytes = 0;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
