@@ -87,6 +87,18 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _on(stream, make, *args):
+    """make(*args), what it allocates being the memory of `stream` (None: of the current one)."""
+    if stream is None:
+        return make(*args)
+    with torch.cuda.stream(stream):
+        return make(*args)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def _dims(t: torch.Tensor, name: str, n: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -245,6 +257,20 @@ def swiglu_backward(dA: torch.Tensor, GU_fp8: torch.Tensor, GU_scale: torch.Tens
     return out
 
 
+def _swiglu_out(R: int, I: int, keep: bool, sd, device) -> SwiGLU:
+    e, u8 = torch.empty, torch.uint8
+    return SwiGLU(e((R, I), dtype=u8, device=device), e((R, I // BLOCK), dtype=sd, device=device),
+                  e((R, 2 * I), dtype=u8, device=device) if keep else None,
+                  e((R, 2 * I // BLOCK), dtype=sd, device=device) if keep else None)
+
+
+def _swiglu_grad_out(R: int, I: int, bf16: bool, fp8: bool, sd, device) -> SwiGLUGrad:
+    e = torch.empty
+    return SwiGLUGrad(e((R, 2 * I), dtype=torch.bfloat16, device=device) if bf16 else None,
+                      e((R, 2 * I), dtype=torch.uint8, device=device) if fp8 else None,
+                      e((R, 2 * I // BLOCK), dtype=sd, device=device) if fp8 else None)
+
+
 def _joined(X_fp8, X_scale, W_fp8, W_scale, expert_offsets, names, backward):
     """The arguments that expert_swiglu and its gradient share: (device, addresses and formats, R, E, H, I)."""
     x_name, w_name = names
@@ -275,13 +301,13 @@ def expert_swiglu(X_fp8: torch.Tensor, X_scale: torch.Tensor, W1_fp8: torch.Tens
     fmt, sd = _scale_format(scale_format), _scale_dtype(scale_format)
     dev, args, R, E, H, I = _joined(X_fp8, X_scale, W1_fp8, W1_scale, expert_offsets, ("X", "W1"), False)
     if out is None:
-        out = SwiGLU(*_coded(R, I, scale_format, X_fp8.device, stream),
-                     *(_coded(R, 2 * I, scale_format, X_fp8.device, stream) if keep else (None, None)))
-    code = lib().moe_expert_swiglu(*args, R, E, H, I, _arg(out.A_fp8, "A_fp8", torch.uint8, (R, I), dev),
-                                   _arg(out.A_scale, "A_scale", sd, (R, I // BLOCK), dev),
-                                   _opt(out.GU_fp8, "GU_fp8", torch.uint8, (R, 2 * I), dev),
-                                   _opt(out.GU_scale, "GU_scale", sd, (R, 2 * I // BLOCK), dev), fmt,
-                                   _status_ptr(status), _raw_stream(stream, dev))
+        out = _on(stream, _swiglu_out, R, I, keep, sd, X_fp8.device)
+        a, sa, k, sk = out.A_fp8.data_ptr(), out.A_scale.data_ptr(), _ptr(out.GU_fp8), _ptr(out.GU_scale)
+    else:
+        a, sa = _arg(out.A_fp8, "A_fp8", torch.uint8, (R, I), dev), _arg(out.A_scale, "A_scale", sd, (R, I // BLOCK), dev)
+        k = _opt(out.GU_fp8, "GU_fp8", torch.uint8, (R, 2 * I), dev)
+        sk = _opt(out.GU_scale, "GU_scale", sd, (R, 2 * I // BLOCK), dev)
+    code = lib().moe_expert_swiglu(*args, R, E, H, I, a, sa, k, sk, fmt, _status_ptr(status), _raw_stream(stream, dev))
     if code:
         _check(code, "moe_expert_swiglu")
     return out
@@ -297,14 +323,16 @@ def expert_swiglu_backward(dY_fp8: torch.Tensor, dY_scale: torch.Tensor, W2_fp8:
     dev, args, R, E, H, I = _joined(dY_fp8, dY_scale, W2_fp8, W2_scale, expert_offsets, ("dY", "W2"), True)
     kept = _arg(GU_fp8, "GU_fp8", torch.uint8, (R, 2 * I), dev)
     gs, gf = _scales(GU_scale, "GU_scale", (R, 2 * I // BLOCK), dev)
+    sd = _scale_dtype(scale_format)
     if out is None:
-        out = SwiGLUGrad(_new((R, 2 * I), torch.bfloat16, dY_fp8.device, stream) if bf16 else None,
-                         *(_coded(R, 2 * I, scale_format, dY_fp8.device, stream) if fp8 else (None, None)))
-    code = lib().moe_expert_swiglu_backward(*args, kept, gs, gf, R, E, H, I,
-                                            _opt(out.dGU, "dGU", torch.bfloat16, (R, 2 * I), dev),
-                                            _opt(out.dGU_fp8, "dGU_fp8", torch.uint8, (R, 2 * I), dev),
-                                            _opt(out.dGU_scale, "dGU_scale", _scale_dtype(scale_format), (R, 2 * I // BLOCK), dev),
-                                            fmt, _status_ptr(status), _raw_stream(stream, dev))
+        out = _on(stream, _swiglu_grad_out, R, I, bf16, fp8, sd, dY_fp8.device)
+        d, q, sq = _ptr(out.dGU), _ptr(out.dGU_fp8), _ptr(out.dGU_scale)
+    else:
+        d = _opt(out.dGU, "dGU", torch.bfloat16, (R, 2 * I), dev)
+        q = _opt(out.dGU_fp8, "dGU_fp8", torch.uint8, (R, 2 * I), dev)
+        sq = _opt(out.dGU_scale, "dGU_scale", sd, (R, 2 * I // BLOCK), dev)
+    code = lib().moe_expert_swiglu_backward(*args, kept, gs, gf, R, E, H, I, d, q, sq, fmt, _status_ptr(status),
+                                            _raw_stream(stream, dev))
     if code:
         _check(code, "moe_expert_swiglu_backward")
     return out

@@ -15,14 +15,14 @@ With ``stream`` a call launches there, and what it allocates is that stream's me
 """
 from __future__ import annotations
 
-import ctypes
+from array import array
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
 import torch
 
 from . import _check, _need, _scale_dtype, _scale_format, lib
-from .experts import BLOCK, _arg, _coded, _dims, _home, _new, _opt, _raw_stream
+from .experts import BLOCK, _arg, _dims, _home, _on, _opt, _ptr, _raw_stream
 
 __all__ = ["rms_norm", "rms_norm_backward", "grad_norm", "clip_grad_norm", "RMSNorm", "RMSNormGrad"]
 
@@ -53,6 +53,14 @@ class RMSNormGrad:
     dweight: torch.Tensor
 
 
+def _rms_out(X: torch.Tensor, N: int, H: int, stream_too: bool, bf16: bool, fp8: bool, sd) -> RMSNorm:
+    e, device = torch.empty, X.device
+    return RMSNorm(torch.empty_like(X) if bf16 else None,
+                   e((N, H), dtype=torch.uint8, device=device) if fp8 else None,
+                   e((N, H // BLOCK), dtype=sd, device=device) if fp8 else None,
+                   torch.empty_like(X) if stream_too else X, e((N,), dtype=torch.float32, device=device))
+
+
 def rms_norm(X: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
              bf16: bool = True, fp8: bool = False, scale_format: str = "fp32", out: Optional[RMSNorm] = None,
              stream=None) -> RMSNorm:
@@ -67,18 +75,24 @@ def rms_norm(X: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     if out is None:
         if fp8 and H % BLOCK != 0:
             raise ValueError("E4M3 rows need H to be a multiple of 128")
-        out = RMSNorm(_new((N, H), torch.bfloat16, X.device, stream) if bf16 else None,
-                      *(_coded(N, H, scale_format, X.device, stream) if fp8 else (None, None)),
-                      X if residual is None else _new((N, H), torch.bfloat16, X.device, stream),
-                      _new((N,), torch.float32, X.device, stream))
-    s = None if residual is None else _arg(out.S, "S", torch.bfloat16, (N, H), dev)
-    code = lib().moe_rms_norm(x, res, w, wt, eps, N, H, s, _opt(out.Y, "Y", torch.bfloat16, (N, H), dev),
-                              _opt(out.Y_fp8, "Y_fp8", torch.uint8, (N, H), dev),
-                              _opt(out.Y_scale, "Y_scale", _scale_dtype(scale_format), (N, H // BLOCK), dev), fmt,
-                              _opt(out.rstd, "rstd", torch.float32, (N,), dev), _raw_stream(stream, dev))
+        out = _on(stream, _rms_out, X, N, H, residual is not None, bf16, fp8, _scale_dtype(scale_format))
+        y, q, sq, r = _ptr(out.Y), _ptr(out.Y_fp8), _ptr(out.Y_scale), out.rstd.data_ptr()
+        s = None if residual is None else out.S.data_ptr()
+    else:
+        y, q = _opt(out.Y, "Y", torch.bfloat16, (N, H), dev), _opt(out.Y_fp8, "Y_fp8", torch.uint8, (N, H), dev)
+        sq = _opt(out.Y_scale, "Y_scale", _scale_dtype(scale_format), (N, H // BLOCK), dev)
+        r = _opt(out.rstd, "rstd", torch.float32, (N,), dev)
+        s = None if residual is None else _arg(out.S, "S", torch.bfloat16, (N, H), dev)
+    code = lib().moe_rms_norm(x, res, w, wt, eps, N, H, s, y, q, sq, fmt, r, _raw_stream(stream, dev))
     if code:
         _check(code, "moe_rms_norm")
     return out
+
+
+def _rms_grad_out(dY: torch.Tensor, H: int, need: int, results: bool):
+    device = dY.device
+    return (RMSNormGrad(torch.empty_like(dY), torch.empty((H,), dtype=torch.float32, device=device)) if results else None,
+            torch.empty((need,), dtype=torch.uint8, device=device))
 
 
 def rms_norm_backward(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
@@ -92,13 +106,13 @@ def rms_norm_backward(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor, r
     w, wt = _weight(weight, H, dev)
     r, ds = _arg(rstd, "rstd", torch.float32, (N,), dev), _opt(dS, "dS", torch.bfloat16, (N, H), dev)
     added = _opt(add, "add", torch.float32, (H,), dev)
-    if out is None:
-        out = RMSNormGrad(_new((N, H), torch.bfloat16, dY.device, stream), _new((H,), torch.float32, dY.device, stream))
     need = lib().moe_rms_norm_backward_workspace_size(N, H)
-    ws = _new((need,), torch.uint8, dY.device, stream)
-    code = lib().moe_rms_norm_backward(dy, s, w, wt, r, ds, added, N, H, _arg(out.dX, "dX", torch.bfloat16, (N, H), dev),
-                                       _arg(out.dweight, "dweight", torch.float32, (H,), dev), ws.data_ptr(), need,
-                                       _raw_stream(stream, dev))
+    new, ws = _on(stream, _rms_grad_out, dY, H, need, out is None)
+    if out is None:
+        out, dx, dw = new, new.dX.data_ptr(), new.dweight.data_ptr()
+    else:
+        dx, dw = _arg(out.dX, "dX", torch.bfloat16, (N, H), dev), _arg(out.dweight, "dweight", torch.float32, (H,), dev)
+    code = lib().moe_rms_norm_backward(dy, s, w, wt, r, ds, added, N, H, dx, dw, ws.data_ptr(), need, _raw_stream(stream, dev))
     if code:
         _check(code, "moe_rms_norm_backward")
     return out
@@ -112,7 +126,7 @@ def _list(tensors: Sequence[torch.Tensor], name: str, dev: int):
         ptrs, sizes, dtypes = list(map(torch.Tensor.data_ptr, tensors)), list(map(torch.Tensor.numel, tensors)), [t.dtype for t in tensors]
     except TypeError:
         raise TypeError(f"{name} must be a list of torch.Tensors") from None
-    if not (flat and where <= {dev} and set(dtypes) <= _TYPES.keys()):
+    if not (flat and where <= {dev} and _TYPES.keys() >= set(dtypes)):
         for i, t in enumerate(tensors):
             if t.dtype not in _TYPES:
                 raise TypeError(f"{name}[{i}] must be torch.float32 or torch.bfloat16, got {t.dtype}")
@@ -120,36 +134,41 @@ def _list(tensors: Sequence[torch.Tensor], name: str, dev: int):
     return ptrs, sizes, dtypes
 
 
+def _norm_out(need: int, device, result: bool):
+    return (torch.empty((1,), dtype=torch.float32, device=device) if result else None,
+            torch.empty((need,), dtype=torch.uint8, device=device))
+
+
 def _norm_call(grads, out, max_norm, norm, stream):
     grads = list(grads)
     dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
     ptrs, sizes, dtypes = _list(grads, "grads", dev)
-    n, device = len(grads), torch.device("cuda", dev) if dev >= 0 else None
-    if device is None:
+    if dev < 0:
         raise ValueError("gradients must be CUDA tensors (the library has no CPU path)")
-    if norm is None:
-        norm = _new((1,), torch.float32, device, stream)
-    P, I64, I32 = ctypes.c_void_p * n, ctypes.c_int64 * n, ctypes.c_int * n
-    src, count, types = P(*ptrs), I64(*sizes), I32(*[_TYPES[t] for t in dtypes])
+    n = len(grads)
+    written = ptrs
+    if out is not None:
+        out = list(out)
+        written, out_sizes, out_dtypes = _list(out, "out", dev)
+        if out_sizes != sizes or out_dtypes != dtypes:
+            raise ValueError("out must have the sizes and types of grads")
+    if max_norm is not None and len(set(written)) != n and len({p for p, k in zip(written, sizes) if k}) != sum(1 for k in sizes if k):
+        raise ValueError("a tensor is listed twice: it would be scaled twice")
     need = lib().moe_grad_norm_workspace_size(n)
-    ws, raw = _new((need,), torch.uint8, device, stream), _raw_stream(stream, dev)
-    res = _arg(norm, "norm", torch.float32, (1,), dev)
+    new, ws = _on(stream, _norm_out, need, torch.device("cuda", dev), norm is None)
+    res = new.data_ptr() if norm is None else _arg(norm, "norm", torch.float32, (1,), dev)
+    # (the arrays live until the call is over: the library reads them during the call only)
+    src, count, types = array("Q", ptrs), array("q", sizes), array("i", map(_TYPES.__getitem__, dtypes))
+    lists, raw = (src.buffer_info()[0], count.buffer_info()[0], types.buffer_info()[0]), _raw_stream(stream, dev)
     if max_norm is None:
-        code = lib().moe_grad_norm(src, count, types, n, res, ws.data_ptr(), need, raw)
+        code = lib().moe_grad_norm(*lists, n, res, ws.data_ptr(), need, raw)
     else:
-        dst, written = None, ptrs
-        if out is not None:
-            out = list(out)
-            written, out_sizes, out_dtypes = _list(out, "out", dev)
-            if out_sizes != sizes or out_dtypes != dtypes:
-                raise ValueError("out must have the sizes and types of grads")
-            dst = P(*written)
-        if len(set(written)) != n and len({p for p, k in zip(written, sizes) if k}) != sum(1 for k in sizes if k):
-            raise ValueError("a tensor is listed twice: it would be scaled twice")
-        code = lib().moe_clip_grad_norm(src, dst, count, types, n, max_norm, res, ws.data_ptr(), need, raw)
+        dst = None if out is None else array("Q", written)
+        code = lib().moe_clip_grad_norm(lists[0], None if dst is None else dst.buffer_info()[0], *lists[1:], n, max_norm,
+                                        res, ws.data_ptr(), need, raw)
     if code:
         _check(code, "moe_grad_norm" if max_norm is None else "moe_clip_grad_norm")
-    return norm
+    return new if norm is None else norm
 
 
 def grad_norm(grads: Sequence[torch.Tensor], out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
