@@ -141,7 +141,7 @@ def lib():
     L.moe_rms_norm.restype = I32
     L.moe_rms_norm_backward_workspace_size.argtypes = [I64, I32]
     L.moe_rms_norm_backward_workspace_size.restype = SZ
-    L.moe_rms_norm_backward.argtypes = [P, P, P, I32, P, P, P, I64, I32, P, P, P, SZ, P]
+    L.moe_rms_norm_backward.argtypes = [P, P, P, I32, P, P, P, I64, I32, P, P, P, P, SZ, P]
     L.moe_rms_norm_backward.restype = I32
     L.moe_grad_norm_workspace_size.argtypes = [I32]
     L.moe_grad_norm_workspace_size.restype = SZ

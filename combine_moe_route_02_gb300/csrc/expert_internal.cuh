@@ -321,6 +321,7 @@ struct RmsNormBackwardArgs {
     void *dX;
     float *dweight;
     void *workspace;             // rms_norm_table_rows(N, H) rows of H floats
+    int32_t *status;
 };
 int rms_norm_table_rows(int64_t N, int H);
 cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs &a, cudaStream_t stream);

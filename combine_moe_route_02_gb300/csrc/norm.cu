@@ -32,7 +32,33 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8])
     return v;
 }
 
+// In pairs, for the packed arithmetic.
+__device__ __forceinline__ void unpack2(const uint4 &x, float2 (&f)[4])
+{
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint4 pack2(const float2 (&f)[4])
+{
+    uint4 v;
+    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[i].x, f[i].y);
+    return v;
+}
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+
 // Chunk c of the weight.
+__device__ __forceinline__ void load_weight2(const void *w, int bf16, int c, float2 (&f)[4])
+{
+    if (bf16) {
+        unpack2(__ldg(static_cast<const uint4 *>(w) + c), f);
+    } else {
+        const float4 a = __ldg(static_cast<const float4 *>(w) + 2 * c), b = __ldg(static_cast<const float4 *>(w) + 2 * c + 1);
+        f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w), f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
+    }
+}
 __device__ __forceinline__ void load_weight(const void *w, int bf16, int c, float (&f)[8])
 {
     if (bf16) {
@@ -45,7 +71,6 @@ __device__ __forceinline__ void load_weight(const void *w, int bf16, int c, floa
 
 constexpr int kWarpRows = 4;      // rows of a CTA where a row is a warp's
 constexpr int kMostThreads = 512;
-constexpr int kTwoThreads = 384;  // the most with two chunks each
 
 // The sum over the threads of a row, the same in each of them.  `part`: a float for each warp; a second call takes
 // another array.
@@ -145,126 +170,184 @@ __global__ void __launch_bounds__(kMostThreads) rms_norm_kernel(const Forward p)
 }
 
 // ---------------------------------------------------------------------------
-// Gradient.  A CTA takes rows blockIdx.x, + gridDim.x, ... (a warp's rows: kWarpRows at a time): its threads keep to
-// their columns and sum dy xh for them.  kFlush rows at a time are summed in registers, those sums in shared memory,
-// and the CTA's own row of the workspace's table is their sum; a second launch adds the table's rows up.  The order
-// is the same in every call.
+// Gradient.  A CTA takes groups of rows blockIdx.x, + gridDim.x, ... (a group is a row, or kWarpRows rows of a warp
+// each): its threads keep to their columns and sum dy xh for them.  The rows come through a ring in shared memory, each
+// input's as one bulk copy, so that what all CTAs of an SM have under way is most of its shared memory whatever the
+// registers hold.  kFlush groups at a time are summed in registers, those sums in the CTA's own row of the workspace's
+// table (a warp's: in shared memory); a second launch adds the table's rows up.  The order is the same in every call.
 // ---------------------------------------------------------------------------
 constexpr int kFlush = 64;
+constexpr int kSlots = 8;
 
 struct Backward {
-    const uint4 *dY, *S, *dS;
+    const uint8_t *dY, *S, *dS;
     const void *w;
     const float *rstd;
     int64_t N;
-    int H, w_bf16;
+    int H, w_bf16, slots;
     uint4 *dX;
     float *table;                 // [gridDim.x][H]
+    int32_t *status;
 };
 
 template <bool kWarp, int kV>
-__global__ void __launch_bounds__(kV <= 2 ? kTwoThreads : kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backward_kernel(const Backward p)
+__global__ void __launch_bounds__(kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backward_kernel(const Backward p)
 {
     __shared__ float part[2][kMostThreads / 32];
-    extern __shared__ float sums[];       // [kV][8][threads], so that neighbouring threads are neighbours
+    __shared__ float sums[kWarp ? kV * 8 * 32 * kWarpRows : 1];      // [kV][8][threads]
+    __shared__ uint64_t full[kSlots];
+    __shared__ volatile int abort;
+    extern __shared__ __align__(128) uint8_t ring[];
     const int T = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x & 31 : threadIdx.x, chunks = p.H >> 3;
-    const int rows = kWarp ? kWarpRows : 1;
+    constexpr int rows = kWarp ? kWarpRows : 1;
+    const uint32_t array = rows * p.H * 2, inputs = p.dS ? 3 : 2, stage = array * inputs;
+    const int64_t groups = (p.N + rows - 1) / rows, mine = (groups - blockIdx.x + gridDim.x - 1) / gridDim.x;
     const float of_H = static_cast<float>(p.H);
-    float acc[kV][8];
+    float *table = p.table + static_cast<int64_t>(blockIdx.x) * p.H;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], 1);
+        abort = 0;
+        fence_mbarrier_init();
+    }
+    __syncthreads();
+    const auto issue = [&](int64_t i, int slot) {
+        const int64_t r = (blockIdx.x + i * gridDim.x) * rows, left = p.N - r;
+        const uint32_t bytes = static_cast<uint32_t>(left < rows ? left : rows) * p.H * 2;
+        const int64_t at = r * p.H * 2;
+        uint8_t *to = ring + slot * stage;
+        mbar_arrive_expect_tx(&full[slot], bytes * inputs);
+        bulk_load(to, p.dY + at, bytes, &full[slot]);
+        bulk_load(to + array, p.S + at, bytes, &full[slot]);
+        if (p.dS) bulk_load(to + 2 * array, p.dS + at, bytes, &full[slot]);
+    };
+    if (threadIdx.x == 0)
+        for (int i = 0; i < p.slots && i < mine; ++i) issue(i, i);
+
+    float2 acc[kV][4];
 #pragma unroll
     for (int j = 0; j < kV; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            acc[j][i] = 0.f;
-            sums[(j * 8 + i) * blockDim.x + threadIdx.x] = 0.f;
+        for (int i = 0; i < 4; ++i) {
+            acc[j][i] = twice(0.f);
+            if (kWarp) sums[(j * 8 + 2 * i) * blockDim.x + threadIdx.x] = sums[(j * 8 + 2 * i + 1) * blockDim.x + threadIdx.x] = 0.f;
         }
-    int n = 0;
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * rows; r < p.N; r += static_cast<int64_t>(gridDim.x) * rows, ++n) {
-        const int64_t row = kWarp ? r + (threadIdx.x >> 5) : r;
-        const bool row_ok = row < p.N;
-        const int64_t base = (row_ok ? row : p.N - 1) * chunks;
-        uint4 dy[kV], s[kV], ds[kV];
+    const auto flush = [&](bool first) {
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
             const int c = t + T * j;
-            dy[j] = s[j] = ds[j] = make_uint4(0, 0, 0, 0);
-            if (c < chunks) {
-                dy[j] = __ldcs(p.dY + base + c);
-                s[j] = __ldcs(p.S + base + c);
-                if (p.dS) ds[j] = __ldcs(p.dS + base + c);
+            if constexpr (kWarp) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sums[(j * 8 + 2 * i) * blockDim.x + threadIdx.x] += acc[j][i].x;
+                    sums[(j * 8 + 2 * i + 1) * blockDim.x + threadIdx.x] += acc[j][i].y;
+                }
+            } else if (c < chunks) {
+                float4 *dst = reinterpret_cast<float4 *>(table) + 2 * c;
+                float4 a = make_float4(acc[j][0].x, acc[j][0].y, acc[j][1].x, acc[j][1].y), b = make_float4(acc[j][2].x, acc[j][2].y, acc[j][3].x, acc[j][3].y);
+                if (!first) {
+                    const float4 x = dst[0], y = dst[1];
+                    a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+                    b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
+                }
+                dst[0] = a;
+                dst[1] = b;
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[j][i] = twice(0.f);
         }
+    };
+    int slot = 0, before = 0, n = 0;
+    uint32_t phase = 0;
+    bool first = true;
+    for (int64_t g = 0; g < mine; ++g, ++n) {
+        const int64_t row = (blockIdx.x + g * gridDim.x) * rows + (kWarp ? threadIdx.x >> 5 : 0);
+        const bool row_ok = !kWarp || row < p.N;
         const float rstd = p.rstd[row_ok ? row : p.N - 1];
         if (n == kFlush) {
+            flush(first);
+            first = false;
             n = 0;
-#pragma unroll
-            for (int j = 0; j < kV; ++j)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    sums[(j * 8 + i) * blockDim.x + threadIdx.x] += acc[j][i];
-                    acc[j][i] = 0.f;
-                }
         }
-        float dot = 0.f;
+        // (a wait that ran out sets `abort`: the loop goes on without copies and without waiting, in step)
+        mbar_wait_bounded(&full[slot], phase, &abort);
+        const uint8_t *at = ring + slot * stage + (kWarp ? (threadIdx.x >> 5) * p.H * 2 : 0);
+        const uint4 *dy = reinterpret_cast<const uint4 *>(at), *s = reinterpret_cast<const uint4 *>(at + array),
+                    *ds = reinterpret_cast<const uint4 *>(at + 2 * array);
+        // dy s, whose sum with the weights has a factor rstd to go, twice
+        float2 dot = twice(0.f);
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
             const int c = t + T * j;
-            float a[8], b[8], w[8];
-            unpack(dy[j], a);
-            unpack(s[j], b);
-            load_weight(p.w, p.w_bf16, c < chunks ? c : chunks - 1, w);
+            if (c < chunks && row_ok) {
+                float2 a[4], b[4], w[4];
+                unpack2(dy[c], a);
+                unpack2(s[c], b);
+                load_weight2(p.w, p.w_bf16, c, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float v = a[i] * (b[i] * rstd);
-                dot = fmaf(v, w[i], dot);
-                if (row_ok) acc[j][i] += v;
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = __fmul2_rn(a[i], b[i]);
+                    dot = __ffma2_rn(v, w[i], dot);
+                    acc[j][i] = __ffma2_rn(v, twice(rstd), acc[j][i]);
+                }
             }
         }
-        const float mean = row_sum<kWarp>(dot, part[n & 1]) / of_H;
+        if (kWarp) __syncthreads();
+        const float by = -rstd * (rstd * (rstd * (row_sum<kWarp>(dot.x + dot.y, part[n & 1]) / of_H)));
+        // every thread is past that barrier, so none reads the group before any more: its place is filled again
+        if (threadIdx.x == 0 && g > 0 && g - 1 + p.slots < mine && !abort) issue(g - 1 + p.slots, before);
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
             const int c = t + T * j;
-            if (c >= chunks) break;
-            float a[8], b[8], e[8], w[8];
-            unpack(dy[j], a);
-            unpack(s[j], b);
-            unpack(ds[j], e);
-            load_weight(p.w, p.w_bf16, c, w);
+            if (c < chunks && row_ok) {
+                float2 a[4], b[4], e[4], w[4];
+                unpack2(dy[c], a);
+                unpack2(s[c], b);
+                unpack2(p.dS ? ds[c] : make_uint4(0, 0, 0, 0), e);
+                load_weight2(p.w, p.w_bf16, c, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) a[i] = fmaf(rstd, a[i] * w[i] - b[i] * rstd * mean, e[i]);
-            if (row_ok) p.dX[base + c] = pack(a);
+                for (int i = 0; i < 4; ++i)
+                    a[i] = __ffma2_rn(__fmul2_rn(a[i], w[i]), twice(rstd), __ffma2_rn(b[i], twice(by), e[i]));
+                p.dX[row * chunks + c] = pack2(a);
+            }
+        }
+        before = slot;
+        if (++slot == p.slots) {
+            slot = 0;
+            phase ^= 1u;
         }
     }
     pdl_launch_dependents();
-#pragma unroll
-    for (int j = 0; j < kV; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[j][i] += sums[(j * 8 + i) * blockDim.x + threadIdx.x];
+    flush(first);
     if constexpr (kWarp) {
         // the warps' sums, added by the first
         __syncthreads();
+        if (threadIdx.x < 32) {
 #pragma unroll
-        for (int j = 0; j < kV; ++j)
+            for (int j = 0; j < kV; ++j) {
+                const int c = t + T * j;
+                float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sums[(j * 8 + i) * blockDim.x + threadIdx.x] = acc[j][i];
-        __syncthreads();
-        if (threadIdx.x >= 32) return;
+                for (int i = 0; i < 8; ++i) {
+                    v[i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kV; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                acc[j][i] = 0.f;
-#pragma unroll
-                for (int k = 0; k < kWarpRows; ++k) acc[j][i] += sums[(j * 8 + i) * blockDim.x + threadIdx.x + 32 * k];
+                    for (int k = 0; k < kWarpRows; ++k) v[i] += sums[(j * 8 + i) * blockDim.x + t + 32 * k];
+                }
+                if (c < chunks) {
+                    float4 *dst = reinterpret_cast<float4 *>(table) + 2 * c;
+                    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+                }
             }
+        }
     }
-#pragma unroll
-    for (int j = 0; j < kV; ++j) {
-        const int c = t + T * j;
-        if (c >= chunks) break;
-        float4 *dst = reinterpret_cast<float4 *>(p.table + static_cast<int64_t>(blockIdx.x) * p.H) + 2 * c;
-        dst[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-        dst[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+    if (threadIdx.x == 0 && abort) {
+        report_status(p.status, MOE_ERR_TIMEOUT);
+        // what may still be under way lands before this CTA's memory is another's
+        for (int i = 0; i < p.slots; ++i) {
+            volatile int no_abort = 0;
+            mbar_wait_bounded(&full[i], phase ^ (i < slot ? 1u : 0u), &no_abort);
+        }
     }
 }
 
@@ -297,7 +380,7 @@ __global__ void __launch_bounds__(kSumThreads) rms_norm_dweight_kernel(const flo
 }
 
 // How a row of H columns is held: a warp of one or two chunks a lane up to 512 columns, else as many threads, whole
-// warps, as two chunks each (beyond 6144 columns four) make of it.
+// warps, as two chunks each (beyond 8192 columns four) make of it.
 struct Shape {
     bool warp;
     int per, threads;
@@ -306,7 +389,7 @@ Shape shape_of(int H)
 {
     const int chunks = H / 8;
     if (chunks <= 64) return Shape{true, chunks <= 32 ? 1 : 2, 32 * kWarpRows};
-    const int per = chunks <= 2 * kTwoThreads ? 2 : 4;
+    const int per = chunks <= 2 * kMostThreads ? 2 : 4;
     return Shape{false, per, ((chunks + per - 1) / per + 31) / 32 * 32};
 }
 
@@ -339,13 +422,41 @@ cudaError_t launch_rms_norm(const RmsNormArgs &a, cudaStream_t stream)
     return cudaGetLastError();
 }
 
+namespace {
+// CTAs of the gradient on an SM: 64 registers a thread (128 where a thread has four chunks), eight at most (a warp's
+// rows: six, so that the ring of each has two places).
+int resident(const Shape &f)
+{
+    const int fit = (f.per <= 2 ? 1024 : 512) / f.threads, most = f.warp ? 6 : 8;
+    return fit < most ? fit : most;
+}
+
+template <bool kWarp, int kV>
+cudaError_t launch_gradient(Backward &p, const Shape &f, int grid, int dev, cudaStream_t stream)
+{
+    // an SM's shared memory but for what the CTAs hold besides (1 KiB of the system's, the kernel's own), in equal parts
+    const int ctas = resident(f), own = 1024 + 512 + (kWarp ? kV * 8 * 32 * kWarpRows * 4 : 0);
+    const int stage = (kWarp ? kWarpRows : 1) * p.H * 2 * (p.dS ? 3 : 2);
+    const int part = ((ctas == 1 ? 227 * 1024 : 228 * 1024 / ctas) - own) / stage;
+    p.slots = part < kSlots ? part : kSlots;          // two at least, whatever H is
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        const cudaError_t err = cudaFuncSetAttribute(rms_norm_backward_kernel<kWarp, kV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     227 * 1024 - own);
+        if (err != cudaSuccess) return err;
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    rms_norm_backward_kernel<kWarp, kV><<<grid, f.threads, p.slots * stage, stream>>>(p);
+    return cudaGetLastError();
+}
+}  // namespace
+
 int rms_norm_table_rows(int64_t N, int H)
 {
-    // as many CTAs as the 152 SMs of a GB300 hold at 80 registers a thread (128 where a thread has four chunks), eight
-    // an SM at most, and no more than there are rows for.  (Of 65536 x 4096 and 16381 x 1032, bursts: 351 and 39 us; with
-    // 64 registers, 4/3 of the threads and some spills 368 and 42; with 96 registers 415 and 42.)
+    // as many CTAs as the 152 SMs of a GB300 hold, and no more than there are rows for
     const Shape f = shape_of(H);
-    const int fit = (f.per <= 2 ? 2 * kTwoThreads : 512) / f.threads, most = 152 * (fit < 8 ? fit : 8);
+    const int most = 152 * resident(f);
     const int64_t n = f.warp ? (N + kWarpRows - 1) / kWarpRows : N;
     return static_cast<int>(n < most ? n : most);
 }
@@ -353,12 +464,12 @@ int rms_norm_table_rows(int64_t N, int H)
 cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs &a, cudaStream_t stream)
 {
     int dev = 0;
-    const cudaError_t err = expert_device(&dev);
+    cudaError_t err = expert_device(&dev);
     if (err != cudaSuccess) return err;
     Backward p;
-    p.dY = static_cast<const uint4 *>(a.dY);
-    p.S = static_cast<const uint4 *>(a.S);
-    p.dS = static_cast<const uint4 *>(a.dS);
+    p.dY = static_cast<const uint8_t *>(a.dY);
+    p.S = static_cast<const uint8_t *>(a.S);
+    p.dS = static_cast<const uint8_t *>(a.dS);
     p.w = a.weight;
     p.rstd = a.rstd;
     p.N = a.N;
@@ -366,31 +477,18 @@ cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs &a, cudaStream_t 
     p.w_bf16 = a.w_bf16;
     p.dX = static_cast<uint4 *>(a.dX);
     p.table = static_cast<float *>(a.workspace);
+    p.status = a.status;
     const int grid = rms_norm_table_rows(a.N, a.H);
-    cudaLaunchConfig_t cfg = {};
-    cfg.stream = stream;
     if (grid > 0) {
         const Shape f = shape_of(a.H);
-        const auto kernel = f.warp ? (f.per == 1 ? rms_norm_backward_kernel<true, 1> : rms_norm_backward_kernel<true, 2>)
-                                   : (f.per == 2 ? rms_norm_backward_kernel<false, 2> : rms_norm_backward_kernel<false, 4>);
-        cfg.gridDim = dim3(grid);
-        cfg.blockDim = dim3(f.threads);
-        cfg.dynamicSmemBytes = f.per * 8 * f.threads * sizeof(float);
-        if (cfg.dynamicSmemBytes > 48 * 1024) {
-            static std::atomic<uint64_t> done{0};
-            const uint64_t bit = 1ull << (dev & 63);
-            if (!(done.load(std::memory_order_relaxed) & bit)) {
-                const cudaError_t e = cudaFuncSetAttribute(rms_norm_backward_kernel<false, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
-                if (e != cudaSuccess) return e;
-                done.fetch_or(bit, std::memory_order_relaxed);
-            }
-        }
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
-        if (e != cudaSuccess) return e;
+        err = f.warp ? (f.per == 1 ? launch_gradient<true, 1>(p, f, grid, dev, stream) : launch_gradient<true, 2>(p, f, grid, dev, stream))
+                     : (f.per == 2 ? launch_gradient<false, 2>(p, f, grid, dev, stream) : launch_gradient<false, 4>(p, f, grid, dev, stream));
+        if (err != cudaSuccess) return err;
     }
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
     cfg.gridDim = dim3((a.H + 31) / 32);
     cfg.blockDim = dim3(kSumThreads);
-    cfg.dynamicSmemBytes = 0;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

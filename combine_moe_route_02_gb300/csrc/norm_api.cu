@@ -42,17 +42,17 @@ size_t moe_rms_norm_backward_workspace_size(int64_t N, int H)
 
 moe_status moe_rms_norm_backward(const void *dY, const void *S, const void *weight, int weight_type, const float *rstd,
                                  const void *dS, const float *add, int64_t N, int H, void *dX, float *dweight,
-                                 void *workspace, size_t workspace_bytes, moe_stream_t stream)
+                                 int32_t *status_word, void *workspace, size_t workspace_bytes, moe_stream_t stream)
 {
     NvtxRange nvtx_range("moe_rms_norm_backward");
     if (!sizes_ok(N, H) || !type_ok(weight_type)) return MOE_ERR_INVALID_ARG;
     if (!dweight || (N > 0 && (!dY || !S || !weight || !rstd || !dX))) return MOE_ERR_INVALID_ARG;
     if (!aligned(dY, 16) || !aligned(S, 16) || !aligned(weight, 16) || !aligned(dS, 16) || !aligned(dX, 16) ||
-        !aligned(rstd, 4) || !aligned(add, 4) || !aligned(dweight, 4))
+        !aligned(rstd, 4) || !aligned(add, 4) || !aligned(dweight, 4) || !aligned(status_word, 4))
         return MOE_ERR_MISALIGNED;
     if (N > 0 && (!workspace || workspace_bytes < moe_rms_norm_backward_workspace_size(N, H))) return MOE_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return MOE_ERR_MISALIGNED;
-    RmsNormBackwardArgs a{dY, S, dS, weight, rstd, add, N, H, weight_type == MOE_GRAD_BF16, dX, dweight, workspace};
+    RmsNormBackwardArgs a{dY, S, dS, weight, rstd, add, N, H, weight_type == MOE_GRAD_BF16, dX, dweight, workspace, status_word};
     return launched(launch_rms_norm_backward(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

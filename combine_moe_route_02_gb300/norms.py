@@ -21,7 +21,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import _check, _need, _scale_dtype, _scale_format, lib
+from . import _check, _need, _scale_dtype, _scale_format, _status_ptr, lib
 from .experts import BLOCK, _arg, _dims, _home, _on, _opt, _ptr, _raw_stream
 
 __all__ = ["rms_norm", "rms_norm_backward", "grad_norm", "clip_grad_norm", "RMSNorm", "RMSNormGrad"]
@@ -97,7 +97,7 @@ def _rms_grad_out(dY: torch.Tensor, H: int, need: int, results: bool):
 
 def rms_norm_backward(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
                       dS: Optional[torch.Tensor] = None, add: Optional[torch.Tensor] = None,
-                      out: Optional[RMSNormGrad] = None, stream=None) -> RMSNormGrad:
+                      out: Optional[RMSNormGrad] = None, status=None, stream=None) -> RMSNormGrad:
     """Gradient of rms_norm from its S and rstd: dX (of X and of the residual alike; dS, the gradient that reaches S
     through the stream, is added) and dweight float32 [H] = add + the sum over the rows."""
     N, H = _dims(dY, "dY", 2)
@@ -112,7 +112,8 @@ def rms_norm_backward(dY: torch.Tensor, S: torch.Tensor, weight: torch.Tensor, r
         out, dx, dw = new, new.dX.data_ptr(), new.dweight.data_ptr()
     else:
         dx, dw = _arg(out.dX, "dX", torch.bfloat16, (N, H), dev), _arg(out.dweight, "dweight", torch.float32, (H,), dev)
-    code = lib().moe_rms_norm_backward(dy, s, w, wt, r, ds, added, N, H, dx, dw, ws.data_ptr(), need, _raw_stream(stream, dev))
+    code = lib().moe_rms_norm_backward(dy, s, w, wt, r, ds, added, N, H, dx, dw, _status_ptr(status), ws.data_ptr(), need,
+                                       _raw_stream(stream, dev))
     if code:
         _check(code, "moe_rms_norm_backward")
     return out

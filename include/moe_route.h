@@ -576,11 +576,12 @@ MOE_API size_t moe_rms_norm_backward_workspace_size(int64_t N, int H);
  *   workspace  moe_rms_norm_backward_workspace_size() bytes, 16-byte aligned, in any state; calls that
  *              may overlap need their own
  * N == 0 writes dweight (add, or zeros).  Sizes as moe_rms_norm.  Two launches.
- * Errors: as moe_rms_norm, and MOE_ERR_WORKSPACE.
+ * Errors: as moe_rms_norm, and MOE_ERR_WORKSPACE; status_word: MOE_ERR_TIMEOUT.
  */
 MOE_API moe_status moe_rms_norm_backward(const void *dY, const void *S, const void *weight, int weight_type,
                              const float *rstd, const void *dS, const float *add, int64_t N, int H,
-                             void *dX, float *dweight, void *workspace, size_t workspace_bytes, moe_stream_t stream);
+                             void *dX, float *dweight, int32_t *status_word,
+                             void *workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* Bytes of device workspace moe_grad_norm and moe_clip_grad_norm need for n tensors. */
 MOE_API size_t moe_grad_norm_workspace_size(int n);
