@@ -186,9 +186,10 @@ def test_rms_norm_backward(dev, N, H, stream, add, wt):  # noqa: F811
         want = want + ds.double()
         slack = slack + 2 * U * want.abs()
     within(g.dX, want, slack)
-    # 64 rows at a time, those sums, four rows of a warp's CTA, then 16 sums of the table's rows: at most 608 / 16
+    # 64 rows at a time, those sums (a CTA has at least N / 608 rows where it has more than one), four rows of a warp's
+    # CTA, then the table's rows (at most 1216) as 32 x 8 sums
     each = N / 608
-    depth = min(each + 1, 64) + each / 64 + 4 + 608 / 16 + 16 + 2
+    depth = min(each + 1, 64) + each / 64 + 4 + 1216 / 256 + 3 + 32 + 2
     dw, mag = (dy.double() * xh).sum(0), (dy.double() * xh).abs().sum(0)
     if add:
         dw, mag = dw + base.double(), mag + base.double().abs()
