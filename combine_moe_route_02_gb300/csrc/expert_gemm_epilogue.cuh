@@ -114,12 +114,6 @@ __device__ __forceinline__ int lane_token(int lane) { return (lane >> 3) * 8 + (
 // What the lane of token s of this lane's eight holds.
 __device__ __forceinline__ uint32_t of_token(uint32_t word, int s, int lane) { return __shfl_sync(kAll, word, 4 * s + (lane & 3)); }
 
-// The larger of each of three bytes.
-__device__ __forceinline__ uint32_t max_bytes(uint32_t a, uint32_t b)
-{
-    return __vmaxu2(a & 0x00FF00FFu, b & 0x00FF00FFu) | max(a & 0xFF00u, b & 0xFF00u);
-}
-
 // Two tokens at a time (i = 0, 1): the values of feature r of chunk column c, and codes of features r = 0 and 1 of
 // both tokens, the first token's in the low half.
 __device__ __forceinline__ float2 both(const float (&v)[32], int at) { return make_float2(v[at], v[at + 1]); }
@@ -260,7 +254,7 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
                 }
             }
             uint32_t word = block_scale_byte(max_of_lanes(ma, lane));
-            if (keep) word |= block_scale_byte(max_of_lanes(mg, lane)) << 8 | block_scale_byte(max_of_lanes(mu, lane)) << 16;
+            if (keep) word |= block_scale_byte(max_of_lanes(mu, lane)) << 16 | block_scale_byte(max_of_lanes(mg, lane)) << 24;
             // eight warps' words for each token; a buffer is written again two chunks later, when the words of the
             // chunk between have come from every warp, which each sent after it had read this one
             const uint32_t slot = words + (n & 1) * 1024;
@@ -270,27 +264,32 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
             send_word(to, word, smem_u32(bar), 0);
             send_word(to, word, smem_u32(bar), 1);
             ok = mbar_wait_bounded(bar, (n >> 1) & 1, &tail.abort);
-            word = 0;
+            // the top byte is the largest word's, the two others are compared as halves
+            uint32_t top = 0, halves = 0;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) word = max_bytes(word, lds32(slot + (k * 32 + tok) * 4));
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t x = lds32(slot + (k * 32 + tok) * 4);
+                top = max(top, x);
+                halves = __vmaxu2(halves, x & 0x00FF00FFu);
+            }
+            const uint32_t ba = halves & 0xFFu, bu = halves >> 16, bg = top >> 24;
             if (e.rank == 0 && c0 + tok < t.rows) {
                 const int64_t row = t.row0 + c0 + tok;
-                if (w == 0) store_scale(p.A_scale, p.out_ue8m0, row * nb + fb, word & 0xFFu);
-                if (keep && w == 1) store_scale(p.K_scale, p.out_ue8m0, row * 2 * nb + fb, (word >> 8) & 0xFFu);
-                if (keep && w == 2) store_scale(p.K_scale, p.out_ue8m0, (row * 2 + 1) * nb + fb, word >> 16);
+                if (w == 0) store_scale(p.A_scale, p.out_ue8m0, row * nb + fb, ba);
+                if (keep && w == 1) store_scale(p.K_scale, p.out_ue8m0, row * 2 * nb + fb, bg);
+                if (keep && w == 2) store_scale(p.K_scale, p.out_ue8m0, (row * 2 + 1) * nb + fb, bu);
             }
-            word = 0x00FEFEFEu - word;                 // the exponents of the scales' reciprocals (no byte is above 254)
+            // the scales' reciprocals: a's, and as two bf16 numbers g's and u's
+            const uint32_t ra = __float_as_uint(scale_reciprocal(ba)), rgu = (254u - bg) << 7 | (254u - bu) << 23;
             uint32_t q[3][4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const uint32_t t0 = of_token(word, 2 * c, lane), t1 = of_token(word, 2 * c + 1, lane);
-                const auto inv = [&](int left) {
-                    return make_float2(__uint_as_float(t0 << left & 0x7F800000u), __uint_as_float(t1 << left & 0x7F800000u));
-                };
-                const float2 ia = inv(23);
+                const float2 ia = make_float2(__uint_as_float(of_token(ra, 2 * c, lane)), __uint_as_float(of_token(ra, 2 * c + 1, lane)));
                 q[0][c] = codes_of(__fmul2_rn(a[c][0], ia), __fmul2_rn(a[c][1], ia));
                 if (keep) {
-                    const float2 ig = inv(15), iu = inv(7);
+                    const uint32_t t0 = of_token(rgu, 2 * c, lane), t1 = of_token(rgu, 2 * c + 1, lane);
+                    const float2 ig = make_float2(__uint_as_float(t0 << 16), __uint_as_float(t1 << 16));
+                    const float2 iu = make_float2(__uint_as_float(t0 & 0xFFFF0000u), __uint_as_float(t1 & 0xFFFF0000u));
                     q[1][c] = codes_of(__fmul2_rn(both(v, 4 * c), ig), __fmul2_rn(both(v, 4 * c + 2), ig));
                     q[2][c] = codes_of(__fmul2_rn(both(v, 16 + 4 * c), iu), __fmul2_rn(both(v, 18 + 4 * c), iu));
                 }
