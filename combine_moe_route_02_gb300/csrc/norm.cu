@@ -190,6 +190,9 @@ struct Backward {
     int32_t *status;
 };
 
+// (out of line, for the loop's sake)
+__device__ __noinline__ void wait_slow(uint64_t *bar, uint32_t phase, volatile int *abort) { mbar_wait_bounded(bar, phase, abort); }
+
 template <bool kWarp, int kV>
 __global__ void __launch_bounds__(kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backward_kernel(const Backward p)
 {
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__(kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backwa
     constexpr int rows = kWarp ? kWarpRows : 1;
     const uint32_t array = rows * p.H * 2, inputs = p.dS ? 3 : 2, stage = array * inputs;
     const int64_t groups = (p.N + rows - 1) / rows, mine = (groups - blockIdx.x + gridDim.x - 1) / gridDim.x;
-    const float of_H = static_cast<float>(p.H);
+    const float per_H = 1.f / static_cast<float>(p.H);
     float *table = p.table + static_cast<int64_t>(blockIdx.x) * p.H;
 
     if (threadIdx.x == 0) {
@@ -260,18 +263,21 @@ __global__ void __launch_bounds__(kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backwa
     int slot = 0, before = 0, n = 0;
     uint32_t phase = 0;
     bool first = true;
-    for (int64_t g = 0; g < mine; ++g, ++n) {
-        const int64_t row = (blockIdx.x + g * gridDim.x) * rows + (kWarp ? threadIdx.x >> 5 : 0);
+    int64_t row = static_cast<int64_t>(blockIdx.x) * rows + (kWarp ? threadIdx.x >> 5 : 0);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
+    uint4 *dx = p.dX + row * chunks + t;
+    const uint8_t *own = ring + (kWarp ? (threadIdx.x >> 5) * p.H * 2 : 0) + t * 16;
+    for (int64_t g = 0; g < mine; ++g, ++n, row += step, dx += step * chunks) {
         const bool row_ok = !kWarp || row < p.N;
-        const float rstd = p.rstd[row_ok ? row : p.N - 1];
+        const float rstd = __ldg(p.rstd + (row_ok ? row : p.N - 1));
         if (n == kFlush) {
             flush(first);
             first = false;
             n = 0;
         }
         // (a wait that ran out sets `abort`: the loop goes on without copies and without waiting, in step)
-        mbar_wait_bounded(&full[slot], phase, &abort);
-        const uint8_t *at = ring + slot * stage + (kWarp ? (threadIdx.x >> 5) * p.H * 2 : 0);
+        if (!mbar_try_wait(smem_u32(&full[slot]), phase)) wait_slow(&full[slot], phase, &abort);
+        const uint8_t *at = own + slot * stage;
         const uint4 *dy = reinterpret_cast<const uint4 *>(at), *s = reinterpret_cast<const uint4 *>(at + array),
                     *ds = reinterpret_cast<const uint4 *>(at + 2 * array);
         // dy s, whose sum with the weights has a factor rstd to go, twice
@@ -281,8 +287,8 @@ __global__ void __launch_bounds__(kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backwa
             const int c = t + T * j;
             if (c < chunks && row_ok) {
                 float2 a[4], b[4], w[4];
-                unpack2(dy[c], a);
-                unpack2(s[c], b);
+                unpack2(dy[T * j], a);
+                unpack2(s[T * j], b);
                 load_weight2(p.w, p.w_bf16, c, w);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -293,7 +299,7 @@ __global__ void __launch_bounds__(kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backwa
             }
         }
         if (kWarp) __syncthreads();
-        const float by = -rstd * (rstd * (rstd * (row_sum<kWarp>(dot.x + dot.y, part[n & 1]) / of_H)));
+        const float by = -rstd * (rstd * (rstd * (row_sum<kWarp>(dot.x + dot.y, part[n & 1]) * per_H)));
         // every thread is past that barrier, so none reads the group before any more: its place is filled again
         if (threadIdx.x == 0 && g > 0 && g - 1 + p.slots < mine && !abort) issue(g - 1 + p.slots, before);
 #pragma unroll
@@ -301,14 +307,14 @@ __global__ void __launch_bounds__(kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backwa
             const int c = t + T * j;
             if (c < chunks && row_ok) {
                 float2 a[4], b[4], e[4], w[4];
-                unpack2(dy[c], a);
-                unpack2(s[c], b);
-                unpack2(p.dS ? ds[c] : make_uint4(0, 0, 0, 0), e);
+                unpack2(dy[T * j], a);
+                unpack2(s[T * j], b);
+                unpack2(p.dS ? ds[T * j] : make_uint4(0, 0, 0, 0), e);
                 load_weight2(p.w, p.w_bf16, c, w);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     a[i] = __ffma2_rn(__fmul2_rn(a[i], w[i]), twice(rstd), __ffma2_rn(b[i], twice(by), e[i]));
-                p.dX[row * chunks + c] = pack2(a);
+                dx[T * j] = pack2(a);
             }
         }
         before = slot;
@@ -351,30 +357,38 @@ __global__ void __launch_bounds__(kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backwa
     }
 }
 
-// dw = the sum of the table's rows (+ add): 32 columns a CTA, 32 threads for the rows of each, eight sums a thread (the
-// table of 16381 x 1032 has 1216 rows: with 16 threads and four sums the loads' latency was 13 of the call's 38 us).
+// dw = the sum of the table's rows (+ add): 8 columns a CTA (a sector of each row), 128 threads for the rows of each,
+// eight sums a thread, so that the whole table is asked for in a round or two by a CTA on most SMs.
 constexpr int kSumThreads = 1024;
 
 __global__ void __launch_bounds__(kSumThreads) rms_norm_dweight_kernel(const float *__restrict__ table, int rows, int H, const float *add, float *dw)
 {
-    constexpr int kStep = kSumThreads / 32, kEach = 8;
-    __shared__ float part[kStep][32];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
+    constexpr int kStep = kSumThreads / 8, kEach = 8;
+    __shared__ float part[kSumThreads / 32][8];
+    const int c = blockIdx.x * 8 + (threadIdx.x & 7), k = threadIdx.x >> 3;      // (H is whole in 8)
     pdl_wait_prior_grids();
     float v[kEach] = {};
-    if (c < H) {
-        const float *at = table + c;
-        for (int r = k; r < rows; r += kEach * kStep)
+    const float *at = table + c;
+    for (int r = k; r < rows; r += kEach * kStep) {
+        // (no condition on the loads, which would make them wait for one another)
+        float x[kEach];
 #pragma unroll
-            for (int i = 0; i < kEach; ++i)
-                if (r + i * kStep < rows) v[i] += at[static_cast<int64_t>(r + i * kStep) * H];
+        for (int i = 0; i < kEach; ++i) {
+            const int of = r + i * kStep;
+            x[i] = at[static_cast<int64_t>(of < rows ? of : r) * H];
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) v[i] += r + i * kStep < rows ? x[i] : 0.f;
     }
-    part[k][threadIdx.x & 31] = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    float sum = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    sum += __shfl_xor_sync(kFull, sum, 8);
+    sum += __shfl_xor_sync(kFull, sum, 16);
+    if ((threadIdx.x & 31) < 8) part[threadIdx.x >> 5][threadIdx.x & 7] = sum;
     __syncthreads();
-    if (k == 0 && c < H) {
-        float sum = 0.f;
+    if (threadIdx.x < 8) {
+        sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kStep; ++i) sum += part[i][threadIdx.x];
+        for (int i = 0; i < kSumThreads / 32; ++i) sum += part[i][threadIdx.x];
         dw[c] = add ? add[c] + sum : sum;
     }
 }
@@ -487,7 +501,7 @@ cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs &a, cudaStream_t 
     }
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
-    cfg.gridDim = dim3((a.H + 31) / 32);
+    cfg.gridDim = dim3(a.H / 8);
     cfg.blockDim = dim3(kSumThreads);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
