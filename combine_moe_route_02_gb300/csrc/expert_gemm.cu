@@ -25,7 +25,7 @@
 //   warps 2, 3 and the last two  scale producers: gather the bytes of 16 128-blocks per row; warp 3
 //               allocates TMEM
 //   warps 4..7  epilogue: TMEM -> registers -> bf16, transposed through shared memory; with the gated
-//               activation or its gradient (expert_gemm_epilogue.cuh) warps 4..15
+//               activation or its gradient (expert_gemm_epilogue.cuh) the warps from 4 on
 //
 // Measured (burst, 1.94 GHz): 16384 tokens on 128 experts, top 8, 2048 x 2048: 354 us, 3.1 PFLOP/s, the
 // tensor pipe 67% busy; the rest is the latency of a ring that 180 KiB in flight per SM do not quite cover
@@ -67,7 +67,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
             mbar_init(&tail.acc_full[b], 1);
             mbar_init(&tail.acc_empty[b], 8 * teams(kMode));
         }
-        for (int i = 0; i < kTeams; ++i) {
+        for (int i = 0; i < teams(kGated); ++i) {
             mbar_init(&tail.words[i][0], 1);
             mbar_init(&tail.words[i][1], 1);
         }
@@ -460,9 +460,9 @@ cudaError_t launch(Params &p, const void *X, const void *W, int rows, int cols, 
 
     CUtensorMap tmY = tmW;
     if (kMode == kGatedGrad && p.Y) {
-        // a warp's 32 features of 32 tokens
+        // a warp's 32 features of a chunk's tokens
         const uint64_t yd[2] = {2 * static_cast<uint64_t>(p.I), static_cast<uint64_t>(p.R)};
-        const uint32_t yb[2] = {32, 32};
+        const uint32_t yb[2] = {32, chunk_tokens(kGatedGrad)};
         if (!encode_map(&tmY, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.Y, 2, yd, yb, CU_TENSOR_MAP_SWIZZLE_64B))
             return cudaErrorInvalidValue;
     }

@@ -89,14 +89,16 @@ __device__ __forceinline__ bool team_all(int team, bool ok)
     return r != 0;
 }
 
-// The teams take a tile's chunks in turn, and with every tile another team begins (a tile of 7 chunks is 3, 2 and 2).
+// The teams take a tile's chunks in turn, and with every tile another team begins (kGated: a tile of 7 chunks is 3, 2
+// and 2).
+template <Mode kMode>
 struct Chunks {
+    static constexpr int kStep = teams(kMode) * chunk_tokens(kMode);
     int first;
     __device__ __forceinline__ explicit Chunks(int team) : first(team) {}
-    __device__ __forceinline__ void next() { first = first == 0 ? kTeams - 1 : first - 1; }
-    __device__ __forceinline__ int begin() const { return first * 32; }
+    __device__ __forceinline__ void next() { first = first == 0 ? teams(kMode) - 1 : first - 1; }
+    __device__ __forceinline__ int begin() const { return first * chunk_tokens(kMode); }
 };
-constexpr int kChunkStep = kTeams * 32;
 
 // The largest of m[s] over the eight lanes that share tokens: lane l is left with that of s = l / 4, which is token
 // lane_token(l).
@@ -116,7 +118,7 @@ __device__ __forceinline__ uint32_t of_token(uint32_t word, int s, int lane) { r
 
 // Two tokens at a time (i = 0, 1): the values of feature r of chunk column c, and codes of features r = 0 and 1 of
 // both tokens, the first token's in the low half.
-__device__ __forceinline__ float2 both(const float (&v)[32], int at) { return make_float2(v[at], v[at + 1]); }
+__device__ __forceinline__ float2 both(const float *v, int at) { return make_float2(v[at], v[at + 1]); }
 __device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
 __device__ __forceinline__ uint32_t codes_of(float2 r0, float2 r1)
 {
@@ -223,7 +225,8 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
     int j = 0;
     uint32_t n = 0;                                    // this team's chunks
     bool ok = true;
-    Chunks chunks(team);
+    Chunks<kGated> chunks(team);
+    constexpr int kChunkStep = Chunks<kGated>::kStep;
     for (Walk walk(e.pair, p.m_tiles); walk.tile < e.tiles; walk.next(e.pairs, p.m_tiles), chunks.next(), ++j) {
         const Tile t = walk.get(tail);
         const int b = j & 1, fb = t.m0 / kTileM;       // its block of 128 features
@@ -321,39 +324,84 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
 // The activation's gradient: the product is da; g and u come from the checkpoint (codes and scales).
 //   s = 1 / (1 + exp(-g));  dg = da u s (1 + g (1 - s));  du = da g s
 // in bf16 and in E4M3.  A CTA's 128 features are a block, its scale bytes are joined over a team's four warps.
+//
+// Chunks of 16 tokens (c = 0, 1; element 8 h + 4 c + 2 r + i of a lane) keep a warp within 96 registers, so that four
+// teams fit: the work of a chunk is a chain of short steps, and what hides their latency is the number of warps.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ void load_fragments16(uint32_t taddr, float (&v)[16])
+{
+    uint32_t r[16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[8 * h]), "=r"(r[8 * h + 1]), "=r"(r[8 * h + 2]), "=r"(r[8 * h + 3]), "=r"(r[8 * h + 4]),
+                       "=r"(r[8 * h + 5]), "=r"(r[8 * h + 6]), "=r"(r[8 * h + 7])
+                     : "r"(taddr + (static_cast<uint32_t>(16 * h) << 16))
+                     : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// As store_transposed(), of 16 tokens.
+__device__ __forceinline__ void store_transposed16(uint32_t buf, int lane, const float (&v)[16])
+{
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        uint32_t m[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            const int at = 8 * (f >> 1) + 4 * c + 2 * (f & 1);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[at], v[at + 1]);
+            m[f] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        const int t = 8 * c + (lane & 7), f = lane >> 3;
+        store_rows(buf + t * 64 + ((f ^ ((t >> 1) & 3)) << 4), m);
+    }
+}
+
+// As max_of_lanes(), of four tokens: lane l is left with that of s = l / 8 (as lane l ^ 4 is).
+__device__ __forceinline__ float max_of_lanes4(const float (&m)[4], int lane)
+{
+    const bool h16 = lane & 16, h8 = lane & 8;
+    const float a = fmaxf(h16 ? m[2] : m[0], __shfl_xor_sync(kAll, h16 ? m[0] : m[2], 16));
+    const float b = fmaxf(h16 ? m[3] : m[1], __shfl_xor_sync(kAll, h16 ? m[1] : m[3], 16));
+    const float c = fmaxf(h8 ? b : a, __shfl_xor_sync(kAll, h8 ? a : b, 8));
+    return fmaxf(c, __shfl_xor_sync(kAll, c, 4));
+}
+
 __device__ __forceinline__ void gated_grad_epilogue(const Params &p, const CUtensorMap &tmY, Tail &tail, const EpilogueWarp &e)
 {
-    const int team = e.team, w = e.w, lane = e.lane, tok = lane_token(lane);
-    const uint32_t rows = smem_u32(e.epi) + (team * 4 + w) * 4096;                       // bf16 rows of both halves, for the TMA
-    const uint32_t buf = smem_u32(e.epi) + kTeams * 4 * 4096 + (team * 4 + w) * 2048;    // codes
-    const uint32_t words = smem_u32(e.epi) + stage_bytes(kGatedGrad) + team * 2 * 512;
+    constexpr int kTok = chunk_tokens(kGatedGrad), kChunkStep = Chunks<kGatedGrad>::kStep;
+    const int team = e.team, w = e.w, lane = e.lane;
+    const int tok = (lane >> 4) * 8 + (lane & 3) * 2 + ((lane >> 3) & 1);       // the token of s = lane / 8
+    const uint32_t rows = smem_u32(e.epi) + (team * 4 + w) * 2048;       // bf16 rows of both halves, for the TMA
+    const uint32_t buf = smem_u32(e.epi) + teams(kGatedGrad) * 4 * 2048 + (team * 4 + w) * 1024;    // codes
+    const uint32_t words = smem_u32(e.epi) + stage_bytes(kGatedGrad) + team * 2 * 4 * kTok * 4;
     const uint32_t lane_addr = e.tmem + (static_cast<uint32_t>(w * 32) << 16);
     const int nb = p.I / kBlk;
     const int64_t pitch = 2 * static_cast<int64_t>(p.I);
-    // E4M3 rows are read and written by two lanes for a token's 32 features
+    // E4M3 rows are read and written by two lanes for a token's 32 features; in shared memory the 16-byte pieces of
+    // the gate's features 0..15, 16..31, the up half's: 16 tokens of each
     const int k_tok = lane >> 1, k_half = lane & 1;
+    const uint32_t k_at = buf + k_half * 256 + k_tok * 16, m_at = buf + (lane >> 4) * 256 + (lane & 15) * 16;
     uint32_t n = 0;
     bool bad = false;
-    uint4 kg[2], ku[2];
+    uint4 kg = make_uint4(0, 0, 0, 0), ku = kg;
     uint32_t sg = 0, su = 0;
     // A chunk's part of the checkpoint is asked for while the chunk before is worked on, across tiles too.
     const auto fetch = [&](const Tile &t, int c0) {
         const int fb = t.m0 / kBlk + e.rank;
         if (fb >= nb || c0 >= t.rows) return;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = c0 + k_tok + 16 * i;
-            const uint8_t *k = p.K + (t.row0 + (r < t.rows ? r : t.rows - 1)) * pitch + fb * kBlk + w * 32 + k_half * 16;
-            kg[i] = __ldcs(reinterpret_cast<const uint4 *>(k));
-            ku[i] = __ldcs(reinterpret_cast<const uint4 *>(k + p.I));
-        }
-        const int r = c0 + lane;
-        const int64_t at = (t.row0 + (r < t.rows ? r : t.rows - 1)) * 2 * nb + fb;
+        const int r = c0 + k_tok;
+        const uint8_t *k = p.K + (t.row0 + (r < t.rows ? r : t.rows - 1)) * pitch + fb * kBlk + w * 32 + k_half * 16;
+        kg = __ldcs(reinterpret_cast<const uint4 *>(k));
+        ku = __ldcs(reinterpret_cast<const uint4 *>(k + p.I));
+        const int q = c0 + (lane & 15);
+        const int64_t at = (t.row0 + (q < t.rows ? q : t.rows - 1)) * 2 * nb + fb;
         sg = load_scale_bits(p.K_scale, p.k_ue8m0, at);
         su = load_scale_bits(p.K_scale, p.k_ue8m0, at + nb);
     };
-    Chunks chunks(team);
+    Chunks<kGatedGrad> chunks(team);
     Walk walk(e.pair, p.m_tiles);
     Tile next{};
     if (walk.tile < e.tiles) {
@@ -377,27 +425,24 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, const CUten
         }
         for (int c0 = begin; c0 < t.rows; c0 += kChunkStep, ++n) {
             const bool last = c0 + kChunkStep >= t.rows;
-            float du[32], dg[32];
-            tmem_ld_fragments(lane_addr + b * kTileN + c0, du);
+            float du[16], dg[16];
+            load_fragments16(lane_addr + b * kTileN + c0, du);
             __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                sts128(buf + k_half * 512 + (k_tok + 16 * i) * 16, in_pairs(kg[i]));
-                sts128(buf + 1024 + k_half * 512 + (k_tok + 16 * i) * 16, in_pairs(ku[i]));
-            }
+            sts128(k_at, in_pairs(kg));
+            sts128(k_at + 512, in_pairs(ku));
             // both scales as bf16 numbers
             const uint32_t scales = __float_as_uint(scale_value(scale_bits_byte(sg, p.k_ue8m0, bad))) >> 16 |
                                     (__float_as_uint(scale_value(scale_bits_byte(su, p.k_ue8m0, bad))) & 0xFFFF0000u);
             __syncwarp();
-            uint32_t k[2][2][4];                       // [gate, up][h][c]
-#pragma unroll
-            for (int x = 0; x < 4; ++x) load_rows(buf + x * 512 + lane * 16, k[x >> 1][x & 1]);
+            uint32_t k[2][4];                          // [gate, up][2 h + c]
+            load_rows(m_at, k[0]);
+            load_rows(m_at + 512, k[1]);
             fetch(last ? next : t, last ? chunks.begin() : c0 + kChunkStep);
             tmem_ld_wait();
             if (last) release_accumulator(tail, b, lane);
-            float mg[8], mu[8];
+            float mg[4], mu[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
                 const uint32_t t0 = __shfl_sync(kAll, scales, 8 * c + 2 * (lane & 3)), t1 = __shfl_sync(kAll, scales, 8 * c + 2 * (lane & 3) + 1);
                 const float2 gs = make_float2(__uint_as_float(t0 << 16), __uint_as_float(t1 << 16));
                 const float2 us = make_float2(__uint_as_float(t0 & 0xFFFF0000u), __uint_as_float(t1 & 0xFFFF0000u));
@@ -405,10 +450,10 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, const CUten
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     // the two tokens' codes of r = 0, then of r = 1
-                    const uint32_t kg4 = __byte_perm(k[0][h][c], 0, 0x3120), ku4 = __byte_perm(k[1][h][c], 0, 0x3120);
+                    const uint32_t kg4 = __byte_perm(k[0][2 * h + c], 0, 0x3120), ku4 = __byte_perm(k[1][2 * h + c], 0, 0x3120);
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const int x = 16 * h + 4 * c + 2 * r;
+                        const int x = 8 * h + 4 * c + 2 * r;
                         const float2 g = __fmul2_rn(e4m3x2_to_f32x2(r ? kg4 >> 16 : kg4 & 0xFFFFu), gs);
                         const float2 u = __fmul2_rn(e4m3x2_to_f32x2(r ? ku4 >> 16 : ku4 & 0xFFFFu), us);
                         const float2 s = sigmoid2(g), as = __fmul2_rn(both(du, x), s);
@@ -421,34 +466,34 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, const CUten
                     }
                 }
             }
-            const uint32_t slot = words + (n & 1) * 512;
-            if (p.Q) sts32(slot + (w * 32 + tok) * 4, block_scale_byte(max_of_lanes(mg, lane)) | block_scale_byte(max_of_lanes(mu, lane)) << 16);
+            const uint32_t slot = words + (n & 1) * 4 * kTok * 4;
+            if (p.Q) sts32(slot + (w * kTok + tok) * 4, block_scale_byte(max_of_lanes4(mg, lane)) | block_scale_byte(max_of_lanes4(mu, lane)) << 16);
             if (p.Y) {
                 if (lane == 0) bulk_wait_read<0>();    // the chunk before
                 __syncwarp();
-                store_transposed(rows, lane, dg);
-                store_transposed(rows + 2048, lane, du);
+                store_transposed16(rows, lane, dg);
+                store_transposed16(rows + 1024, lane, du);
                 const int f = fb * kBlk + w * 32;
-                if (c0 + 32 <= t.rows) {
+                if (c0 + kTok <= t.rows) {
                     // whole: two boxes (pieces of 16 bytes lie as the TMA's swizzle of 64 bytes has them)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
                         const int32_t r = static_cast<int32_t>(t.row0) + c0;
                         tma_store_2d(&tmY, rows, f, r);
-                        tma_store_2d(&tmY, rows + 2048, f + p.I, r);
+                        tma_store_2d(&tmY, rows + 1024, f + p.I, r);
                         bulk_commit();
                     }
                 } else {
                     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.Y) + (t.row0 + c0 + (lane >> 2)) * pitch + f + (lane & 3) * 8;
                     __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         const int at = i * 8 + (lane >> 2);
                         const uint32_t y = rows + at * 64 + (((lane & 3) ^ ((at >> 1) & 3)) << 4);
                         if (c0 + at < t.rows) {
                             *reinterpret_cast<uint4 *>(dst + 8 * i * pitch) = lds128(y);
-                            *reinterpret_cast<uint4 *>(dst + 8 * i * pitch + p.I) = lds128(y + 2048);
+                            *reinterpret_cast<uint4 *>(dst + 8 * i * pitch + p.I) = lds128(y + 1024);
                         }
                     }
                 }
@@ -458,37 +503,32 @@ __device__ __forceinline__ void gated_grad_epilogue(const Params &p, const CUten
                 named_barrier_sync(2 + team, 128);
                 uint32_t word = 0;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) word = __vmaxu2(word, lds32(slot + (x * 32 + tok) * 4));
-                if (c0 + tok < t.rows && w < 2)
+                for (int x = 0; x < 4; ++x) word = __vmaxu2(word, lds32(slot + (x * kTok + tok) * 4));
+                if (c0 + tok < t.rows && w < 2 && !(lane & 4))
                     store_scale(p.Q_scale, p.out_ue8m0, (t.row0 + c0 + tok) * 2 * nb + w * nb + fb, w ? word >> 16 : word & 0xFFu);
                 word = (0x00FE00FEu - word) << 7;      // the scales' reciprocals as bf16 numbers
-                uint32_t q[2][2][4];
+                uint32_t q[2][4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t t0 = of_token(word, 2 * c, lane), t1 = of_token(word, 2 * c + 1, lane);
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t t0 = __shfl_sync(kAll, word, 16 * c + (lane & 3)), t1 = __shfl_sync(kAll, word, 16 * c + 8 + (lane & 3));
                     const float2 ig = make_float2(__uint_as_float(t0 << 16), __uint_as_float(t1 << 16));
                     const float2 iu = make_float2(__uint_as_float(t0 & 0xFFFF0000u), __uint_as_float(t1 & 0xFFFF0000u));
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int x = 16 * h + 4 * c;
-                        q[0][h][c] = codes_of(__fmul2_rn(both(dg, x), ig), __fmul2_rn(both(dg, x + 2), ig));
-                        q[1][h][c] = codes_of(__fmul2_rn(both(du, x), iu), __fmul2_rn(both(du, x + 2), iu));
+                        const int x = 8 * h + 4 * c;
+                        q[0][2 * h + c] = codes_of(__fmul2_rn(both(dg, x), ig), __fmul2_rn(both(dg, x + 2), ig));
+                        q[1][2 * h + c] = codes_of(__fmul2_rn(both(du, x), iu), __fmul2_rn(both(du, x + 2), iu));
                     }
                 }
                 __syncwarp();
-#pragma unroll
-                for (int x = 0; x < 4; ++x) store_rows(buf + x * 512 + lane * 16, q[x >> 1][x & 1]);
+                store_rows(m_at, q[0]);
+                store_rows(m_at + 512, q[1]);
                 __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int at = k_tok + 16 * i;
-                    const uint4 yg = in_order(lds128(buf + k_half * 512 + at * 16));
-                    const uint4 yu = in_order(lds128(buf + 1024 + k_half * 512 + at * 16));
-                    if (c0 + at < t.rows) {
-                        uint8_t *dst = p.Q + (t.row0 + c0 + at) * pitch + fb * kBlk + w * 32 + k_half * 16;
-                        *reinterpret_cast<uint4 *>(dst) = yg;
-                        *reinterpret_cast<uint4 *>(dst + p.I) = yu;
-                    }
+                const uint4 yg = in_order(lds128(k_at)), yu = in_order(lds128(k_at + 512));
+                if (c0 + k_tok < t.rows) {
+                    uint8_t *dst = p.Q + (t.row0 + c0 + k_tok) * pitch + fb * kBlk + w * 32 + k_half * 16;
+                    *reinterpret_cast<uint4 *>(dst) = yg;
+                    *reinterpret_cast<uint4 *>(dst + p.I) = yu;
                 }
             }
         }
