@@ -68,6 +68,7 @@ moe_status check_list(const void *const *grads, void *const *out, const int64_t 
         if (bytes > int64_t(1) << 44 || (sizes[i] > 0 && (!grads[i] || (out && !out[i])))) return MOE_ERR_INVALID_ARG;
     }
     for (int i = 0; i < n; ++i) {
+        if (sizes[i] == 0) continue;
         const uintptr_t by = types[i] == MOE_GRAD_BF16 ? 2 : 4;
         if (!aligned(grads[i], by) || (out && !aligned(out[i], by))) return MOE_ERR_MISALIGNED;
     }
