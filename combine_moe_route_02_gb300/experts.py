@@ -6,17 +6,17 @@ for weights.  A training step of one layer's MLP::
 
     W1q, W1s = quantize_weight(W1)                     # after each optimizer step
     d  = dispatch(idx, E, X, fp8=True, bf16=False)
-    gu = expert_gemm(d.X_fp8, d.X_scale, W1q, W1s, d.expert_offsets)
-    h  = swiglu(gu)                                    # gu itself is not needed any more
+    h  = expert_swiglu(d.X_fp8, d.X_scale, W1q, W1s, d.expert_offsets)
     y  = expert_gemm(h.A_fp8, h.A_scale, W2q, W2s, d.expert_offsets)
     ...
-    dA  = expert_gemm(dY_fp8, dY_scale, W2q, W2s, d.expert_offsets, transpose=True)
+    b   = expert_swiglu_backward(dY_fp8, dY_scale, W2q, W2s, h.GU_fp8, h.GU_scale, d.expert_offsets)
     dW2 = expert_wgrad(dY, h.A_fp8, h.A_scale, d.expert_offsets)
-    b   = swiglu_backward(dA, h.GU_fp8, h.GU_scale)
     dX  = expert_gemm(b.dGU_fp8, b.dGU_scale, W1q, W1s, d.expert_offsets, transpose=True)
     dW1 = expert_wgrad(b.dGU, d.X_fp8, d.X_scale, d.expert_offsets)
 
-Kept from the forward to the backward pass: E4M3 rows only.  For serving a few tokens,
+Kept from the forward to the backward pass: E4M3 rows only.  ``expert_swiglu`` is ``expert_gemm`` and ``swiglu`` in
+one launch, ``expert_swiglu_backward`` the transposed ``expert_gemm`` and ``swiglu_backward``; what the single calls
+round to bf16 between them stays in 32 bits there.  For serving a few tokens,
 ``moe_layer`` is the whole layer in one launch.
 
 With ``stream`` a call launches there, and what it allocates is that stream's memory, as under

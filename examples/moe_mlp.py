@@ -27,8 +27,7 @@ def forward(X, W_gate, K, W1q, W2q):
     E = W_gate.shape[1]
     idx, w = moe.route(X, W_gate, K)
     d = moe.dispatch(idx, E, X, fp8=True, bf16=False, scale_format="ue8m0")
-    gu = moe.expert_gemm(d.X_fp8, d.X_scale, *W1q, d.expert_offsets)
-    h = moe.swiglu(gu, scale_format="ue8m0")
+    h = moe.expert_swiglu(d.X_fp8, d.X_scale, *W1q, d.expert_offsets, scale_format="ue8m0")
     y = moe.expert_gemm(h.A_fp8, h.A_scale, *W2q, d.expert_offsets)
     return moe.combine(y, d.row_map, w), (d, h, w)
 
@@ -43,8 +42,7 @@ def backward(dout, saved, W1q, W2q, dW1=None, dW2=None):
     dY = (dout[slot // K].float() * w.flatten()[slot, None]).to(torch.bfloat16)
     rows = torch.arange(dY.shape[0], dtype=torch.int32, device=dY.device)
     dY8, dY8s = moe.permute(dY, rows, K=1, fp8=True, bf16=False, scale_format="ue8m0")[1:3]
-    dA = moe.expert_gemm(dY8, dY8s, *W2q, off, transpose=True)
-    g = moe.swiglu_backward(dA, h.GU_fp8, h.GU_scale, scale_format="ue8m0")
+    g = moe.expert_swiglu_backward(dY8, dY8s, *W2q, h.GU_fp8, h.GU_scale, off, scale_format="ue8m0")
     dW2 = moe.expert_wgrad(dY, h.A_fp8, h.A_scale, off, add=dW2, out=dW2)
     dW1 = moe.expert_wgrad(g.dGU, d.X_fp8, d.X_scale, off, add=dW1, out=dW1)
     dXr = moe.expert_gemm(g.dGU_fp8, g.dGU_scale, *W1q, off, transpose=True)
