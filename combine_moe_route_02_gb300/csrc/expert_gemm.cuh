@@ -22,9 +22,12 @@ constexpr int kScaleSlotBytes = 4 * kScaleQuadBytes;
 // input), or the activation's gradient (the product is the gradient of its output).
 enum Mode { kPlain, kGated, kGatedGrad };
 // The activation's modes have teams of four epilogue warps, which take chunks of tokens in turn, and one team of scale
-// producers instead of two.  kGated: three teams and chunks of 32 tokens, 16 warps, the most that have 128 registers a
-// thread; kGatedGrad: four and 16, 20 warps of 96 (16384 tokens, 128 experts, H = 2048, I = 1024, back to back: 321 us; three
-// teams and 32 tokens 344, five teams and 80 registers 355).
+// producers instead of two.  What a chunk costs is a chain of short steps, so the number of warps decides, and that goes by
+// their registers.  kGated: three teams and chunks of 32 tokens, 16 warps, the most that have 128 registers a thread (16384
+// tokens, 128 experts, H = 2048, I = 1024 / 16381 tokens of H = 1024, I = 2048 without checkpoint, graphs of 20 passes:
+// 433 / 134 us; chunks of 16 tokens and four teams 452 / 169, three 461 / 169, five 468 / 181: the exchange of words
+// is paid for each chunk).  kGatedGrad, where no words cross the CTAs: four and 16, 20 warps of 96 (the first case: 321; three teams and
+// 32 tokens 344, five teams and 80 registers 355).
 constexpr int teams(Mode m) { return m == kPlain ? 1 : m == kGated ? 3 : 4; }
 constexpr int chunk_tokens(Mode m) { return m == kGatedGrad ? 16 : 32; }
 constexpr int scale_teams(Mode m) { return m == kPlain ? 2 : 1; }

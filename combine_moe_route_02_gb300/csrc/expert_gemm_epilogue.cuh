@@ -209,6 +209,11 @@ __device__ __forceinline__ void send_word(uint32_t addr, uint32_t word, uint32_t
 // the same 16 of the up half (h = 0 and 1 of the fragments): a lane has both.  A block of 128 features is the pair's
 // eight warps; each finds the scale bytes of its 16 features (the byte of the largest is the largest byte), sends a
 // word of three for each token to both CTAs, and takes the largest of eight.
+//
+// Measured (bursts): 16384 tokens, 128 experts, top 8, H = 2048, I = 1024: 386 to 400 us, 2.75 to 2.85 PFLOP/s, where the
+// product alone with its bf16 rows takes 371 to 390 on the same boxes, and the launch without any epilogue 328; back to back
+// 451 (the board's power).  The tensor pipe is 66% busy, DRAM 59%.  16381 tokens of 64 experts, H = 1024, I = 2048, no
+// checkpoint: 127 (99 without epilogue), 134 back to back: a tile has 8 blocks of reduction, and the epilogue sets the pace.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, const EpilogueWarp &e)
 {
@@ -327,6 +332,9 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
 //
 // Chunks of 16 tokens (c = 0, 1; element 8 h + 4 c + 2 r + i of a lane) keep a warp within 96 registers, so that four
 // teams fit: the work of a chunk is a chain of short steps, and what hides their latency is the number of warps.
+//
+// Measured: 16384 tokens, 128 experts, top 8, H = 2048, I = 1024: 321 us in short graphs, 351 back to back (power), 4.6
+// TB/s of its bytes; without any epilogue 200, the bytes alone 239.  Issue slots 51% busy, DRAM 70%.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void load_fragments16(uint32_t taddr, float (&v)[16])
 {

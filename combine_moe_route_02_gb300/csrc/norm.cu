@@ -5,7 +5,9 @@
 //
 // One pass over the rows: a row stays in the registers of its threads (a warp's for short rows, else a CTA's; kV
 // chunks of 16 bytes each, neighbouring threads neighbouring chunks) between its sum and what is written.  The sums
-// are held in 32 bits.
+// are held in 32 bits.  HBM's bound: 65536 x 4096 with the residual and E4M3 rows 349 us (6.9 TB/s), the gradient of
+// the same 332 (6.5 TB/s); one row 2.4 us in a graph.  The gradient of 16381 x 1032 takes 29 us in a graph where its
+// bytes take 15: some 1100 instructions a row of 129 chunks on three warps (issue slots 57% busy), and the second launch.
 #include "expert_internal.cuh"
 
 namespace moe {
