@@ -6,8 +6,9 @@
 // One pass over the rows: a row stays in the registers of its threads (a warp's for short rows, else a CTA's; kV
 // chunks of 16 bytes each, neighbouring threads neighbouring chunks) between its sum and what is written.  The sums
 // are held in 32 bits.  HBM's bound: 65536 x 4096 with the residual and E4M3 rows 349 us (6.9 TB/s), the gradient of
-// the same 332 (6.5 TB/s); one row 2.4 us in a graph.  The gradient of 16381 x 1032 takes 29 us in a graph where its
-// bytes take 15: some 1100 instructions a row of 129 chunks on three warps (issue slots 57% busy), and the second launch.
+// the same 332 (6.5 TB/s); one row 2.4 us in a graph.  The gradient of 16381 x 1032 takes 27 us in a graph where its
+// bytes take 15: two launches and the ring's start are 7 of it, and a row's 129 chunks are five to a lane, the last nearly
+// empty (H = 1024: 23; three warps to a row: 29; a condition on each chunk's loads: 30).
 #include "expert_internal.cuh"
 
 namespace moe {
@@ -72,6 +73,7 @@ __device__ __forceinline__ void load_weight(const void *w, int bf16, int c, floa
 }
 
 constexpr int kWarpRows = 4;      // rows of a CTA where a row is a warp's
+constexpr int warp_ctas(int per) { return per <= 2 ? 6 : 4; }      // of the gradient's on an SM then
 constexpr int kMostThreads = 512;
 
 // The sum over the threads of a row, the same in each of them.  `part`: a float for each warp; a second call takes
@@ -176,7 +178,8 @@ __global__ void __launch_bounds__(kMostThreads) rms_norm_kernel(const Forward p)
 // each): its threads keep to their columns and sum dy xh for them.  The rows come through a ring in shared memory, each
 // input's as one bulk copy, so that what all CTAs of an SM have under way is most of its shared memory whatever the
 // registers hold.  kFlush groups at a time are summed in registers, those sums in the CTA's own row of the workspace's
-// table (a warp's: in shared memory); a second launch adds the table's rows up.  The order is the same in every call.
+// table (by one warp after the other where a row is a warp's); a second launch adds the table's rows up.  The order is
+// the same in every call.
 // ---------------------------------------------------------------------------
 constexpr int kFlush = 64;
 constexpr int kSlots = 8;
@@ -196,10 +199,9 @@ struct Backward {
 __device__ __noinline__ void wait_slow(uint64_t *bar, uint32_t phase, volatile int *abort) { mbar_wait_bounded(bar, phase, abort); }
 
 template <bool kWarp, int kV>
-__global__ void __launch_bounds__(kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backward_kernel(const Backward p)
+__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMostThreads, kWarp ? warp_ctas(kV) : kV <= 2 ? 2 : 1) rms_norm_backward_kernel(const Backward p)
 {
     __shared__ float part[2][kMostThreads / 32];
-    __shared__ float sums[kWarp ? kV * 8 * 32 * kWarpRows : 1];      // [kV][8][threads]
     __shared__ uint64_t full[kSlots];
     __shared__ volatile int abort;
     extern __shared__ __align__(128) uint8_t ring[];
@@ -233,21 +235,12 @@ __global__ void __launch_bounds__(kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backwa
 #pragma unroll
     for (int j = 0; j < kV; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            acc[j][i] = twice(0.f);
-            if (kWarp) sums[(j * 8 + 2 * i) * blockDim.x + threadIdx.x] = sums[(j * 8 + 2 * i + 1) * blockDim.x + threadIdx.x] = 0.f;
-        }
-    const auto flush = [&](bool first) {
+        for (int i = 0; i < 4; ++i) acc[j][i] = twice(0.f);
+    const auto add_to_table = [&](bool first) {
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
             const int c = t + T * j;
-            if constexpr (kWarp) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    sums[(j * 8 + 2 * i) * blockDim.x + threadIdx.x] += acc[j][i].x;
-                    sums[(j * 8 + 2 * i + 1) * blockDim.x + threadIdx.x] += acc[j][i].y;
-                }
-            } else if (c < chunks) {
+            if (c < chunks) {
                 float4 *dst = reinterpret_cast<float4 *>(table) + 2 * c;
                 float4 a = make_float4(acc[j][0].x, acc[j][0].y, acc[j][1].x, acc[j][1].y), b = make_float4(acc[j][2].x, acc[j][2].y, acc[j][3].x, acc[j][3].y);
                 if (!first) {
@@ -262,6 +255,16 @@ __global__ void __launch_bounds__(kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backwa
             for (int i = 0; i < 4; ++i) acc[j][i] = twice(0.f);
         }
     };
+    const auto flush = [&](bool first) {
+        if constexpr (kWarp) {
+            for (int w = 0; w < kWarpRows; ++w) {
+                if (static_cast<int>(threadIdx.x >> 5) == w) add_to_table(first && w == 0);
+                __syncthreads();
+            }
+        } else {
+            add_to_table(first);
+        }
+    };
     int slot = 0, before = 0, n = 0;
     uint32_t phase = 0;
     bool first = true;
@@ -269,9 +272,11 @@ __global__ void __launch_bounds__(kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backwa
     const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
     uint4 *dx = p.dX + row * chunks + t;
     const uint8_t *own = ring + (kWarp ? (threadIdx.x >> 5) * p.H * 2 : 0) + t * 16;
+    float rstd_next = __ldg(p.rstd + (row < p.N ? row : p.N - 1));       // a group ahead
     for (int64_t g = 0; g < mine; ++g, ++n, row += step, dx += step * chunks) {
         const bool row_ok = !kWarp || row < p.N;
-        const float rstd = __ldg(p.rstd + (row_ok ? row : p.N - 1));
+        const float rstd = rstd_next;
+        rstd_next = __ldg(p.rstd + (row + step < p.N ? row + step : p.N - 1));
         if (n == kFlush) {
             flush(first);
             first = false;
@@ -283,11 +288,14 @@ __global__ void __launch_bounds__(kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backwa
         const uint4 *dy = reinterpret_cast<const uint4 *>(at), *s = reinterpret_cast<const uint4 *>(at + array),
                     *ds = reinterpret_cast<const uint4 *>(at + 2 * array);
         // dy s, whose sum with the weights has a factor rstd to go, twice
+        // (only the last chunk of a thread may not be there: the loads of the others carry no condition, which would make
+        // them wait for one another)
         float2 dot = twice(0.f);
+        if (row_ok) {
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            const int c = t + T * j;
-            if (c < chunks && row_ok) {
+            for (int j = 0; j < kV; ++j) {
+                const int c = t + T * j;
+                if (j + 1 == kV && c >= chunks) break;
                 float2 a[4], b[4], w[4];
                 unpack2(dy[T * j], a);
                 unpack2(s[T * j], b);
@@ -304,10 +312,11 @@ __global__ void __launch_bounds__(kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backwa
         const float by = -rstd * (rstd * (rstd * (row_sum<kWarp>(dot.x + dot.y, part[n & 1]) * per_H)));
         // every thread is past that barrier, so none reads the group before any more: its place is filled again
         if (threadIdx.x == 0 && g > 0 && g - 1 + p.slots < mine && !abort) issue(g - 1 + p.slots, before);
+        if (row_ok) {
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            const int c = t + T * j;
-            if (c < chunks && row_ok) {
+            for (int j = 0; j < kV; ++j) {
+                const int c = t + T * j;
+                if (j + 1 == kV && c >= chunks) break;
                 float2 a[4], b[4], e[4], w[4];
                 unpack2(dy[T * j], a);
                 unpack2(s[T * j], b);
@@ -327,28 +336,6 @@ __global__ void __launch_bounds__(kMostThreads, kV <= 2 ? 2 : 1) rms_norm_backwa
     }
     pdl_launch_dependents();
     flush(first);
-    if constexpr (kWarp) {
-        // the warps' sums, added by the first
-        __syncthreads();
-        if (threadIdx.x < 32) {
-#pragma unroll
-            for (int j = 0; j < kV; ++j) {
-                const int c = t + T * j;
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[i] = 0.f;
-#pragma unroll
-                    for (int k = 0; k < kWarpRows; ++k) v[i] += sums[(j * 8 + i) * blockDim.x + t + 32 * k];
-                }
-                if (c < chunks) {
-                    float4 *dst = reinterpret_cast<float4 *>(table) + 2 * c;
-                    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-                    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-                }
-            }
-        }
-    }
     if (threadIdx.x == 0 && abort) {
         report_status(p.status, MOE_ERR_TIMEOUT);
         // what may still be under way lands before this CTA's memory is another's
@@ -395,8 +382,9 @@ __global__ void __launch_bounds__(kSumThreads) rms_norm_dweight_kernel(const flo
     }
 }
 
-// How a row of H columns is held: a warp of one or two chunks a lane up to 512 columns, else as many threads, whole
-// warps, as two chunks each (beyond 8192 columns four) make of it.
+// How a row of H columns is held: by a warp of up to five chunks a lane up to 1184 columns (the gradient's ring then still
+// has two places for four rows of three inputs in a quarter of an SM), else by as many threads, whole warps, as two chunks
+// each (beyond 8192 columns four) make of it.
 struct Shape {
     bool warp;
     int per, threads;
@@ -404,7 +392,7 @@ struct Shape {
 Shape shape_of(int H)
 {
     const int chunks = H / 8;
-    if (chunks <= 64) return Shape{true, chunks <= 32 ? 1 : 2, 32 * kWarpRows};
+    if (chunks <= 148) return Shape{true, (chunks + 31) / 32, 32 * kWarpRows};
     const int per = chunks <= 2 * kMostThreads ? 2 : 4;
     return Shape{false, per, ((chunks + per - 1) / per + 31) / 32 * 32};
 }
@@ -432,26 +420,27 @@ cudaError_t launch_rms_norm(const RmsNormArgs &a, cudaStream_t stream)
     p.rstd = a.rstd;
     const Shape f = shape_of(a.H);
     const unsigned grid = static_cast<unsigned>(f.warp ? (a.N + kWarpRows - 1) / kWarpRows : a.N);
-    const auto kernel = f.warp ? (f.per == 1 ? rms_norm_kernel<true, 1> : rms_norm_kernel<true, 2>)
-                               : (f.per == 2 ? rms_norm_kernel<false, 2> : rms_norm_kernel<false, 4>);
+    constexpr decltype(&rms_norm_kernel<true, 1>) of_warps[5] = {rms_norm_kernel<true, 1>, rms_norm_kernel<true, 2>, rms_norm_kernel<true, 3>,
+                                                                 rms_norm_kernel<true, 4>, rms_norm_kernel<true, 5>};
+    const auto kernel = f.warp ? of_warps[f.per - 1] : f.per == 2 ? rms_norm_kernel<false, 2> : rms_norm_kernel<false, 4>;
     kernel<<<grid, f.threads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 namespace {
-// CTAs of the gradient on an SM: 64 registers a thread (128 where a thread has four chunks), eight at most (a warp's
-// rows: six, so that the ring of each has two places).
+// CTAs of the gradient on an SM: 64 registers a thread (128 where a thread has four chunks), eight at most; a warp's rows: by
+// warp_ctas().
 int resident(const Shape &f)
 {
-    const int fit = (f.per <= 2 ? 1024 : 512) / f.threads, most = f.warp ? 6 : 8;
-    return fit < most ? fit : most;
+    const int fit = (f.per <= 2 ? 1024 : 512) / f.threads;
+    return f.warp ? warp_ctas(f.per) : fit < 8 ? fit : 8;
 }
 
 template <bool kWarp, int kV>
 cudaError_t launch_gradient(Backward &p, const Shape &f, int grid, int dev, cudaStream_t stream)
 {
     // an SM's shared memory but for what the CTAs hold besides (1 KiB of the system's, the kernel's own), in equal parts
-    const int ctas = resident(f), own = 1024 + 512 + (kWarp ? kV * 8 * 32 * kWarpRows * 4 : 0);
+    const int ctas = resident(f), own = 1024 + 512;
     const int stage = (kWarp ? kWarpRows : 1) * p.H * 2 * (p.dS ? 3 : 2);
     const int part = ((ctas == 1 ? 227 * 1024 : 228 * 1024 / ctas) - own) / stage;
     p.slots = part < kSlots ? part : kSlots;          // two at least, whatever H is
@@ -497,8 +486,10 @@ cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs &a, cudaStream_t 
     const int grid = rms_norm_table_rows(a.N, a.H);
     if (grid > 0) {
         const Shape f = shape_of(a.H);
-        err = f.warp ? (f.per == 1 ? launch_gradient<true, 1>(p, f, grid, dev, stream) : launch_gradient<true, 2>(p, f, grid, dev, stream))
-                     : (f.per == 2 ? launch_gradient<false, 2>(p, f, grid, dev, stream) : launch_gradient<false, 4>(p, f, grid, dev, stream));
+        constexpr decltype(&launch_gradient<true, 1>) of_warps[5] = {launch_gradient<true, 1>, launch_gradient<true, 2>, launch_gradient<true, 3>,
+                                                                     launch_gradient<true, 4>, launch_gradient<true, 5>};
+        const auto launch = f.warp ? of_warps[f.per - 1] : f.per == 2 ? launch_gradient<false, 2> : launch_gradient<false, 4>;
+        err = launch(p, f, grid, dev, stream);
         if (err != cudaSuccess) return err;
     }
     cudaLaunchConfig_t cfg = {};
