@@ -67,10 +67,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
             mbar_init(&tail.acc_full[b], 1);
             mbar_init(&tail.acc_empty[b], 8 * teams(kMode));
         }
-        for (int i = 0; i < teams(kGated); ++i) {
-            mbar_init(&tail.words[i][0], 1);
-            mbar_init(&tail.words[i][1], 1);
-        }
+        for (int i = 0; i < teams(kGated); ++i)
+            for (int k = 0; k < 4; ++k) mbar_init(&tail.words[i][k], 1);
         mbar_init(&tail.drain, 1);
         tail.abort = tail.bad_index = tail.bad_scale = 0;
         fence_mbarrier_init();
@@ -144,7 +142,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
                 uint8_t *a = ring + s * kStageBytes, *b = a + kABytes;
                 if (elect_one()) {
                     mbar_arrive_expect_tx(&tail.full[s], bytes);
-                    if constexpr (kMode == kGated) {
+                    if constexpr (gated(kMode)) {
                         // 16 rows of the gate half, then the same 16 of the up half, four times
 #pragma unroll
                         for (int g = 0; g < 4; ++g)
@@ -275,8 +273,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
                 const int n = blocks - k0;
                 uint32_t feat[4], tok[4][4];
                 if (half == 0) {
-                    // (kGated: lane and row, modulo 32, are a row of the gate half below 16, of the up half from 16)
-                    const int mb = kMode == kGated ? t.m0 / kTileM + (lane < 16 ? 0 : m_blocks >> 1)
+                    // (gated: lane and row, modulo 32, are a row of the gate half below 16, of the up half from 16)
+                    const int mb = gated(kMode) ? t.m0 / kTileM + (lane < 16 ? 0 : m_blocks >> 1)
                                    : t.m0 / kBlk + rank < m_blocks ? t.m0 / kBlk + rank : m_blocks - 1;
                     const int step = p.transpose ? m_blocks : 1;
                     const int64_t at = p.transpose ? static_cast<int64_t>(t.e) * blocks * m_blocks + mb
@@ -369,11 +367,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
             plain_epilogue(p, tail, wp);
         else if constexpr (kMode == kGated)
             gated_epilogue(p, tail, wp);
+        else if constexpr (kMode == kGatedOnly)
+            gated_only_epilogue(p, tail, wp);
         else
             gated_grad_epilogue(p, tmY, tail, wp);
     }
 
-    if constexpr (kMode == kGated) {
+    if constexpr (gated(kMode)) {
         // a CTA that gave up a wait may have words on their way to the other's memory: they have landed long
         // before this time is over
         if (*abort_flag) __nanosleep(1000000);
@@ -431,7 +431,7 @@ bool encode_map(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes, cons
 
 namespace {
 
-// What the three launches share: the tensor maps of the rows and (but for kGated) of the weights, the scales' vector
+// What the three launches share: the tensor maps of the rows and of the weights, the scales' vector
 // width, the grid.
 template <Mode kMode>
 cudaError_t launch(Params &p, const void *X, const void *W, int rows, int cols, cudaStream_t stream)
@@ -447,7 +447,7 @@ cudaError_t launch(Params &p, const void *X, const void *W, int rows, int cols, 
         const uint32_t xb[2] = {kBlk, static_cast<uint32_t>(box_rows(i))};
         if (!encode_map(&tmX.map[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, X, 2, xd, xb)) return cudaErrorInvalidValue;
     }
-    if (kMode == kGated) {
+    if (gated(kMode)) {
         // 16 rows of either half in one box
         const uint64_t wd[5] = {static_cast<uint64_t>(cols), 16, static_cast<uint64_t>(rows / 32), 2, static_cast<uint64_t>(p.E)};
         const uint32_t wb[5] = {kBlk, 16, 1, 2, 1};
@@ -531,7 +531,8 @@ cudaError_t launch_expert_swiglu(const ExpertSwigluArgs &a, cudaStream_t stream)
     p.Q = static_cast<uint8_t *>(a.dGU_fp8);
     p.Q_scale = a.dGU_scale;
     p.status = a.status;
-    return a.backward ? launch<kGatedGrad>(p, a.X, a.W, a.H, a.I, stream) : launch<kGated>(p, a.X, a.W, 2 * a.I, a.H, stream);
+    if (a.backward) return launch<kGatedGrad>(p, a.X, a.W, a.H, a.I, stream);
+    return a.GU ? launch<kGated>(p, a.X, a.W, 2 * a.I, a.H, stream) : launch<kGatedOnly>(p, a.X, a.W, 2 * a.I, a.H, stream);
 }
 
 }  // namespace moe

@@ -19,27 +19,29 @@ constexpr int kScaleQuadBytes = 512 + 1024;   // four blocks: 128 feature words,
 constexpr int kScaleSlotBytes = 4 * kScaleQuadBytes;
 
 // What follows the product: nothing (bf16 rows out), the gated activation (the product is both halves of its
-// input), or the activation's gradient (the product is the gradient of its output).
-enum Mode { kPlain, kGated, kGatedGrad };
+// input) with or without their checkpoint, or the activation's gradient (the product is the gradient of its output).
+enum Mode { kPlain, kGated, kGatedOnly, kGatedGrad };
+constexpr bool gated(Mode m) { return m == kGated || m == kGatedOnly; }
 // The activation's modes have teams of four epilogue warps, which take chunks of tokens in turn, and one team of scale
 // producers instead of two.  What a chunk costs is a chain of short steps, so the number of warps decides, and that goes by
-// their registers.  kGated: three teams and chunks of 32 tokens, 16 warps, the most that have 128 registers a thread (16384
-// tokens, 128 experts, H = 2048, I = 1024 / 16381 tokens of H = 1024, I = 2048 without checkpoint, graphs of 20 passes:
-// 433 / 134 us; chunks of 16 tokens and four teams 452 / 169, three 461 / 169, five 468 / 181: the exchange of words
-// is paid for each chunk).  kGatedGrad, where no words cross the CTAs: four and 16, 20 warps of 96 (the first case: 321; three teams and
+// their registers.  kGated, kGatedOnly: three teams and chunks of 32 tokens, 16 warps, the most that have 128 registers a
+// thread (16384 tokens, 128 experts, H = 2048, I = 1024 / 16381 tokens of H = 1024, I = 2048 without checkpoint, graphs of
+// 20 passes, with kGated's epilogue for both: 433 / 134 us; chunks of 16 tokens and four teams 452 / 169, three 461 / 169,
+// five 468 / 181: the exchange of words is paid for each chunk).  kGatedGrad, where no words cross the CTAs: four and 16, 20 warps of 96 (the first case: 321; three teams and
 // 32 tokens 344, five teams and 80 registers 355).
-constexpr int teams(Mode m) { return m == kPlain ? 1 : m == kGated ? 3 : 4; }
+constexpr int teams(Mode m) { return m == kPlain ? 1 : gated(m) ? 3 : 4; }
 constexpr int chunk_tokens(Mode m) { return m == kGatedGrad ? 16 : 32; }
 constexpr int scale_teams(Mode m) { return m == kPlain ? 2 : 1; }
 constexpr int threads(Mode m) { return 32 * (2 + 2 * scale_teams(m) + 4 * teams(m)); }
 constexpr int stages(Mode m) { return m == kGatedGrad ? 4 : 6; }
 // Staging of the epilogue.  kPlain: 32 tokens x 64 bytes a warp; kGated: three arrays of that (codes of the activation
-// and of both halves) a team; kGatedGrad, 16 tokens: two of 64 bytes for the TMA (bf16 rows of both halves) and two of
-// 32 (codes) a warp.  Then the words in which warps tell each other scales: two buffers in turn for each team, of a
-// word for each token and warp (kGated: of both CTAs).
-constexpr int stage_bytes(Mode m) { return m == kPlain ? 4 * 2048 : m == kGated ? teams(m) * 3 * 2048 : teams(m) * 4 * 3072; }
-constexpr int word_warps(Mode m) { return m == kPlain ? 0 : m == kGated ? 8 : 4; }
-constexpr int epi_bytes(Mode m) { return stage_bytes(m) + teams(m) * 2 * word_warps(m) * chunk_tokens(m) * 4; }
+// and of both halves) a team; kGatedOnly: two in turn; kGatedGrad, 16 tokens: two of 64 bytes for the TMA (bf16 rows of both halves) and two of
+// 32 (codes) a warp.  Then the words in which warps tell each other scales: two buffers in turn for each team (kGatedOnly: four), of a
+// word for each token and warp (but for kGatedGrad of both CTAs).
+constexpr int stage_bytes(Mode m) { return m == kPlain ? 4 * 2048 : m == kGated ? teams(m) * 3 * 2048 : m == kGatedOnly ? teams(m) * 2 * 2048 : teams(m) * 4 * 3072; }
+constexpr int word_buffers(Mode m) { return m == kGatedOnly ? 4 : 2; }
+constexpr int word_warps(Mode m) { return m == kPlain ? 0 : gated(m) ? 8 : 4; }
+constexpr int epi_bytes(Mode m) { return stage_bytes(m) + teams(m) * word_buffers(m) * word_warps(m) * chunk_tokens(m) * 4; }
 constexpr uint32_t kTmemCols = 512;
 // Scales lie behind the two accumulators: 4 + 8 columns for four blocks.  Five places in turn: when one is
 // written again its MMAs have completed, those of the tile before the last by the wait for its accumulator,
@@ -52,7 +54,7 @@ struct Tail {
     uint64_t full[6], empty[6];
     uint64_t sf_full[kScaleSlots], sf_empty[kScaleSlots];
     uint64_t acc_full[2], acc_empty[2], drain;
-    uint64_t words[teams(kGated)][2];    // kGated: the scale words of a team's chunk, two in turn
+    uint64_t words[teams(kGated)][4];    // kGated, kGatedOnly: the scale words of a team's chunk, two or four in turn
     uint32_t tmem_base;
     int abort, bad_index, bad_scale;
     int tiles;                    // token tiles of all groups
@@ -64,7 +66,8 @@ constexpr size_t smem_bytes(Mode m)
 {
     return 1024 + stages(m) * kStageBytes + kScaleSlots * kScaleSlotBytes + epi_bytes(m) + sizeof(Tail);
 }
-static_assert(smem_bytes(kPlain) <= 227 * 1024 && smem_bytes(kGated) <= 227 * 1024 && smem_bytes(kGatedGrad) <= 227 * 1024,
+static_assert(smem_bytes(kPlain) <= 227 * 1024 && smem_bytes(kGated) <= 227 * 1024 &&
+                  smem_bytes(kGatedOnly) <= 227 * 1024 && smem_bytes(kGatedGrad) <= 227 * 1024,
               "shared memory");
 
 // Boxes of token rows: a tile takes the smallest that holds its half, so that a stage is two copies

@@ -212,8 +212,7 @@ __device__ __forceinline__ void send_word(uint32_t addr, uint32_t word, uint32_t
 //
 // Measured (bursts): 16384 tokens, 128 experts, top 8, H = 2048, I = 1024: 386 to 400 us, 2.75 to 2.85 PFLOP/s, where the
 // product alone with its bf16 rows takes 371 to 390 on the same boxes, and the launch without any epilogue 328; back to back
-// 451 (the board's power).  The tensor pipe is 66% busy, DRAM 59%.  16381 tokens of 64 experts, H = 1024, I = 2048, no
-// checkpoint: 127 (99 without epilogue), 134 back to back: a tile has 8 blocks of reduction, and the epilogue sets the pace.
+// 451 (the board's power).  The tensor pipe is 66% busy, DRAM 59%.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, const EpilogueWarp &e)
 {
@@ -226,7 +225,6 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
     const uint32_t take = stage + out_tok * 64 + ((piece ^ ((out_tok >> 1) & 3)) << 4);
     const uint32_t lane_addr = e.tmem + (static_cast<uint32_t>(w * 32) << 16);
     const int nb = p.I / kBlk;
-    const bool keep = p.K != nullptr;
     int j = 0;
     uint32_t n = 0;                                    // this team's chunks
     bool ok = true;
@@ -262,7 +260,7 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
                 }
             }
             uint32_t word = block_scale_byte(max_of_lanes(ma, lane));
-            if (keep) word |= block_scale_byte(max_of_lanes(mu, lane)) << 16 | block_scale_byte(max_of_lanes(mg, lane)) << 24;
+            word |= block_scale_byte(max_of_lanes(mu, lane)) << 16 | block_scale_byte(max_of_lanes(mg, lane)) << 24;
             // eight warps' words for each token; a buffer is written again two chunks later, when the words of the
             // chunk between have come from every warp, which each sent after it had read this one
             const uint32_t slot = words + (n & 1) * 1024;
@@ -284,8 +282,8 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
             if (e.rank == 0 && c0 + tok < t.rows) {
                 const int64_t row = t.row0 + c0 + tok;
                 if (w == 0) store_scale(p.A_scale, p.out_ue8m0, row * nb + fb, ba);
-                if (keep && w == 1) store_scale(p.K_scale, p.out_ue8m0, row * 2 * nb + fb, bg);
-                if (keep && w == 2) store_scale(p.K_scale, p.out_ue8m0, (row * 2 + 1) * nb + fb, bu);
+                if (w == 1) store_scale(p.K_scale, p.out_ue8m0, row * 2 * nb + fb, bg);
+                if (w == 2) store_scale(p.K_scale, p.out_ue8m0, (row * 2 + 1) * nb + fb, bu);
             }
             // the scales' reciprocals: a's, and as two bf16 numbers g's and u's
             const uint32_t ra = __float_as_uint(scale_reciprocal(ba)), rgu = (254u - bg) << 7 | (254u - bu) << 23;
@@ -294,35 +292,127 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
             for (int c = 0; c < 4; ++c) {
                 const float2 ia = make_float2(__uint_as_float(of_token(ra, 2 * c, lane)), __uint_as_float(of_token(ra, 2 * c + 1, lane)));
                 q[0][c] = codes_of(__fmul2_rn(a[c][0], ia), __fmul2_rn(a[c][1], ia));
-                if (keep) {
-                    const uint32_t t0 = of_token(rgu, 2 * c, lane), t1 = of_token(rgu, 2 * c + 1, lane);
-                    const float2 ig = make_float2(__uint_as_float(t0 << 16), __uint_as_float(t1 << 16));
-                    const float2 iu = make_float2(__uint_as_float(t0 & 0xFFFF0000u), __uint_as_float(t1 & 0xFFFF0000u));
-                    q[1][c] = codes_of(__fmul2_rn(both(v, 4 * c), ig), __fmul2_rn(both(v, 4 * c + 2), ig));
-                    q[2][c] = codes_of(__fmul2_rn(both(v, 16 + 4 * c), iu), __fmul2_rn(both(v, 18 + 4 * c), iu));
-                }
+                const uint32_t t0 = of_token(rgu, 2 * c, lane), t1 = of_token(rgu, 2 * c + 1, lane);
+                const float2 ig = make_float2(__uint_as_float(t0 << 16), __uint_as_float(t1 << 16));
+                const float2 iu = make_float2(__uint_as_float(t0 & 0xFFFF0000u), __uint_as_float(t1 & 0xFFFF0000u));
+                q[1][c] = codes_of(__fmul2_rn(both(v, 4 * c), ig), __fmul2_rn(both(v, 4 * c + 2), ig));
+                q[2][c] = codes_of(__fmul2_rn(both(v, 16 + 4 * c), iu), __fmul2_rn(both(v, 18 + 4 * c), iu));
             }
             // (the codes of the chunk before have been read: its words came after that)
             store_rows(put, q[0]);
-            if (keep) {
-                store_rows(put + 2048, q[1]);
-                store_rows(put + 4096, q[2]);
-            }
+            store_rows(put + 2048, q[1]);
+            store_rows(put + 4096, q[2]);
             ok = team_all(team, ok);
             if (!ok) break;
             if (c0 + out_tok < t.rows) {
                 const int64_t row = t.row0 + c0 + out_tok;
                 const int f = fb * kBlk + e.rank * 64 + piece * 16;
                 *reinterpret_cast<uint4 *>(p.A + row * p.I + f) = in_order(lds128(take));
-                if (keep) {
-                    uint8_t *k = p.K + row * 2 * p.I + f;
-                    *reinterpret_cast<uint4 *>(k) = in_order(lds128(take + 2048));
-                    *reinterpret_cast<uint4 *>(k + p.I) = in_order(lds128(take + 4096));
-                }
+                uint8_t *k = p.K + row * 2 * p.I + f;
+                *reinterpret_cast<uint4 *>(k) = in_order(lds128(take + 2048));
+                *reinterpret_cast<uint4 *>(k + p.I) = in_order(lds128(take + 4096));
             }
         }
         if (!ok) break;
     }
+}
+
+// ---------------------------------------------------------------------------
+// Without the checkpoint a lane keeps 16 values of a chunk, and there is room for two chunks: the words of one are on
+// their way while the next is computed, across tiles too.
+//
+// A warp sends chunk n's words before it has read those of n - 1, and after those of n - 2 have come from every warp,
+// which says that every warp has read those of n - 4: four buffers in turn.  The codes of chunk n are put where those of
+// n - 2 lay, which the team has read before its barrier of n - 1: two.
+//
+// Measured: 16381 tokens of 64 experts, H = 1024, I = 2048 (8 blocks of reduction a tile: the epilogue sets the pace): 114 us
+// in bursts, 127 back to back (waiting for each chunk's words at once 127 and 137); 99 and 110 without an epilogue.
+// ---------------------------------------------------------------------------
+struct PendingChunk {
+    float2 a[4][2];
+    int64_t row0;                 // its first row, how many it has, their block of features
+    int rows, fb;
+};
+
+__device__ __forceinline__ bool finish_chunk(const Params &p, Tail &tail, const EpilogueWarp &e, const PendingChunk &c, uint32_t n)
+{
+    const int team = e.team, w = e.w, lane = e.lane, tok = lane_token(lane), nb = p.I / kBlk;
+    const uint32_t stage = smem_u32(e.epi) + (team * 2 + (n & 1)) * 2048;
+    const uint32_t slot = smem_u32(e.epi) + stage_bytes(kGatedOnly) + (team * 4 + (n & 3)) * 1024;
+    const int out_tok = w * 8 + (lane >> 2), piece = lane & 3;
+    bool ok = mbar_wait_bounded(&tail.words[team][n & 3], (n >> 2) & 1, &tail.abort);
+    uint32_t word = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) word = max(word, lds32(slot + (k * 32 + tok) * 4));
+    if (e.rank == 0 && w == 0 && tok < c.rows) store_scale(p.A_scale, p.out_ue8m0, (c.row0 + tok) * nb + c.fb, word);
+    const uint32_t inv = __float_as_uint(scale_reciprocal(word));
+    uint32_t q[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const float2 i = make_float2(__uint_as_float(of_token(inv, 2 * x, lane)), __uint_as_float(of_token(inv, 2 * x + 1, lane)));
+        q[x] = codes_of(__fmul2_rn(c.a[x][0], i), __fmul2_rn(c.a[x][1], i));
+    }
+    store_rows(stage + lane * 64 + ((w ^ ((lane >> 1) & 3)) << 4), q);
+    ok = team_all(team, ok);
+    if (ok && out_tok < c.rows)
+        *reinterpret_cast<uint4 *>(p.A + (c.row0 + out_tok) * p.I + c.fb * kBlk + e.rank * 64 + piece * 16) =
+            in_order(lds128(stage + out_tok * 64 + ((piece ^ ((out_tok >> 1) & 3)) << 4)));
+    return ok;
+}
+
+__device__ __forceinline__ void gated_only_epilogue(const Params &p, Tail &tail, const EpilogueWarp &e)
+{
+    constexpr int kChunkStep = Chunks<kGatedOnly>::kStep;
+    const int team = e.team, w = e.w, lane = e.lane, tok = lane_token(lane);
+    const uint32_t words = smem_u32(e.epi) + stage_bytes(kGatedOnly) + team * 4 * 1024;
+    const uint32_t lane_addr = e.tmem + (static_cast<uint32_t>(w * 32) << 16);
+    int j = 0;
+    uint32_t n = 0;                                    // this team's chunks
+    bool ok = true;
+    PendingChunk before;
+    Chunks<kGatedOnly> chunks(team);
+    for (Walk walk(e.pair, p.m_tiles); walk.tile < e.tiles; walk.next(e.pairs, p.m_tiles), chunks.next(), ++j) {
+        const Tile t = walk.get(tail);
+        const int b = j & 1;
+        ok = team_all(team, mbar_wait_bounded(&tail.acc_full[b], (j >> 1) & 1, &tail.abort, 64));
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (chunks.begin() >= t.rows) release_accumulator(tail, b, lane);
+        for (int c0 = chunks.begin(); c0 < t.rows; c0 += kChunkStep, ++n) {
+            float v[32];
+            tmem_ld_fragments(lane_addr + b * kTileN + c0, v);
+            tmem_ld_wait();
+            if (c0 + kChunkStep >= t.rows) release_accumulator(tail, b, lane);
+            PendingChunk now;
+            now.row0 = t.row0 + c0;
+            now.rows = t.rows - c0;
+            now.fb = t.m0 / kTileM;
+            float m[8];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float2 g = both(v, 4 * c + 2 * r);
+                    now.a[c][r] = __fmul2_rn(__fmul2_rn(g, sigmoid2(g)), both(v, 16 + 4 * c + 2 * r));
+                }
+                m[2 * c] = fmaxf(fabsf(now.a[c][0].x), fabsf(now.a[c][1].x));
+                m[2 * c + 1] = fmaxf(fabsf(now.a[c][0].y), fabsf(now.a[c][1].y));
+            }
+            const uint32_t word = block_scale_byte(max_of_lanes(m, lane));
+            uint64_t *bar = &tail.words[team][n & 3];
+            if (w == 0 && lane == 0) mbar_arrive_expect_tx(bar, 8 * 32 * 4);
+            const uint32_t to = words + (n & 3) * 1024 + ((e.rank * 4 + w) * 32 + tok) * 4;
+            send_word(to, word, smem_u32(bar), 0);
+            send_word(to, word, smem_u32(bar), 1);
+            if (n > 0) {
+                ok = finish_chunk(p, tail, e, before, n - 1);
+                if (!ok) break;
+            }
+            before = now;
+        }
+        if (!ok) break;
+    }
+    if (ok && n > 0) finish_chunk(p, tail, e, before, n - 1);
 }
 
 // ---------------------------------------------------------------------------

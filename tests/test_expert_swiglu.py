@@ -206,6 +206,9 @@ def test_repeated_calls_and_every_position(dev):  # noqa: F811
         assert all(torch.equal(a, b) for a, b in zip(vars(again).values(), vars(h).values()))
         again = moe.expert_swiglu_backward(x8, xs, W2, s2, h.GU_fp8, h.GU_scale, off)
         assert all(torch.equal(a, b) for a, b in zip(vars(again).values(), vars(r).values()))
+    for _ in range(30):
+        again = moe.expert_swiglu(x8, xs, W1, s1, off, keep=False)
+        assert again.GU_fp8 is None and torch.equal(again.A_fp8, h.A_fp8) and torch.equal(again.A_scale, h.A_scale)
     e = max(range(24), key=lambda i: counts[i])
     at = slice(offs[e] + 3, offs[e] + 100)
     part = moe.expert_swiglu(x8[at].contiguous(), xs[at].contiguous(), W1[e], s1[e])
