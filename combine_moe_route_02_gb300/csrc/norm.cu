@@ -9,6 +9,7 @@
 // the same 332 (6.5 TB/s); one row 2.4 us in a graph.  The gradient of 16381 x 1032 takes 27 us in a graph where its
 // bytes take 15: two launches and the ring's start are 7 of it, and a row's 129 chunks are five to a lane, the last nearly
 // empty (H = 1024: 23; three warps to a row: 29; a condition on each chunk's loads: 30).
+#include "bulk_ring.cuh"
 #include "expert_internal.cuh"
 
 namespace moe {
@@ -204,6 +205,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMostThreads, kWarp ?
     __shared__ float part[2][kMostThreads / 32];
     __shared__ uint64_t full[kSlots];
     __shared__ volatile int abort;
+    __shared__ uint32_t issued;   // groups asked for (thread 0's)
     extern __shared__ __align__(128) uint8_t ring[];
     const int T = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x & 31 : threadIdx.x, chunks = p.H >> 3;
     constexpr int rows = kWarp ? kWarpRows : 1;
@@ -227,6 +229,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMostThreads, kWarp ?
         bulk_load(to, p.dY + at, bytes, &full[slot]);
         bulk_load(to + array, p.S + at, bytes, &full[slot]);
         if (p.dS) bulk_load(to + 2 * array, p.dS + at, bytes, &full[slot]);
+        issued = static_cast<uint32_t>(i) + 1;
     };
     if (threadIdx.x == 0)
         for (int i = 0; i < p.slots && i < mine; ++i) issue(i, i);
@@ -336,12 +339,13 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMostThreads, kWarp ?
     }
     pdl_launch_dependents();
     flush(first);
+    __syncthreads();              // (a thread may have given up at the last group)
     if (threadIdx.x == 0 && abort) {
         report_status(p.status, MOE_ERR_TIMEOUT);
         // what may still be under way lands before this CTA's memory is another's
-        for (int i = 0; i < p.slots; ++i) {
+        for (uint32_t x = ring_first_open(issued, p.slots); x < issued; ++x) {
             volatile int no_abort = 0;
-            mbar_wait_bounded(&full[i], phase ^ (i < slot ? 1u : 0u), &no_abort);
+            mbar_wait_bounded(&full[ring_place(x, p.slots)], ring_parity(x, p.slots), &no_abort);
         }
     }
 }
