@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMostThreads, kWarp ?
         const uint8_t *at = own + slot * stage;
         const uint4 *dy = reinterpret_cast<const uint4 *>(at), *s = reinterpret_cast<const uint4 *>(at + array),
                     *ds = reinterpret_cast<const uint4 *>(at + 2 * array);
-        // dy s, whose sum with the weights has a factor rstd to go, twice
+        // d = dy w times xh = s rstd, and the weight's sum.  (s rstd comes first: dy s may be beyond 32 bits where rstd is 0, and
+        // that row's part of the sums would be a NaN.)
         // (only the last chunk of a thread may not be there: the loads of the others carry no condition, which would make
         // them wait for one another)
         float2 dot = twice(0.f);
@@ -305,14 +306,14 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMostThreads, kWarp ?
                 load_weight2(p.w, p.w_bf16, c, w);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 v = __fmul2_rn(a[i], b[i]);
-                    dot = __ffma2_rn(v, w[i], dot);
-                    acc[j][i] = __ffma2_rn(v, twice(rstd), acc[j][i]);
+                    const float2 xh = __fmul2_rn(b[i], twice(rstd));
+                    dot = __ffma2_rn(__fmul2_rn(a[i], w[i]), xh, dot);
+                    acc[j][i] = __ffma2_rn(a[i], xh, acc[j][i]);
                 }
             }
         }
         if (kWarp) __syncthreads();
-        const float by = -rstd * (rstd * (rstd * (row_sum<kWarp>(dot.x + dot.y, part[n & 1]) * per_H)));
+        const float minus_mean = -(row_sum<kWarp>(dot.x + dot.y, part[n & 1]) * per_H);
         // every thread is past that barrier, so none reads the group before any more: its place is filled again
         if (threadIdx.x == 0 && g > 0 && g - 1 + p.slots < mine && !abort) issue(g - 1 + p.slots, before);
         if (row_ok) {
@@ -326,8 +327,10 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMostThreads, kWarp ?
                 unpack2(p.dS ? ds[T * j] : make_uint4(0, 0, 0, 0), e);
                 load_weight2(p.w, p.w_bf16, c, w);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    a[i] = __ffma2_rn(__fmul2_rn(a[i], w[i]), twice(rstd), __ffma2_rn(b[i], twice(by), e[i]));
+                for (int i = 0; i < 4; ++i) {
+                    const float2 d = __ffma2_rn(__fmul2_rn(b[i], twice(rstd)), twice(minus_mean), __fmul2_rn(a[i], w[i]));
+                    a[i] = __ffma2_rn(d, twice(rstd), e[i]);
+                }
                 dx[T * j] = pack2(a);
             }
         }

@@ -575,6 +575,8 @@ MOE_API size_t moe_rms_norm_backward_workspace_size(int64_t N, int H);
  *   dweight fp32 [H], summed in fp32 in an order that depends on N and H alone
  *   workspace  moe_rms_norm_backward_workspace_size() bytes, 16-byte aligned, in any state; calls that
  *              may overlap need their own
+ * A row with rstd 0 (its squares left fp32) gives dS to dX, or zeros, and nothing to dweight.  Infinities and NaNs reach
+ * their own row of dX, and dweight.
  * N == 0 writes dweight (add, or zeros).  Sizes as moe_rms_norm.  Two launches.
  * Errors: as moe_rms_norm, and MOE_ERR_WORKSPACE; status_word: MOE_ERR_TIMEOUT.
  */
