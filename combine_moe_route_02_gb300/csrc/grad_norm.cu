@@ -219,9 +219,10 @@ __global__ void __launch_bounds__(kThreads)
     const double v = norm_of(sums, n, part);
     if (threadIdx.x == 0) {
         const double c = max_norm / (v + 1e-6);
-        // a norm that is no finite number leaves the tensors as they are
-        by = c < 1 && v <= 1.7976931348623157e308 ? static_cast<float>(c) : 1.f;
-        if (norm && blockIdx.x == 0) *norm = static_cast<float>(v);
+        // a norm that is no finite number leaves the tensors as they are, and what decides is the norm that the caller sees
+        const float seen = static_cast<float>(v);
+        by = c < 1 && seen <= 3.402823466e38f ? static_cast<float>(c) : 1.f;
+        if (norm && blockIdx.x == 0) *norm = seen;
     }
     __syncthreads();
     const float c = by;

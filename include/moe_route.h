@@ -610,7 +610,7 @@ MOE_API moe_status moe_grad_norm(const void *const *grads, const int64_t *sizes,
  *   out   HOST array of n device pointers of the same types, or NULL: in place (nothing is written if c is 1).
  *         out[i] may be grads[i]; any other overlap, and a tensor that is listed twice, is undefined
  *   max_norm >= 0
- * If any value is infinite or NaN, c is 1: the caller sees it in norm.
+ * If norm is infinite or NaN (a value is, or the norm of finite ones is beyond fp32), c is 1.
  * Errors: as moe_grad_norm.
  */
 MOE_API moe_status moe_clip_grad_norm(const void *const *grads, void *const *out, const int64_t *sizes,
