@@ -28,6 +28,7 @@ moe_status moe_rms_norm(const void *X, const void *residual, const void *weight,
     if ((residual == nullptr) != (S == nullptr) && N > 0) return MOE_ERR_INVALID_ARG;
     if (N == 0) return MOE_OK;
     if (!X || !weight || (!Y && !Y_fp8)) return MOE_ERR_INVALID_ARG;
+    if (S && S == Y) return MOE_ERR_INVALID_ARG;       // (both may be X, but not at once)
     if (!aligned(X, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(S, 16) || !aligned(Y, 16) ||
         !aligned(Y_fp8, 16) || !aligned(rstd, 4) || (scale_format == MOE_SCALE_FP32 && !aligned(Y_scale, 4)))
         return MOE_ERR_MISALIGNED;

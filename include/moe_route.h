@@ -549,7 +549,7 @@ typedef enum moe_grad_type { MOE_GRAD_FP32 = 0, MOE_GRAD_BF16 = 1 } moe_grad_typ
  *   y = s * rstd * weight
  *   X, residual bf16 [N, H] (residual may be NULL), weight [H] (weight_type: a moe_grad_type), 0 < eps <= 1
  *   S bf16 [N, H]: with a residual, and only then; may be the residual or X
- *   Y bf16 [N, H] or NULL (may be X): what moe_route and moe_dispatch read
+ *   Y bf16 [N, H] or NULL (may be X, but not S): what moe_route and moe_dispatch read
  *   Y_fp8 uint8 [N, H], Y_scale [N, H/128] (scale_format) or both NULL (H % 128 == 0): y in E4M3 by the
  *   rule of moe_permute, quantised from the unrounded y, for products of all rows (a shared expert)
  *   rstd fp32 [N] or NULL: what moe_rms_norm_backward reads
