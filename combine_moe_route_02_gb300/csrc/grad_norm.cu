@@ -343,7 +343,7 @@ cudaError_t launch_grad_norm(const GradArgs &a, cudaStream_t stream)
 size_t grad_norm_workspace_bytes(int n)
 {
     // a sum for each CTA of each launch
-    return static_cast<size_t>(n <= kFew ? 1 : (n + kMany - 1) / kMany) * kGradNormCtas * sizeof(double);
+    return static_cast<size_t>(n <= kFew ? 1 : (n - 1) / kMany + 1) * kGradNormCtas * sizeof(double);
 }
 
 }  // namespace moe
