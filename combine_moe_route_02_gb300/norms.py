@@ -66,7 +66,8 @@ def rms_norm(X: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
              stream=None) -> RMSNorm:
     """y = s * rstd * weight with s = bf16(X + residual) (S; X itself without a residual) and rstd = 1 / sqrt(mean
     s^2 + eps): in bf16 (Y) and/or in E4M3 with 1x128 scales (Y_fp8, Y_scale).  X, residual bf16 [N, H], weight [H]
-    float32 or bfloat16.  `out` names the tensors to write (None: not wanted; its S may be the residual)."""
+    float32 or bfloat16.  `out` names the tensors to write (None: not wanted; its S may be the residual, or X where Y
+is not; without a residual it is X or None)."""
     fmt = _scale_format(scale_format)
     N, H = _dims(X, "X", 2)
     dev = _home(X, "X")
@@ -82,7 +83,12 @@ def rms_norm(X: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
         y, q = _opt(out.Y, "Y", torch.bfloat16, (N, H), dev), _opt(out.Y_fp8, "Y_fp8", torch.uint8, (N, H), dev)
         sq = _opt(out.Y_scale, "Y_scale", _scale_dtype(scale_format), (N, H // BLOCK), dev)
         r = _opt(out.rstd, "rstd", torch.float32, (N,), dev)
-        s = None if residual is None else _arg(out.S, "S", torch.bfloat16, (N, H), dev)
+        if residual is not None:
+            s = _arg(out.S, "S", torch.bfloat16, (N, H), dev)
+        else:
+            s = None
+            if out.S is not None and out.S.data_ptr() != x:
+                raise ValueError("without a residual the stream is X itself: S of `out` must be X or None")
     code = lib().moe_rms_norm(x, res, w, wt, eps, N, H, s, y, q, sq, fmt, r, _raw_stream(stream, dev))
     if code:
         _check(code, "moe_rms_norm")

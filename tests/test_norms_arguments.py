@@ -1,6 +1,10 @@
 """Calls of the norms that no result can be right for: refused, with what is wrong."""
-from test_experts import A, B, C, D, F, INVALID, L  # noqa: F401
-from test_norms import BF16, F32, weight
+import pytest
+import torch
+
+import combine_moe_route_02_gb300 as moe
+from test_experts import A, B, C, D, F, INVALID, L, dev, gpu, normal  # noqa: F401
+from test_norms import F32, weight
 
 
 def test_the_stream_and_the_normed_rows_are_not_one_tensor(L):  # noqa: F811
@@ -14,3 +18,15 @@ def test_workspace_of_the_longest_lists(L):  # noqa: F811
     one = L.moe_grad_norm_workspace_size(1)
     for n in (2 ** 31 - 1024, 2 ** 31 - 1023, 2 ** 31 - 1):
         assert L.moe_grad_norm_workspace_size(n) == -(-n // 1024) * one
+
+
+@gpu
+def test_no_stale_stream_without_a_residual(dev):  # noqa: F811
+    """Without a residual the stream is X itself: another tensor of `out` would stay what it was."""
+    x, w = normal((5, 256), 1, dev), weight(256, F32, dev)
+    y, s, r = torch.empty_like(x), torch.zeros_like(x), torch.empty(5, device=dev)
+    with pytest.raises(ValueError, match="S"):
+        moe.rms_norm(x, w, out=moe.RMSNorm(y, None, None, s, r))
+    for own in (x, None):
+        out = moe.rms_norm(x, w, out=moe.RMSNorm(y, None, None, own, r))
+        assert torch.equal(out.Y, moe.rms_norm(x, w).Y) and out.S is own
