@@ -141,6 +141,16 @@ def _list(tensors: Sequence[torch.Tensor], name: str, dev: int):
     return ptrs, sizes, dtypes
 
 
+def _distinct(ptrs, written, sizes):
+    """Refuses a tensor that would be scaled twice, or into another one that is still to be read."""
+    pairs = [(p, q) for p, q, k in zip(ptrs, written, sizes) if k]
+    if len({q for _, q in pairs}) != len(pairs):
+        raise ValueError("a tensor is listed twice: it would be scaled twice")
+    read = {p for p, _ in pairs}
+    if any(p != q and q in read for p, q in pairs):
+        raise ValueError("out[i] may be grads[i], but no other of the gradients")
+
+
 def _norm_out(need: int, device, result: bool):
     return (torch.empty((1,), dtype=torch.float32, device=device) if result else None,
             torch.empty((need,), dtype=torch.uint8, device=device))
@@ -159,8 +169,8 @@ def _norm_call(grads, out, max_norm, norm, stream):
         written, out_sizes, out_dtypes = _list(out, "out", dev)
         if out_sizes != sizes or out_dtypes != dtypes:
             raise ValueError("out must have the sizes and types of grads")
-    if max_norm is not None and len(set(written)) != n and len({p for p, k in zip(written, sizes) if k}) != sum(1 for k in sizes if k):
-        raise ValueError("a tensor is listed twice: it would be scaled twice")
+    if max_norm is not None and len(set(ptrs if out is None else ptrs + written)) != (n if out is None else 2 * n):
+        _distinct(ptrs, written, sizes)
     need = lib().moe_grad_norm_workspace_size(n)
     new, ws = _on(stream, _norm_out, need, torch.device("cuda", dev), norm is None)
     res = new.data_ptr() if norm is None else _arg(norm, "norm", torch.float32, (1,), dev)
@@ -187,7 +197,7 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
                    norm: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Scale the tensors by min(1, max_norm / (norm + 1e-6)), in place or into the tensors of `out`, without the
     host seeing the norm; returns it (before the scaling), float32 [1].  If it is not finite, the tensors are left
-    as they are (copied to `out`)."""
+    as they are (copied to `out`).  out[i] may be grads[i]; no tensor that is written may overlap another otherwise."""
     max_norm = float(max_norm)
     if not max_norm >= 0:
         raise ValueError("max_norm must not be negative or NaN")

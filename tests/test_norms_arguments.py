@@ -30,3 +30,15 @@ def test_no_stale_stream_without_a_residual(dev):  # noqa: F811
     for own in (x, None):
         out = moe.rms_norm(x, w, out=moe.RMSNorm(y, None, None, own, r))
         assert torch.equal(out.Y, moe.rms_norm(x, w).Y) and out.S is own
+
+
+@gpu
+def test_clipping_into_another_gradient_is_refused(dev):  # noqa: F811
+    a, b = torch.ones(100, device=dev), torch.ones(100, device=dev)
+    with pytest.raises(ValueError, match="out"):
+        moe.clip_grad_norm([a, b], 1.0, out=[b, a])
+    with pytest.raises(ValueError, match="out"):
+        moe.clip_grad_norm([a, b], 1.0, out=[torch.empty_like(a), a])
+    moe.clip_grad_norm([a, b], 1.0, out=[a, torch.empty_like(b)])           # its own place is allowed
+    e = torch.empty(0, device=dev)
+    moe.clip_grad_norm([a, e, e], 1.0, out=[a, e, e])
