@@ -27,9 +27,10 @@
 //   warps 4..7  epilogue: TMEM -> registers -> bf16, transposed through shared memory; with the gated
 //               activation or its gradient (expert_gemm_epilogue.cuh) the warps from 4 on
 //
-// Measured (burst, 1.94 GHz): 16384 tokens on 128 experts, top 8, 2048 x 2048: 354 us, 3.1 PFLOP/s, the
-// tensor pipe 67% busy; the rest is the latency of a ring that 180 KiB in flight per SM do not quite cover
-// (back to back the board's power limit makes it 417 us).  The input gradient of 16381 unevenly routed
+// Measured (bursts, 1.94 GHz): 16384 tokens on 128 experts, top 8, 2048 x 2048: 354 to 372 us, 3.0 PFLOP/s, the
+// tensor pipe 67% busy; the rest is the latency of a ring that 180 KiB in flight per SM do not quite cover (no unit
+// is at its limit: the joined products, whose loop it is too, have L2 at 51 to 59% and read 12 to 13 TB/s from it; back
+// to back the board's power limit makes it 417 us, and uniformly random codes draw so much that they take 391 in bursts).  The input gradient of 16381 unevenly routed
 // tokens, 64 experts of 1024 x 4096: 122 us against 85 for its bytes.
 #include <mutex>
 

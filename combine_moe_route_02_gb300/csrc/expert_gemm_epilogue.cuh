@@ -156,7 +156,8 @@ __device__ __forceinline__ uint4 in_pairs(const uint4 &x)
                       __byte_perm(x.y, x.w, 0x7362));
 }
 
-// Shared memory by its address (through a pointer that went through a struct the accesses are generic ones).
+// Shared memory by its address (the ring's start is rounded up through an integer, so that accesses through pointers
+// derived from it are generic ones).
 __device__ __forceinline__ uint4 lds128(uint32_t a)
 {
     uint4 v;
@@ -210,9 +211,9 @@ __device__ __forceinline__ void send_word(uint32_t addr, uint32_t word, uint32_t
 // eight warps; each finds the scale bytes of its 16 features (the byte of the largest is the largest byte), sends a
 // word of three for each token to both CTAs, and takes the largest of eight.
 //
-// Measured (bursts): 16384 tokens, 128 experts, top 8, H = 2048, I = 1024: 386 to 400 us, 2.75 to 2.85 PFLOP/s, where the
-// product alone with its bf16 rows takes 371 to 390 on the same boxes, and the launch without any epilogue 328; back to back
-// 451 (the board's power).  The tensor pipe is 66% busy, DRAM 59%.
+// Measured: 16384 tokens, 128 experts, top 8, H = 2048, I = 1024: 381 us in graphs of 20 after a pause, 2.9 PFLOP/s (in
+// bursts of 5: 389), where the product alone with its bf16 rows and the same operands takes 367 (372); the launch without
+// any epilogue 328; back to back 444, the product alone 420 (the board's power).  The tensor pipe is 63 to 66% busy, DRAM 59%.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, const EpilogueWarp &e)
 {
@@ -325,8 +326,8 @@ __device__ __forceinline__ void gated_epilogue(const Params &p, Tail &tail, cons
 // which says that every warp has read those of n - 4: four buffers in turn.  The codes of chunk n are put where those of
 // n - 2 lay, which the team has read before its barrier of n - 1: two.
 //
-// Measured: 16381 tokens of 64 experts, H = 1024, I = 2048 (8 blocks of reduction a tile: the epilogue sets the pace): 114 us
-// in bursts, 127 back to back (waiting for each chunk's words at once 127 and 137); 99 and 110 without an epilogue.
+// Measured: 16381 tokens of 64 experts, H = 1024, I = 2048 (8 blocks of reduction a tile: the epilogue sets the pace): 111 to
+// 114 us in bursts, 127 back to back (waiting for each chunk's words at once 127 and 137); 99 and 110 without an epilogue.
 // ---------------------------------------------------------------------------
 struct PendingChunk {
     float2 a[4][2];
@@ -420,11 +421,12 @@ __device__ __forceinline__ void gated_only_epilogue(const Params &p, Tail &tail,
 //   s = 1 / (1 + exp(-g));  dg = da u s (1 + g (1 - s));  du = da g s
 // in bf16 and in E4M3.  A CTA's 128 features are a block, its scale bytes are joined over a team's four warps.
 //
-// Chunks of 16 tokens (c = 0, 1; element 8 h + 4 c + 2 r + i of a lane) keep a warp within 96 registers, so that four
-// teams fit: the work of a chunk is a chain of short steps, and what hides their latency is the number of warps.
+// Chunks of 16 tokens (c = 0, 1; element 8 h + 4 c + 2 r + i of a lane) keep a warp near 96 registers (two words are
+// spilled), so that four teams fit: the work of a chunk is a chain of short steps, and what hides their latency is the
+// number of warps.
 //
-// Measured: 16384 tokens, 128 experts, top 8, H = 2048, I = 1024: 321 us in short graphs, 351 back to back (power), 4.6
-// TB/s of its bytes; without any epilogue 200, the bytes alone 239.  Issue slots 51% busy, DRAM 70%.
+// Measured: 16384 tokens, 128 experts, top 8, H = 2048, I = 1024: 314 to 321 us in short graphs, 348 back to back (power),
+// 5.1 TB/s of its bytes; without any epilogue 200, the bytes alone 239.  Issue slots 50% busy, DRAM 70%.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void load_fragments16(uint32_t taddr, float (&v)[16])
 {

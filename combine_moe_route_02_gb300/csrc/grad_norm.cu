@@ -12,6 +12,9 @@
 // in the opposite order, since the last ones are what is left in L2 (24 blocks of 152 MB in bf16: 78 us against 81).
 // HBM's bound: 402M fp32 gradients (1.6 GB) read twice and written once in 731 us, 6.6 TB/s.  Chunks of 16 KiB and twice
 // the CTAs 747, a CTA for each chunk in the second launch 869, five CTAs an SM there 753, stores that stay in L2 737.
+// 1024 tensors of 65536 fp32 values 132 us in a graph, one of as many values 128; 2500 of 26840 (three launches of either
+// kernel) 160.  An output whose address differs from the input's modulo 16 is written by single values: 67M bf16 values
+// 230 us against 64, fp32 278 against 128.
 #include "expert_internal.cuh"
 
 namespace moe {

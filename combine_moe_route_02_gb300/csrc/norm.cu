@@ -6,9 +6,11 @@
 // One pass over the rows: a row stays in the registers of its threads (a warp's for short rows, else a CTA's; kV
 // chunks of 16 bytes each, neighbouring threads neighbouring chunks) between its sum and what is written.  The sums
 // are held in 32 bits.  HBM's bound: 65536 x 4096 with the residual and E4M3 rows 349 us (6.9 TB/s), the gradient of
-// the same 332 (6.5 TB/s); one row 2.4 us in a graph.  The gradient of 16381 x 1032 takes 27 us in a graph where its
-// bytes take 15: two launches and the ring's start are 7 of it, and a row's 129 chunks are five to a lane, the last nearly
-// empty (H = 1024: 23; three warps to a row: 29; a condition on each chunk's loads: 30).
+// the same 334 (6.4 TB/s); one row 2.4 us in a graph.  Rows of a warp: 65536 x 1024 with the residual and E4M3 rows 91 us
+// (6.6 TB/s), 262144 x 128 69 (4.4: a lane has one chunk or none, and what is under way is little).  The gradient of
+// 16381 x 1032 takes 27 us in a graph where its bytes take 15: two launches and the ring's start are 7 of it, and a row's
+// 129 chunks are five to a lane, the last nearly empty (H = 1024: 24; three warps to a row: 29; a condition on each
+// chunk's loads: 30).
 #include "bulk_ring.cuh"
 #include "expert_internal.cuh"
 
