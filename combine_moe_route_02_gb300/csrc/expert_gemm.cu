@@ -374,17 +374,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
             gated_grad_epilogue(p, tmY, tail, wp);
     }
 
-    if constexpr (gated(kMode)) {
-        // a CTA that gave up a wait may have words on their way to the other's memory: they have landed long
-        // before this time is over
-        if (*abort_flag) __nanosleep(1000000);
-    }
     tc_fence_before_sync();
     cluster_sync();               // the leader's MMAs have read the other CTA's memory
     tc_fence_after_sync();
     if (warp == 3) tmem_dealloc_pair(tmem, kTmemCols);
     if (threadIdx.x == 0) {
-        if (tail.abort) report_status(p.status, MOE_ERR_TIMEOUT);
+        if (tail.abort) {
+            report_status(p.status, MOE_ERR_TIMEOUT);
+            if constexpr (gated(kMode)) {
+                // This CTA may have given up a wait for scale words.  The other one sends none any more, being past its
+                // last chunk too, and those on their way here land long before this time (1 ms by the clock) is over.
+                // (A CTA that gave up no wait has had all of its words.)
+                const uint64_t t0 = globaltimer_ns();
+                for (int i = 0; i < (1 << 20) && globaltimer_ns() - t0 < 1000000; ++i) __nanosleep(1000);
+            }
+        }
         if (tail.bad_index) report_status(p.status, MOE_ERR_BAD_INDEX);
         if (tail.bad_scale) report_status(p.status, MOE_ERR_BAD_SCALE);
     }
