@@ -169,6 +169,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
                 mbar_wait_bounded(&tail.full[x % kRing], (x / kRing) & 1u, &no_abort);
             }
         }
+        if (rank != 0) {
+            // the leader's commits arrive in this CTA's memory too: it stays until the last of them has
+            volatile int no_abort = 0;
+            mbar_wait_bounded(&tail.drain, 0, &no_abort, 32);
+        }
     } else if (warp == 1 && rank != 0) {
         uint32_t s = 0, ph = 0;
         bool ok = true;

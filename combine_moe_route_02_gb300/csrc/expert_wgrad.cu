@@ -307,6 +307,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mbar_wait_bounded(&tail.full[x % kStages], (x / kStages) & 1u, &no_abort);
             }
         }
+        if (rank != 0) {
+            // the leader's commits arrive in this CTA's memory too: it stays until the last of them has
+            volatile int no_abort = 0;
+            mbar_wait_bounded(&tail.drain, 0, &no_abort, 32);
+        }
     } else if (warp == 1 && rank == 0) {
         const uint64_t a0 = make_smem_desc_sw128(smem_u32(ring), kBox, 1024);
         const uint64_t b0 = make_smem_desc_sw128(smem_u32(ring + kABytes), kBox, 1024);
